@@ -8,7 +8,12 @@
  *   ssm_causal_conv1d_fwd   the causal depthwise convolution + SiLU that feeds the scan;
  *   ssm_causal_conv1d_step  its one-token form on a carried window, updated in place;
  *   ssm_selective_scan_bwd  the gradients of the scan (training), states recomputed;
- *   ssm_ssd_fwd             Mamba-2's state-space dual by chunks, on tensor cores.
+ *   ssm_ssd_fwd             Mamba-2's state-space dual by chunks, on tensor cores;
+ *   ssm_delta_rule_fwd      the gated delta rule over a whole sequence, its gradients
+ *   ssm_delta_rule_bwd      and its decode tokens on a carried state, updated in place;
+ *   ssm_delta_rule_step
+ *   ssm_layer_norm_fwd      layer norm over rows, and its gradients.
+ *   ssm_layer_norm_bwd
  *
  * The scan and the state step compute, per sequence b and channel d, with an N-wide fp32 state h:
  *     Delta_t = softplus(delta[b,d,t] + delta_bias[d])   (bias and softplus optional)
@@ -24,9 +29,10 @@
  *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers owned by the caller; the library keeps
- *    no state between calls.  Two calls may take a temporary scratch buffer with
+ *    no state between calls.  Four calls may take a temporary scratch buffer with
  *    cudaMallocAsync / cudaFreeAsync on cuda_stream: ssm_selective_scan_fwd (and _ex)
- *    for long sequences with few channels (see below), and ssm_selective_scan_bwd.
+ *    for long sequences with few channels (see below), ssm_selective_scan_bwd,
+ *    ssm_delta_rule_bwd and ssm_layer_norm_bwd.
  *    ssm_selective_scan_fwd_noalloc is the scan's form that never allocates; every
  *    other call allocates nothing.
  *  - Every pointer must be 16-byte aligned (SSM_ERR_ALIGNMENT otherwise).
@@ -37,9 +43,10 @@
  *  - dtype codes: SSM_F32 (fp32) or SSM_BF16 (bf16).  A, D, delta_bias and the state
  *    are always fp32; the state arithmetic is fp32 whatever the input dtype.
  *  - For the S6 calls (scan, backward, state steps) dstate (N) must be in 1..16
- *    (SSM_ERR_UNSUPPORTED above 16); ssm_ssd_fwd takes its own sizes (below).
- *  - Output buffers must not overlap input buffers (the convolution checks and returns
- *    SSM_ERR_INVALID_ARG; for the scan the result of an overlap is undefined).
+ *    (SSM_ERR_UNSUPPORTED above 16); ssm_ssd_fwd and the delta rule take their own (below).
+ *  - Output buffers must not overlap input buffers (the convolution, the delta rule and the
+ *    layer norm check and return SSM_ERR_INVALID_ARG; for the scan the result of an overlap
+ *    is undefined).
  */
 #ifndef SSM_H_
 #define SSM_H_
@@ -297,6 +304,103 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
                 const float *initial_state, float *final_state,
                 int batch, int seqlen, int heads, int headdim, int dstate,
                 int in_dtype, int out_dtype, void *cuda_stream);
+
+/*
+ * The gated delta rule over whole sequences: the state-space dual's headdim x dstate state
+ * per head with the delta correction (what the state already answers for the key is taken
+ * off the value before it is written).  Per sequence and head,
+ *     S' = exp(a_t) S,   e_t = v_t - S' k_t,   S = S' + beta_t e_t k_t^T,   y_t = scale S q_t
+ * computed by chunks of 16 tokens: inside a chunk the corrections e solve a triangular
+ * system, between chunks the state stays in registers.
+ *
+ *   q, k          : [batch][seqlen][qk_heads][dstate], in_dtype.  qk_heads divides heads:
+ *                   head h reads key head h / (heads / qk_heads).
+ *   v, y          : [batch][seqlen][heads][headdim], in_dtype / out_dtype (y written).
+ *   a, beta       : [batch][seqlen][heads] fp32.  a is the log decay (any value, -inf forgets
+ *                   everything before the token); beta any value, 0 writes nothing.
+ *   initial_state : [batch][heads][headdim][dstate] fp32 or NULL (zero).
+ *   final_state   : the same, or NULL (not written).  May be initial_state itself.
+ * headdim and dstate must be multiples of 8, headdim <= 256 and dstate <= 128
+ * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on bf16 pieces of the
+ * fp32 operands with fp32 accumulation: the final state and an fp32 y are good to a few
+ * 2^-20 of their size (normwise), a bf16 y to its own rounding and 2^-16.  A value that is
+ * not finite spreads over the rest of its chunk, earlier tokens included.
+ * seqlen = 0 copies the start state through.  Allocates nothing.
+ */
+int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
+                       void *y, const float *initial_state, float *final_state, float scale,
+                       int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
+                       int in_dtype, int out_dtype, void *cuda_stream);
+
+/*
+ * Decode tokens of the gated delta rule on a carried state: ntok tokens per sequence, the
+ * state read and written once.
+ *
+ *   state   : [batch][heads][headdim][dstate] fp32, read and overwritten.
+ *   q, k    : [ntok][batch][qk_heads][dstate], in_dtype.   v, y: [ntok][batch][heads][headdim].
+ *   a, beta : [ntok][batch][heads] fp32.
+ * Sizes and heads as for ssm_delta_rule_fwd; the arithmetic is fp32.  Several tokens in one
+ * call give bit for bit what as many calls of one token give.  ntok = 0 does nothing.
+ */
+int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *v, const float *a,
+                        const float *beta, void *y, float scale, int ntok, int batch, int heads,
+                        int qk_heads, int headdim, int dstate, int in_dtype, int out_dtype,
+                        void *cuda_stream);
+
+/*
+ * Backward of the gated delta rule: the gradients of
+ *     loss = sum dy . y + sum dfinal_state . final_state
+ * with respect to every input of ssm_delta_rule_fwd.  The states are recomputed; with mu the
+ * adjoint of S_t, lambda = mu + scale dy_t q_t^T, de_t = beta_t lambda k_t: dv_t = de_t,
+ * dq_t = scale S_t^T dy_t, dk_t = lambda^T (beta_t e_t) - S'_t^T de_t, dbeta_t = e_t.(lambda k_t),
+ * da_t = <lambda - de_t k_t^T, S'_t>, and mu <- exp(a_t) (lambda - de_t k_t^T).
+ *
+ *   inputs        : as ssm_delta_rule_fwd.
+ *   dy            : [batch][seqlen][heads][headdim], grad_dtype.
+ *   dfinal_state  : [batch][heads][headdim][dstate] fp32 or NULL (zero).
+ *   dq, dk        : [batch][seqlen][qk_heads][dstate], grad_dtype, written: the sums over the
+ *                   heads that share the key head.
+ *   dv            : [batch][seqlen][heads][headdim], grad_dtype, written.
+ *   da, dbeta     : [batch][seqlen][heads] fp32, written.
+ *   dinitial_state: [batch][heads][headdim][dstate] fp32 or NULL.
+ * Every sum has a fixed order: results are deterministic.  Takes a stream-ordered scratch
+ * buffer (cudaMallocAsync / cudaFreeAsync on cuda_stream) of about
+ * 8 * batch * heads * headdim * (seqlen + dstate * (seqlen / 64 + 2)) bytes.
+ * seqlen = 0 writes dinitial_state = dfinal_state.
+ */
+int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
+                       const float *initial_state, const void *dy, const float *dfinal_state,
+                       void *dq, void *dk, void *dv, float *da, float *dbeta, float *dinitial_state,
+                       float scale, int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
+                       int in_dtype, int grad_dtype, void *cuda_stream);
+
+/*
+ * Layer norm over rows (the norm in front of a mixer, or of its output per token and head):
+ *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *
+ *   x, y         : [rows][dim], in_dtype / out_dtype (y written).
+ *   weight, bias : [dim] fp32, or NULL (1 and 0).
+ *   mean, rstd   : [rows] fp32, written, or NULL.  ssm_layer_norm_bwd reads them.
+ * 1 <= dim <= 8192 (SSM_ERR_UNSUPPORTED above); eps >= 0.  Statistics are fp32, the variance
+ * from the centred values.  rows = 0 does nothing.
+ */
+int ssm_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y, float *mean,
+                       float *rstd, float eps, int rows, int dim, int in_dtype, int out_dtype,
+                       void *cuda_stream);
+
+/*
+ * Backward of the layer norm.  With xhat = (x - mean) rstd and g = dy weight:
+ *     dx = rstd (g - mean(g) - xhat mean(g xhat)),   dweight = sum_rows dy xhat,   dbias = sum_rows dy
+ *
+ *   dy, dx         : [rows][dim], grad_dtype (dx written).   x: [rows][dim], in_dtype.
+ *   weight         : [dim] fp32 or NULL (1).   mean, rstd: [rows] fp32, as the forward wrote them.
+ *   dweight, dbias : [dim] fp32, written, or NULL.
+ * The sums over rows have a fixed order (deterministic).  Takes a stream-ordered scratch
+ * buffer of at most 148 * 32 * 8 * dim bytes.  rows = 0 writes zero dweight and dbias.
+ */
+int ssm_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *mean,
+                       const float *rstd, void *dx, float *dweight, float *dbias, int rows, int dim,
+                       int in_dtype, int grad_dtype, void *cuda_stream);
 
 /*
  * Number of times, since the library was loaded on the current device, that a kernel gave

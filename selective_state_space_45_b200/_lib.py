@@ -65,6 +65,17 @@ def load_library(path: str | None = None):
         lib.ssm_selective_scan_bwd.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, vp,
                                                vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                i, i, i, i, i, i, vp]
+        fl = ctypes.c_float
+        lib.ssm_delta_rule_fwd.restype = i
+        lib.ssm_delta_rule_fwd.argtypes = [vp] * 8 + [fl] + [i] * 8 + [vp]
+        lib.ssm_delta_rule_step.restype = i
+        lib.ssm_delta_rule_step.argtypes = [vp] * 7 + [fl] + [i] * 8 + [vp]
+        lib.ssm_delta_rule_bwd.restype = i
+        lib.ssm_delta_rule_bwd.argtypes = [vp] * 14 + [fl] + [i] * 8 + [vp]
+        lib.ssm_layer_norm_fwd.restype = i
+        lib.ssm_layer_norm_fwd.argtypes = [vp] * 6 + [fl] + [i] * 4 + [vp]
+        lib.ssm_layer_norm_bwd.restype = i
+        lib.ssm_layer_norm_bwd.argtypes = [vp] * 8 + [i] * 4 + [vp]
         lib.ssm_status_string.restype = ctypes.c_char_p
         lib.ssm_status_string.argtypes = [i]
         lib.ssm_version.restype = i
@@ -297,3 +308,153 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
     ssm_selective_scan_fwd_ex(x, delta, delta_bias, delta_softplus, A, B, C, D, z, y, fs,
                               initial_state, zoh_exact, stream)
     return (y, fs) if return_final_state else y
+
+
+def _require(shapes):
+    """Raise ValueError unless every (name, tensor or None, shape, dtype) is given as asked:
+    the kernels read what the sizes say, so a wrong shape or dtype must not reach them.  All
+    tensors have to be on one device."""
+    device = None
+    for name, t, shape, dtype in shapes:
+        if t is None:
+            continue
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+        if t.dtype != dtype:
+            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            raise ValueError("%s is on %s, other tensors on %s" % (name, t.device, device))
+    return device
+
+
+def _call_on(device, fn, *args):
+    """Run a library call with ``device`` current (its kernels and scratch live there)."""
+    if device.type != "cuda":
+        raise ValueError("libssm needs CUDA tensors, got %s" % device)
+    with torch.cuda.device(device):
+        _check(fn(*args))
+
+
+def _delta_shapes(lead, q, k, v, a, beta):
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must have four dimensions")
+    (H, P), (K, N) = v.shape[2:], q.shape[2:]
+    return H, K, P, N, [("q", q, (*lead, K, N), v.dtype), ("k", k, (*lead, K, N), v.dtype),
+                        ("v", v, (*lead, H, P), v.dtype), ("a", a, (*lead, H), torch.float32),
+                        ("beta", beta, (*lead, H), torch.float32)]
+
+
+def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None, scale=1.0, stream=None):
+    """Gated delta rule over whole sequences (see include/ssm.h): q, k [batch, L, qk_heads, N];
+    v, y [batch, L, heads, P]; a, beta [batch, L, heads] fp32; states [batch, heads, P, N] fp32.
+    Writes y and final_state in place."""
+    lead = tuple(v.shape[:2])
+    H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
+    st = (lead[0], H, P, N)
+    dev = _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
+                             ("final_state", final_state, st, torch.float32)])
+    _call_on(dev, load_library().ssm_delta_rule_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y),
+             _ptr(initial_state), _ptr(final_state), float(scale), lead[0], lead[1], H, K, P, N,
+             _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype], _stream(stream, v))
+
+
+def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0, out_dtype=None, return_final_state=True,
+               stream=None):
+    """Allocate y (and the final state) with torch and run ``ssm_delta_rule_fwd``."""
+    y = torch.empty(v.shape, device=v.device, dtype=out_dtype or v.dtype)
+    fs = (torch.empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1]), device=v.device, dtype=torch.float32)
+          if return_final_state else None)
+    ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state, fs, scale, stream)
+    return (y, fs) if return_final_state else y
+
+
+def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
+    """Decode tokens of the gated delta rule (see include/ssm.h): state [batch, heads, P, N]
+    fp32 updated in place; q, k [ntok, batch, qk_heads, N]; v, y [ntok, batch, heads, P]; a,
+    beta [ntok, batch, heads] fp32."""
+    lead = tuple(v.shape[:2])
+    H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
+    dev = _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
+    _call_on(dev, load_library().ssm_delta_rule_step, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
+             _ptr(y), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype],
+             _stream(stream, v))
+
+
+def delta_rule_step(state, q, k, v, a, beta, scale=1.0, out_dtype=None, stream=None):
+    """Allocate y with torch and run ``ssm_delta_rule_step``."""
+    y = torch.empty(v.shape, device=v.device, dtype=out_dtype or v.dtype)
+    ssm_delta_rule_step(state, q, k, v, a, beta, y, scale, stream)
+    return y
+
+
+def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk, dv, da, dbeta,
+                       dinitial_state=None, scale=1.0, stream=None):
+    """Backward of the gated delta rule (see include/ssm.h).  dq, dk, dv share dy's dtype; da,
+    dbeta, dinitial_state are fp32.  Writes the gradients in place."""
+    lead = tuple(v.shape[:2])
+    H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
+    st, f32 = (lead[0], H, P, N), torch.float32
+    dev = _require(shapes + [
+        ("initial_state", initial_state, st, f32), ("dy", dy, v.shape, dy.dtype),
+        ("dfinal_state", dfinal_state, st, f32), ("dq", dq, q.shape, dy.dtype), ("dk", dk, k.shape, dy.dtype),
+        ("dv", dv, v.shape, dy.dtype), ("da", da, a.shape, f32), ("dbeta", dbeta, beta.shape, f32),
+        ("dinitial_state", dinitial_state, st, f32)])
+    _call_on(dev, load_library().ssm_delta_rule_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
+             _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(da), _ptr(dbeta),
+             _ptr(dinitial_state), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype],
+             _DTYPE_CODE[dy.dtype], _stream(stream, v))
+
+
+def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, scale=1.0, stream=None):
+    """Allocate the gradients with torch and run ``ssm_delta_rule_bwd``; returns a dict dq, dk,
+    dv (dy's dtype), da, dbeta, dinitial_state (fp32; None without an initial_state)."""
+    g = dict(dq=torch.empty_like(q, dtype=dy.dtype), dk=torch.empty_like(k, dtype=dy.dtype),
+             dv=torch.empty_like(v, dtype=dy.dtype), da=torch.empty_like(a), dbeta=torch.empty_like(beta),
+             dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
+    ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, g["dq"], g["dk"], g["dv"], g["da"],
+                       g["dbeta"], g["dinitial_state"], scale, stream)
+    return g
+
+
+def ssm_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
+    """Layer norm over the last dimension (see include/ssm.h): x, y [..., dim]; weight, bias
+    [dim] fp32 or None; mean, rstd fp32, one value per row, or None.  Writes in place."""
+    dim, f32 = x.shape[-1], torch.float32
+    dev = _require([("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32), ("bias", bias, (dim,), f32),
+                    ("y", y, x.shape, y.dtype), ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32)])
+    _call_on(dev, load_library().ssm_layer_norm_fwd, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
+             _ptr(rstd), float(eps), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype],
+             _DTYPE_CODE[y.dtype], _stream(stream, x))
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats=False, stream=None):
+    """Allocate y (and mean, rstd) with torch and run the layer norm; returns y, or (y, mean,
+    rstd) for the backward."""
+    y = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
+    mean, rstd = ((torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32) for _ in range(2))
+                  if return_stats else (None, None))
+    ssm_layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, stream)
+    return (y, mean, rstd) if return_stats else y
+
+
+def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, stream=None):
+    """Backward of the layer norm (see include/ssm.h): dx in dy's dtype; dweight, dbias [dim]
+    fp32 or None.  Writes the gradients in place."""
+    dim, f32 = x.shape[-1], torch.float32
+    dev = _require([("dy", dy, x.shape, dy.dtype), ("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32),
+                    ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32),
+                    ("dx", dx, x.shape, dy.dtype), ("dweight", dweight, (dim,), f32), ("dbias", dbias, (dim,), f32)])
+    _call_on(dev, load_library().ssm_layer_norm_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+             _ptr(dx), _ptr(dweight), _ptr(dbias), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype],
+             _DTYPE_CODE[dy.dtype], _stream(stream, x))
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, stream=None):
+    """Allocate the gradients with torch and run ``ssm_layer_norm_bwd``; returns a dict dx
+    (dy's dtype), dweight, dbias (fp32)."""
+    g = dict(dx=torch.empty_like(dy), dweight=torch.empty(x.shape[-1], device=x.device, dtype=torch.float32),
+             dbias=torch.empty(x.shape[-1], device=x.device, dtype=torch.float32))
+    ssm_layer_norm_bwd(dy, x, weight, mean, rstd, g["dx"], g["dweight"], g["dbias"], stream)
+    return g

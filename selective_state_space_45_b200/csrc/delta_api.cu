@@ -1,0 +1,92 @@
+// delta_api.cu -- C ABI of the gated delta rule over whole sequences (ssm_delta_rule_fwd) and
+// over decode tokens (ssm_delta_rule_step).  Arguments are checked on the host before
+// anything is launched; nothing is allocated.
+#include "delta_host.cuh"
+#include "delta_step.cuh"
+
+using namespace ssm_host;
+
+namespace {
+
+template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs &a, cudaStream_t s) {
+    const long long blocks = ((long long)a.batch * a.heads * (a.P / 8) + 7) / 8;
+    if (blocks > INT_MAX) return SSM_ERR_UNSUPPORTED;
+    const unsigned n = unsigned(blocks);
+    if (a.N <= 32) ssm::delta_step_kernel<1, Tin, Tout><<<n, 256, 0, s>>>(a);
+    else if (a.N <= 64) ssm::delta_step_kernel<2, Tin, Tout><<<n, 256, 0, s>>>(a);
+    else if (a.N <= 96) ssm::delta_step_kernel<3, Tin, Tout><<<n, 256, 0, s>>>(a);
+    else ssm::delta_step_kernel<4, Tin, Tout><<<n, 256, 0, s>>>(a);
+    return status_of(cudaGetLastError());
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
+                       void *y, const float *initial_state, float *final_state, float scale,
+                       int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
+                       int in_dtype, int out_dtype, void *cuda_stream) {
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return SSM_ERR_INVALID_ARG;
+    if (const int st = delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate)) return st;
+    const long long all = (long long)batch * heads;
+    const bool work = all > 0 && seqlen > 0;
+    if (work && (!q || !k || !v || !a || !beta || !y)) return SSM_ERR_INVALID_ARG;
+    for (const void *x : {q, k, v, (const void *)a, (const void *)beta, (const void *)y, (const void *)initial_state,
+                          (const void *)final_state})
+        if (x && !aligned16(x)) return SSM_ERR_ALIGNMENT;
+    if (all == 0) return SSM_OK;
+    const size_t tok = size_t(batch) * seqlen, is = dtype_size(in_dtype), os = dtype_size(out_dtype);
+    const size_t sb = size_t(all) * headdim * dstate * 4, yb = tok * heads * headdim * os;
+    const struct { const void *p; size_t n; } in[] = {
+        {q, tok * qk_heads * dstate * is}, {k, tok * qk_heads * dstate * is}, {v, tok * heads * headdim * is},
+        {a, tok * heads * 4}, {beta, tok * heads * 4}};
+    for (const auto &x : in)
+        if (overlaps(y, yb, x.p, x.n) || overlaps(final_state, sb, x.p, x.n)) return SSM_ERR_INVALID_ARG;
+    if (overlaps(y, yb, initial_state, sb) || overlaps(y, yb, final_state, sb)) return SSM_ERR_INVALID_ARG;
+    if (final_state != initial_state && overlaps(final_state, sb, initial_state, sb)) return SSM_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    if (!work) {   // no tokens: the final state is the start state
+        if (!final_state || final_state == initial_state) return SSM_OK;
+        if (initial_state) return status_of(cudaMemcpyAsync(final_state, initial_state, sb, cudaMemcpyDeviceToDevice, s));
+        return status_of(cudaMemsetAsync(final_state, 0, sb, s));
+    }
+    ssm::DeltaArgs g{};
+    g.q = q; g.k = k; g.v = v; g.a = a; g.beta = beta; g.y = y; g.h0 = initial_state; g.hN = final_state;
+    g.batch = batch; g.seqlen = seqlen; g.heads = heads; g.qk_heads = qk_heads; g.P = headdim; g.N = dstate;
+    g.scale = scale;
+    using bf16 = __nv_bfloat16;
+    if (in_dtype == SSM_BF16)
+        return out_dtype == SSM_BF16 ? dispatch_chain<bf16, bf16, bf16, bf16, 0>(g, s)
+                                     : dispatch_chain<bf16, bf16, bf16, float, 0>(g, s);
+    return out_dtype == SSM_BF16 ? dispatch_chain<float, float, float, bf16, 0>(g, s)
+                                 : dispatch_chain<float, float, float, float, 0>(g, s);
+}
+
+int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *v, const float *a,
+                        const float *beta, void *y, float scale, int ntok, int batch, int heads,
+                        int qk_heads, int headdim, int dstate, int in_dtype, int out_dtype,
+                        void *cuda_stream) {
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return SSM_ERR_INVALID_ARG;
+    if (const int st = delta_sizes(batch, ntok, heads, qk_heads, headdim, dstate)) return st;
+    const long long all = (long long)batch * heads;
+    if (all == 0 || ntok == 0) return SSM_OK;
+    if (!state || !q || !k || !v || !a || !beta || !y) return SSM_ERR_INVALID_ARG;
+    for (const void *x : {(const void *)state, q, k, v, (const void *)a, (const void *)beta, (const void *)y})
+        if (!aligned16(x)) return SSM_ERR_ALIGNMENT;
+    const size_t tok = size_t(batch) * ntok, is = dtype_size(in_dtype);
+    const size_t sb = size_t(all) * headdim * dstate * 4, yb = tok * heads * headdim * dtype_size(out_dtype);
+    const struct { const void *p; size_t n; } in[] = {
+        {q, tok * qk_heads * dstate * is}, {k, tok * qk_heads * dstate * is}, {v, tok * heads * headdim * is},
+        {a, tok * heads * 4}, {beta, tok * heads * 4}};
+    for (const auto &x : in)
+        if (overlaps(y, yb, x.p, x.n) || overlaps(state, sb, x.p, x.n)) return SSM_ERR_INVALID_ARG;
+    if (overlaps(y, yb, state, sb)) return SSM_ERR_INVALID_ARG;
+    const ssm::DeltaStepArgs g{state, q, k, v, a, beta, y, ntok, batch, heads, qk_heads, headdim, dstate, scale};
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    using bf16 = __nv_bfloat16;
+    if (in_dtype == SSM_BF16) return out_dtype == SSM_BF16 ? launch_step<bf16, bf16>(g, s) : launch_step<bf16, float>(g, s);
+    return out_dtype == SSM_BF16 ? launch_step<float, bf16>(g, s) : launch_step<float, float>(g, s);
+}
+
+}  // extern "C"

@@ -1,13 +1,12 @@
 // ssm_api.cu -- library-wide entry points of libssm.so: version and status strings, and
-// the SFU throughput probe.  The operations live in scan_api.cu, step_api.cu,
-// conv_api.cu, bwd_api.cu and ssd_api.cu.
+// the SFU throughput probe.  The operations live in the other *_api.cu files.
 #include "api_host.cuh"
 #include "common.cuh"
 
 using namespace ssm_host;
 
 namespace {
-constexpr int kVersion = 1 * 10000 + 1 * 100 + 0;
+constexpr int kVersion = 1 * 10000 + 2 * 100 + 0;
 constexpr int kProbeThreads = 256;
 constexpr int kProbeChains = 8;
 
@@ -45,7 +44,7 @@ const char *ssm_status_string(int status) {
     switch (status) {
     case SSM_OK: return "ok";
     case SSM_ERR_INVALID_ARG: return "invalid argument (null pointer, negative size or bad dtype)";
-    case SSM_ERR_UNSUPPORTED: return "unsupported size (dstate above 16, conv width above 8, or a grid too large)";
+    case SSM_ERR_UNSUPPORTED: return "unsupported size (dstate, headdim, conv width or row width out of the call's range, or a grid too large)";
     case SSM_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
     case SSM_ERR_CUDA: return "CUDA runtime error at launch";
     case SSM_ERR_SCRATCH:
