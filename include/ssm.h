@@ -29,10 +29,13 @@
  *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers owned by the caller; the library keeps
- *    no state between calls.  Four calls may take a temporary scratch buffer with
+ *    no state between calls.  Two calls may take a temporary scratch buffer with
  *    cudaMallocAsync / cudaFreeAsync on cuda_stream: ssm_selective_scan_fwd (and _ex)
- *    for long sequences with few channels (see below), ssm_selective_scan_bwd,
- *    ssm_delta_rule_bwd and ssm_layer_norm_bwd.
+ *    for long sequences with few channels (see below), and ssm_selective_scan_bwd.  Three
+ *    more (ssm_delta_rule_fwd, ssm_delta_rule_bwd, ssm_layer_norm_bwd) do so unless they
+ *    are given a workspace: device memory of at least the bytes that the call's _workspace
+ *    function returns for the same sizes (0 for sizes that the call refuses).  Its contents
+ *    need not be anything and are not kept; calls that may overlap on the GPU need one each.
  *    ssm_selective_scan_fwd_noalloc is the scan's form that never allocates; every
  *    other call allocates nothing.
  *  - Every pointer must be 16-byte aligned (SSM_ERR_ALIGNMENT otherwise).
@@ -51,6 +54,8 @@
 #ifndef SSM_H_
 #define SSM_H_
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -66,7 +71,8 @@ typedef enum {
     SSM_ERR_UNSUPPORTED = 2,   /* dstate above 16, conv width above 8, sizes out of range */
     SSM_ERR_ALIGNMENT = 3,     /* a pointer not 16-byte aligned                            */
     SSM_ERR_CUDA = 4,          /* the CUDA runtime reported an error at launch             */
-    SSM_ERR_SCRATCH = 5        /* ssm_selective_scan_fwd_noalloc: fixed scratch too small  */
+    SSM_ERR_SCRATCH = 5        /* ssm_selective_scan_fwd_noalloc: fixed scratch too small;
+                                  a given workspace smaller than its _workspace() says   */
 } ssm_status;
 
 /*
@@ -325,12 +331,16 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * fp32 operands with fp32 accumulation: the final state and an fp32 y are good to a few
  * 2^-20 of their size (normwise), a bf16 y to its own rounding and 2^-16.  A value that is
  * not finite spreads over the rest of its chunk, earlier tokens included.
- * seqlen = 0 copies the start state through.  Allocates nothing.
+ * seqlen = 0 copies the start state through.  Takes scratch (about 150 bytes per token and
+ * head, and the keys and queries again when they are fp32): see the conventions above.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        void *y, const float *initial_state, float *final_state, float scale,
                        int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
-                       int in_dtype, int out_dtype, void *cuda_stream);
+                       int in_dtype, int out_dtype, void *workspace, size_t workspace_bytes,
+                       void *cuda_stream);
+size_t ssm_delta_rule_fwd_workspace(int batch, int seqlen, int heads, int qk_heads, int headdim,
+                                    int dstate, int in_dtype, int out_dtype);
 
 /*
  * Decode tokens of the gated delta rule on a carried state: ntok tokens per sequence, the
@@ -363,16 +373,19 @@ int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *
  *   dv            : [batch][seqlen][heads][headdim], grad_dtype, written.
  *   da, dbeta     : [batch][seqlen][heads] fp32, written.
  *   dinitial_state: [batch][heads][headdim][dstate] fp32 or NULL.
- * Every sum has a fixed order: results are deterministic.  Takes a stream-ordered scratch
- * buffer (cudaMallocAsync / cudaFreeAsync on cuda_stream) of about
- * 8 * batch * heads * headdim * (seqlen + dstate * (seqlen / 64 + 2)) bytes.
+ * Every sum has a fixed order: results are deterministic.  Takes scratch (see the
+ * conventions above) of about 8 * batch * heads * headdim * (seqlen + dstate * (seqlen / 64 + 2))
+ * bytes, mostly the state and its gradient every 64 tokens.
  * seqlen = 0 writes dinitial_state = dfinal_state.
  */
 int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        const float *initial_state, const void *dy, const float *dfinal_state,
                        void *dq, void *dk, void *dv, float *da, float *dbeta, float *dinitial_state,
                        float scale, int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
-                       int in_dtype, int grad_dtype, void *cuda_stream);
+                       int in_dtype, int grad_dtype, void *workspace, size_t workspace_bytes,
+                       void *cuda_stream);
+size_t ssm_delta_rule_bwd_workspace(int batch, int seqlen, int heads, int qk_heads, int headdim,
+                                    int dstate, int in_dtype, int grad_dtype);
 
 /*
  * Layer norm over rows (the norm in front of a mixer, or of its output per token and head):
@@ -395,12 +408,15 @@ int ssm_layer_norm_fwd(const void *x, const float *weight, const float *bias, vo
  *   dy, dx         : [rows][dim], grad_dtype (dx written).   x: [rows][dim], in_dtype.
  *   weight         : [dim] fp32 or NULL (1).   mean, rstd: [rows] fp32, as the forward wrote them.
  *   dweight, dbias : [dim] fp32, written, or NULL.
- * The sums over rows have a fixed order (deterministic).  Takes a stream-ordered scratch
- * buffer of at most 148 * 32 * 8 * dim bytes.  rows = 0 writes zero dweight and dbias.
+ * The sums over rows have a fixed order (deterministic).  Takes scratch (see the conventions
+ * above): the CTAs' column sums, at most 148 * 64 * dim bytes.  rows = 0 writes zero dweight
+ * and dbias.
  */
 int ssm_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *mean,
                        const float *rstd, void *dx, float *dweight, float *dbias, int rows, int dim,
-                       int in_dtype, int grad_dtype, void *cuda_stream);
+                       int in_dtype, int grad_dtype, void *workspace, size_t workspace_bytes,
+                       void *cuda_stream);
+size_t ssm_layer_norm_bwd_workspace(int rows, int dim);
 
 /*
  * Number of times, since the library was loaded on the current device, that a kernel gave

@@ -65,17 +65,20 @@ def load_library(path: str | None = None):
         lib.ssm_selective_scan_bwd.argtypes = [vp, vp, vp, i, vp, vp, vp, vp, vp, vp, vp, vp,
                                                vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                                i, i, i, i, i, i, vp]
-        fl = ctypes.c_float
+        fl, sz = ctypes.c_float, ctypes.c_size_t
         lib.ssm_delta_rule_fwd.restype = i
-        lib.ssm_delta_rule_fwd.argtypes = [vp] * 8 + [fl] + [i] * 8 + [vp]
+        lib.ssm_delta_rule_fwd.argtypes = [vp] * 8 + [fl] + [i] * 8 + [vp, sz, vp]
         lib.ssm_delta_rule_step.restype = i
         lib.ssm_delta_rule_step.argtypes = [vp] * 7 + [fl] + [i] * 8 + [vp]
         lib.ssm_delta_rule_bwd.restype = i
-        lib.ssm_delta_rule_bwd.argtypes = [vp] * 14 + [fl] + [i] * 8 + [vp]
+        lib.ssm_delta_rule_bwd.argtypes = [vp] * 14 + [fl] + [i] * 8 + [vp, sz, vp]
         lib.ssm_layer_norm_fwd.restype = i
         lib.ssm_layer_norm_fwd.argtypes = [vp] * 6 + [fl] + [i] * 4 + [vp]
         lib.ssm_layer_norm_bwd.restype = i
-        lib.ssm_layer_norm_bwd.argtypes = [vp] * 8 + [i] * 4 + [vp]
+        lib.ssm_layer_norm_bwd.argtypes = [vp] * 8 + [i] * 4 + [vp, sz, vp]
+        for name, n in (("ssm_delta_rule_fwd", 8), ("ssm_delta_rule_bwd", 8), ("ssm_layer_norm_bwd", 2)):
+            getattr(lib, name + "_workspace").restype = sz
+            getattr(lib, name + "_workspace").argtypes = [i] * n
         lib.ssm_status_string.restype = ctypes.c_char_p
         lib.ssm_status_string.argtypes = [i]
         lib.ssm_version.restype = i
@@ -313,12 +316,12 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
 def _require(shapes):
     """Raise ValueError unless every (name, tensor or None, shape, dtype) is given as asked:
     the kernels read what the sizes say, so a wrong shape or dtype must not reach them.  All
-    tensors have to be on one device."""
+    tensors have to be on one CUDA device, which is returned."""
     device = None
     for name, t, shape, dtype in shapes:
         if t is None:
             continue
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
         if t.dtype != dtype:
             raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
@@ -326,15 +329,36 @@ def _require(shapes):
             device = t.device
         elif t.device != device:
             raise ValueError("%s is on %s, other tensors on %s" % (name, t.device, device))
+    if device.type != "cuda":
+        raise ValueError("libssm needs CUDA tensors, got %s" % device)
     return device
 
 
-def _call_on(device, fn, *args):
+class _Workspace:
+    """Scratch of one call from torch's allocator, on the stream that the call runs on (so the
+    memory is not handed out again before the call's kernels are done with it)."""
+
+    def __init__(self, nbytes, device, stream):
+        if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
+            self.t = torch.empty(nbytes, device=device, dtype=torch.uint8)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+                self.t = torch.empty(nbytes, device=device, dtype=torch.uint8)
+        self.args = (self.t.data_ptr() if nbytes else None, nbytes)
+
+
+def _call_on(device, stream, name, *args, workspace=None):
     """Run a library call with ``device`` current (its kernels and scratch live there)."""
-    if device.type != "cuda":
-        raise ValueError("libssm needs CUDA tensors, got %s" % device)
-    with torch.cuda.device(device):
-        _check(fn(*args))
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call_on(device, stream, name, *args, workspace=workspace)
+    lib = load_library()
+    stream = (torch.cuda.current_stream(device).cuda_stream if stream is None else
+              stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if workspace is not None:
+        ws = _Workspace(getattr(lib, name + "_workspace")(*workspace), device, stream)
+        args += ws.args
+    _check(getattr(lib, name)(*args, stream))
 
 
 def _delta_shapes(lead, q, k, v, a, beta):
@@ -355,9 +379,9 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
     st = (lead[0], H, P, N)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
                              ("final_state", final_state, st, torch.float32)])
-    _call_on(dev, load_library().ssm_delta_rule_fwd, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y),
-             _ptr(initial_state), _ptr(final_state), float(scale), lead[0], lead[1], H, K, P, N,
-             _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype], _stream(stream, v))
+    sizes = (lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype])
+    _call_on(dev, stream, "ssm_delta_rule_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y),
+             _ptr(initial_state), _ptr(final_state), float(scale), *sizes, workspace=sizes)
 
 
 def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0, out_dtype=None, return_final_state=True,
@@ -377,9 +401,8 @@ def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
     lead = tuple(v.shape[:2])
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
-    _call_on(dev, load_library().ssm_delta_rule_step, _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
-             _ptr(y), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype],
-             _stream(stream, v))
+    _call_on(dev, stream, "ssm_delta_rule_step", _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
+             _ptr(y), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype])
 
 
 def delta_rule_step(state, q, k, v, a, beta, scale=1.0, out_dtype=None, stream=None):
@@ -401,10 +424,10 @@ def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk
         ("dfinal_state", dfinal_state, st, f32), ("dq", dq, q.shape, dy.dtype), ("dk", dk, k.shape, dy.dtype),
         ("dv", dv, v.shape, dy.dtype), ("da", da, a.shape, f32), ("dbeta", dbeta, beta.shape, f32),
         ("dinitial_state", dinitial_state, st, f32)])
-    _call_on(dev, load_library().ssm_delta_rule_bwd, _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
+    sizes = (lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[dy.dtype])
+    _call_on(dev, stream, "ssm_delta_rule_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
              _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(da), _ptr(dbeta),
-             _ptr(dinitial_state), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype],
-             _DTYPE_CODE[dy.dtype], _stream(stream, v))
+             _ptr(dinitial_state), float(scale), *sizes, workspace=sizes)
 
 
 def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, scale=1.0, stream=None):
@@ -424,9 +447,8 @@ def ssm_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, strea
     dim, f32 = x.shape[-1], torch.float32
     dev = _require([("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32), ("bias", bias, (dim,), f32),
                     ("y", y, x.shape, y.dtype), ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32)])
-    _call_on(dev, load_library().ssm_layer_norm_fwd, _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
-             _ptr(rstd), float(eps), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype],
-             _DTYPE_CODE[y.dtype], _stream(stream, x))
+    _call_on(dev, stream, "ssm_layer_norm_fwd", _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
+             _ptr(rstd), float(eps), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype], _DTYPE_CODE[y.dtype])
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats=False, stream=None):
@@ -446,9 +468,10 @@ def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, 
     dev = _require([("dy", dy, x.shape, dy.dtype), ("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32),
                     ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32),
                     ("dx", dx, x.shape, dy.dtype), ("dweight", dweight, (dim,), f32), ("dbias", dbias, (dim,), f32)])
-    _call_on(dev, load_library().ssm_layer_norm_bwd, _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-             _ptr(dx), _ptr(dweight), _ptr(dbias), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype],
-             _DTYPE_CODE[dy.dtype], _stream(stream, x))
+    rows = x.numel() // dim if dim else 0
+    _call_on(dev, stream, "ssm_layer_norm_bwd", _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
+             _ptr(dx), _ptr(dweight), _ptr(dbias), rows, dim, _DTYPE_CODE[x.dtype], _DTYPE_CODE[dy.dtype],
+             workspace=(rows, dim))
 
 
 def layer_norm_bwd(dy, x, weight, mean, rstd, stream=None):

@@ -1,6 +1,7 @@
 // delta_api.cu -- C ABI of the gated delta rule over whole sequences (ssm_delta_rule_fwd) and
 // over decode tokens (ssm_delta_rule_step).  Arguments are checked on the host before
-// anything is launched; nothing is allocated.
+// anything is launched.  The forward takes scratch (the caller's workspace or a stream-ordered
+// buffer), the step none.
 #include "delta_host.cuh"
 #include "delta_step.cuh"
 
@@ -19,21 +20,49 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
     return status_of(cudaGetLastError());
 }
 
+// Forward: the chunk blocks, then the chains.
+template <typename Tin, typename Tout> size_t fwd_bytes(int batch, int seqlen, int heads, int qk_heads, int N) {
+    return prep_bytes<ssm::DeltaBlock<sizeof(Tout) == 4 ? 3 : 2, false>>(batch, seqlen, heads) +
+           pieces_bytes(batch, seqlen, qk_heads, N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
+}
+
+template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *workspace, size_t bytes, cudaStream_t s) {
+    using Block = ssm::DeltaBlock<sizeof(Tout) == 4 ? 3 : 2, false>;
+    Scratch ws;
+    if (const int st = ws.take(workspace, bytes, fwd_bytes<Tin, Tout>(a.batch, a.seqlen, a.heads, a.qk_heads, a.N), s))
+        return st;
+    int st = dispatch_prep<Tin, Block>(a, ws.p, ws.p + prep_bytes<Block>(a.batch, a.seqlen, a.heads), s);
+    if (st == SSM_OK) st = dispatch_chain<sizeof(Tin) == 4 ? 3 : 1, Tin, Tin, Tout, 0>(a, s);
+    return ws.release(st);
+}
+
 }  // namespace
 
 extern "C" {
 
+size_t ssm_delta_rule_fwd_workspace(int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
+                                    int in_dtype, int out_dtype) {
+    if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return 0;
+    if (delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate) != SSM_OK) return 0;
+    using bf16 = __nv_bfloat16;
+    if (in_dtype == SSM_BF16)
+        return out_dtype == SSM_BF16 ? fwd_bytes<bf16, bf16>(batch, seqlen, heads, qk_heads, dstate)
+                                     : fwd_bytes<bf16, float>(batch, seqlen, heads, qk_heads, dstate);
+    return out_dtype == SSM_BF16 ? fwd_bytes<float, bf16>(batch, seqlen, heads, qk_heads, dstate)
+                                 : fwd_bytes<float, float>(batch, seqlen, heads, qk_heads, dstate);
+}
+
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        void *y, const float *initial_state, float *final_state, float scale,
                        int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
-                       int in_dtype, int out_dtype, void *cuda_stream) {
+                       int in_dtype, int out_dtype, void *workspace, size_t workspace_bytes, void *cuda_stream) {
     if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return SSM_ERR_INVALID_ARG;
     if (const int st = delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate)) return st;
     const long long all = (long long)batch * heads;
     const bool work = all > 0 && seqlen > 0;
     if (work && (!q || !k || !v || !a || !beta || !y)) return SSM_ERR_INVALID_ARG;
     for (const void *x : {q, k, v, (const void *)a, (const void *)beta, (const void *)y, (const void *)initial_state,
-                          (const void *)final_state})
+                          (const void *)final_state, (const void *)workspace})
         if (x && !aligned16(x)) return SSM_ERR_ALIGNMENT;
     if (all == 0) return SSM_OK;
     const size_t tok = size_t(batch) * seqlen, is = dtype_size(in_dtype), os = dtype_size(out_dtype);
@@ -43,6 +72,11 @@ int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float 
         {a, tok * heads * 4}, {beta, tok * heads * 4}};
     for (const auto &x : in)
         if (overlaps(y, yb, x.p, x.n) || overlaps(final_state, sb, x.p, x.n)) return SSM_ERR_INVALID_ARG;
+    for (const auto &x : in)
+        if (overlaps(workspace, workspace_bytes, x.p, x.n)) return SSM_ERR_INVALID_ARG;
+    if (overlaps(workspace, workspace_bytes, y, yb) || overlaps(workspace, workspace_bytes, final_state, sb) ||
+        overlaps(workspace, workspace_bytes, initial_state, sb))
+        return SSM_ERR_INVALID_ARG;
     if (overlaps(y, yb, initial_state, sb) || overlaps(y, yb, final_state, sb)) return SSM_ERR_INVALID_ARG;
     if (final_state != initial_state && overlaps(final_state, sb, initial_state, sb)) return SSM_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
@@ -57,10 +91,10 @@ int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float 
     g.scale = scale;
     using bf16 = __nv_bfloat16;
     if (in_dtype == SSM_BF16)
-        return out_dtype == SSM_BF16 ? dispatch_chain<bf16, bf16, bf16, bf16, 0>(g, s)
-                                     : dispatch_chain<bf16, bf16, bf16, float, 0>(g, s);
-    return out_dtype == SSM_BF16 ? dispatch_chain<float, float, float, bf16, 0>(g, s)
-                                 : dispatch_chain<float, float, float, float, 0>(g, s);
+        return out_dtype == SSM_BF16 ? run_fwd<bf16, bf16>(g, workspace, workspace_bytes, s)
+                                     : run_fwd<bf16, float>(g, workspace, workspace_bytes, s);
+    return out_dtype == SSM_BF16 ? run_fwd<float, bf16>(g, workspace, workspace_bytes, s)
+                                 : run_fwd<float, float>(g, workspace, workspace_bytes, s);
 }
 
 int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *v, const float *a,

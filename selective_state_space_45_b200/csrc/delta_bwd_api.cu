@@ -20,52 +20,78 @@ template <int NP, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGra
     return status_of(cudaGetLastError());
 }
 
+using Block = ssm::DeltaBlock<3, true>;
+
+// The parts of a call's scratch, in this order; each starts on 16 bytes.
+struct BwdParts {
+    size_t prep, pieces, e, w, ck, dck, dyy, vw, edu, zsum, all;
+    BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
+        const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
+        const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
+        const size_t sum = size_t(delta_slices(P)) * tok * 4, state = bh * nbound * P * N * 4;
+        size_t at = 0;
+        auto part = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
+        part(prep, prep_bytes<Block>(batch, seqlen, heads));
+        part(pieces, pieces_bytes(batch, seqlen, qk_heads, N, in_dtype));
+        part(e, tok * P * 4);
+        part(w, grad_dtype == SSM_F32 ? 0 : tok * P * 4);       // fp32 gradients: w is dv itself
+        part(ck, state);
+        part(dck, state);
+        part(dyy, sum);
+        part(vw, sum);
+        part(edu, sum);
+        part(zsum, size_t(delta_slices(P)) * kDeltaWarps * bh * nbound * 4);
+        all = at;
+    }
+};
+
+template <typename T> constexpr int code_of() { return sizeof(T) == 4 ? SSM_F32 : SSM_BF16; }
+
 template <typename Tin, typename Tg>
 int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal, void *dq, void *dk, void *dv, float *da,
-            float *dbeta, float *dh0, cudaStream_t s) {
-    const size_t all = size_t(f.batch) * f.heads, tok = all * f.seqlen;
-    const size_t nbound = (size_t(f.seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
-    const int slices = (f.P + 63) / 64, zparts = 4 * slices;
-    const size_t n_e = tok * f.P, n_w = sizeof(Tg) == 4 ? 0 : n_e, n_ck = all * nbound * f.P * f.N;
-    const size_t n_sum = size_t(slices) * tok, n_z = size_t(zparts) * all * nbound;
-    auto up = [](size_t n) { return (n + 3) / 4 * 4; };        // 16-byte parts
-    float *ws = nullptr;
-    if (cudaMallocAsync(reinterpret_cast<void **>(&ws),
-                        (up(n_e) + up(n_w) + 2 * up(n_ck) + 3 * up(n_sum) + up(n_z)) * sizeof(float), s) != cudaSuccess) {
-        cudaGetLastError();
-        return SSM_ERR_CUDA;
-    }
-    float *at = ws;
-    auto take = [&](size_t n) { float *r = at; at += up(n); return r; };
-    float *e = take(n_e), *w = n_w ? take(n_w) : static_cast<float *>(dv), *ck = take(n_ck), *dck = take(n_ck);
-    float *dyy = take(n_sum), *vw = take(n_sum), *edu = take(n_sum), *zsum = take(n_z);
-
-    f.v = v; f.v2 = dy; f.y = nullptr; f.hN = nullptr; f.e = e; f.ck = ck; f.sum0 = dyy;
-    int st = dispatch_chain<Tin, Tin, Tg, float, 1>(f, s);
+            float *dbeta, float *dh0, void *workspace, size_t bytes, cudaStream_t s) {
+    const BwdParts at(f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N, code_of<Tin>(), code_of<Tg>());
+    Scratch ws;
+    if (const int st = ws.take(workspace, bytes, at.all, s)) return st;
+    auto part = [&](size_t off) { return reinterpret_cast<float *>(ws.p + off); };
+    const void *q = f.q, *k = f.k;
+    float *w = sizeof(Tg) == 4 ? static_cast<float *>(dv) : part(at.w);
+    constexpr int KP = sizeof(Tin) == 4 ? 3 : 1;
+    int st = dispatch_prep<Tin, Block>(f, ws.p + at.prep, ws.p + at.pieces, s);
+    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum0 = part(at.dyy);
+    if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
-        r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = n_w ? w : nullptr; r.dck = dck;
-        r.sum0 = vw; r.sum1 = edu; r.zsum = zsum;
-        st = dispatch_chain<Tin, Tg, Tin, Tg, 2>(r, s);
+        r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = sizeof(Tg) == 4 ? nullptr : w;
+        r.dck = part(at.dck); r.sum0 = part(at.vw); r.sum1 = part(at.edu); r.zsum = part(at.zsum);
+        st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
-        const ssm::DeltaGradArgs g{f.q, f.k, dy, f.a, f.beta, e, w, ck, dck, dyy, vw, edu, zsum, dq, dk, da, dbeta,
-                                   f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N, slices, zparts, f.scale};
+        const int slices = delta_slices(f.P);
+        const ssm::DeltaGradArgs g{q, k, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
+                                   part(at.vw), part(at.edu), part(at.zsum), dq, dk, da, dbeta, f.batch, f.seqlen,
+                                   f.heads, f.qk_heads, f.P, f.N, slices, slices * kDeltaWarps, f.scale};
         st = f.N <= 64 ? launch_grad<64, Tin, Tg>(g, s) : launch_grad<128, Tin, Tg>(g, s);
     }
-    const cudaError_t fe = cudaFreeAsync(ws, s);
-    return st == SSM_OK && fe != cudaSuccess ? int(SSM_ERR_CUDA) : st;
+    return ws.release(st);
 }
 
 }  // namespace
 
 extern "C" {
 
+size_t ssm_delta_rule_bwd_workspace(int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
+                                    int in_dtype, int grad_dtype) {
+    if (!valid_dtype(in_dtype) || !valid_dtype(grad_dtype)) return 0;
+    if (delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate) != SSM_OK) return 0;
+    return BwdParts(batch, seqlen, heads, qk_heads, headdim, dstate, in_dtype, grad_dtype).all;
+}
+
 int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        const float *initial_state, const void *dy, const float *dfinal_state,
                        void *dq, void *dk, void *dv, float *da, float *dbeta, float *dinitial_state,
                        float scale, int batch, int seqlen, int heads, int qk_heads, int headdim, int dstate,
-                       int in_dtype, int grad_dtype, void *cuda_stream) {
+                       int in_dtype, int grad_dtype, void *workspace, size_t workspace_bytes, void *cuda_stream) {
     if (!valid_dtype(in_dtype) || !valid_dtype(grad_dtype)) return SSM_ERR_INVALID_ARG;
     if (const int st = delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate)) return st;
     const long long all = (long long)batch * heads;
@@ -83,7 +109,12 @@ int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float 
         if (x.p && !aligned16(x.p)) return SSM_ERR_ALIGNMENT;
     for (const auto &x : out)
         if (x.p && !aligned16(x.p)) return SSM_ERR_ALIGNMENT;
+    if (workspace && !aligned16(workspace)) return SSM_ERR_ALIGNMENT;
     if (all == 0) return SSM_OK;
+    for (const auto &x : in)
+        if (overlaps(workspace, workspace_bytes, x.p, x.n)) return SSM_ERR_INVALID_ARG;
+    for (const auto &x : out)
+        if (overlaps(workspace, workspace_bytes, x.p, x.n)) return SSM_ERR_INVALID_ARG;
     for (const auto &x : out) {
         for (const auto &y : in)
             if (overlaps(x.p, x.n, y.p, y.n)) return SSM_ERR_INVALID_ARG;
@@ -102,10 +133,14 @@ int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float 
     f.scale = scale;
     using bf16 = __nv_bfloat16;
     if (in_dtype == SSM_BF16)
-        return grad_dtype == SSM_BF16 ? run_bwd<bf16, bf16>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, s)
-                                      : run_bwd<bf16, float>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, s);
-    return grad_dtype == SSM_BF16 ? run_bwd<float, bf16>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, s)
-                                  : run_bwd<float, float>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, s);
+        return grad_dtype == SSM_BF16 ? run_bwd<bf16, bf16>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, workspace,
+                                                                workspace_bytes, s)
+                                      : run_bwd<bf16, float>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, workspace,
+                                                                workspace_bytes, s);
+    return grad_dtype == SSM_BF16 ? run_bwd<float, bf16>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, workspace,
+                                                                workspace_bytes, s)
+                                  : run_bwd<float, float>(f, v, dy, dfinal_state, dq, dk, dv, da, dbeta, dinitial_state, workspace,
+                                                                workspace_bytes, s);
 }
 
 }  // extern "C"

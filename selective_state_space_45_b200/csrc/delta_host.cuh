@@ -16,12 +16,49 @@ inline int delta_sizes(int batch, int tokens, int heads, int qk_heads, int headd
     return SSM_OK;
 }
 
-// The chain kernel for one set of types: a warp per 16 rows of the state, four of them and
-// the producer per CTA.
-template <int NP, typename Tin, typename Tv, typename Tv2, typename Tout, int MODE>
+inline size_t delta_chunks(int seqlen) { return (size_t(seqlen) + ssm::kDeltaC - 1) / ssm::kDeltaC; }
+
+// Bytes of the prep kernel's blocks, and of the pieces of fp32 q and k.
+template <class Block> size_t prep_bytes(int batch, int seqlen, int heads) {
+    return size_t(batch) * heads * delta_chunks(seqlen) * Block::BYTES;
+}
+inline size_t piece_values(int batch, int seqlen, int qk_heads, int N) { return size_t(batch) * seqlen * qk_heads * N; }
+inline size_t pieces_bytes(int batch, int seqlen, int qk_heads, int N, int in_dtype) {
+    return in_dtype == SSM_F32 ? round16(2 * 3 * piece_values(batch, seqlen, qk_heads, N) * 2) : 0;
+}
+
+// The chunk blocks into `prep` (and the pieces of fp32 q, k behind `pieces`); on return a's
+// q and k are what the chains read.
+template <int NP, typename Tin, class Block> int launch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
+    const long long blocks = ((long long)a.batch * a.heads * (long long)delta_chunks(a.seqlen) + 7) / 8;
+    if (blocks > INT_MAX) return SSM_ERR_UNSUPPORTED;
+    ssm::delta_prep_kernel<NP, Tin, Block><<<unsigned(blocks), 256, 0, s>>>(a);
+    return status_of(cudaGetLastError());
+}
+template <typename Tin, class Block>
+int dispatch_prep(ssm::DeltaArgs &a, unsigned char *prep, unsigned char *pieces, cudaStream_t s) {
+    a.prep = prep;
+    if (sizeof(Tin) == 4) {
+        a.piece = piece_values(a.batch, a.seqlen, a.qk_heads, a.N);
+        a.kp = reinterpret_cast<__nv_bfloat16 *>(pieces);
+        a.qp = a.kp + 3 * a.piece;
+    }
+    const int st = a.N <= 32   ? launch_prep<32, Tin, Block>(a, s)
+                   : a.N <= 64 ? launch_prep<64, Tin, Block>(a, s)
+                   : a.N <= 96 ? launch_prep<96, Tin, Block>(a, s)
+                               : launch_prep<128, Tin, Block>(a, s);
+    if (sizeof(Tin) == 4) { a.q = a.qp; a.k = a.kp; }
+    return st;
+}
+
+// The chain kernel for one set of types: a warp per 16 rows of the state, four per CTA.
+constexpr int kDeltaWarps = 4;
+inline int delta_slices(int P) { return (P + 16 * kDeltaWarps - 1) / (16 * kDeltaWarps); }
+
+template <int NP, int KP, typename Tv, typename Tv2, typename Tout, int MODE>
 int launch_chain(ssm::DeltaArgs a, cudaStream_t s) {
-    using Cfg = ssm::DeltaCfg<NP, 4, Tin, Tv, Tv2, Tout, MODE>;
-    a.slices = (a.P + 16 * Cfg::NW - 1) / (16 * Cfg::NW);
+    using Cfg = ssm::DeltaCfg<NP, kDeltaWarps, KP, Tv, Tv2, Tout, MODE>;
+    a.slices = delta_slices(a.P);
     const long long ctas = (long long)a.batch * a.heads * a.slices;
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
     if (cudaFuncSetAttribute(ssm::delta_chain_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -32,12 +69,12 @@ int launch_chain(ssm::DeltaArgs a, cudaStream_t s) {
 }
 
 // dstate padded to the next multiple of 32 (zero columns): the products' inner length.
-template <typename Tin, typename Tv, typename Tv2, typename Tout, int MODE>
+template <int KP, typename Tv, typename Tv2, typename Tout, int MODE>
 int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s) {
-    if (a.N <= 32) return launch_chain<32, Tin, Tv, Tv2, Tout, MODE>(a, s);
-    if (a.N <= 64) return launch_chain<64, Tin, Tv, Tv2, Tout, MODE>(a, s);
-    if (a.N <= 96) return launch_chain<96, Tin, Tv, Tv2, Tout, MODE>(a, s);
-    return launch_chain<128, Tin, Tv, Tv2, Tout, MODE>(a, s);
+    if (a.N <= 32) return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, s);
+    if (a.N <= 64) return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, s);
+    if (a.N <= 96) return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, s);
+    return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, s);
 }
 
 }  // namespace ssm_host

@@ -12,9 +12,11 @@
 // Every row of S (one value of headdim) goes through this on its own, given k, q, T and Pm,
 // so a warp owns 16 rows and keeps them in registers as accumulator tiles [16 x dstate]:
 // the state enters each product as a register operand and no step of the chain goes through
-// shared memory or waits for another warp.  One more warp per CTA (the producer) copies the
-// chunks in (cp.async, three ahead) and forms T and Pm one chunk ahead; one barrier per
-// chunk joins them.
+// shared memory or waits for another warp.  What depends on k, q, a and beta alone (T, Pm and
+// the decays) is formed for all chunks in parallel by delta_prep_kernel, one warp per chunk,
+// and read back by the chains with the chunk's rows (cp.async, three chunks ahead).  Formed
+// by an extra warp inside each chain's CTA instead it took 5100 cycles a chunk against the
+// chain's own 2800 and set the pace.
 //
 // Precision: the products run on the tensor cores in bf16 with fp32 accumulation.  q, k, v
 // in bf16 are exact operands; an fp32 operand goes in as bf16 pieces whose sum it is (three
@@ -27,12 +29,18 @@
 // do not, and the inverse of a 16 x 16 triangle is short enough to hide in one warp.
 #pragma once
 
+#include <type_traits>
+
 #include "mma_common.cuh"
 
 namespace ssm {
 
 struct DeltaArgs {
-    const void *q, *k;      // [batch][seqlen][qk_heads][dstate]
+    const void *q, *k;      // [batch][seqlen][qk_heads][dstate]; the chains: bf16, or the pieces
+                            // that the prep kernel made of fp32 ones, `piece` values apart
+    size_t piece;
+    unsigned char *prep;    // [batch][heads][chunks] blocks of the prep kernel
+    __nv_bfloat16 *qp, *kp; // prep kernel: where the pieces of fp32 q, k go
     const void *v;          // [batch][seqlen][heads][headdim]; the reverse pass: dy
     const void *v2;         // backward: dy, and v in the reverse pass
     const float *a, *beta;  // [batch][seqlen][heads]
@@ -53,42 +61,44 @@ struct DeltaArgs {
 
 constexpr int kDeltaC = 16;          // tokens per chunk
 constexpr int kDeltaSave = 64;       // tokens between the states kept for the backward
-constexpr int kTriRow = 48;          // bytes per row of a 16 x 16 bf16 tile: ldmatrix without conflicts
+constexpr int kTri = 512;            // bytes of a 16 x 16 bf16 tile, rows of 32
+constexpr int kOutRow = 48;          // bytes per row of a warp's output tile
 
-// NP: dstate rounded up; NW: warps with 16 rows each.  MODE 0: forward (y); 1: forward of the
-// backward pass (e and the kept states, no y); 2: the reverse pass.
-template <int NP_, int NW_, typename Tin_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
-    static constexpr int NP = NP_, NW = NW_, MODE = MODE_;
-    using Tin = Tin_;      // q, k
+// Byte offset of the 16-byte half `c` of row r in such a tile: the halves change places every
+// four rows, so that eight rows' halves are eight different bank groups (ldmatrix).
+__device__ __forceinline__ int tri_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
+
+// What the prep kernel leaves per chunk and head: T - I in two bf16 pieces, Pm in PP pieces,
+// for the backward n / beta in two, then fp32 vectors over the chunk's tokens (gam, scale
+// gam, beta, end, end beta) and gam of the last token.
+template <int PP_, bool BWD_> struct DeltaBlock {
+    static constexpr int PP = PP_;
+    static constexpr bool BWD = BWD_;
+    static constexpr int NTRI = 2 + PP + (BWD ? 2 : 0);
+    static constexpr int OFF_VEC = NTRI * kTri, BYTES = OFF_VEC + 6 * kDeltaC * 4;
+};
+
+// NP: dstate rounded up; NW: warps with 16 rows each.  KP: bf16 pieces of q and k.  MODE 0:
+// forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass.
+template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
+    static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
     using Tv = Tv_;        // v, or dy in the reverse pass
     using Tv2 = Tv2_;      // the other one
     using Tout = Tout_;
-    static constexpr int C = kDeltaC, NT = 32 * (NW + 1), STAGES = 4;
-    static constexpr bool F32K = sizeof(Tin) == 4, F32V = sizeof(Tv) == 4;
-    static constexpr int KP = F32K ? 3 : 1;                                   // pieces of q and k
+    static constexpr int C = kDeltaC, NT = 32 * NW, STAGES = 4;
+    static constexpr bool F32V = sizeof(Tv) == 4;
     static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 3 : 2;         // pieces behind y
-    static constexpr int PP = PO;                                             // pieces of Pm
-    static constexpr int KROW = NP * 2 + 16;                                  // padded rows (bytes): operands
-    static constexpr int RAWROW = NP * int(sizeof(Tin)) + 16;                 // and staged rows
+    using Block = DeltaBlock<PO, MODE != 0>;
+    static constexpr int KROW = NP * 2 + 16;                                  // padded rows (bytes)
     static constexpr int VROW = NW * 16 * int(sizeof(Tv)) + 16;
-    static constexpr int OFF_K = 0, OFF_Q = C * RAWROW, OFF_V = 2 * C * RAWROW;
     static constexpr int V2ROW = NW * 16 * int(sizeof(Tv2)) + 16;
-    static constexpr int OFF_V2 = OFF_V + C * VROW;
-    static constexpr int STAGE = OFF_V2 + (MODE != 0 ? C * V2ROW : 0);
-    static constexpr int OFF_PIECES = STAGES * STAGE;                         // fp32 inputs: split q, k (2 buffers)
     static constexpr int PIECE = C * KROW;
-    static constexpr int PIECES = F32K ? 2 * 2 * KP * PIECE : 0;
-    static constexpr int TRI = C * kTriRow;
-    static constexpr int OFF_TRI = OFF_PIECES + PIECES;                       // 2 buffers of triangles
-    static constexpr int NTRI = 2 + PP + (MODE == 2 ? 2 : 0);                 // T - I (2), Pm, n / beta (2)
-    static constexpr int TRIBUF = NTRI * TRI;
-    static constexpr int OFF_VEC = OFF_TRI + 2 * TRIBUF;                      // 2 buffers of vectors
-    static constexpr int VECBUF = 6 * C * 4;
-    static constexpr int OFF_SCR = OFF_VEC + 2 * VECBUF;                      // the producer's scratch
-    static constexpr int RATROW = 18, NROW = 20;                              // floats
-    static constexpr int SCR = (C * RATROW + C * NROW) * 4;
-    static constexpr int OFF_OUT = (OFF_SCR + SCR + 15) / 16 * 16;            // per-warp output tiles
-    static constexpr int OFF_RED = OFF_OUT + NW * C * kTriRow;                // 2 buffers of token sums
+    static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_V = 2 * KP * PIECE;
+    static constexpr int OFF_V2 = OFF_V + C * VROW;
+    static constexpr int OFF_TRI = OFF_V2 + (MODE != 0 ? C * V2ROW : 0);
+    static constexpr int STAGE = OFF_TRI + Block::BYTES;
+    static constexpr int OFF_OUT = STAGES * STAGE;                            // per-warp output tiles
+    static constexpr int OFF_RED = OFF_OUT + NW * C * kOutRow;                // 2 buffers of token sums
     static constexpr int NRED = MODE;                                         // sums per token
     static constexpr int REDBUF = NRED * NW * C * 4;
     static constexpr int OFF_ST = OFF_RED + 2 * REDBUF;                       // reverse pass: kept states
@@ -113,211 +123,168 @@ __device__ __forceinline__ void mma_pieces(float (&big)[4], float (&small)[4], c
             }
 }
 
-// The producer warp: stages chunks and forms what depends on k, q, a and beta alone.
-template <class Cfg> struct DeltaProducer {
-    using Tin = typename Cfg::Tin;
-    using Tv = typename Cfg::Tv;
-    static constexpr int C = Cfg::C, NP = Cfg::NP;
-    const DeltaArgs &p;
-    unsigned char *smem;
-    int lane, b, h, hk, p0, nchunk;
-
-    template <typename T> __device__ __forceinline__ void issue_v(unsigned dst, int rowbytes, const void *src, int t0) {
-        constexpr int EV = 16 / sizeof(T), CV = Cfg::NW * 16 / EV;
-        const size_t vrow = size_t(p.heads) * p.P;
-        const T *vp = static_cast<const T *>(src) + (size_t(b) * p.seqlen * p.heads + h) * p.P;
-#pragma unroll
-        for (int i = 0; i < (C * CV + 31) / 32; ++i) {
-            const int x = lane + 32 * i, r = x / CV, n = (x % CV) * EV;
-            if (C * CV % 32 == 0 || x < C * CV) {
-                const bool ok = t0 + r < p.seqlen && p0 + n < p.P;
-                const size_t off = ok ? size_t(t0 + r) * vrow + p0 + n : 0;
-                cp_async_16z(dst + r * rowbytes + n * int(sizeof(T)), vp + off, ok);
-            }
-        }
-    }
-
-    // The sums over the warps' rows of chunk c, left in buffer `buf` by the consumers.
-    __device__ __forceinline__ void flush_sums(int c, int buf, int slice) {
-        const int t = c * C + (lane & 15), m = lane >> 4;
-        if (m >= Cfg::NRED || t >= p.seqlen) return;
-        const float *red = reinterpret_cast<const float *>(smem + Cfg::OFF_RED + buf * Cfg::REDBUF) + m * Cfg::NW * C;
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < Cfg::NW; ++w) x += red[w * C + (lane & 15)];
-        const size_t bh = size_t(b) * p.heads + h, all = size_t(p.batch) * p.heads;
-        (m ? p.sum1 : p.sum0)[(size_t(slice) * all + bh) * p.seqlen + t] = x;
-    }
-
-    __device__ __forceinline__ void issue(int c, int stage) {
-        if (c >= 0 && c < nchunk) {
-            const unsigned base = smem_u32(smem + stage * Cfg::STAGE);
-            const int t0 = c * C;
-            constexpr int EK = 16 / sizeof(Tin), CK = NP / EK;       // values per 16 bytes, copies per row
-            const size_t krow = size_t(p.qk_heads) * p.N;
-            const size_t k0 = (size_t(b) * p.seqlen * p.qk_heads + hk) * p.N;
-            const Tin *kp = static_cast<const Tin *>(p.k) + k0, *qp = static_cast<const Tin *>(p.q) + k0;
-#pragma unroll
-            for (int i = 0; i < (C * CK + 31) / 32; ++i) {
-                const int x = lane + 32 * i, r = x / CK, n = (x % CK) * EK;
-                if (C * CK % 32 == 0 || x < C * CK) {
-                    const bool ok = t0 + r < p.seqlen && n < p.N;
-                    const size_t off = ok ? size_t(t0 + r) * krow + n : 0;
-                    const unsigned d = base + r * Cfg::RAWROW + n * int(sizeof(Tin));
-                    cp_async_16z(d + Cfg::OFF_K, kp + off, ok);
-                    cp_async_16z(d + Cfg::OFF_Q, qp + off, ok);
-                }
-            }
-            issue_v<Tv>(base + Cfg::OFF_V, Cfg::VROW, p.v, t0);
-            if constexpr (Cfg::MODE != 0) issue_v<typename Cfg::Tv2>(base + Cfg::OFF_V2, Cfg::V2ROW, p.v2, t0);
-        }
-        cp_async_commit();
-    }
+// One warp per chunk and head forms the chunk's block; of fp32 q and k also their bf16 pieces
+// (by the first head of each key head).
+template <int NP, typename Tin, class Block>
+__global__ void __launch_bounds__(256) delta_prep_kernel(const DeltaArgs p) {
+    constexpr int C = kDeltaC, RATROW = 18, NROW = 20, KP = sizeof(Tin) == 4 ? 3 : 1, J = NP / 32;
+    __shared__ __align__(16) float scratch[8][C * RATROW + C * NROW];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
+    const int nchunk = (p.seqlen + C - 1) / C;
+    const long long id = (long long)blockIdx.x * 8 + warp;      // head fastest: neighbours share q and k rows
+    if (id >= (long long)p.batch * p.heads * nchunk) return;
+    const int h = int(id % p.heads);
+    const long long bc = id / p.heads;
+    const int c = int(bc % nchunk), b = int(bc / nchunk);
+    const int group = p.heads / p.qk_heads, hk = h / group, t0 = c * C;
+    float *rat = scratch[warp], *nt = rat + C * RATROW;         // rat[t][s + 1] = r(t, s), nt[s][t] = n(t, s)
 
     // lanes 0..15: a of the chunk's token `lane`; lanes 16..31: beta of token lane - 16
-    __device__ __forceinline__ float load_gate(int c) const {
-        const int t = c * C + (lane & 15);
-        if (c < 0 || c >= nchunk || t >= p.seqlen) return 0.f;
-        return (lane < 16 ? p.a : p.beta)[(size_t(b) * p.seqlen + t) * p.heads + h];
-    }
+    float gate = 0.f;
+    if (t0 + (lane & 15) < p.seqlen)
+        gate = (lane < 16 ? p.a : p.beta)[(size_t(b) * p.seqlen + t0 + (lane & 15)) * p.heads + h];
 
-    // T - I, Pm and the vectors of the chunk whose rows are in `stage`, into buffer `buf`.
-    __device__ __forceinline__ void prepare(int stage, int buf, float gate) {
-        unsigned char *raw = smem + stage * Cfg::STAGE;
-        unsigned kbase, qbase;
-        if constexpr (Cfg::F32K) {       // split the fp32 rows into bf16 pieces
-            unsigned char *pc = smem + Cfg::OFF_PIECES + buf * 2 * Cfg::KP * Cfg::PIECE;
-            for (int x = lane; x < 2 * C * (NP / 4); x += 32) {
-                const int m = x / (C * (NP / 4)), y = x % (C * (NP / 4)), r = y / (NP / 4), n = (y % (NP / 4)) * 4;
-                const float4 f = *reinterpret_cast<const float4 *>(raw + (m ? Cfg::OFF_Q : Cfg::OFF_K) +
-                                                                   r * Cfg::RAWROW + n * 4);
-                unsigned u[3], w[3];
-                split_pair<3>(f.x, f.y, u);
-                split_pair<3>(f.z, f.w, w);
+    // k.k and q.k.  The inner index may be permuted at will, so a lane takes 8 neighbouring
+    // values of its rows g and g + 8: two steps' operands in one 16-byte load.
+    float kk[2][4], qk[2][4], kks[2][4], qks[2][4];
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    *reinterpret_cast<uint2 *>(pc + (m * Cfg::KP + i) * Cfg::PIECE + r * Cfg::KROW + n * 2) =
-                        make_uint2(u[i], w[i]);
+    for (int i = 0; i < 2; ++i) { zero4(kk[i]); zero4(qk[i]); zero4(kks[i]); zero4(qks[i]); }
+    const size_t krow = size_t(p.qk_heads) * p.N;
+    const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
+    uint4 rows[2][2][J][KP];                                    // [k, q][row half][32 columns][piece]
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const int t = g + 8 * r, n = 32 * j + 8 * t4;
+                const bool ok = t0 + t < p.seqlen && n < p.N;
+                const size_t off = k0 + size_t(t) * krow + n;
+                const Tin *src = static_cast<const Tin *>(m ? p.q : p.k);
+                uint4 (&w)[KP] = rows[m][r][j];
+                if constexpr (KP == 1) {
+                    w[0] = ok ? __ldg(reinterpret_cast<const uint4 *>(src + off)) : make_uint4(0, 0, 0, 0);
+                } else {
+                    float f[8] = {};
+                    if (ok) load8<float>(src + off, f);
+                    unsigned x[4][3];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) split_pair<3>(f[2 * y], f[2 * y + 1], x[y]);
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        w[i] = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
+                        if (ok && h == hk * group)
+                            *reinterpret_cast<uint4 *>((m ? p.qp : p.kp) + i * p.piece + off) = w[i];
+                    }
+                }
             }
-            __syncwarp();
-            kbase = smem_u32(pc);
-            qbase = kbase + Cfg::KP * Cfg::PIECE;
-        } else {
-            kbase = smem_u32(raw + Cfg::OFF_K);
-            qbase = smem_u32(raw + Cfg::OFF_Q);
-        }
-        float *vec = reinterpret_cast<float *>(smem + Cfg::OFF_VEC + buf * Cfg::VECBUF);
-        float *rat = reinterpret_cast<float *>(smem + Cfg::OFF_SCR);        // rat[t][s + 1] = r(t, s)
-        float *nt = rat + C * Cfg::RATROW;                                  // nt[s][t] = n(t, s)
-        // k.k and q.k
-        float kk[2][4], qk[2][4], kks[2][4], qks[2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) { zero4(kk[i]); zero4(qk[i]); zero4(kks[i]); zero4(qks[i]); }
-        // A operand order: rows 0-7 then 8-15 of columns 0-7, then of columns 8-15
-        const unsigned aoff = ((lane >> 3 & 1) * 8 + (lane & 7)) * Cfg::KROW + (lane >> 4) * 16;
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-        for (int j = 0; j < NP / 16; ++j) {
-            unsigned ka[Cfg::KP][4], qa[Cfg::KP][4], kb[Cfg::KP][4];
+        for (int st = 0; st < 2; ++st) {
+            unsigned ka[KP][4], qa[KP][4], kb[KP][4];
 #pragma unroll
-            for (int i = 0; i < Cfg::KP; ++i) {
-                ldsm4(ka[i], kbase + i * Cfg::PIECE + aoff + j * 32);
-                ldsm4(qa[i], qbase + i * Cfg::PIECE + aoff + j * 32);
-                kb[i][0] = ka[i][0]; kb[i][1] = ka[i][2]; kb[i][2] = ka[i][1]; kb[i][3] = ka[i][3];
+            for (int i = 0; i < KP; ++i) {
+                auto half = [&](const uint4 &w, int x) { return st ? (x ? w.w : w.z) : (x ? w.y : w.x); };
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        ka[i][2 * x + r] = half(rows[0][r][j][i], x);
+                        qa[i][2 * x + r] = half(rows[1][r][j][i], x);
+                        kb[i][2 * r + x] = ka[i][2 * x + r];
+                    }
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                mma_pieces<Cfg::KP, Cfg::KP>(kk[i], kks[i], ka, kb, i);
-                mma_pieces<Cfg::KP, Cfg::KP>(qk[i], qks[i], qa, kb, i);
+                mma_pieces<KP, KP>(kk[i], kks[i], ka, kb, i);
+                mma_pieces<KP, KP>(qk[i], qks[i], qa, kb, i);
             }
         }
-        // r(t, s): lane s + 1 adds up a from token s + 1 on (no differences of long sums, so
-        // a = -inf, a full reset, is exact); lane 0 is the chunk's start
-        float acc = 0.f;
+    // r(t, s): lane s + 1 adds up a from token s + 1 on (no differences of long sums, so
+    // a = -inf, a full reset, is exact); lane 0 is the chunk's start
+    float acc = 0.f;
 #pragma unroll
-        for (int t = 0; t < C; ++t) {
-            const float at = __shfl_sync(0xffffffffu, gate, t);
-            acc = t >= lane ? acc + at : 0.f;
-            if (lane <= C) rat[t * Cfg::RATROW + lane] = t >= lane - 1 ? ex2_approx(acc * kLog2e) : 0.f;
-        }
-        __syncwarp();
-        const float beta = __shfl_sync(0xffffffffu, gate, 16 + (lane & 15));
-        if (lane < C) {
-            const float gam = rat[lane * Cfg::RATROW], end = rat[(C - 1) * Cfg::RATROW + lane + 1];
-            vec[lane] = gam;
-            vec[C + lane] = p.scale * gam;
-            vec[2 * C + lane] = beta;
-            vec[3 * C + lane] = end;
-            vec[4 * C + lane] = end * beta;
-            if (lane == C - 1) vec[5 * C] = gam;
-        }
-        const int g = lane >> 2, t4 = lane & 3;
-        unsigned char *tri = smem + Cfg::OFF_TRI + buf * Cfg::TRIBUF;
+    for (int t = 0; t < C; ++t) {
+        const float at = __shfl_sync(0xffffffffu, gate, t);
+        acc = t >= lane ? acc + at : 0.f;
+        if (lane <= C) rat[t * RATROW + lane] = t >= lane - 1 ? ex2_approx(acc * kLog2e) : 0.f;
+    }
+    __syncwarp();
+    unsigned char *out = p.prep + ((size_t(b) * p.heads + h) * nchunk + c) * Block::BYTES;
+    float *vec = reinterpret_cast<float *>(out + Block::OFF_VEC);
+    const float beta = __shfl_sync(0xffffffffu, gate, 16 + (lane & 15));
+    if (lane < C) {
+        const float gam = rat[lane * RATROW], end = rat[(C - 1) * RATROW + lane + 1];
+        vec[lane] = gam;
+        vec[C + lane] = p.scale * gam;
+        vec[2 * C + lane] = beta;
+        vec[3 * C + lane] = end;
+        vec[4 * C + lane] = end * beta;
+        if (lane == C - 1) vec[5 * C] = gam;
+    }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int s0 = 8 * i + 2 * t4;
-            const float b0 = __shfl_sync(0xffffffffu, beta, s0), b1 = __shfl_sync(0xffffffffu, beta, s0 + 1);
+    for (int i = 0; i < 2; ++i) {
+        const int s0 = 8 * i + 2 * t4;
+        const float b0 = __shfl_sync(0xffffffffu, beta, s0), b1 = __shfl_sync(0xffffffffu, beta, s0 + 1);
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int t = g + 8 * r;
-                const float r0 = rat[t * Cfg::RATROW + s0 + 1], r1 = rat[t * Cfg::RATROW + s0 + 2];
-                const float k0 = kk[i][2 * r] + kks[i][2 * r], k1 = kk[i][2 * r + 1] + kks[i][2 * r + 1];
-                nt[s0 * Cfg::NROW + t] = s0 < t ? k0 * r0 * b0 : 0.f;
-                nt[(s0 + 1) * Cfg::NROW + t] = s0 + 1 < t ? k1 * r1 * b1 : 0.f;
-                if constexpr (Cfg::MODE == 2) {
-                    unsigned x[2];
-                    split_pair<2>(s0 < t ? k0 * r0 : 0.f, s0 + 1 < t ? k1 * r1 : 0.f, x);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-                        *reinterpret_cast<unsigned *>(tri + (2 + Cfg::PP + m) * Cfg::TRI + t * kTriRow + s0 * 2) = x[m];
-                }
-                const float q0 = s0 <= t ? (qk[i][2 * r] + qks[i][2 * r]) * r0 * p.scale : 0.f;
-                const float q1 = s0 + 1 <= t ? (qk[i][2 * r + 1] + qks[i][2 * r + 1]) * r1 * p.scale : 0.f;
-                unsigned w[Cfg::PP];
-                split_pair<Cfg::PP>(q0, q1, w);
-#pragma unroll
-                for (int m = 0; m < Cfg::PP; ++m)
-                    *reinterpret_cast<unsigned *>(tri + (2 + m) * Cfg::TRI + t * kTriRow + s0 * 2) = w[m];
-            }
-        }
-        __syncwarp();
-        // lane t solves row t of T (I + n) = I from the diagonal leftwards
-        if (lane < C) {
-            float T[C];
-#pragma unroll
-            for (int s = C - 1; s >= 0; --s) {
-                float x0 = 0.f, x1 = 0.f;
-#pragma unroll
-                for (int r4 = (s + 1) / 4; r4 < C / 4; ++r4) {
-                    const float4 n4 = *reinterpret_cast<const float4 *>(nt + s * Cfg::NROW + 4 * r4);
-                    const float nv[4] = {n4.x, n4.y, n4.z, n4.w};
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        if (4 * r4 + m > s) {
-                            if (m & 1) x1 = fmaf(-T[4 * r4 + m], nv[m], x1);
-                            else x0 = fmaf(-T[4 * r4 + m], nv[m], x0);
-                        }
-                }
-                T[s] = s == lane ? 1.f : (s < lane ? x0 + x1 : 0.f);
-            }
-#pragma unroll
-            for (int s = 0; s < C; ++s) T[s] = s == lane ? 0.f : T[s];
-            unsigned w[2][C / 2];
-#pragma unroll
-            for (int s = 0; s < C / 2; ++s) {
+        for (int r = 0; r < 2; ++r) {
+            const int t = g + 8 * r;
+            const float r0 = rat[t * RATROW + s0 + 1], r1 = rat[t * RATROW + s0 + 2];
+            const float k0 = s0 < t ? (kk[i][2 * r] + kks[i][2 * r]) * r0 : 0.f;
+            const float k1 = s0 + 1 < t ? (kk[i][2 * r + 1] + kks[i][2 * r + 1]) * r1 : 0.f;
+            nt[s0 * NROW + t] = s0 < t ? k0 * b0 : 0.f;
+            nt[(s0 + 1) * NROW + t] = s0 + 1 < t ? k1 * b1 : 0.f;
+            unsigned char *at = out + tri_at(t, i) + t4 * 4;
+            if constexpr (Block::BWD) {
                 unsigned x[2];
-                split_pair<2>(T[2 * s], T[2 * s + 1], x);
-                w[0][s] = x[0]; w[1][s] = x[1];
+                split_pair<2>(k0, k1, x);
+#pragma unroll
+                for (int m = 0; m < 2; ++m) *reinterpret_cast<unsigned *>(at + (2 + Block::PP + m) * kTri) = x[m];
             }
+            const float q0 = s0 <= t ? (qk[i][2 * r] + qks[i][2 * r]) * r0 * p.scale : 0.f;
+            const float q1 = s0 + 1 <= t ? (qk[i][2 * r + 1] + qks[i][2 * r + 1]) * r1 * p.scale : 0.f;
+            unsigned w[Block::PP];
+            split_pair<Block::PP>(q0, q1, w);
+#pragma unroll
+            for (int m = 0; m < Block::PP; ++m) *reinterpret_cast<unsigned *>(at + (2 + m) * kTri) = w[m];
+        }
+    }
+    __syncwarp();
+    // lane t solves row t of T (I + n) = I from the diagonal leftwards
+    if (lane < C) {
+        float T[C];
+#pragma unroll
+        for (int s = C - 1; s >= 0; --s) {
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+            for (int r4 = (s + 1) / 4; r4 < C / 4; ++r4) {
+                const float4 n4 = *reinterpret_cast<const float4 *>(nt + s * NROW + 4 * r4);
+                const float nv[4] = {n4.x, n4.y, n4.z, n4.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+                    if (4 * r4 + m > s) {
+                        if (m & 1) x1 = fmaf(-T[4 * r4 + m], nv[m], x1);
+                        else x0 = fmaf(-T[4 * r4 + m], nv[m], x0);
+                    }
+            }
+            T[s] = s == lane ? 1.f : (s < lane ? x0 + x1 : 0.f);
+        }
+#pragma unroll
+        for (int s = 0; s < C; ++s) T[s] = s == lane ? 0.f : T[s];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            unsigned x[4][2];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) split_pair<2>(T[8 * half + 2 * y], T[8 * half + 2 * y + 1], x[y]);
 #pragma unroll
             for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int s = 0; s < C / 8; ++s)
-                    *reinterpret_cast<uint4 *>(tri + m * Cfg::TRI + lane * kTriRow + s * 16) =
-                        make_uint4(w[m][4 * s], w[m][4 * s + 1], w[m][4 * s + 2], w[m][4 * s + 3]);
+                *reinterpret_cast<uint4 *>(out + m * kTri + tri_at(lane, half)) =
+                    make_uint4(x[0][m], x[1][m], x[2][m], x[3][m]);
         }
-        __syncwarp();
     }
-};
+}
 
 // Addresses of a 16 x 16 tile's B operand (n-tiles 0, 1) for ldmatrix: rows are n (plain
 // load) or k (transposing load).
@@ -327,6 +294,8 @@ __device__ __forceinline__ unsigned b_rows_n(int lane, int rowbytes) {
 __device__ __forceinline__ unsigned b_rows_k(int lane, int rowbytes) {
     return unsigned(((lane >> 3 & 1) * 8 + (lane & 7)) * rowbytes + (lane >> 4) * 16);
 }
+__device__ __forceinline__ unsigned tri_rows_n(int lane) { return tri_at((lane >> 4) * 8 + (lane & 7), lane >> 3 & 1); }
+__device__ __forceinline__ unsigned tri_rows_k(int lane) { return tri_at((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4); }
 
 // One warp's [16 rows x 16 tokens] tile of staged rows [token][row] in accumulator layout.
 template <typename T>
@@ -360,10 +329,10 @@ __device__ __forceinline__ void store_tok_tile(T *out, size_t stride, int ntok, 
         unsigned r[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m) r[m] = pack_bf16x2(o[m & 1][2 * (m >> 1)], o[m & 1][2 * (m >> 1) + 1]);
-        stsm4_t(smem_u32(tile) + b_rows_k(lane, kTriRow), r);
+        stsm4_t(smem_u32(tile) + b_rows_k(lane, kOutRow), r);
         __syncwarp();
         const int tok = lane >> 1, half = lane & 1;
-        const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok * kTriRow + half * 16);
+        const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok * kOutRow + half * 16);
         if (tok < ntok && half * 8 < nrow) *reinterpret_cast<uint4 *>(out + size_t(tok) * stride + half * 8) = w;
         __syncwarp();
     } else {
@@ -393,29 +362,58 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
     // chunk of loop step i: forwards, or backwards in the reverse pass
     auto chunk_of = [&](int i) { return MODE == 2 ? nchunk - 1 - i : i; };
 
-    if (warp == NW) {
-        DeltaProducer<Cfg> pr{p, smem, lane, b, h, h / (p.heads / p.qk_heads), slice * NW * 16, nchunk};
-        auto chunk_or_none = [&](int i) { return i < nchunk ? chunk_of(i) : -1; };
+    // The CTA's threads copy a chunk's rows and its block, one commit group per chunk.
+    const int tid = threadIdx.x, hk = h / (p.heads / p.qk_heads);
+    const size_t krow = size_t(p.qk_heads) * p.N, vrow = size_t(p.heads) * p.P;
+    const size_t koff = size_t(b) * p.seqlen * krow + size_t(hk) * p.N;
+    const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
+    auto copy_rows = [&](unsigned dst, int rowbytes, const auto *src, size_t stride, auto width, int limit, int t0) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
+        constexpr int E = 16 / sizeof(T), CR = decltype(width)::value / E;      // values per copy, copies per row
 #pragma unroll
-        for (int i = 0; i < 3; ++i) pr.issue(chunk_or_none(i), i);
-        float gate = pr.load_gate(chunk_or_none(0)), next = pr.load_gate(chunk_or_none(1));
-        cp_async_wait<2>();
-        __syncwarp();
-        pr.prepare(0, 0, gate);
-        __syncthreads();
-        for (int i = 0; i < nchunk; ++i) {
-            if constexpr (MODE != 0) if (i > 0) pr.flush_sums(chunk_of(i - 1), (i - 1) & 1, slice);
-            pr.issue(chunk_or_none(i + 3), (i + 3) & 3);
-            gate = next;
-            next = pr.load_gate(chunk_or_none(i + 2));
-            cp_async_wait<2>();
-            __syncwarp();
-            if (i + 1 < nchunk) pr.prepare((i + 1) & 3, (i + 1) & 1, gate);
-            __syncthreads();
+        for (int i = 0; i < (C * CR + Cfg::NT - 1) / Cfg::NT; ++i) {
+            const int x = tid + Cfg::NT * i, r = x / CR, n = (x % CR) * E;
+            if (C * CR % Cfg::NT == 0 || x < C * CR) {
+                const bool ok = t0 + r < p.seqlen && n < limit;
+                cp_async_16z(dst + r * rowbytes + n * int(sizeof(T)), src + (ok ? size_t(t0 + r) * stride + n : 0), ok);
+            }
         }
-        if constexpr (MODE != 0) pr.flush_sums(chunk_of(nchunk - 1), (nchunk - 1) & 1, slice);
-        return;
-    }
+    };
+    auto issue = [&](int i) {
+        if (i < nchunk) {
+            const int c = chunk_of(i), t0 = c * C;
+            const unsigned base = smem_u32(smem + (i & 3) * Cfg::STAGE);
+            const std::integral_constant<int, NP> kw;
+            const std::integral_constant<int, NW * 16> vw;
+#pragma unroll
+            for (int m = 0; m < KP; ++m) {
+                copy_rows(base + Cfg::OFF_K + m * Cfg::PIECE, Cfg::KROW,
+                          static_cast<const __nv_bfloat16 *>(p.k) + m * p.piece + koff, krow, kw, p.N, t0);
+                copy_rows(base + Cfg::OFF_Q + m * Cfg::PIECE, Cfg::KROW,
+                          static_cast<const __nv_bfloat16 *>(p.q) + m * p.piece + koff, krow, kw, p.N, t0);
+            }
+            copy_rows(base + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + voff, vrow, vw, p.P - slice * NW * 16, t0);
+            if constexpr (MODE != 0)
+                copy_rows(base + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const typename Cfg::Tv2 *>(p.v2) + voff, vrow, vw,
+                          p.P - slice * NW * 16, t0);
+            const unsigned char *blk = p.prep + (size_t(bh) * nchunk + c) * Cfg::Block::BYTES;
+            for (int x = tid; x < Cfg::Block::BYTES / 16; x += Cfg::NT)
+                cp_async_16z(base + Cfg::OFF_TRI + 16 * x, blk + 16 * x, true);
+        }
+        cp_async_commit();
+    };
+    // The sums over the warps' rows of loop step i, left in shared memory at its end.
+    auto flush_sums = [&](int i) {
+        const int t = chunk_of(i) * C + (lane & 15), m = lane >> 4;
+        if (m >= Cfg::NRED || t >= p.seqlen) return;
+        const float *red = reinterpret_cast<const float *>(smem + Cfg::OFF_RED + (i & 1) * Cfg::REDBUF) + m * NW * C;
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) x += red[w * C + (lane & 15)];
+        (m ? p.sum1 : p.sum0)[(size_t(slice) * p.batch * p.heads + bh) * p.seqlen + t] = x;
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i) issue(i);
 
     const int g = lane >> 2, t4 = lane & 3;
     const int p0 = slice * NW * 16 + warp * 16;           // the warp's first row
@@ -438,10 +436,10 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             const float2 f = *reinterpret_cast<const float2 *>(p.h0 + sbase + off);
             x = f.x; y = f.y;
         });
-    unsigned char *tile = smem + Cfg::OFF_OUT + warp * C * kTriRow;
+    unsigned char *tile = smem + Cfg::OFF_OUT + warp * C * kOutRow;
     const unsigned bn = b_rows_n(lane, Cfg::KROW), bk = b_rows_k(lane, Cfg::KROW);
-    const unsigned tn = b_rows_n(lane, kTriRow), tk = b_rows_k(lane, kTriRow);
-    const size_t ostride = size_t(p.heads) * p.P;
+    const unsigned tn = tri_rows_n(lane), tk = tri_rows_k(lane);
+    const size_t ostride = vrow;
     const int nbound = (p.seqlen + kDeltaSave - 1) / kDeltaSave + 1;       // boundaries, the end among them
     auto bound_at = [&](int x) { return (size_t(bh) * nbound + x) * p.P * p.N; };
     auto keep_state = [&](float *ck, int x) {
@@ -458,7 +456,6 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             const bool ok = r < nrow && n < p.N;
             cp_async_16z(smem_u32(strow + r * Cfg::STROW + n * 4), base + (ok ? size_t(p0 + r) * p.N + n : 0), ok);
         }
-        cp_async_commit();
     };
     auto dot_state = [&](int x) {
         cp_async_wait<0>();
@@ -502,22 +499,28 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
         if constexpr (MODE == 2)
             for (int x = lane; x < nbound; x += 32)
                 p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = 0.f;
-        __syncthreads();
-        for (int i = 0; i < nchunk; ++i) __syncthreads();
+        for (int i = 0; i < nchunk; ++i) {
+            cp_async_wait<2>();
+            __syncthreads();
+            issue(i + 3);
+        }
+        cp_async_wait<0>();
+        if constexpr (MODE != 0) __syncthreads();
         return;
     }
-    if constexpr (MODE == 2) fetch_state(nbound - 1);
-    __syncthreads();
+    if constexpr (MODE == 2) {
+        fetch_state(nbound - 1);
+        cp_async_commit();
+    }
 
     for (int i = 0; i < nchunk; ++i) {
         const int c = chunk_of(i);
+        cp_async_wait<2>();
+        __syncthreads();
         const unsigned char *stage = smem + (i & 3) * Cfg::STAGE;
-        const unsigned char *tri = smem + Cfg::OFF_TRI + (i & 1) * Cfg::TRIBUF;
-        const float *vec = reinterpret_cast<const float *>(smem + Cfg::OFF_VEC + (i & 1) * Cfg::VECBUF);
-        const unsigned kbase = Cfg::F32K ? smem_u32(smem + Cfg::OFF_PIECES + (i & 1) * 2 * KP * Cfg::PIECE)
-                                         : smem_u32(stage + Cfg::OFF_K);
-        const unsigned qbase = Cfg::F32K ? kbase + KP * Cfg::PIECE : smem_u32(stage + Cfg::OFF_Q);
-        const unsigned tbase = smem_u32(tri);
+        const unsigned char *tri = stage + Cfg::OFF_TRI;
+        const float *vec = reinterpret_cast<const float *>(tri + Cfg::Block::OFF_VEC);
+        const unsigned kbase = smem_u32(stage + Cfg::OFF_K), qbase = smem_u32(stage + Cfg::OFF_Q), tbase = smem_u32(tri);
         const size_t tok0 = (size_t(b) * p.seqlen + size_t(c) * C) * p.heads + h;
         const int ntok = min(C, p.seqlen - c * C);
         constexpr int CS = kDeltaSave / C;
@@ -536,8 +539,10 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 keep_state(p.dck, c / CS + 1);
                 dot_state(c / CS + 1);
             }
-            if (c % CS == 0) fetch_state(c / CS);
+            if (c % CS == 0) fetch_state(c / CS);          // in the commit group of issue()
         }
+        issue(i + 3);
+        if constexpr (MODE != 0) if (i > 0 && warp == 0) flush_sums(i - 1);
 
         // S K^T, and S Q^T for y
         float sk[2][4], sks[2][4], sq[2][4], sqs[2][4];
@@ -586,7 +591,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             unsigned A[Cfg::F32V ? 3 : 1][4], pb[3][4];
             split_tiles<Cfg::F32V ? 3 : 1>(v[0], v[1], A);
 #pragma unroll
-            for (int m = 0; m < 3; ++m) ldsm4_t(pb[m], tbase + (2 + m) * Cfg::TRI + tk);
+            for (int m = 0; m < 3; ++m) ldsm4_t(pb[m], tbase + (2 + m) * kTri + tk);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 zero4(lo[n]); zero4(los[n]);
@@ -604,8 +609,8 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             float d[2][4], ds[2][4];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                if constexpr (MODE == 2) ldsm4_t(tb[m], tbase + m * Cfg::TRI + tk);
-                else ldsm4(tb[m], tbase + m * Cfg::TRI + tn);
+                if constexpr (MODE == 2) ldsm4_t(tb[m], tbase + m * kTri + tk);
+                else ldsm4(tb[m], tbase + m * kTri + tn);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -686,7 +691,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             }
             split_tiles<PO>(w[0], w[1], A);
 #pragma unroll
-            for (int m = 0; m < PO; ++m) ldsm4(pb[m], tbase + (2 + m) * Cfg::TRI + tn);
+            for (int m = 0; m < PO; ++m) ldsm4(pb[m], tbase + (2 + m) * kTri + tn);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 zero4(o[n]); zero4(os[n]);
@@ -715,7 +720,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             float vv[2][4];
             split_tiles<2>(x[0], x[1], A);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) ldsm4_t(nb[m], tbase + (2 + Cfg::PP + m) * Cfg::TRI + tk);
+            for (int m = 0; m < 2; ++m) ldsm4_t(nb[m], tbase + (2 + PO + m) * kTri + tk);
             load_tok_tile<typename Cfg::Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(typename Cfg::Tv2)), Cfg::V2ROW,
                                              lane, vv);
 #pragma unroll
@@ -734,7 +739,11 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             if (p.w != nullptr) store_tok_tile<float>(p.w + tok0 * p.P + p0, ostride, ntok, nrow, tile, lane, x);
             store_tok_tile<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, ostride, ntok, nrow, tile, lane, x);
         }
+    }
+    cp_async_wait<0>();
+    if constexpr (MODE != 0) {
         __syncthreads();
+        if (warp == 0) flush_sums(nchunk - 1);
     }
     if constexpr (MODE == 1) keep_state(p.ck, nbound - 1);
     if constexpr (MODE == 2) dot_state(0);

@@ -27,47 +27,41 @@ template <bool BWD, typename F> int by_width(int dim, F f) {
     return f(integral_constant<int, 0>(), integral_constant<int, 2>(), (dim + 511) / 512 * 32);
 }
 
-// CTAs that the GPU holds at once, or fewer if the rows need fewer.
-template <typename K> int grid_of(K kernel, int threads, size_t smem, long long rows, int rows_per_cta, int *grid) {
-    int per = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, smem) != cudaSuccess || per < 1)
-        return SSM_ERR_CUDA;
-    *grid = int(std::min<long long>((rows + rows_per_cta - 1) / rows_per_cta, (long long)kSMs * per));
-    return SSM_OK;
+// CTAs: one for the rows it takes, at most what the GPU's SMs hold at `per_sm` threads each
+// (the kernels' registers allow 512 of the widest variants; a CTA walks the rest of its rows).
+int grid_of(int lanes, int threads, int per_sm, int rows) {
+    const int per_cta = lanes ? threads / lanes : 1;
+    return std::min((rows - 1) / per_cta + 1, kSMs * std::max(1, per_sm / threads));
 }
 
 template <bool VEC, typename Tin, typename Tout> int run_fwd(const ssm::NormArgs &a, cudaStream_t s) {
     return by_width<false>(a.dim, [&](auto lanes, auto v, int threads) {
         auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), VEC, Tin, Tout>;
-        int grid = 0;
-        if (const int st = grid_of(kernel, threads, 0, a.rows, lanes() ? threads / std::max(1, lanes()) : 1, &grid)) return st;
-        kernel<<<grid, threads, 0, s>>>(a);
+        kernel<<<grid_of(lanes(), threads, 1024, int(a.rows)), threads, 0, s>>>(a);
         return status_of(cudaGetLastError());
     });
 }
 
+int bwd_grid(int rows, int dim) {
+    return by_width<true>(dim, [&](auto lanes, auto, int threads) { return grid_of(lanes(), threads, 512, rows); });
+}
+
 template <bool VEC, typename Tin, typename Tg>
-int run_bwd(ssm::NormArgs a, float *dw, float *db, cudaStream_t s) {
-    return by_width<true>(a.dim, [&](auto lanes, auto v, int threads) {
+int run_bwd(ssm::NormArgs a, float *dw, float *db, void *workspace, size_t bytes, cudaStream_t s) {
+    const int grid = bwd_grid(int(a.rows), a.dim);
+    Scratch ws;
+    if (const int st = ws.take(workspace, bytes, ssm_layer_norm_bwd_workspace(int(a.rows), a.dim), s)) return st;
+    a.part = reinterpret_cast<float *>(ws.p);
+    int st = by_width<true>(a.dim, [&](auto lanes, auto v, int threads) {
         auto kernel = ssm::layer_norm_bwd_kernel<lanes(), v(), VEC, Tin, Tg>;
-        const size_t smem = lanes() ? 2 * size_t(a.dim) * sizeof(float) : 0;
-        int grid = 0;
-        if (const int st = grid_of(kernel, threads, smem, a.rows, lanes() ? threads / std::max(1, lanes()) : 1, &grid)) return st;
-        float *ws = nullptr;
-        if (cudaMallocAsync(reinterpret_cast<void **>(&ws), size_t(grid) * 2 * a.dim * sizeof(float), s) != cudaSuccess) {
-            cudaGetLastError();
-            return int(SSM_ERR_CUDA);
-        }
-        a.part = ws;
-        kernel<<<grid, threads, smem, s>>>(a);
-        int st = status_of(cudaGetLastError());
-        if (st == SSM_OK && (dw != nullptr || db != nullptr)) {
-            ssm::layer_norm_cols_kernel<<<(2 * a.dim + 31) / 32, 256, 0, s>>>(ws, grid, a.dim, dw, db);
-            st = status_of(cudaGetLastError());
-        }
-        const cudaError_t fe = cudaFreeAsync(ws, s);
-        return st == SSM_OK && fe != cudaSuccess ? int(SSM_ERR_CUDA) : st;
+        kernel<<<grid, threads, lanes() ? 2 * size_t(a.dim) * sizeof(float) : 0, s>>>(a);
+        return status_of(cudaGetLastError());
     });
+    if (st == SSM_OK && (dw != nullptr || db != nullptr)) {
+        ssm::layer_norm_cols_kernel<<<(2 * a.dim + 31) / 32, 256, 0, s>>>(a.part, grid, a.dim, dw, db);
+        st = status_of(cudaGetLastError());
+    }
+    return ws.release(st);
 }
 
 template <typename F> int by_types(int ta, int tb, F f) {
@@ -109,20 +103,28 @@ int ssm_layer_norm_fwd(const void *x, const float *weight, const float *bias, vo
     });
 }
 
+size_t ssm_layer_norm_bwd_workspace(int rows, int dim) {
+    if (rows < 1 || dim < 1 || dim > kMaxDim) return 0;
+    return size_t(bwd_grid(rows, dim)) * 2 * dim * sizeof(float);
+}
+
 int ssm_layer_norm_bwd(const void *dy, const void *x, const float *weight, const float *mean,
                        const float *rstd, void *dx, float *dweight, float *dbias, int rows, int dim,
-                       int in_dtype, int grad_dtype, void *cuda_stream) {
+                       int in_dtype, int grad_dtype, void *workspace, size_t workspace_bytes, void *cuda_stream) {
     if (!valid_dtype(in_dtype) || !valid_dtype(grad_dtype)) return SSM_ERR_INVALID_ARG;
     if (rows < 0 || dim < 1) return SSM_ERR_INVALID_ARG;
     if (dim > kMaxDim) return SSM_ERR_UNSUPPORTED;
     if (rows > 0 && (!dy || !x || !mean || !rstd || !dx)) return SSM_ERR_INVALID_ARG;
     for (const void *q : {dy, x, (const void *)weight, (const void *)mean, (const void *)rstd, (const void *)dx,
-                          (const void *)dweight, (const void *)dbias})
+                          (const void *)dweight, (const void *)dbias, (const void *)workspace})
         if (q && !aligned16(q)) return SSM_ERR_ALIGNMENT;
     const size_t n = size_t(rows) * dim, wb = size_t(dim) * 4, sb = size_t(rows) * 4, gb = n * dtype_size(grad_dtype);
     const struct { const void *p; size_t n; } in[] = {{x, n * dtype_size(in_dtype)}, {weight, wb}, {dy, gb}, {mean, sb}, {rstd, sb}};
     const struct { const void *p; size_t n; } out[] = {{dx, gb}, {dweight, wb}, {dbias, wb}};
+    for (const auto &q : in)
+        if (overlaps(workspace, workspace_bytes, q.p, q.n)) return SSM_ERR_INVALID_ARG;
     for (const auto &o : out) {
+        if (overlaps(workspace, workspace_bytes, o.p, o.n)) return SSM_ERR_INVALID_ARG;
         for (const auto &q : in)
             if (overlaps(o.p, o.n, q.p, q.n)) return SSM_ERR_INVALID_ARG;
         for (const auto &q : out)
@@ -140,7 +142,8 @@ int ssm_layer_norm_bwd(const void *dy, const void *x, const float *weight, const
     return by_types(in_dtype, grad_dtype, [&](auto ti, auto tg) {
         using Ti = decltype(ti);
         using Tg = decltype(tg);
-        return dim % 8 == 0 ? run_bwd<true, Ti, Tg>(a, dweight, dbias, s) : run_bwd<false, Ti, Tg>(a, dweight, dbias, s);
+        return dim % 8 == 0 ? run_bwd<true, Ti, Tg>(a, dweight, dbias, workspace, workspace_bytes, s)
+                            : run_bwd<false, Ti, Tg>(a, dweight, dbias, workspace, workspace_bytes, s);
     });
 }
 
