@@ -24,7 +24,7 @@ using Block = ssm::DeltaBlock<3, true>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, pieces, e, w, ck, dck, dyy, vw, edu, zsum, all;
+    size_t prep, pieces, e, w, ck, dck, dyy, edu, zsum, all;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
@@ -38,7 +38,6 @@ struct BwdParts {
         part(ck, state);
         part(dck, state);
         part(dyy, sum);
-        part(vw, sum);
         part(edu, sum);
         part(zsum, size_t(delta_slices(P)) * kDeltaWarps * bh * nbound * 4);
         all = at;
@@ -58,18 +57,18 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     float *w = sizeof(Tg) == 4 ? static_cast<float *>(dv) : part(at.w);
     constexpr int KP = sizeof(Tin) == 4 ? 3 : 1;
     int st = dispatch_prep<Tin, Block>(f, ws.p + at.prep, ws.p + at.pieces, s);
-    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum0 = part(at.dyy);
+    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
-        r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = sizeof(Tg) == 4 ? nullptr : w;
-        r.dck = part(at.dck); r.sum0 = part(at.vw); r.sum1 = part(at.edu); r.zsum = part(at.zsum);
-        st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
+        r.v = dy; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = sizeof(Tg) == 4 ? nullptr : w;
+        r.dck = part(at.dck); r.sum = part(at.edu); r.zsum = part(at.zsum);
+        st = dispatch_chain<KP, Tg, Tg, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
         const int slices = delta_slices(f.P);
-        const ssm::DeltaGradArgs g{q, k, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
-                                   part(at.vw), part(at.edu), part(at.zsum), dq, dk, da, dbeta, f.batch, f.seqlen,
+        const ssm::DeltaGradArgs g{q, k, v, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
+                                   part(at.edu), part(at.zsum), dq, dk, da, dbeta, f.batch, f.seqlen,
                                    f.heads, f.qk_heads, f.P, f.N, slices, slices * kDeltaWarps, f.scale};
         st = f.N <= 64 ? launch_grad<64, Tin, Tg>(g, s) : launch_grad<128, Tin, Tg>(g, s);
     }

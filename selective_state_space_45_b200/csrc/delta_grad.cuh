@@ -21,10 +21,10 @@
 namespace ssm {
 
 struct DeltaGradArgs {
-    const void *q, *k, *dy;
+    const void *q, *k, *v, *dy;
     const float *a, *beta, *e, *w;
     const float *ck, *dck;             // states and their gradients at the boundaries
-    const float *dyy, *vw, *edu;       // [slices][batch][heads][seqlen]
+    const float *dyy, *edu;            // [slices][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
     void *dq, *dk;
     float *da, *dbeta;
@@ -97,6 +97,25 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaGradArgs p) 
         const Tg *dyp = static_cast<const Tg *>(p.dy) + v0;
         const float *ep = p.e + v0, *wp = p.w + v0;
         const float *S0 = p.ck + (bh * nbound + c) * p.P * p.N, *dE = p.dck + (bh * nbound + c + 1) * p.P * p.N;
+        // v.w of every token: four threads per token, sixteen bytes of v at a time
+        float vw = 0.f;
+        {
+            const int r = tid >> 2;
+            if (r < nt) {
+                const Tin *vp = static_cast<const Tin *>(p.v) + v0 + size_t(r) * vrow;
+                for (int x = (tid & 3) * 8; x < p.P; x += 32) {
+                    float a[8], f[8];
+                    load8(vp + x, a);
+                    load8(wp + size_t(r) * vrow + x, f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) vw = fmaf(a[i], f[i], vw);
+                }
+            }
+            vw += __shfl_xor_sync(0xffffffffu, vw, 1);
+            vw += __shfl_xor_sync(0xffffffffu, vw, 2);
+        }
+        __syncthreads();
+        if ((tid & 3) == 0) dec.d[tid >> 2] = vw;
         __syncthreads();
         if (tid < C) {
             const size_t at = (size_t(b) * p.seqlen + t0 + tid) * p.heads + h;
@@ -106,10 +125,10 @@ __global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaGradArgs p) 
             if (tid < nt)
                 for (int s = 0; s < p.slices; ++s) {
                     const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                    d += p.dyy[x] - p.vw[x];
+                    d += p.dyy[x];
                     db += p.edu[x];
                 }
-            dec.d[tid] = d;
+            dec.d[tid] = d - dec.d[tid];
             if (tid < nt) p.dbeta[at] = db;
         }
         __syncthreads();

@@ -27,12 +27,24 @@ inline size_t pieces_bytes(int batch, int seqlen, int qk_heads, int N, int in_dt
     return in_dtype == SSM_F32 ? round16(2 * 3 * piece_values(batch, seqlen, qk_heads, N) * 2) : 0;
 }
 
+// Dynamic shared memory of a kernel, with the SM's memory split for as many CTAs as fit (the
+// default split left one chain CTA per SM where two fit).
+template <typename K> int set_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+                   cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                        int(cudaSharedmemCarveoutMaxShared)) == cudaSuccess
+               ? SSM_OK
+               : SSM_ERR_CUDA;
+}
+
 // The chunk blocks into `prep` (and the pieces of fp32 q, k behind `pieces`); on return a's
 // q and k are what the chains read.
 template <int NP, typename Tin, class Block> int launch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
-    const long long blocks = ((long long)a.batch * a.heads * (long long)delta_chunks(a.seqlen) + 7) / 8;
+    const long long blocks = ((long long)a.batch * a.heads * (long long)delta_chunks(a.seqlen) + 3) / 4;
     if (blocks > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    ssm::delta_prep_kernel<NP, Tin, Block><<<unsigned(blocks), 256, 0, s>>>(a);
+    constexpr int smem = 4 * int(sizeof(ssm::PrepScratch<Block>));
+    if (const int st = set_smem(ssm::delta_prep_kernel<NP, Tin, Block>, smem)) return st;
+    ssm::delta_prep_kernel<NP, Tin, Block><<<unsigned(blocks), 128, smem, s>>>(a);
     return status_of(cudaGetLastError());
 }
 template <typename Tin, class Block>
@@ -61,9 +73,7 @@ int launch_chain(ssm::DeltaArgs a, cudaStream_t s) {
     a.slices = delta_slices(a.P);
     const long long ctas = (long long)a.batch * a.heads * a.slices;
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    if (cudaFuncSetAttribute(ssm::delta_chain_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(Cfg::SMEM_BYTES)) != cudaSuccess)
-        return SSM_ERR_CUDA;
+    if (const int st = set_smem(ssm::delta_chain_kernel<Cfg>, int(Cfg::SMEM_BYTES))) return st;
     ssm::delta_chain_kernel<Cfg><<<unsigned(ctas), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
     return status_of(cudaGetLastError());
 }
