@@ -20,7 +20,7 @@ template <int NP, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGra
     return status_of(cudaGetLastError());
 }
 
-using Block = ssm::DeltaBlock<3, true>;
+using Block = ssm::DeltaBlock<2, true>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
@@ -55,7 +55,7 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     auto part = [&](size_t off) { return reinterpret_cast<float *>(ws.p + off); };
     const void *q = f.q, *k = f.k;
     float *w = sizeof(Tg) == 4 ? static_cast<float *>(dv) : part(at.w);
-    constexpr int KP = sizeof(Tin) == 4 ? 3 : 1;
+    constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
     int st = dispatch_prep<Tin, Block>(f, ws.p + at.prep, ws.p + at.pieces, s);
     f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);

@@ -18,13 +18,13 @@ inline int delta_sizes(int batch, int tokens, int heads, int qk_heads, int headd
 
 inline size_t delta_chunks(int seqlen) { return (size_t(seqlen) + ssm::kDeltaC - 1) / ssm::kDeltaC; }
 
-// Bytes of the prep kernel's blocks, and of the pieces of fp32 q and k.
+// Bytes of the prep kernel's blocks, and of the pieces of fp32 q and k (two of 2 bytes each).
 template <class Block> size_t prep_bytes(int batch, int seqlen, int heads) {
     return size_t(batch) * heads * delta_chunks(seqlen) * Block::BYTES;
 }
 inline size_t piece_values(int batch, int seqlen, int qk_heads, int N) { return size_t(batch) * seqlen * qk_heads * N; }
 inline size_t pieces_bytes(int batch, int seqlen, int qk_heads, int N, int in_dtype) {
-    return in_dtype == SSM_F32 ? round16(2 * 3 * piece_values(batch, seqlen, qk_heads, N) * 2) : 0;
+    return in_dtype == SSM_F32 ? round16(2 * 2 * piece_values(batch, seqlen, qk_heads, N) * 2) : 0;
 }
 
 // Dynamic shared memory of a kernel, with the SM's memory split for as many CTAs as fit (the
@@ -52,8 +52,8 @@ int dispatch_prep(ssm::DeltaArgs &a, unsigned char *prep, unsigned char *pieces,
     a.prep = prep;
     if (sizeof(Tin) == 4) {
         a.piece = piece_values(a.batch, a.seqlen, a.qk_heads, a.N);
-        a.kp = reinterpret_cast<__nv_bfloat16 *>(pieces);
-        a.qp = a.kp + 3 * a.piece;
+        a.kp = reinterpret_cast<__half *>(pieces);
+        a.qp = a.kp + 2 * a.piece;
     }
     const int st = a.N <= 32   ? launch_prep<32, Tin, Block>(a, s)
                    : a.N <= 64 ? launch_prep<64, Tin, Block>(a, s)

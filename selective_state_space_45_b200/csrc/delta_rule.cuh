@@ -19,13 +19,13 @@
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
 //     w = T^T (beta (end (dS k) + Pm^T dO)) = dv,  dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
 //
-// Precision: the products run on the tensor cores in bf16 with fp32 accumulation.  q, k, v
-// in bf16 are exact operands; an fp32 operand goes in as three bf16 pieces that hold all its
-// bits, and products of pieces below 2^-24 of the leading one are left out.  Only what is
-// behind a bf16 y takes two pieces (2^-16).  Sums into the state are fp32 additions outside
-// the tensor core, which cuts off instead of rounding.  Against the definition in 64 bits
-// the state comes out at 2e-7, as from fp32 arithmetic; two pieces everywhere gave 6e-6 at
-// four fifths of the time.
+// Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
+// operand scaled by a power of two (one per chunk for k, q and the triangles, one per warp and
+// chunk for the state and what follows from it) so that its range does not matter.  bf16
+// inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), those
+// behind a bf16 y as one.  Against the definition in 64 bits the state comes out at 2e-7, as
+// from fp32 arithmetic.  Three bf16 pieces hold the same bits but cost half as many products
+// again; two bf16 pieces gave 6e-6.
 #pragma once
 
 #include <type_traits>
@@ -35,11 +35,11 @@
 namespace ssm {
 
 struct DeltaArgs {
-    const void *q, *k;      // [batch][seqlen][qk_heads][dstate]; the chains: bf16, or the pieces
-                            // that the prep kernel made of fp32 ones, `piece` values apart
+    const void *q, *k;      // [batch][seqlen][qk_heads][dstate]; the chains: bf16, or the scaled
+                            // fp16 pieces that the prep kernel made of fp32 ones, `piece` values apart
     size_t piece;
     unsigned char *prep;    // [batch][heads][chunks] blocks of the prep kernel
-    __nv_bfloat16 *qp, *kp; // prep kernel: where the pieces of fp32 q, k go
+    __half *qp, *kp;        // prep kernel: where the pieces of fp32 q, k go
     const void *v;          // [batch][seqlen][heads][headdim]; the reverse pass: dy
     const void *v2;         // forward of the backward pass: dy
     const float *a, *beta;  // [batch][seqlen][heads]
@@ -68,17 +68,28 @@ constexpr int kOutRow = 48;          // bytes per row of a warp's output tile
 __device__ __forceinline__ int tri_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
 
 // What the prep kernel leaves per chunk and head.  A triangle is the three 16 x 16 tiles
-// (0,0), (1,0), (1,1) per piece.  T - I in three pieces, Pm in PP, fp32 vectors over the
-// chunk's tokens (gam, scale gam, beta, end, end beta) and gam of the last token; for the
-// reverse pass n / beta in three pieces behind them.
+// (0,0), (1,0), (1,1) per fp16 piece, scaled by a power of two: T - I in two pieces, Pm in PP,
+// and for the reverse pass n / beta in two behind the vectors.  Vectors over the chunk's
+// tokens, the scales of k and q (ck, cq) taken back out where a product with them is used:
+enum {
+    kVecGk,        // gam / ck: S k -> gam S k
+    kVecSgq,       // scale gam / cq
+    kVecBeta,
+    kVecEk,        // end / ck
+    kVecEbk,       // end beta / ck
+    kVecScalars,   // then the scalars below
+    kVecs
+};
+enum { kGamLast, kCk, kCq, kInvT, kInvP, kInvN, kMaxBeta, kMaxEbk, kMaxGk, kMaxSgq };   // 1 / scales; largest magnitudes
 template <int PP_, bool BWD_> struct DeltaBlock {
     static constexpr int PP = PP_;
     static constexpr bool BWD = BWD_;
-    static constexpr int OFF_P = 9 * kTri, OFF_VEC = OFF_P + 3 * PP * kTri, OFF_N = OFF_VEC + 6 * kDeltaC * 4;
-    static constexpr int BYTES = OFF_N + (BWD ? 9 * kTri : 0);
+    static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 3 * PP * kTri, OFF_N = OFF_VEC + kVecs * kDeltaC * 4;
+    static constexpr int BYTES = OFF_N + (BWD ? 6 * kTri : 0);
 };
 
-// NP: dstate rounded up; NW: warps with 16 rows each.  KP: bf16 pieces of q and k.  MODE 0:
+// NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k
+// (1: bf16 inputs, scaled to fp16 here).  MODE 0:
 // forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass.
 template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
@@ -86,8 +97,8 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     using Tv2 = Tv2_;      // MODE 1: dy
     using Tout = Tout_;
     static constexpr int C = kDeltaC, NT = 32 * NW;
-    static constexpr int PV = sizeof(Tv) == 4 ? 3 : 1;                        // pieces of v (dy)
-    static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 3 : 2;         // pieces behind y
+    static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
+    static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 2 : 1;         // pieces behind y
     using Block = DeltaBlock<PO, MODE != 0>;
     static constexpr int BLOCK = MODE == 2 ? Block::BYTES : Block::OFF_N;     // the part that is read
     static constexpr int KROW = NP * 2 + 16;                                  // padded rows (bytes)
@@ -106,21 +117,14 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int SMEM_BYTES = OFF_ST + (MODE == 2 ? NW * 16 * STROW : 0);
 };
 
-// acc += A B over the piece products that matter: all of them when one side is a single
-// piece, else those whose pieces' ranks sum below the smaller count.  The leading product
-// goes to `big`, the others to `small` (two short chains instead of one long one).
-template <int PA, int PB>
-__device__ __forceinline__ void mma_pieces(float (&big)[4], float (&small)[4], const unsigned (&a)[PA][4],
-                                           const unsigned (&b)[PB][4], int tile) {
-    constexpr int LIM = (PA == 1 || PB == 1) ? (PA > PB ? PA : PB) : (PA < PB ? PA : PB);
+// acc += A B of operands in KP bf16 pieces (1: exact, 3: all bits of fp32), the products of
+// pieces below 2^-24 of the leading one left out.
+template <int KP>
+__device__ __forceinline__ void mma_exact(float (&acc)[4], const unsigned (&a)[KP][4], const unsigned (&b)[KP][4], int tile) {
 #pragma unroll
-    for (int i = 0; i < PA; ++i)
+    for (int i = KP - 1; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < PB; ++j)
-            if (i + j < LIM) {
-                if (i + j == 0) mma_bf16(big, a[i], b[j][2 * tile], b[j][2 * tile + 1]);
-                else mma_bf16(small, a[i], b[j][2 * tile], b[j][2 * tile + 1]);
-            }
+        for (int j = KP - 1 - i; j >= 0; --j) mma_bf16(acc, a[i], b[j][2 * tile], b[j][2 * tile + 1]);
 }
 
 // One warp per chunk and head forms the chunk's block; of fp32 q and k also their bf16 pieces
@@ -164,6 +168,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
     for (int i = 0; i < 6; ++i) { zero4(kk[i]); zero4(qk[i]); }
     const size_t krow = size_t(p.qk_heads) * p.N;
     const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
+    unsigned big[2] = {0, 0};                                   // largest |k|, |q| of the lane (bits; bf16: packed pairs)
 #pragma unroll (KP == 1 ? 2 : 1)
     for (int j = 0; j < NP / 32; ++j) {
         uint4 rows[2][4][KP];                                   // [k, q][row / 8][piece]
@@ -178,18 +183,19 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
                 uint4 (&w)[KP] = rows[m][r];
                 if constexpr (KP == 1) {
                     w[0] = ok ? __ldg(reinterpret_cast<const uint4 *>(src + off)) : make_uint4(0, 0, 0, 0);
+                    const unsigned x4[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) big[m] = __vmaxu2(big[m], x4[y] & 0x7fff7fffu);
                 } else {
                     float f[8] = {};
                     if (ok) load8<float>(src + off, f);
                     unsigned x[4][3];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) split_pair<3>(f[2 * y], f[2 * y + 1], x[y]);
+                    for (int y = 0; y < 4; ++y) split_bf16(f[2 * y], f[2 * y + 1], x[y]);
 #pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        w[i] = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
-                        if (ok && h == hk * group)
-                            *reinterpret_cast<uint4 *>((m ? p.qp : p.kp) + i * p.piece + off) = w[i];
-                    }
+                    for (int i = 0; i < 3; ++i) w[i] = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) big[m] = max(big[m], __float_as_uint(fabsf(f[y])));
                 }
             }
 #pragma unroll
@@ -221,11 +227,37 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         float (&ck)[4] = kk[2 * (m + n) + i], (&cq)[4] = qk[2 * (m + n) + i];
-                        mma_pieces<KP, KP>(ck, ck, ka, kb[n], i);
-                        mma_pieces<KP, KP>(cq, cq, qa, kb[n], i);
+                        mma_exact<KP>(ck, ka, kb[n], i);
+                        mma_exact<KP>(cq, qa, kb[n], i);
                     }
             }
         }
+    }
+    Pow2 cs[2];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        if constexpr (KP == 1) big[m] = max(big[m] << 16, big[m] & 0xffff0000u);
+        cs[m] = pow2_for(__reduce_max_sync(0xffffffffu, big[m]));
+    }
+    if constexpr (KP != 1) {        // the scaled fp16 pieces of fp32 rows, read again (from L1)
+        if (h == hk * group)
+            for (int x = lane; x < C * (NP / 8); x += 32) {
+                const int t = x / (NP / 8), n = (x % (NP / 8)) * 8;
+                if (t0 + t >= p.seqlen || n >= p.N) continue;
+                const size_t off = k0 + size_t(t) * krow + n;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float f[8];
+                    load8<float>(static_cast<const float *>(m ? p.q : p.k) + off, f);
+                    unsigned w[4][2];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) split_f16<2>(f2(f[2 * y], f[2 * y + 1]), cs[m].c, w[y]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        *reinterpret_cast<uint4 *>((m ? p.qp : p.kp) + i * p.piece + off) =
+                            make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+                }
+            }
     }
     // r(t, s): lane s + 1 adds up a from token s + 1 on (no differences of long sums, so
     // a = -inf, a full reset, is exact); lane 0 is the chunk's start
@@ -238,16 +270,25 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
     }
     rat[lane * RATROW + C] = lane == C - 1 ? 1.f : 0.f;
     __syncwarp();
+    float *vec = reinterpret_cast<float *>(sc.block + Block::OFF_VEC), *one = vec + kVecScalars * C;
+    auto max_of = [&](float x) { return __uint_as_float(warp_max_bits(fabsf(x))); };
     {
-        float *vec = reinterpret_cast<float *>(sc.block + Block::OFF_VEC);
         const float gam = rat[lane * RATROW], end = rat[(C - 1) * RATROW + lane + 1];
-        vec[lane] = gam;
-        vec[C + lane] = p.scale * gam;
-        vec[2 * C + lane] = beta;
-        vec[3 * C + lane] = end;
-        vec[4 * C + lane] = end * beta;
-        vec[5 * C + lane] = lane == 0 ? rat[(C - 1) * RATROW] : 0.f;
+        const float gk = gam * cs[0].inv, sgq = p.scale * gam * cs[1].inv, ebk = end * beta * cs[0].inv;
+        vec[kVecGk * C + lane] = gk;
+        vec[kVecSgq * C + lane] = sgq;
+        vec[kVecBeta * C + lane] = beta;
+        vec[kVecEk * C + lane] = end * cs[0].inv;
+        vec[kVecEbk * C + lane] = ebk;
+        const float mb = max_of(beta), me = max_of(ebk), mg = max_of(gk), ms = max_of(sgq);
+        if (lane == 0) {
+            one[kGamLast] = rat[(C - 1) * RATROW];
+            one[kCk] = cs[0].c; one[kCq] = cs[1].c;
+            one[kMaxBeta] = mb; one[kMaxEbk] = me; one[kMaxGk] = mg; one[kMaxSgq] = ms;
+        }
     }
+    // n, Pm and n / beta: the products times their decays, in place of kk (n / beta) and qk
+    float mp = 0.f, mn = 0.f;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -259,26 +300,41 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int t = 16 * m + 8 * r + g;
-                    const float *ck = kk[2 * (m + n) + i], *cq = qk[2 * (m + n) + i];
+                    float *ck = kk[2 * (m + n) + i] + 2 * r, *cq = qk[2 * (m + n) + i] + 2 * r;
                     const float r0 = rat[t * RATROW + s0 + 1], r1 = rat[t * RATROW + s0 + 2];
-                    const float x0 = s0 < t ? ck[2 * r] * r0 : 0.f, x1 = s0 + 1 < t ? ck[2 * r + 1] * r1 : 0.f;
-                    nt[s0 * NROW + t] = s0 < t ? x0 * b0 : 0.f;
-                    nt[(s0 + 1) * NROW + t] = s0 + 1 < t ? x1 * b1 : 0.f;
-                    unsigned char *at = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
-                    if constexpr (Block::BWD) {
-                        unsigned x[3];
-                        split_pair<3>(x0, x1, x);
-#pragma unroll
-                        for (int y = 0; y < 3; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_N + 3 * y * kTri) = x[y];
-                    }
-                    const float q0 = s0 <= t ? cq[2 * r] * r0 * p.scale : 0.f;
-                    const float q1 = s0 + 1 <= t ? cq[2 * r + 1] * r1 * p.scale : 0.f;
-                    unsigned w[Block::PP];
-                    split_pair<Block::PP>(q0, q1, w);
-#pragma unroll
-                    for (int y = 0; y < Block::PP; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_P + 3 * y * kTri) = w[y];
+                    ck[0] = s0 < t ? ck[0] * r0 : 0.f;
+                    ck[1] = s0 + 1 < t ? ck[1] * r1 : 0.f;
+                    nt[s0 * NROW + t] = s0 < t ? ck[0] * b0 : 0.f;
+                    nt[(s0 + 1) * NROW + t] = s0 + 1 < t ? ck[1] * b1 : 0.f;
+                    cq[0] = s0 <= t ? cq[0] * r0 * p.scale : 0.f;
+                    cq[1] = s0 + 1 <= t ? cq[1] * r1 * p.scale : 0.f;
+                    mp = fmaxf(mp, fmaxf(fabsf(cq[0]), fabsf(cq[1])));
+                    mn = fmaxf(mn, fmaxf(fabsf(ck[0]), fabsf(ck[1])));
                 }
             }
+    const Pow2 sp = pow2_for(warp_max_bits(mp)), sn = pow2_for(warp_max_bits(mn));
+    if (lane == 0) { one[kInvP] = sp.inv; one[kInvN] = sn.inv; }
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int n = 0; n <= m; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float *ck = kk[2 * (m + n) + i] + 2 * r, *cq = qk[2 * (m + n) + i] + 2 * r;
+                    unsigned char *at = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
+                    unsigned w[Block::PP];
+                    split_f16<Block::PP>(f2(cq[0], cq[1]), sp.c, w);
+#pragma unroll
+                    for (int y = 0; y < Block::PP; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_P + 3 * y * kTri) = w[y];
+                    if constexpr (Block::BWD) {
+                        unsigned x[2];
+                        split_f16<2>(f2(ck[0], ck[1]), sn.c, x);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_N + 3 * y * kTri) = x[y];
+                    }
+                }
     __syncwarp();
     // T of the two diagonal tiles: lane t solves row t of T (I + n) = I from the diagonal
     // leftwards within its tile
@@ -303,24 +359,12 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
             T[s] = s == tl ? 1.f : (s < tl ? x0 + x1 : 0.f);
         }
     }
-    // 8 or 16 values of a row of a triangle's tile, in three pieces
-    auto put = [&](int tile, int row, int half, const float *f) {
-        unsigned x[4][3];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) split_pair<3>(f[2 * y], f[2 * y + 1], x[y]);
-#pragma unroll
-        for (int y = 0; y < 3; ++y)
-            *reinterpret_cast<uint4 *>(sc.block + (3 * y + tile) * kTri + tri_at(row, half)) =
-                make_uint4(x[0][y], x[1][y], x[2][y], x[3][y]);
-    };
     float *Td = rat, *Z = rat + 2 * 16 * 20;                    // T11 and T22, then Z, rows of 20
 #pragma unroll
     for (int x = 0; x < 4; ++x)
         *reinterpret_cast<float4 *>(Td + (blk * 16 + tl) * 20 + 4 * x) = make_float4(T[4 * x], T[4 * x + 1], T[4 * x + 2], T[4 * x + 3]);
 #pragma unroll
     for (int s = 0; s < 16; ++s) T[s] = s == tl ? 0.f : T[s];
-    put(2 * blk, tl, 0, T);
-    put(2 * blk, tl, 1, T + 8);
     __syncwarp();
     // T21 = -T22 (n21 T11): a lane forms 8 values of row tl, columns 8 blk on
     float z[8] = {};
@@ -343,6 +387,22 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) z[x] = fmaf(t, zr[x], z[x]);
     }
+    float mt = 0.f;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) mt = fmaxf(mt, fmaxf(fabsf(T[x]), fabsf(z[x & 7])));
+    const Pow2 st = pow2_for(warp_max_bits(mt));
+    if (lane == 0) one[kInvT] = st.inv;
+    auto put = [&](int tile, int row, int half, const float *f) {     // 8 values of a row of T's tile
+        unsigned x[4][2];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) split_f16<2>(f2(f[2 * y], f[2 * y + 1]), st.c, x[y]);
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            *reinterpret_cast<uint4 *>(sc.block + (3 * y + tile) * kTri + tri_at(row, half)) =
+                make_uint4(x[0][y], x[1][y], x[2][y], x[3][y]);
+    };
+    put(2 * blk, tl, 0, T);
+    put(2 * blk, tl, 1, T + 8);
     put(1, tl, blk, z);
     // the block to global memory, one bulk copy
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -429,16 +489,23 @@ __device__ __forceinline__ void store_tok(T *out, size_t stride, int ntok, int n
     }
 }
 
-// A Tok as the pieces of two A operands (tokens 0-15 and 16-31 as the inner index).
-template <int NP> __device__ __forceinline__ void split_tok(const Tok &x, unsigned (&a)[2][NP][4]) {
-    split_tiles<NP>(x[0], x[1], a[0]);
-    split_tiles<NP>(x[2], x[3], a[1]);
+// A Tok times c as the pieces of two A operands (tokens 0-15 and 16-31 as the inner index).
+template <int NP> __device__ __forceinline__ void split_tok(const Tok &x, float c, unsigned (&a)[2][NP][4]) {
+    split_tiles<NP>(x[0], x[1], c, a[0]);
+    split_tiles<NP>(x[2], x[3], c, a[1]);
 }
 
-// d + ds += x M^T (d[., t] = sum_s x[., s] M(t, s)), or with REV x M, for a lower triangle M at
+__device__ __forceinline__ unsigned max_tok(const Tok &x) {        // over the warp, as bits
+    float m = 0.f;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) m = fmaxf(fmaxf(m, fmaxf(fabsf(x[n][0]), fabsf(x[n][1]))), fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+    return warp_max_bits(m);
+}
+
+// d += x M^T (d[., t] = sum_s x[., s] M(t, s)), or with REV x M, for a lower triangle M at
 // `at` in PB pieces; x in PA pieces.
 template <int PA, int PB, bool REV>
-__device__ __forceinline__ void mma_triangle(Tok &d, Tok &ds, const unsigned (&x)[2][PA][4], unsigned at) {
+__device__ __forceinline__ void mma_triangle(Tok &d, const unsigned (&x)[2][PA][4], unsigned at) {
 #pragma unroll
     for (int bt = 0; bt < 2; ++bt)
 #pragma unroll
@@ -452,7 +519,7 @@ __device__ __forceinline__ void mma_triangle(Tok &d, Tok &ds, const unsigned (&x
             }
             const int out = REV ? bs : bt, in = REV ? bt : bs;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) mma_pieces<PA, PB>(d[2 * out + n], ds[2 * out + n], x[in], m, n);
+            for (int n = 0; n < 2; ++n) mma_pieces<PA, PB>(d[2 * out + n], x[in], m, n);
         }
 }
 
@@ -506,6 +573,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             }
         }
     };
+    float ck = 1.f, cq = 1.f;                              // scales of the chunk that is on its way
     auto issue = [&](int i) {
         if (i < nchunk) {
             const int c = chunk_of(i), t0 = c * C;
@@ -515,14 +583,19 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 #pragma unroll
             for (int m = 0; m < KP; ++m) {
                 copy_rows(base + Cfg::OFF_K + m * Cfg::PIECE, Cfg::KROW,
-                          static_cast<const __nv_bfloat16 *>(p.k) + m * p.piece + koff, krow, kw, p.N, t0);
+                          static_cast<const __half *>(p.k) + m * p.piece + koff, krow, kw, p.N, t0);
                 copy_rows(base + Cfg::OFF_Q + m * Cfg::PIECE, Cfg::KROW,
-                          static_cast<const __nv_bfloat16 *>(p.q) + m * p.piece + koff, krow, kw, p.N, t0);
+                          static_cast<const __half *>(p.q) + m * p.piece + koff, krow, kw, p.N, t0);
             }
             copy_rows(base + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + voff, vrow, vw, prow, t0);
             if constexpr (MODE == 1)
                 copy_rows(base + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + voff, vrow, vw, prow, t0);
             const unsigned char *blk = p.prep + (size_t(bh) * nchunk + c) * Block::BYTES;
+            if constexpr (KP == 1) {
+                const float *one = reinterpret_cast<const float *>(blk + Block::OFF_VEC) + kVecScalars * C;
+                ck = __ldg(one + kCk);
+                cq = __ldg(one + kCq);
+            }
 #pragma unroll
             for (int k = 0; k < (Cfg::BLOCK / 16 + Cfg::NT - 1) / Cfg::NT; ++k) {
                 const int x = tid + Cfg::NT * k;
@@ -530,6 +603,32 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             }
         }
         cp_async_commit();
+    };
+    // Step i's rows are here (this thread's copies of them): bf16 k and q become scaled fp16 in
+    // place, each thread doing what it copied; the next barrier shows them to the others.
+    auto arrive = [&](int i) {
+        cp_async_wait<0>();
+        if constexpr (KP == 1) {
+            if (i >= nchunk) return;
+            constexpr int CR = NP / 8;
+#pragma unroll
+            for (int y = 0; y < (C * CR + Cfg::NT - 1) / Cfg::NT; ++y) {
+                const int x = tid + Cfg::NT * y, r = x / CR, n = (x % CR) * 8;
+                if (C * CR % Cfg::NT == 0 || x < C * CR)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        uint4 *at = reinterpret_cast<uint4 *>(smem + (i & 1) * Cfg::STAGE + (m ? Cfg::OFF_Q : Cfg::OFF_K) +
+                                                              r * Cfg::KROW + n * 2);
+                        const uint4 w = *at;
+                        const float c = m ? cq : ck;
+                        auto cvt = [&](unsigned u) {
+                            const float2 f = fmul2(bf16x2_to_f2(u), f2(c, c));
+                            return pack_f16x2(f.x, f.y);
+                        };
+                        *at = make_uint4(cvt(w.x), cvt(w.y), cvt(w.z), cvt(w.w));
+                    }
+            }
+        }
     };
     // The sums over the warps' rows of loop step i, left in shared memory at its end.
     auto flush_sums = [&](int i) {
@@ -624,7 +723,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             for (int x = lane; x < nbound; x += 32)
                 p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = 0.f;
         for (int i = 0; i < nchunk; ++i) {
-            cp_async_wait<0>();
+            arrive(i);
             __syncthreads();
             issue(i + 1);
         }
@@ -638,7 +737,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 
     for (int i = 0; i < nchunk; ++i) {
         const int c = chunk_of(i);
-        cp_async_wait<0>();
+        arrive(i);
         __syncthreads();
         constexpr int CS = kDeltaSave / C;
         const unsigned char *stage = smem + (i & 1) * Cfg::STAGE;
@@ -667,9 +766,14 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
         issue(i + 1);
         if constexpr (MODE != 0) if (i > 0 && warp == 0) flush_sums(i - 1);
 
+        const float *one = vec + kVecScalars * C;
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
-        Tok sk, sks, sq;
-        zero_tok(sk); zero_tok(sks); zero_tok(sq);
+        float ms = 0.f;
+#pragma unroll
+        for (int j = 0; j < NP / 8; ++j) ms = fmaxf(fmaxf(ms, fmaxf(fabsf(s[j][0]), fabsf(s[j][1]))), fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
+        const Pow2 cS = pow2_for(warp_max_bits(ms));
+        Tok sk, sq;
+        zero_tok(sk); zero_tok(sq);
         unsigned kb[2][KP][4], qb[2][KP][4];
         auto load_kq = [&](int j) {
 #pragma unroll
@@ -683,127 +787,130 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
         load_kq(0);
 #pragma unroll
         for (int j = 0; j < NP / 16; ++j) {
-            unsigned A[3][4];
-            split_tiles<3>(s[2 * j], s[2 * j + 1], A);
+            unsigned A[2][4];
+            split_tiles<2>(s[2 * j], s[2 * j + 1], cS.c, A);
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    mma_pieces<3, KP>(sk[2 * h2 + n], sks[2 * h2 + n], A, kb[h2], n);
+                    mma_pieces<2, KP>(sk[2 * h2 + n], A, kb[h2], n);
                     if constexpr (MODE != 2) {
                         unsigned Ao[PO][4];
 #pragma unroll
                         for (int m = 0; m < PO; ++m)
 #pragma unroll
                             for (int r = 0; r < 4; ++r) Ao[m][r] = A[m][r];
-                        mma_pieces<PO, KP>(sq[2 * h2 + n], sq[2 * h2 + n], Ao, qb[h2], n);
+                        mma_pieces<PO, KP>(sq[2 * h2 + n], Ao, qb[h2], n);
                     }
                 }
             if (j + 1 < NP / 16) load_kq(j + 1);
         }
         Tok v, x, du;
         load_tok<Tv>(stage + Cfg::OFF_V + warp * 16 * int(sizeof(Tv)), Cfg::VROW, lane, v);
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int m = 0; m < 4; ++m) sk[n][m] += sks[n][m];
+        unsigned mv = 0;                                   // reverse pass: largest |dO|
         if constexpr (!REV) {
             // R = v - gam S k
-            scale_tok(sk, sk, vec, t4);
+            scale_tok(sk, sk, vec + kVecGk * C, t4);
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) x[n][m] = v[n][m] - sk[n][m];
+                for (int m = 0; m < 4; ++m) x[n][m] = fmaf(-cS.inv, sk[n][m], v[n][m]);
         } else {
             // rhs = end (dS k) + Pm^T dO, times beta
-            Tok lo, los;
+            Tok lo;
             unsigned A[2][PV][4];
-            zero_tok(lo); zero_tok(los);
-            split_tok<PV>(v, A);
-            mma_triangle<PV, 3, true>(lo, los, A, tbase + Block::OFF_P);
-            scale_tok(sk, sk, vec + 3 * C, t4);
+            mv = max_tok(v);
+            const Pow2 cv = pow2_for(mv);
+            split_tok<PV>(v, cv.c, A);
+            zero_tok(lo);
+            mma_triangle<PV, 2, true>(lo, A, tbase + Block::OFF_P);
+            scale_tok(sk, sk, vec + kVecEk * C, t4);
+            const float f = one[kInvP] * cv.inv;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] = sk[n][m] + (lo[n][m] + los[n][m]);
-            scale_tok(x, du, vec + 2 * C, t4);
+                for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv, sk[n][m], f * lo[n][m]);
+            scale_tok(x, du, vec + kVecBeta * C, t4);
         }
         {   // e = R + (T - I) R, or w with the transpose
-            unsigned A[2][3][4];
-            Tok d, ds;
-            zero_tok(d); zero_tok(ds);
-            split_tok<3>(x, A);
-            mma_triangle<3, 3, REV>(d, ds, A, tbase);
+            unsigned A[2][2][4];
+            Tok d;
+            const Pow2 cx = pow2_for(max_tok(x));
+            split_tok<2>(x, cx.c, A);
+            zero_tok(d);
+            mma_triangle<2, 2, REV>(d, A, tbase);
+            const float f = one[kInvT] * cx.inv;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) x[n][m] += d[n][m] + ds[n][m];
+                for (int m = 0; m < 4; ++m) x[n][m] = fmaf(f, d[n][m], x[n][m]);
         }
+        // The scales of x times a vector over the tokens follow from their largest magnitudes.
+        const unsigned mx = max_tok(x);
+        auto scale_by = [&](unsigned m, float most) {
+            const float b = __uint_as_float(m) * most;
+            return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
+        };
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
-        const float glast = vec[5 * C];
+        const float glast = one[kGamLast];
         {
-            unsigned A1[2][3][4], A2[2][REV ? 3 : 1][4];
+            unsigned A1[2][2][4], A2[2][REV ? 2 : 1][4];
             Tok w;
+            const Pow2 c1 = scale_by(mx, one[REV ? kMaxGk : kMaxEbk]), c2 = REV ? scale_by(mv, one[kMaxSgq]) : Pow2{0.f, 0.f};
+            scale_tok(w, x, vec + (REV ? kVecGk : kVecEbk) * C, t4);
+            split_tok<2>(w, c1.c, A1);
             if constexpr (REV) {
-                scale_tok(w, x, vec, t4);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) w[n][m] = -w[n][m];
-                split_tok<3>(w, A1);
-                scale_tok(w, v, vec + C, t4);
-                split_tok<3>(w, A2);
-            } else {
-                scale_tok(w, x, vec + 4 * C, t4);
-                split_tok<3>(w, A1);
+                scale_tok(w, v, vec + kVecSgq * C, t4);
+                split_tok<2>(w, c2.c, A2);
             }
             auto load_t = [&](unsigned (&f)[KP][4], unsigned base, int h2, int j) {
 #pragma unroll
                 for (int m = 0; m < KP; ++m) ldsm4_t(f[m], base + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bk + j * 32);
             };
+            const float2 f1 = REV ? f2(-c1.inv, -c1.inv) : f2(c1.inv, c1.inv), gl = f2(glast, glast), f2v = f2(c2.inv, c2.inv);
 #pragma unroll
             for (int j = 0; j < NP / 16; ++j) {
-                float d[2][4];
-                zero4(d[0]); zero4(d[1]);
+                float d[2][4], d2[2][4];
+                zero4(d[0]); zero4(d[1]); zero4(d2[0]); zero4(d2[1]);
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                     unsigned f[KP][4];
                     load_t(f, kbase, h2, j);
 #pragma unroll
-                    for (int m = 2; m >= 0; --m)           // the small pieces first: one sum per tile
-#pragma unroll
-                        for (int q = (KP == 1 ? 0 : 2 - m); q >= 0; --q)
-#pragma unroll
-                            for (int n = 0; n < 2; ++n) mma_bf16(d[n], A1[h2][m], f[q][2 * n], f[q][2 * n + 1]);
+                    for (int n = 0; n < 2; ++n) mma_pieces<2, KP>(d[n], A1[h2], f, n);
                     if constexpr (REV) {
                         load_t(f, qbase, h2, j);
 #pragma unroll
-                        for (int m = 2; m >= 0; --m)
-#pragma unroll
-                            for (int q = (KP == 1 ? 0 : 2 - m); q >= 0; --q)
-#pragma unroll
-                                for (int n = 0; n < 2; ++n) mma_bf16(d[n], A2[h2][m], f[q][2 * n], f[q][2 * n + 1]);
+                        for (int n = 0; n < 2; ++n) mma_pieces<2, KP>(d2[n], A2[h2], f, n);
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) s[2 * j + n][m] = fmaf(glast, s[2 * j + n][m], d[n][m]);
+                    for (int m = 0; m < 4; m += 2) {
+                        float *at = s[2 * j + n] + m;
+                        float2 u = fmul2(gl, f2(at[0], at[1]));
+                        if constexpr (REV) u = ffma2(f2v, f2(d2[n][m], d2[n][m + 1]), u);
+                        u = ffma2(f1, f2(d[n][m], d[n][m + 1]), u);
+                        at[0] = u.x; at[1] = u.y;
+                    }
             }
         }
         if constexpr (!REV) {
             // y = scale gam S q + Pm (beta e)
             unsigned A[2][PO][4];
-            Tok o, os;
-            scale_tok(o, x, vec + 2 * C, t4);
-            split_tok<PO>(o, A);
-            scale_tok(o, sq, vec + C, t4);
-            zero_tok(os);
-            mma_triangle<PO, PO, false>(o, os, A, tbase + Block::OFF_P);
+            Tok o;
+            const Pow2 cu = scale_by(mx, one[kMaxBeta]);
+            scale_tok(o, x, vec + kVecBeta * C, t4);
+            split_tok<PO>(o, cu.c, A);
+            zero_tok(o);
+            mma_triangle<PO, PO, false>(o, A, tbase + Block::OFF_P);
+            scale_tok(sq, sq, vec + kVecSgq * C, t4);
+            const float f = one[kInvP] * cu.inv;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) o[n][m] += os[n][m];
+                for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f, o[n][m], cS.inv * sq[n][m]);
             if constexpr (MODE == 0) {
                 store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, o);
             } else {
@@ -818,15 +925,17 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             }
         } else {
             // du = rhs - (n / beta)^T w, the gradient of beta e: with e it gives beta's
-            unsigned A[2][3][4];
-            Tok d, ds;
-            zero_tok(d); zero_tok(ds);
-            split_tok<3>(x, A);
-            mma_triangle<3, 3, true>(d, ds, A, tbase + Block::OFF_N);
+            unsigned A[2][2][4];
+            Tok d;
+            const Pow2 cx = pow2_for(mx);
+            split_tok<2>(x, cx.c, A);
+            zero_tok(d);
+            mma_triangle<2, 2, true>(d, A, tbase + Block::OFF_N);
+            const float f = -one[kInvN] * cx.inv;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] = er[n][m] * (du[n][m] - (d[n][m] + ds[n][m]));
+                for (int m = 0; m < 4; ++m) du[n][m] = er[n][m] * fmaf(f, d[n][m], du[n][m]);
             token_sums(du, i & 1);
             if (p.w != nullptr) store_tok<float>(p.w + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
