@@ -25,6 +25,10 @@ inline bool overlaps(const void *p, size_t pb, const void *q, size_t qb) {
     return a < b + qb && b < a + pb;
 }
 
+// Where kernels count the waits that they gave up on (ssm_device_timeouts reads it); NULL if it
+// cannot be had on this device.
+unsigned *wait_counter();
+
 inline size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 // A call's scratch: the caller's workspace if one is given, else a stream-ordered buffer

@@ -20,10 +20,10 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
     return status_of(cudaGetLastError());
 }
 
-// Forward: the chunk blocks, then the chains.
+// Forward: the chunk blocks and operands, then the chains.
 template <typename Tin, typename Tout> size_t fwd_bytes(int batch, int seqlen, int heads, int qk_heads, int N) {
     return prep_bytes<ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1, false>>(batch, seqlen, heads) +
-           pieces_bytes(batch, seqlen, qk_heads, N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
+           rows_bytes(batch, seqlen, qk_heads, N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
 }
 
 template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *workspace, size_t bytes, cudaStream_t s) {
@@ -31,7 +31,10 @@ template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *works
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, fwd_bytes<Tin, Tout>(a.batch, a.seqlen, a.heads, a.qk_heads, a.N), s))
         return st;
-    int st = dispatch_prep<Tin, Block>(a, ws.p, ws.p + prep_bytes<Block>(a.batch, a.seqlen, a.heads), s);
+    a.prep = ws.p;
+    a.rows = ws.p + prep_bytes<Block>(a.batch, a.seqlen, a.heads);
+    a.timeouts = wait_counter();
+    int st = a.timeouts ? dispatch_prep<Tin, Block>(a, s) : int(SSM_ERR_CUDA);
     if (st == SSM_OK) st = dispatch_chain<sizeof(Tin) == 4 ? 2 : 1, Tin, Tin, Tout, 0>(a, s);
     return ws.release(st);
 }

@@ -24,7 +24,7 @@ using Block = ssm::DeltaBlock<2, true>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, pieces, e, w, ck, dck, dyy, edu, zsum, all;
+    size_t prep, rows, e, w, ck, dck, dyy, edu, zsum, all;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
@@ -32,7 +32,7 @@ struct BwdParts {
         size_t at = 0;
         auto part = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         part(prep, prep_bytes<Block>(batch, seqlen, heads));
-        part(pieces, pieces_bytes(batch, seqlen, qk_heads, N, in_dtype));
+        part(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
         part(e, tok * P * 4);
         part(w, grad_dtype == SSM_F32 ? 0 : tok * P * 4);       // fp32 gradients: w is dv itself
         part(ck, state);
@@ -53,10 +53,12 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, at.all, s)) return st;
     auto part = [&](size_t off) { return reinterpret_cast<float *>(ws.p + off); };
-    const void *q = f.q, *k = f.k;
     float *w = sizeof(Tg) == 4 ? static_cast<float *>(dv) : part(at.w);
     constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
-    int st = dispatch_prep<Tin, Block>(f, ws.p + at.prep, ws.p + at.pieces, s);
+    f.prep = ws.p + at.prep;
+    f.rows = ws.p + at.rows;
+    f.timeouts = wait_counter();
+    int st = f.timeouts ? dispatch_prep<Tin, Block>(f, s) : int(SSM_ERR_CUDA);
     f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
@@ -67,7 +69,7 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     }
     if (st == SSM_OK) {
         const int slices = delta_slices(f.P);
-        const ssm::DeltaGradArgs g{q, k, v, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
+        const ssm::DeltaGradArgs g{f.q, f.k, v, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
                                    part(at.edu), part(at.zsum), dq, dk, da, dbeta, f.batch, f.seqlen,
                                    f.heads, f.qk_heads, f.P, f.N, slices, slices * kDeltaWarps, f.scale};
         st = f.N <= 64 ? launch_grad<64, Tin, Tg>(g, s) : launch_grad<128, Tin, Tg>(g, s);

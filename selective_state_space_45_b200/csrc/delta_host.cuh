@@ -18,13 +18,17 @@ inline int delta_sizes(int batch, int tokens, int heads, int qk_heads, int headd
 
 inline size_t delta_chunks(int seqlen) { return (size_t(seqlen) + ssm::kDeltaC - 1) / ssm::kDeltaC; }
 
-// Bytes of the prep kernel's blocks, and of the pieces of fp32 q and k (two of 2 bytes each).
+// Bytes of the prep kernel's blocks.
 template <class Block> size_t prep_bytes(int batch, int seqlen, int heads) {
     return size_t(batch) * heads * delta_chunks(seqlen) * Block::BYTES;
 }
-inline size_t piece_values(int batch, int seqlen, int qk_heads, int N) { return size_t(batch) * seqlen * qk_heads * N; }
-inline size_t pieces_bytes(int batch, int seqlen, int qk_heads, int N, int in_dtype) {
-    return in_dtype == SSM_F32 ? round16(2 * 2 * piece_values(batch, seqlen, qk_heads, N) * 2) : 0;
+// dstate padded to the next multiple of 32 (zero columns): the products' inner length.
+inline int padded_state(int N) { return (N + 31) / 32 * 32; }
+
+// Bytes of k and q as operands: 32 rows per chunk, two pieces of fp32 ones.
+inline size_t rows_bytes(int batch, int seqlen, int qk_heads, int N, int in_dtype) {
+    return size_t(batch) * qk_heads * delta_chunks(seqlen) *
+           (2 * (in_dtype == SSM_F32 ? 2 : 1) * ssm::kDeltaC * (padded_state(N) * 2 + 16));
 }
 
 // Dynamic shared memory of a kernel, with the SM's memory split for as many CTAs as fit (the
@@ -37,30 +41,22 @@ template <typename K> int set_smem(K kernel, int bytes) {
                : SSM_ERR_CUDA;
 }
 
-// The chunk blocks into `prep` (and the pieces of fp32 q, k behind `pieces`); on return a's
-// q and k are what the chains read.
+// The chunk blocks into a.prep, k and q as operands into a.rows.
 template <int NP, typename Tin, class Block> int launch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
     const long long blocks = ((long long)a.batch * a.heads * (long long)delta_chunks(a.seqlen) + 3) / 4;
     if (blocks > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    constexpr int smem = 4 * int(sizeof(ssm::PrepScratch<Block>));
+    constexpr int smem = 4 * int(sizeof(ssm::PrepScratch<NP, Tin, Block>));
     if (const int st = set_smem(ssm::delta_prep_kernel<NP, Tin, Block>, smem)) return st;
     ssm::delta_prep_kernel<NP, Tin, Block><<<unsigned(blocks), 128, smem, s>>>(a);
     return status_of(cudaGetLastError());
 }
-template <typename Tin, class Block>
-int dispatch_prep(ssm::DeltaArgs &a, unsigned char *prep, unsigned char *pieces, cudaStream_t s) {
-    a.prep = prep;
-    if (sizeof(Tin) == 4) {
-        a.piece = piece_values(a.batch, a.seqlen, a.qk_heads, a.N);
-        a.kp = reinterpret_cast<__half *>(pieces);
-        a.qp = a.kp + 2 * a.piece;
+template <typename Tin, class Block> int dispatch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
+    switch (padded_state(a.N)) {
+    case 32: return launch_prep<32, Tin, Block>(a, s);
+    case 64: return launch_prep<64, Tin, Block>(a, s);
+    case 96: return launch_prep<96, Tin, Block>(a, s);
+    default: return launch_prep<128, Tin, Block>(a, s);
     }
-    const int st = a.N <= 32   ? launch_prep<32, Tin, Block>(a, s)
-                   : a.N <= 64 ? launch_prep<64, Tin, Block>(a, s)
-                   : a.N <= 96 ? launch_prep<96, Tin, Block>(a, s)
-                               : launch_prep<128, Tin, Block>(a, s);
-    if (sizeof(Tin) == 4) { a.q = a.qp; a.k = a.kp; }
-    return st;
 }
 
 // The chain kernel for one set of types: a warp per 16 rows of the state, four per CTA.
@@ -78,13 +74,14 @@ int launch_chain(ssm::DeltaArgs a, cudaStream_t s) {
     return status_of(cudaGetLastError());
 }
 
-// dstate padded to the next multiple of 32 (zero columns): the products' inner length.
 template <int KP, typename Tv, typename Tv2, typename Tout, int MODE>
 int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s) {
-    if (a.N <= 32) return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, s);
-    if (a.N <= 64) return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, s);
-    if (a.N <= 96) return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, s);
-    return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, s);
+    switch (padded_state(a.N)) {
+    case 32: return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, s);
+    case 64: return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, s);
+    case 96: return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, s);
+    default: return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, s);
+    }
 }
 
 }  // namespace ssm_host

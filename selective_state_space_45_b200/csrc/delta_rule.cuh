@@ -14,7 +14,9 @@
 // the state enters each product as a register operand and no step of the chain goes through
 // shared memory or waits for another warp.  What depends on k, q, a and beta alone (T, Pm and
 // the decays) is formed for all chunks in parallel by delta_prep_kernel, one warp per chunk,
-// and read back by the chains with the chunk's rows (cp.async, one chunk ahead).
+// which also lays the chunk's k and q out as the chains' operands; the chains read both back
+// with two bulk copies a chunk (cp.async.bulk, one chunk ahead).  Copying and converting the
+// rows in the chains instead cost 1100 of 3700 cycles a chunk.
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
 //     w = T^T (beta (end (dS k) + Pm^T dO)) = dv,  dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
@@ -31,15 +33,15 @@
 #include <type_traits>
 
 #include "mma_common.cuh"
+#include "tc_common.cuh"
 
 namespace ssm {
 
 struct DeltaArgs {
-    const void *q, *k;      // [batch][seqlen][qk_heads][dstate]; the chains: bf16, or the scaled
-                            // fp16 pieces that the prep kernel made of fp32 ones, `piece` values apart
-    size_t piece;
+    const void *q, *k;      // prep kernel: [batch][seqlen][qk_heads][dstate]
     unsigned char *prep;    // [batch][heads][chunks] blocks of the prep kernel
-    __half *qp, *kp;        // prep kernel: where the pieces of fp32 q, k go
+    unsigned char *rows;    // [batch][qk_heads][chunks] k and q as operands, from the prep kernel
+    unsigned *timeouts;     // counts waits that gave up
     const void *v;          // [batch][seqlen][heads][headdim]; the reverse pass: dy
     const void *v2;         // forward of the backward pass: dy
     const float *a, *beta;  // [batch][seqlen][heads]
@@ -88,8 +90,15 @@ template <int PP_, bool BWD_> struct DeltaBlock {
     static constexpr int BYTES = OFF_N + (BWD ? 6 * kTri : 0);
 };
 
-// NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k
-// (1: bf16 inputs, scaled to fp16 here).  MODE 0:
+// k and q of a chunk as the chains read them: scaled fp16, KP pieces of k, then of q, each 32
+// rows of NP values (zeros past dstate and seqlen) padded by 16 bytes against bank conflicts.
+template <int NP, int KP> struct DeltaRows {
+    static constexpr int ROW = NP * 2 + 16, PIECE = kDeltaC * ROW, BYTES = 2 * KP * PIECE;
+};
+
+constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's limit, about a second
+
+// NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k.  MODE 0:
 // forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass.
 template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
@@ -101,15 +110,16 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 2 : 1;         // pieces behind y
     using Block = DeltaBlock<PO, MODE != 0>;
     static constexpr int BLOCK = MODE == 2 ? Block::BYTES : Block::OFF_N;     // the part that is read
-    static constexpr int KROW = NP * 2 + 16;                                  // padded rows (bytes)
+    using Rows = DeltaRows<NP, KP>;
+    static constexpr int KROW = Rows::ROW;
     static constexpr int VROW = NW * 16 * int(sizeof(Tv)) + 16;
     static constexpr int V2ROW = NW * 16 * int(sizeof(Tv2)) + 16;
-    static constexpr int PIECE = C * KROW;
-    static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_V = 2 * KP * PIECE;
-    static constexpr int OFF_V2 = OFF_V + C * VROW;
-    static constexpr int OFF_TRI = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);
-    static constexpr int STAGE = OFF_TRI + BLOCK;                             // two stages
-    static constexpr int OFF_OUT = 2 * STAGE;                                 // per-warp output tiles
+    static constexpr int PIECE = Rows::PIECE;
+    static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
+    static constexpr int OFF_V = OFF_TRI + BLOCK, OFF_V2 = OFF_V + C * VROW;
+    static constexpr int STAGE = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);        // two stages
+    static constexpr int OFF_BAR = 2 * STAGE;                                 // their mbarriers
+    static constexpr int OFF_OUT = OFF_BAR + 16;                              // per-warp output tiles
     static constexpr int OFF_RED = OFF_OUT + NW * 16 * kOutRow;               // 2 buffers of token sums
     static constexpr int REDBUF = MODE != 0 ? NW * C * 4 : 0;
     static constexpr int OFF_ST = OFF_RED + 2 * REDBUF;                       // reverse pass: kept states
@@ -127,19 +137,26 @@ __device__ __forceinline__ void mma_exact(float (&acc)[4], const unsigned (&a)[K
         for (int j = KP - 1 - i; j >= 0; --j) mma_bf16(acc, a[i], b[j][2 * tile], b[j][2 * tile + 1]);
 }
 
-// One warp per chunk and head forms the chunk's block; of fp32 q and k also their bf16 pieces
-// (by the first head of each key head).  Four warps per CTA, each with its own scratch.
-template <class Block> struct PrepScratch {
-    static constexpr int RATROW = 33, NROW = 36;
-    unsigned char block[Block::BYTES];                          // as it goes out
-    float nt[kDeltaC * NROW];                                   // nt[s][t] = n(t, s)
-    float rat[kDeltaC * RATROW + 4];                            // rat[t][s + 1] = r(t, s); later T11, T22, Z
+// One warp per chunk and head forms the chunk's block; the first head of each key head also
+// writes the chunk's k and q as operands.  Four warps per CTA, each with its own scratch.
+template <int NP, typename Tin, class Block> struct PrepScratch {
+    static constexpr int RATROW = 33, NROW = 36, ROW = NP * int(sizeof(Tin)) + 16;
+    union {
+        unsigned char rows[2][kDeltaC * ROW];                   // k and q as they come
+        struct {
+            unsigned char block[Block::BYTES];                  // as it goes out
+            float nt[kDeltaC * NROW];                           // nt[s][t] = n(t, s)
+            float rat[kDeltaC * RATROW + 4];                    // rat[t][s + 1] = r(t, s); later T11, T22, Z
+        };
+    };
 };
 
 template <int NP, typename Tin, class Block>
 __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
-    using Scratch = PrepScratch<Block>;
-    constexpr int C = kDeltaC, RATROW = Scratch::RATROW, NROW = Scratch::NROW, KP = sizeof(Tin) == 4 ? 3 : 1;
+    using Scratch = PrepScratch<NP, Tin, Block>;
+    constexpr int C = kDeltaC, RATROW = Scratch::RATROW, NROW = Scratch::NROW, ROW = Scratch::ROW;
+    constexpr int KP = sizeof(Tin) == 4 ? 3 : 1, OP = sizeof(Tin) == 4 ? 2 : 1;      // pieces here, and as operands
+    using Rows = DeltaRows<NP, OP>;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C;
@@ -150,8 +167,24 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
     const int c = int(bc % nchunk), b = int(bc / nchunk);
     const int group = p.heads / p.qk_heads, hk = h / group, t0 = c * C;
     Scratch &sc = reinterpret_cast<Scratch *>(delta_smem)[warp];
-    float *rat = sc.rat, *nt = sc.nt;
 
+    // the chunk's rows, all on their way at once
+    {
+        constexpr int E = 16 / sizeof(Tin), CR = NP / E;
+        const size_t krow = size_t(p.qk_heads) * p.N;
+        const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
+        const Tin *kp = static_cast<const Tin *>(p.k) + k0, *qp = static_cast<const Tin *>(p.q) + k0;
+        const unsigned to = smem_u32(sc.rows);
+#pragma unroll 8
+        for (int x = lane; x < C * CR; x += 32) {
+            const int r = x / CR, n = (x % CR) * E;
+            const bool ok = t0 + r < p.seqlen && n < p.N;
+            const size_t off = ok ? size_t(r) * krow + n : 0;
+            cp_async_16z(to + r * ROW + n * int(sizeof(Tin)), kp + off, ok);
+            cp_async_16z(to + C * ROW + r * ROW + n * int(sizeof(Tin)), qp + off, ok);
+        }
+        cp_async_commit();
+    }
     // lane t: a and beta of the chunk's token t
     float av = 0.f, beta = 0.f;
     if (t0 + lane < p.seqlen) {
@@ -159,78 +192,57 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
         av = p.a[at];
         beta = p.beta[at];
     }
+    cp_async_wait<0>();
+    __syncwarp();
 
-    // k.k and q.k in tiles [16 x 8]: rows 0-15 against tokens 0-15, rows 16-31 against all.  The
-    // inner index may be permuted at will, so a lane takes 8 neighbouring values of its rows
-    // g, g + 8, ..: two steps' operands in one 16-byte load.
+    // k.k and q.k in tiles [16 x 8]: rows 0-15 against tokens 0-15, rows 16-31 against all
     float kk[6][4], qk[6][4];
 #pragma unroll
     for (int i = 0; i < 6; ++i) { zero4(kk[i]); zero4(qk[i]); }
-    const size_t krow = size_t(p.qk_heads) * p.N;
-    const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
     unsigned big[2] = {0, 0};                                   // largest |k|, |q| of the lane (bits; bf16: packed pairs)
-#pragma unroll (KP == 1 ? 2 : 1)
-    for (int j = 0; j < NP / 32; ++j) {
-        uint4 rows[2][4][KP];                                   // [k, q][row / 8][piece]
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+    for (int j = 0; j < NP / 16; ++j) {
+        unsigned ka[2][KP][4], qa[2][KP][4];                    // A operands of rows 0-15 and 16-31
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = g + 8 * r, n = 32 * j + 8 * t4;
-                const bool ok = t0 + t < p.seqlen && n < p.N;
-                const size_t off = k0 + size_t(t) * krow + n;
-                const Tin *src = static_cast<const Tin *>(m ? p.q : p.k);
-                uint4 (&w)[KP] = rows[m][r];
-                if constexpr (KP == 1) {
-                    w[0] = ok ? __ldg(reinterpret_cast<const uint4 *>(src + off)) : make_uint4(0, 0, 0, 0);
-                    const unsigned x4[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+        for (int m = 0; m < 2; ++m) {
+            if constexpr (KP == 1) {
+                const unsigned at = smem_u32(sc.rows) + (16 * m + (lane & 15)) * ROW + (lane >> 4) * 16 + j * 32;
+                ldsm4(ka[m][0], at);
+                ldsm4(qa[m][0], at + C * ROW);
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) big[m] = __vmaxu2(big[m], x4[y] & 0x7fff7fffu);
-                } else {
-                    float f[8] = {};
-                    if (ok) load8<float>(src + off, f);
-                    unsigned x[4][3];
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) split_bf16(f[2 * y], f[2 * y + 1], x[y]);
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) w[i] = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) big[m] = max(big[m], __float_as_uint(fabsf(f[y])));
+                for (int y = 0; y < 4; ++y) {
+                    big[0] = __vmaxu2(big[0], ka[m][0][y] & 0x7fff7fffu);
+                    big[1] = __vmaxu2(big[1], qa[m][0][y] & 0x7fff7fffu);
                 }
-            }
+            } else {
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-            auto half = [&](const uint4 &w, int x) { return st ? (x ? w.w : w.z) : (x ? w.y : w.x); };
-            unsigned kb[2][KP][4];
+                for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+                    for (int z = 0; z < 2; ++z) {
+                        const float2 f = *reinterpret_cast<const float2 *>(sc.rows[z] + (16 * m + g + 8 * (y & 1)) * ROW +
+                                                                           (16 * j + 8 * (y >> 1) + 2 * t4) * 4);
+                        unsigned x[3];
+                        split_bf16(f.x, f.y, x);
 #pragma unroll
-                for (int i = 0; i < KP; ++i)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) kb[n][i][2 * r + x] = half(rows[0][2 * n + r][i], x);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                unsigned ka[KP][4], qa[KP][4];
-#pragma unroll
-                for (int i = 0; i < KP; ++i)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            ka[i][2 * x + r] = half(rows[0][2 * m + r][i], x);
-                            qa[i][2 * x + r] = half(rows[1][2 * m + r][i], x);
-                        }
-#pragma unroll
-                for (int n = 0; n <= m; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float (&ck)[4] = kk[2 * (m + n) + i], (&cq)[4] = qk[2 * (m + n) + i];
-                        mma_exact<KP>(ck, ka, kb[n], i);
-                        mma_exact<KP>(cq, qa, kb[n], i);
+                        for (int i = 0; i < 3; ++i) (z ? qa : ka)[m][i][y] = x[i];
+                        big[z] = max(big[z], max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
                     }
             }
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            unsigned kb[KP][4];
+#pragma unroll
+            for (int i = 0; i < KP; ++i) {
+                kb[i][0] = ka[n][i][0]; kb[i][1] = ka[n][i][2]; kb[i][2] = ka[n][i][1]; kb[i][3] = ka[n][i][3];
+            }
+#pragma unroll
+            for (int m = n; m < 2; ++m)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mma_exact<KP>(kk[2 * (m + n) + i], ka[m], kb, i);
+                    mma_exact<KP>(qk[2 * (m + n) + i], qa[m], kb, i);
+                }
         }
     }
     Pow2 cs[2];
@@ -239,26 +251,28 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
         if constexpr (KP == 1) big[m] = max(big[m] << 16, big[m] & 0xffff0000u);
         cs[m] = pow2_for(__reduce_max_sync(0xffffffffu, big[m]));
     }
-    if constexpr (KP != 1) {        // the scaled fp16 pieces of fp32 rows, read again (from L1)
-        if (h == hk * group)
-            for (int x = lane; x < C * (NP / 8); x += 32) {
-                const int t = x / (NP / 8), n = (x % (NP / 8)) * 8;
-                if (t0 + t >= p.seqlen || n >= p.N) continue;
-                const size_t off = k0 + size_t(t) * krow + n;
+    if (h == hk * group) {          // the rows as operands
+        unsigned char *out = p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Rows::BYTES;
+        constexpr int CR = NP / 8;
+#pragma unroll 4
+        for (int x = lane; x < C * CR; x += 32) {
+            const int r = x / CR, n = (x % CR) * 8;
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    float f[8];
-                    load8<float>(static_cast<const float *>(m ? p.q : p.k) + off, f);
-                    unsigned w[4][2];
+            for (int m = 0; m < 2; ++m) {
+                float f[8];
+                load8<Tin>(reinterpret_cast<const Tin *>(sc.rows[m] + r * ROW) + n, f);
+                unsigned w[4][OP];
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) split_f16<2>(f2(f[2 * y], f[2 * y + 1]), cs[m].c, w[y]);
+                for (int y = 0; y < 4; ++y) split_f16<OP>(f2(f[2 * y], f[2 * y + 1]), cs[m].c, w[y]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        *reinterpret_cast<uint4 *>((m ? p.qp : p.kp) + i * p.piece + off) =
-                            make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
-                }
+                for (int i = 0; i < OP; ++i)
+                    *reinterpret_cast<uint4 *>(out + (m * OP + i) * Rows::PIECE + r * Rows::ROW + n * 2) =
+                        make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
             }
+        }
     }
+    __syncwarp();                   // the rows' memory is the scratch of what follows
+    float *rat = sc.rat, *nt = sc.nt;
     // r(t, s): lane s + 1 adds up a from token s + 1 on (no differences of long sums, so
     // a = -inf, a full reset, is exact); lane 0 is the chunk's start
     float acc = 0.f;
@@ -556,78 +570,52 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
     // chunk of loop step i: forwards, or backwards in the reverse pass
     auto chunk_of = [&](int i) { return REV ? nchunk - 1 - i : i; };
 
-    // The CTA's threads copy a chunk's rows and its block, one commit group per chunk.
+    // Loop step i's data: two bulk copies by one thread on the stage's mbarrier, and the rows of
+    // v by every thread (cp.async).
     const int hk = h / (p.heads / p.qk_heads), prow = p.P - slice * NW * 16;
-    const size_t krow = size_t(p.qk_heads) * p.N, vrow = size_t(p.heads) * p.P;
-    const size_t koff = size_t(b) * p.seqlen * krow + size_t(hk) * p.N;
+    const size_t vrow = size_t(p.heads) * p.P;
     const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
-    auto copy_rows = [&](unsigned dst, int rowbytes, const auto *src, size_t stride, auto width, int limit, int t0) {
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
+    if (tid == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        mbar_fence_init();
+    }
+    __syncthreads();
+    auto copy_v = [&](unsigned dst, int rowbytes, const auto *src, int left) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
-        constexpr int E = 16 / sizeof(T), CR = decltype(width)::value / E;      // values per copy, copies per row
+        constexpr int E = 16 / sizeof(T), CR = NW * 16 / E, STEP = Cfg::NT / CR;     // copies per row, rows per round
+        const int r0 = tid / CR, n = (tid % CR) * E, rows = n < prow ? left - r0 : 0;
+        const T *at = src + r0 * vrow + n;
 #pragma unroll
-        for (int i = 0; i < (C * CR + Cfg::NT - 1) / Cfg::NT; ++i) {
-            const int x = tid + Cfg::NT * i, r = x / CR, n = (x % CR) * E;
-            if (C * CR % Cfg::NT == 0 || x < C * CR) {
-                const bool ok = t0 + r < p.seqlen && n < limit;
-                cp_async_16z(dst + r * rowbytes + n * int(sizeof(T)), src + (ok ? size_t(t0 + r) * stride + n : 0), ok);
-            }
+        for (int i = 0; i < C / STEP; ++i) {
+            cp_async_16z(dst + (r0 + i * STEP) * rowbytes + n * int(sizeof(T)), i * STEP < rows ? at : src, i * STEP < rows);
+            at += STEP * vrow;
         }
     };
-    float ck = 1.f, cq = 1.f;                              // scales of the chunk that is on its way
     auto issue = [&](int i) {
         if (i < nchunk) {
-            const int c = chunk_of(i), t0 = c * C;
-            const unsigned base = smem_u32(smem + (i & 1) * Cfg::STAGE);
-            const std::integral_constant<int, NP> kw;
-            const std::integral_constant<int, NW * 16> vw;
-#pragma unroll
-            for (int m = 0; m < KP; ++m) {
-                copy_rows(base + Cfg::OFF_K + m * Cfg::PIECE, Cfg::KROW,
-                          static_cast<const __half *>(p.k) + m * p.piece + koff, krow, kw, p.N, t0);
-                copy_rows(base + Cfg::OFF_Q + m * Cfg::PIECE, Cfg::KROW,
-                          static_cast<const __half *>(p.q) + m * p.piece + koff, krow, kw, p.N, t0);
+            const int c = chunk_of(i), left = p.seqlen - c * C;
+            unsigned char *st = smem + (i & 1) * Cfg::STAGE;
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&full[i & 1], Cfg::Rows::BYTES + Cfg::BLOCK);
+                bulk_load(st, p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Cfg::Rows::BYTES, Cfg::Rows::BYTES,
+                          &full[i & 1]);
+                bulk_load(st + Cfg::OFF_TRI, p.prep + (size_t(bh) * nchunk + c) * Block::BYTES, Cfg::BLOCK, &full[i & 1]);
             }
-            copy_rows(base + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + voff, vrow, vw, prow, t0);
-            if constexpr (MODE == 1)
-                copy_rows(base + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + voff, vrow, vw, prow, t0);
-            const unsigned char *blk = p.prep + (size_t(bh) * nchunk + c) * Block::BYTES;
-            if constexpr (KP == 1) {
-                const float *one = reinterpret_cast<const float *>(blk + Block::OFF_VEC) + kVecScalars * C;
-                ck = __ldg(one + kCk);
-                cq = __ldg(one + kCq);
-            }
-#pragma unroll
-            for (int k = 0; k < (Cfg::BLOCK / 16 + Cfg::NT - 1) / Cfg::NT; ++k) {
-                const int x = tid + Cfg::NT * k;
-                if (x < Cfg::BLOCK / 16) cp_async_16z(base + Cfg::OFF_TRI + 16 * x, blk + 16 * x, true);
-            }
+            const size_t vat = voff + size_t(c) * C * vrow;
+            copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + vat, left);
+            if constexpr (MODE == 1) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + vat, left);
         }
         cp_async_commit();
     };
-    // Step i's rows are here (this thread's copies of them): bf16 k and q become scaled fp16 in
-    // place, each thread doing what it copied; the next barrier shows them to the others.
+    // Step i's data are here, for every thread after the barrier that follows.
+    bool alive = true;
     auto arrive = [&](int i) {
         cp_async_wait<0>();
-        if constexpr (KP == 1) {
-            if (i >= nchunk) return;
-            constexpr int CR = NP / 8;
-#pragma unroll
-            for (int y = 0; y < (C * CR + Cfg::NT - 1) / Cfg::NT; ++y) {
-                const int x = tid + Cfg::NT * y, r = x / CR, n = (x % CR) * 8;
-                if (C * CR % Cfg::NT == 0 || x < C * CR)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        uint4 *at = reinterpret_cast<uint4 *>(smem + (i & 1) * Cfg::STAGE + (m ? Cfg::OFF_Q : Cfg::OFF_K) +
-                                                              r * Cfg::KROW + n * 2);
-                        const uint4 w = *at;
-                        const float c = m ? cq : ck;
-                        auto cvt = [&](unsigned u) {
-                            const float2 f = fmul2(bf16x2_to_f2(u), f2(c, c));
-                            return pack_f16x2(f.x, f.y);
-                        };
-                        *at = make_uint4(cvt(w.x), cvt(w.y), cvt(w.z), cvt(w.w));
-                    }
-            }
+        if (alive && !mbar_wait(&full[i & 1], uint32_t(i >> 1) & 1, kDeltaWaitCycles)) {
+            alive = false;
+            atomicAdd(p.timeouts, 1u);
         }
     };
     // The sums over the warps' rows of loop step i, left in shared memory at its end.
@@ -735,6 +723,13 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
         cp_async_commit();
     }
 
+    // the largest magnitude of the state, kept up with its updates
+    float ms = 0.f;
+#pragma unroll
+    for (int j = 0; j < NP / 8; ++j)
+#pragma unroll
+        for (int m = 0; m < 4; ++m) ms = fmaxf(ms, fabsf(s[j][m]));
+
     for (int i = 0; i < nchunk; ++i) {
         const int c = chunk_of(i);
         arrive(i);
@@ -768,9 +763,6 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 
         const float *one = vec + kVecScalars * C;
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
-        float ms = 0.f;
-#pragma unroll
-        for (int j = 0; j < NP / 8; ++j) ms = fmaxf(fmaxf(ms, fmaxf(fabsf(s[j][0]), fabsf(s[j][1]))), fmaxf(fabsf(s[j][2]), fabsf(s[j][3])));
         const Pow2 cS = pow2_for(warp_max_bits(ms));
         Tok sk, sq;
         zero_tok(sk); zero_tok(sq);
@@ -851,6 +843,22 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             const float b = __uint_as_float(m) * most;
             return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
         };
+        Tok o;
+        if constexpr (!REV) {
+            // y = scale gam S q + Pm (beta e)
+            unsigned A[2][PO][4];
+            const Pow2 cu = scale_by(mx, one[kMaxBeta]);
+            scale_tok(o, x, vec + kVecBeta * C, t4);
+            split_tok<PO>(o, cu.c, A);
+            zero_tok(o);
+            mma_triangle<PO, PO, false>(o, A, tbase + Block::OFF_P);
+            scale_tok(sq, sq, vec + kVecSgq * C, t4);
+            const float f = one[kInvP] * cu.inv;
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f, o[n][m], cS.inv * sq[n][m]);
+        }
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
         const float glast = one[kGamLast];
         {
@@ -868,6 +876,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 for (int m = 0; m < KP; ++m) ldsm4_t(f[m], base + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bk + j * 32);
             };
             const float2 f1 = REV ? f2(-c1.inv, -c1.inv) : f2(c1.inv, c1.inv), gl = f2(glast, glast), f2v = f2(c2.inv, c2.inv);
+            ms = 0.f;
 #pragma unroll
             for (int j = 0; j < NP / 16; ++j) {
                 float d[2][4], d2[2][4];
@@ -893,24 +902,11 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                         if constexpr (REV) u = ffma2(f2v, f2(d2[n][m], d2[n][m + 1]), u);
                         u = ffma2(f1, f2(d[n][m], d[n][m + 1]), u);
                         at[0] = u.x; at[1] = u.y;
+                        ms = fmaxf(ms, fmaxf(fabsf(u.x), fabsf(u.y)));
                     }
             }
         }
         if constexpr (!REV) {
-            // y = scale gam S q + Pm (beta e)
-            unsigned A[2][PO][4];
-            Tok o;
-            const Pow2 cu = scale_by(mx, one[kMaxBeta]);
-            scale_tok(o, x, vec + kVecBeta * C, t4);
-            split_tok<PO>(o, cu.c, A);
-            zero_tok(o);
-            mma_triangle<PO, PO, false>(o, A, tbase + Block::OFF_P);
-            scale_tok(sq, sq, vec + kVecSgq * C, t4);
-            const float f = one[kInvP] * cu.inv;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f, o[n][m], cS.inv * sq[n][m]);
             if constexpr (MODE == 0) {
                 store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, o);
             } else {

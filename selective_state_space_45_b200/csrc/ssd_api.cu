@@ -14,6 +14,11 @@ using namespace ssm_host;
 // here (read by ssm_device_timeouts).
 static __device__ unsigned g_wait_timeouts;
 
+unsigned *ssm_host::wait_counter() {
+    void *counter = nullptr;
+    return cudaGetSymbolAddress(&counter, g_wait_timeouts) == cudaSuccess ? static_cast<unsigned *>(counter) : nullptr;
+}
+
 namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -58,9 +63,8 @@ int launch_ssd(const void *x, const void *B, const void *C, ssm::SsdTcArgs a, cu
         !make_map(&mb, B, N, a.heads, a.seqlen, a.batch, 64, Cfg::Q) ||
         !make_map(&mc, C, N, a.heads, a.seqlen, a.batch, 64, Cfg::Q))
         return SSM_ERR_CUDA;
-    void *counter = nullptr;
-    if (cudaGetSymbolAddress(&counter, g_wait_timeouts) != cudaSuccess) return SSM_ERR_CUDA;
-    a.timeouts = static_cast<unsigned *>(counter);
+    a.timeouts = wait_counter();
+    if (!a.timeouts) return SSM_ERR_CUDA;
     if (cudaFuncSetAttribute(ssm::ssd_tc_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(Cfg::SMEM_BYTES)) != cudaSuccess ||
         cudaFuncSetAttribute(ssm::ssd_tc_kernel<Cfg>, cudaFuncAttributePreferredSharedMemoryCarveout,
