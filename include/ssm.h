@@ -326,7 +326,7 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  *                   everything before the token); beta any value, 0 writes nothing.
  *   initial_state : [batch][heads][headdim][dstate] fp32 or NULL (zero).
  *   final_state   : the same, or NULL (not written).  May be initial_state itself.
- * headdim and dstate must be multiples of 8, headdim <= 256 and dstate <= 128
+ * headdim and dstate must be multiples of 8 and at most 128
  * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on bf16 pieces of the
  * fp32 operands with fp32 accumulation: the final state and an fp32 y are good to a few
  * 2^-20 of their size (normwise), a bf16 y to its own rounding and 2^-16.  A value that is

@@ -9,37 +9,50 @@ using namespace ssm_host;
 
 namespace {
 
-template <int NP, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
+template <int NP, int PW, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
+    using Cfg = ssm::GradCfg<NP, PW, sizeof(Tin) == 4 ? 2 : 1, Tin, Tg>;
     const long long ctas = (long long)a.batch * a.qk_heads * ((a.seqlen + ssm::kGradC - 1) / ssm::kGradC);
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    constexpr int smem = ssm::delta_grad_smem<NP>();
-    if (cudaFuncSetAttribute(ssm::delta_grad_kernel<NP, Tin, Tg>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-        cudaSuccess)
-        return SSM_ERR_CUDA;
-    ssm::delta_grad_kernel<NP, Tin, Tg><<<unsigned(ctas), 256, smem, s>>>(a);
+    if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
+    ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
     return status_of(cudaGetLastError());
+}
+template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
+    switch (padded_state(a.N)) {
+    case 32: return launch_grad<32, PW, Tin, Tg>(a, s);
+    case 64: return launch_grad<64, PW, Tin, Tg>(a, s);
+    case 96: return launch_grad<96, PW, Tin, Tg>(a, s);
+    default: return launch_grad<128, PW, Tin, Tg>(a, s);
+    }
 }
 
 using Block = ssm::DeltaBlock<2, true>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, w, ck, dck, dyy, edu, zsum, all;
+    size_t prep, rows, e, w, ck, dck, dyy, edu, zsum, smax, dsmax, emax, wmax, ymax, part, all;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
         const size_t sum = size_t(delta_slices(P)) * tok * 4, state = bh * nbound * P * N * 4;
         size_t at = 0;
-        auto part = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
-        part(prep, prep_bytes<Block>(batch, seqlen, heads));
-        part(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
-        part(e, tok * P * 4);
-        part(w, grad_dtype == SSM_F32 ? 0 : tok * P * 4);       // fp32 gradients: w is dv itself
-        part(ck, state);
-        part(dck, state);
-        part(dyy, sum);
-        part(edu, sum);
-        part(zsum, size_t(delta_slices(P)) * kDeltaWarps * bh * nbound * 4);
+        auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
+        add(prep, prep_bytes<Block>(batch, seqlen, heads));
+        add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
+        add(e, tok * P * 4);
+        add(w, grad_dtype == SSM_F32 ? 0 : tok * P * 4);       // fp32 gradients: w is dv itself
+        add(ck, state);
+        add(dck, state);
+        add(dyy, sum);
+        add(edu, sum);
+        const size_t parts = size_t(delta_slices(P)) * kDeltaWarps * 4;
+        add(zsum, parts * bh * nbound);
+        add(smax, parts * bh * nbound);             // these five together: zeroed
+        add(dsmax, parts * bh * nbound);
+        add(emax, parts * bh * delta_chunks(seqlen));
+        add(wmax, parts * bh * delta_chunks(seqlen));
+        add(ymax, parts * bh * delta_chunks(seqlen));
+        add(part, heads > qk_heads ? 2 * size_t(batch) * seqlen * qk_heads * N * 4 : 0);
         all = at;
     }
 };
@@ -58,21 +71,27 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     f.prep = ws.p + at.prep;
     f.rows = ws.p + at.rows;
     f.timeouts = wait_counter();
+    auto bits = [&](size_t off) { return reinterpret_cast<unsigned *>(ws.p + off); };
     int st = f.timeouts ? dispatch_prep<Tin, Block>(f, s) : int(SSM_ERR_CUDA);
+    if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
+    f.smax = bits(at.smax); f.emax = bits(at.emax);
     f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
         r.v = dy; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = sizeof(Tg) == 4 ? nullptr : w;
         r.dck = part(at.dck); r.sum = part(at.edu); r.zsum = part(at.zsum);
+        r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
         st = dispatch_chain<KP, Tg, Tg, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
         const int slices = delta_slices(f.P);
-        const ssm::DeltaGradArgs g{f.q, f.k, v, dy, f.a, f.beta, part(at.e), w, part(at.ck), part(at.dck), part(at.dyy),
-                                   part(at.edu), part(at.zsum), dq, dk, da, dbeta, f.batch, f.seqlen,
-                                   f.heads, f.qk_heads, f.P, f.N, slices, slices * kDeltaWarps, f.scale};
-        st = f.N <= 64 ? launch_grad<64, Tin, Tg>(g, s) : launch_grad<128, Tin, Tg>(g, s);
+        const ssm::DeltaGradArgs g{v, dy, f.a, f.beta, part(at.e), w, f.rows, f.prep, Block::BYTES, part(at.ck),
+                                   part(at.dck), part(at.dyy), part(at.edu), part(at.zsum), bits(at.smax),
+                                   bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
+                                   da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N, slices,
+                                   slices * kDeltaWarps, f.scale};
+        st = f.P <= 64 ? dispatch_grad<64, Tin, Tg>(g, s) : dispatch_grad<128, Tin, Tg>(g, s);
     }
     return ws.release(st);
 }

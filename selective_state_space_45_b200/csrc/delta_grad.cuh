@@ -14,234 +14,384 @@
 //     da_t = <dS, S>(chunk's end) + sum_{t'>=t} (dy.y - v.w)_t'
 //          = <dS, S>(chunk's start) - sum_{t'<t} (dy.y - v.w)_t'
 // with the inner products taken afresh every 64 tokens: at most 32 terms are summed.
+//
+// Four warps with 16 tokens (rows) each; every product on the tensor cores with scaled fp16
+// operands: one piece behind bf16 gradients (2^-12 against their 2^-9), two behind fp32 ones.
+// The token-by-token matrices never leave the registers: each is formed in the layout of an
+// accumulator whose rows are the rows it is then used with (dy e^T for dq, e dy^T, e w^T and
+// w e^T for dk), so that it becomes the next product's A operand as it stands, and tiles off
+// the triangle are skipped; every warp has ten of them.  The largest magnitudes that set the
+// scales come from the passes.
 #pragma once
 
-#include "mma_common.cuh"
+#include "delta_rule.cuh"
 
 namespace ssm {
 
 struct DeltaGradArgs {
-    const void *q, *k, *v, *dy;
+    const void *v, *dy;
     const float *a, *beta, *e, *w;
+    const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
+    size_t block;                      // bytes of a chunk block
     const float *ck, *dck;             // states and their gradients at the boundaries
     const float *dyy, *edu;            // [slices][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
+    const unsigned *smax, *dsmax;      // [batch][heads][boundaries][zparts]
+    const unsigned *emax, *wmax, *ymax;// [batch][heads][chunks of 32][zparts]
+    float *part;                       // heads that share a key head: running sums of dq, dk, [2][tokens][qk_heads][N]
     void *dq, *dk;
     float *da, *dbeta;
     int batch, seqlen, heads, qk_heads, P, N, slices, zparts;
     float scale;
 };
 
-constexpr int kGradC = 64, kGradK = 16, kGradPad = 4;
+constexpr int kGradC = 64, kGradN = 64;        // tokens per CTA, state columns per pass
 
-// The decays of a chunk of 64 tokens of one head, from 64-bit prefix sums (a below -1e4
-// counts as -1e4: its exponential is 0 either way, and sums stay finite).
-struct GradDecay {
-    double G[kGradC];
-    float gam[kGradC], end[kGradC], beta[kGradC], d[kGradC];
+// PW: headdim padded to 64 or 128; NP: dstate padded; KP: pieces of k and q; PG: of the others.
+template <int NP_, int PW_, int KP_, typename Tin_, typename Tg_> struct GradCfg {
+    static constexpr int NP = NP_, PW = PW_, KP = KP_, PG = sizeof(Tg_) == 4 ? 2 : 1;
+    using Tin = Tin_;
+    using Tg = Tg_;
+    static constexpr int W = NP < kGradN ? NP : kGradN;
+    static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16;                // padded rows (bytes)
+    static constexpr int TOK = kGradC * PROW, ST = PW * NROW, KT = kGradC * NROW;
+    static constexpr int OFF_Y = 0, OFF_E = OFF_Y + PG * TOK, OFF_W = OFF_E + PG * TOK;
+    static constexpr int OFF_S = OFF_W + PG * TOK, OFF_D = OFF_S + PG * ST;
+    static constexpr int OFF_K = OFF_D + PG * ST, OFF_Q = OFF_K + KP * KT;
+    static constexpr int OFF_VEC = OFF_Q + KP * KT;
+    static constexpr int SMEM_BYTES = OFF_VEC + 8 * kGradC * 4;
 };
 
-template <int NP, typename Tin, typename Tg>
-__global__ void __launch_bounds__(256) delta_grad_kernel(const DeltaGradArgs p) {
-    constexpr int C = kGradC, KS = kGradK, CT = NP / 64;          // CT: quads of columns per thread
-    constexpr int AR = C + kGradPad, BR = NP + kGradPad;
+template <class Cfg>
+__global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) {
+    using Tin = typename Cfg::Tin;
+    using Tg = typename Cfg::Tg;
+    constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W;
+    using Rows = DeltaRows<NP, KP>;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
-    float *A0 = reinterpret_cast<float *>(smem), *A1 = A0 + KS * AR, *A2 = A1 + KS * AR;
-    float *B0 = A2 + KS * AR, *B1 = B0 + KS * BR;
-    float *M1 = B1 + KS * BR, *M2 = M1 + C * AR;
-    GradDecay &dec = *reinterpret_cast<GradDecay *>(M2 + C * AR);
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1;
+    float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
+    float *bend = bet + C, *dtok = bend + C;
+    const int tid = threadIdx.x, lane = tid & 31, rt = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
     const int c = int(blockIdx.x % unsigned(nchunk)), bk = int(blockIdx.x / unsigned(nchunk));
     const int b = bk / p.qk_heads, hk = bk - b * p.qk_heads;
     const int t0 = c * C, nt = min(C, p.seqlen - t0), group = p.heads / p.qk_heads;
-    const size_t krow = size_t(p.qk_heads) * p.N, k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
-    const Tin *qp = static_cast<const Tin *>(p.q) + k0, *kp = static_cast<const Tin *>(p.k) + k0;
+    const int c32 = 2 * c, n32 = min(2, nck - c32);
+    const size_t all = size_t(p.batch) * p.heads, krow = size_t(p.qk_heads) * p.N, vrow = size_t(p.heads) * p.P;
+    const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
 
-    // [64 tokens][x0 .. x0 + 16) of rows of `stride` values -> X[column][token], times f(token)
-    auto load_t = [&](float *X, const auto *src, size_t stride, int x0, int width, auto f) {
-        const int r = tid >> 2, x = (tid & 3) * 4;
-        float v[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < nt && x0 + x < width) {
-            loadn<4>(src + size_t(r) * stride + x0 + x, v);
-            const float s = f(r);
+    // 1 / scales of k and q in the chunk's halves
+    float ick[2], icq[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] *= s;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) X[(x + i) * AR + r] = v[i];
-    };
-    // rows [r0, r0 + 16) of N values -> X[row][column]
-    auto load_n = [&](float *X, const auto *src, size_t stride, int r0, int rows) {
-        for (int y = tid; y < KS * (NP / 4); y += 256) {
-            const int r = y / (NP / 4), n = (y % (NP / 4)) * 4;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (r0 + r < rows && n < p.N) loadn<4>(src + size_t(r0 + r) * stride + n, v);
-            *reinterpret_cast<float4 *>(X + r * BR + n) = make_float4(v[0], v[1], v[2], v[3]);
-        }
-    };
-    auto one = [](int) { return 1.f; };
-    // acc[i][:] += x[i] * (four columns)
-    auto fma4 = [](float2 (&acc)[2], float x, float4 y) {
-        acc[0] = ffma2(f2(x, x), f2(y.x, y.y), acc[0]);
-        acc[1] = ffma2(f2(x, x), f2(y.z, y.w), acc[1]);
-    };
-    auto quad = [](const float *x) { return *reinterpret_cast<const float4 *>(x); };
+    for (int x = 0; x < 2; ++x) {
+        const int cc = c32 + (x < n32 ? x : 0);
+        const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * p.block +
+                                                           DeltaBlock<2, true>::OFF_VEC) + kVecScalars * kDeltaC;
+        ick[x] = 1.f / one[kCk];         // powers of two: exact
+        icq[x] = 1.f / one[kCq];
+    }
+    const unsigned an = unsigned((16 * rt + (lane & 15)) * Cfg::PROW + (lane >> 4) * 16);      // A: this warp's rows
+    const unsigned bp = b_rows_n(lane, Cfg::PROW), bn = b_rows_k(lane, Cfg::NROW);
 
-    float2 dq[4][CT][2] = {}, dk[4][CT][2] = {};
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
-        const size_t bh = size_t(b) * p.heads + h, all = size_t(p.batch) * p.heads;
-        const size_t vrow = size_t(p.heads) * p.P, v0 = (size_t(b) * p.seqlen + t0) * vrow + size_t(h) * p.P;
+        const size_t bh = size_t(b) * p.heads + h;
+        const size_t v0 = (size_t(b) * p.seqlen + t0) * vrow + size_t(h) * p.P;
+        // scales: the largest magnitudes over the rows' warps (and the chunk's halves)
+        auto most = [&](const unsigned *m, size_t first, int n) {
+            unsigned x = 0;
+            for (int i = lane; i < n; i += 32) x = max(x, m[first + i]);
+            return pow2_for(__reduce_max_sync(0xffffffffu, x));
+        };
+        const Pow2 cS = most(p.smax, (bh * nbound + c) * p.zparts, p.zparts);
+        const Pow2 cD = most(p.dsmax, (bh * nbound + c + 1) * p.zparts, p.zparts);
+        const Pow2 cE = most(p.emax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
+        const Pow2 cW = most(p.wmax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
+        const Pow2 cY = most(p.ymax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
+        __syncthreads();                 // the last head's tiles and vectors are done with
+
+        // dy, e and w as operands [token][headdim]; v.w on the way
         const Tg *dyp = static_cast<const Tg *>(p.dy) + v0;
+        const Tin *vp = static_cast<const Tin *>(p.v) + v0;
         const float *ep = p.e + v0, *wp = p.w + v0;
-        const float *S0 = p.ck + (bh * nbound + c) * p.P * p.N, *dE = p.dck + (bh * nbound + c + 1) * p.P * p.N;
-        // v.w of every token: four threads per token, sixteen bytes of v at a time
-        float vw = 0.f;
-        {
-            const int r = tid >> 2;
-            if (r < nt) {
-                const Tin *vp = static_cast<const Tin *>(p.v) + v0 + size_t(r) * vrow;
-                for (int x = (tid & 3) * 8; x < p.P; x += 32) {
-                    float a[8], f[8];
-                    load8(vp + x, a);
-                    load8(wp + size_t(r) * vrow + x, f);
+        auto put = [&](unsigned char *at, int piece, const float (&f)[8], float scale) {
+            unsigned x[4][PG];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) vw = fmaf(a[i], f[i], vw);
-                }
+            for (int y = 0; y < 4; ++y) split_f16<PG>(f2(f[2 * y], f[2 * y + 1]), scale, x[y]);
+#pragma unroll
+            for (int i = 0; i < PG; ++i)
+                *reinterpret_cast<uint4 *>(at + i * piece) = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
+        };
+        constexpr int CP = PW / 8;       // lanes per row: 8 or 16, so a row stays within a warp
+#pragma unroll 2
+        for (int i = tid; i < C * CP; i += 128) {
+            const int r = i / CP, x = (i % CP) * 8;
+            const bool ok = r < nt && x < p.P;
+            float fy[8] = {}, fe[8] = {}, fw[8] = {}, fv[8] = {};
+            if (ok) {
+                const size_t off = size_t(r) * vrow + x;
+                load8(dyp + off, fy);
+                load8(ep + off, fe);
+                load8(wp + off, fw);
+                load8(vp + off, fv);
             }
-            vw += __shfl_xor_sync(0xffffffffu, vw, 1);
-            vw += __shfl_xor_sync(0xffffffffu, vw, 2);
+            unsigned char *at = smem + r * Cfg::PROW + x * 2;
+            put(at + Cfg::OFF_Y, Cfg::TOK, fy, cY.c);
+            put(at + Cfg::OFF_E, Cfg::TOK, fe, cE.c);
+            put(at + Cfg::OFF_W, Cfg::TOK, fw, cW.c);
+            float vw = 0.f;
+#pragma unroll
+            for (int y = 0; y < 8; ++y) vw = fmaf(fv[y], fw[y], vw);
+#pragma unroll
+            for (int o = 1; o < CP; o <<= 1) vw += __shfl_xor_sync(0xffffffffu, vw, o);
+            if (i % CP == 0) dtok[r] = vw;
         }
-        __syncthreads();
-        if ((tid & 3) == 0) dec.d[tid >> 2] = vw;
-        __syncthreads();
+        // decays: prefix sums of a as a pair of floats (a below -1e4 counts as -1e4: its
+        // exponential is 0 either way, and the sums stay finite)
         if (tid < C) {
             const size_t at = (size_t(b) * p.seqlen + t0 + tid) * p.heads + h;
-            dec.G[tid] = tid < nt ? double(fmaxf(p.a[at], -1e4f)) : 0.0;
-            dec.beta[tid] = tid < nt ? p.beta[at] : 0.f;
-            float d = 0.f, db = 0.f;
-            if (tid < nt)
-                for (int s = 0; s < p.slices; ++s) {
-                    const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                    d += p.dyy[x];
-                    db += p.edu[x];
-                }
-            dec.d[tid] = d - dec.d[tid];
-            if (tid < nt) p.dbeta[at] = db;
+            Gh[tid] = tid < nt ? fmaxf(p.a[at], -1e4f) : 0.f;
+            bet[tid] = tid < nt ? p.beta[at] : 0.f;
         }
         __syncthreads();
-        double G = 0.0;
+        double G = 0.0, Gend = 0.0;
         if (tid < C)
-            for (int x = 0; x <= tid; ++x) G += dec.G[x];
-        __syncthreads();
-        if (tid < C) dec.G[tid] = G;
+            for (int x = 0; x < C; ++x) {
+                const double av = Gh[x];
+                Gend += av;
+                if (x <= tid) G += av;
+            }
+        float dt = 0.f;
+        if (tid < nt) {
+            const size_t at = (size_t(b) * p.seqlen + t0 + tid) * p.heads + h;
+            float db = 0.f;
+            dt = -dtok[tid];
+            for (int s = 0; s < p.slices; ++s) {
+                const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
+                dt += p.dyy[x];
+                db += p.edu[x];
+            }
+            p.dbeta[at] = db;
+        }
         __syncthreads();
         if (tid < C) {
-            dec.gam[tid] = expf(float(G));
-            dec.end[tid] = expf(float(dec.G[C - 1] - G));
-            if (tid < nt) {
-                float z = 0.f;
-                const bool front = 2 * tid < nt;
-                for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
-                if (front) for (int x = 0; x < tid; ++x) z -= dec.d[x];
-                else for (int x = nt - 1; x >= tid; --x) z += dec.d[x];
-                p.da[(size_t(b) * p.seqlen + t0 + tid) * p.heads + h] = z;
-            }
+            Gh[tid] = float(G);
+            Gl[tid] = float(G - double(float(G)));
+            gam[tid] = expf(float(G));
+            bend[tid] = bet[tid] * expf(float(Gend - G));
+            dtok[tid] = dt;
         }
-        // dy.e and w.e, then M1 and M2
-        float2 de[4][2] = {}, we[4][2] = {};
-        for (int x0 = 0; x0 < p.P; x0 += KS) {
-            __syncthreads();
-            load_t(A0, dyp, vrow, x0, p.P, one);
-            load_t(A1, wp, vrow, x0, p.P, one);
-            load_t(A2, ep, vrow, x0, p.P, one);
-            __syncthreads();
-#pragma unroll
-            for (int x = 0; x < KS; ++x) {
-                const float4 da = quad(A0 + x * AR + 4 * ty), wa = quad(A1 + x * AR + 4 * ty), eb = quad(A2 + x * AR + 4 * tx);
-                const float d4[4] = {da.x, da.y, da.z, da.w}, w4[4] = {wa.x, wa.y, wa.z, wa.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) { fma4(de[i], d4[i], eb); fma4(we[i], w4[i], eb); }
-            }
+        __syncthreads();
+        if (tid < nt) {
+            float z = 0.f;
+            const bool front = 2 * tid < nt;
+            for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
+            if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
+            else for (int x = nt - 1; x >= tid; --x) z += dtok[x];
+            p.da[(size_t(b) * p.seqlen + t0 + tid) * p.heads + h] = z;
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 4 * ty + i, s = 4 * tx + j;
-                const float r = s <= t ? expf(float(dec.G[t] - dec.G[s])) * dec.beta[s] : 0.f;
-                M1[t * AR + s] = s <= t ? r * p.scale * (j & 1 ? de[i][j >> 1].y : de[i][j >> 1].x) : 0.f;
-                M2[t * AR + s] = s < t ? r * (j & 1 ? we[i][j >> 1].y : we[i][j >> 1].x) : 0.f;
-            }
-        // the products with the states
-        for (int x0 = 0; x0 < p.P; x0 += KS) {
-            __syncthreads();
-            load_t(A0, dyp, vrow, x0, p.P, [&](int r) { return p.scale * dec.gam[r]; });
-            load_t(A1, wp, vrow, x0, p.P, [&](int r) { return -dec.gam[r]; });
-            load_t(A2, ep, vrow, x0, p.P, [&](int r) { return dec.beta[r] * dec.end[r]; });
-            load_n(B0, S0, p.N, x0, p.P);
-            load_n(B1, dE, p.N, x0, p.P);
-            __syncthreads();
-#pragma unroll 4
-            for (int x = 0; x < KS; ++x) {
-                const float4 da = quad(A0 + x * AR + 4 * ty), wa = quad(A1 + x * AR + 4 * ty), ea = quad(A2 + x * AR + 4 * ty);
-                const float d4[4] = {da.x, da.y, da.z, da.w}, w4[4] = {wa.x, wa.y, wa.z, wa.w}, e4[4] = {ea.x, ea.y, ea.z, ea.w};
-#pragma unroll
-                for (int m = 0; m < CT; ++m) {
-                    const float4 sb = quad(B0 + x * BR + 64 * m + 4 * tx), db = quad(B1 + x * BR + 64 * m + 4 * tx);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fma4(dq[i][m], d4[i], sb);
-                        fma4(dk[i][m], w4[i], sb);
-                        fma4(dk[i][m], e4[i], db);
-                    }
-                }
-            }
-        }
-        // the products between the tokens
-        for (int s0 = 0; s0 < C; s0 += KS) {
-            __syncthreads();
-            load_n(B0, qp, krow, s0, nt);
-            load_n(B1, kp, krow, s0, nt);
-            __syncthreads();
-#pragma unroll 4
-            for (int x = 0; x < KS; ++x) {
-                const float4 m1t = quad(M1 + (s0 + x) * AR + 4 * ty), m2t = quad(M2 + (s0 + x) * AR + 4 * ty);
-                const float a1[4] = {m1t.x, m1t.y, m1t.z, m1t.w}, a2[4] = {m2t.x, m2t.y, m2t.z, m2t.w};
-#pragma unroll
-                for (int m = 0; m < CT; ++m) {
-                    const float4 qb = quad(B0 + x * BR + 64 * m + 4 * tx), kb = quad(B1 + x * BR + 64 * m + 4 * tx);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        fma4(dq[i][m], M1[(4 * ty + i) * AR + s0 + x], kb);
-                        fma4(dk[i][m], a1[i], qb);
-                        fma4(dk[i][m], -(a2[i] + M2[(4 * ty + i) * AR + s0 + x]), kb);
-                    }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = 4 * ty + i;
-        if (t >= nt) continue;
-#pragma unroll
-        for (int m = 0; m < CT; ++m) {
-            const int n = 64 * m + 4 * tx;
-            if (n >= p.N) continue;
-            const float xq[4] = {dq[i][m][0].x, dq[i][m][0].y, dq[i][m][1].x, dq[i][m][1].y};
-            const float xk[4] = {dk[i][m][0].x, dk[i][m][0].y, dk[i][m][1].x, dk[i][m][1].y};
-            storen<4>(static_cast<Tg *>(p.dq) + k0 + size_t(t) * krow + n, xq);
-            storen<4>(static_cast<Tg *>(p.dk) + k0 + size_t(t) * krow + n, xk);
-        }
-    }
-}
 
-template <int NP> constexpr int delta_grad_smem() {
-    return (3 * kGradK * (kGradC + kGradPad) + 2 * kGradK * (NP + kGradPad) + 2 * kGradC * (kGradC + kGradPad)) * 4 +
-           int(sizeof(GradDecay));
+        // The token-by-token matrices of this warp's rows, in four tiles of 16 columns.
+        const unsigned sy = smem_u32(smem + Cfg::OFF_Y), se = smem_u32(smem + Cfg::OFF_E), sw = smem_u32(smem + Cfg::OFF_W);
+        float x1[4][2][4], x2[4][2][4], x3[4][2][4], x4[2][4];   // dy e^T; e dy^T; w e^T, e w^T past the diagonal; e w^T on it
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) { zero4(x1[u][n]); zero4(x2[u][n]); zero4(x3[u][n]); }
+        zero4(x4[0]); zero4(x4[1]);
+#pragma unroll
+        for (int k = 0; k < PW / 16; ++k) {
+            unsigned ay[PG][4], ae[PG][4], aw[PG][4];
+#pragma unroll
+            for (int i = 0; i < PG; ++i) {
+                ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
+                ldsm4(ae[i], se + i * Cfg::TOK + an + k * 32);
+                ldsm4(aw[i], sw + i * Cfg::TOK + an + k * 32);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                unsigned be[PG][4], by[PG][4], bw[PG][4];
+                const unsigned at = 16 * u * Cfg::PROW + bp + k * 32;
+                if (u <= rt) {
+#pragma unroll
+                    for (int i = 0; i < PG; ++i) ldsm4(be[i], se + i * Cfg::TOK + at);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma_pieces<PG, PG>(x1[u][n], ay, be, n);
+                        mma_pieces<PG, PG>(x3[u][n], aw, be, n);
+                    }
+                }
+                if (u >= rt) {
+#pragma unroll
+                    for (int i = 0; i < PG; ++i) {
+                        ldsm4(by[i], sy + i * Cfg::TOK + at);
+                        ldsm4(bw[i], sw + i * Cfg::TOK + at);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma_pieces<PG, PG>(x2[u][n], ae, by, n);
+                        if (u == rt) mma_pieces<PG, PG>(x4[n], ae, bw, n);
+                        else mma_pieces<PG, PG>(x3[u][n], ae, bw, n);
+                    }
+                }
+            }
+        }
+        // times the decays, beta and the scales taken back out: M1 / ck for dq; M1^T scale / cq
+        // and -(M2 + M2^T) / ck for dk
+        float m1 = 0.f, m2 = 0.f;
+        const float fye = cY.inv * cE.inv, fwe = cW.inv * cE.inv;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int r = 16 * rt + g + 8 * (m >> 1), q = 16 * u + 8 * n + 2 * t4 + (m & 1);
+                    const float gd = (Gh[r] - Gh[q]) + (Gl[r] - Gl[q]);
+                    const float up = ex2_approx((q <= r ? gd : -gd) * kLog2e);     // r(the later, the earlier)
+                    const float b0 = bet[q < r ? q : r], back = u < 2 ? ick[0] : ick[1], backq = u < 2 ? icq[0] : icq[1];
+                    const float d = up * b0;
+                    x1[u][n][m] = q <= r ? x1[u][n][m] * (d * p.scale * fye * back) : 0.f;
+                    x2[u][n][m] = q >= r ? x2[u][n][m] * (d * p.scale * fye * backq) : 0.f;
+                    const float w3 = (u == rt && q > r) ? x4[n][m] : x3[u][n][m];
+                    x3[u][n][m] = q != r ? -w3 * (d * fwe * back) : 0.f;
+                    m1 = fmaxf(m1, fabsf(x1[u][n][m]));
+                    m2 = fmaxf(m2, fmaxf(fabsf(x2[u][n][m]), fabsf(x3[u][n][m])));
+                }
+        const Pow2 c1 = pow2_for(warp_max_bits(m1)), c2 = pow2_for(warp_max_bits(m2));
+        unsigned a1[4][PG][4], a2[4][PG][4], a3[4][PG][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            split_tiles<PG>(x1[u][0], x1[u][1], c1.c, a1[u]);
+            split_tiles<PG>(x2[u][0], x2[u][1], c2.c, a2[u]);
+            split_tiles<PG>(x3[u][0], x3[u][1], c2.c, a3[u]);
+        }
+        float fq[2], fw[2], fe[2];       // row factors of the products with the states
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = 16 * rt + g + 8 * r;
+            fq[r] = p.scale * gam[t] * (cY.inv * cS.inv);
+            fw[r] = -gam[t] * (cW.inv * cS.inv);
+            fe[r] = bend[t] * (cE.inv * cD.inv);
+        }
+
+        const float *S0 = p.ck + (bh * nbound + c) * p.P * p.N, *dE = p.dck + (bh * nbound + c + 1) * p.P * p.N;
+        for (int n0 = 0; n0 < NP; n0 += W) {
+            if (n0 > 0) __syncthreads();
+            // this pass's columns of the states and of k and q
+            constexpr int CN = W / 8;
+#pragma unroll 2
+            for (int i = tid; i < PW * CN; i += 128) {
+                const int r = i / CN, x = (i % CN) * 8;
+                float fs[8] = {}, fd[8] = {};
+                if (r < p.P && n0 + x < p.N) {
+                    load8(S0 + size_t(r) * p.N + n0 + x, fs);
+                    load8(dE + size_t(r) * p.N + n0 + x, fd);
+                }
+                unsigned char *at = smem + r * Cfg::NROW + x * 2;
+                put(at + Cfg::OFF_S, Cfg::ST, fs, cS.c);
+                put(at + Cfg::OFF_D, Cfg::ST, fd, cD.c);
+            }
+#pragma unroll 2
+            for (int i = tid; i < C * CN; i += 128) {
+                const int r = i / CN, x = (i % CN) * 8, half = r / kDeltaC;
+                const unsigned char *src = p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + (half < n32 ? half : 0)) * Rows::BYTES +
+                                           (r % kDeltaC) * Rows::ROW + (n0 + x) * 2;
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int y = 0; y < KP; ++y) {
+                        const uint4 w = half < n32 && n0 + x < NP
+                                            ? __ldg(reinterpret_cast<const uint4 *>(src + (m * KP + y) * Rows::PIECE))
+                                            : make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(smem + (m ? Cfg::OFF_Q : Cfg::OFF_K) + y * Cfg::KT + r * Cfg::NROW + x * 2) = w;
+                    }
+            }
+            __syncthreads();
+            const unsigned sS = smem_u32(smem + Cfg::OFF_S), sD = smem_u32(smem + Cfg::OFF_D);
+            const unsigned sk = smem_u32(smem + Cfg::OFF_K), sq = smem_u32(smem + Cfg::OFF_Q);
+            // 32 columns at a time
+#pragma unroll 1
+            for (int j0 = 0; j0 < W / 32; ++j0) {
+                float aq[4][4], ak[4][4], aw[4][4], ae[4][4], am[4][4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) { zero4(aq[n]); zero4(ak[n]); zero4(aw[n]); zero4(ae[n]); zero4(am[n]); }
+#pragma unroll
+                for (int k = 0; k < PW / 16; ++k) {
+                    unsigned ay[PG][4], aE[PG][4], aW[PG][4];
+#pragma unroll
+                    for (int i = 0; i < PG; ++i) {
+                        ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
+                        ldsm4(aE[i], se + i * Cfg::TOK + an + k * 32);
+                        ldsm4(aW[i], sw + i * Cfg::TOK + an + k * 32);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        unsigned bS[PG][4], bD[PG][4];
+                        const unsigned at = 16 * k * Cfg::NROW + bn + j0 * 64 + j * 32;
+#pragma unroll
+                        for (int i = 0; i < PG; ++i) {
+                            ldsm4_t(bS[i], sS + i * Cfg::ST + at);
+                            ldsm4_t(bD[i], sD + i * Cfg::ST + at);
+                        }
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma_pieces<PG, PG>(aq[2 * j + n], ay, bS, n);
+                            mma_pieces<PG, PG>(aw[2 * j + n], aW, bS, n);
+                            mma_pieces<PG, PG>(ae[2 * j + n], aE, bD, n);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        unsigned bK[KP][4], bQ[KP][4];
+                        const unsigned at = 16 * u * Cfg::NROW + bn + j0 * 64 + j * 32;
+#pragma unroll
+                        for (int i = 0; i < KP; ++i) ldsm4_t(bK[i], sk + i * Cfg::KT + at);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            if (u <= rt) mma_pieces<PG, KP>(ak[2 * j + n], a1[u], bK, n);
+                            mma_pieces<PG, KP>(am[2 * j + n], a3[u], bK, n);
+                        }
+                        if (u >= rt) {
+#pragma unroll
+                            for (int i = 0; i < KP; ++i) ldsm4_t(bQ[i], sq + i * Cfg::KT + at);
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) mma_pieces<PG, KP>(am[2 * j + n], a2[u], bQ, n);
+                        }
+                    }
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int t = 16 * rt + g + 8 * r, col = n0 + 32 * j0 + 8 * n + 2 * t4;
+                        if (t >= nt || col >= p.N) continue;
+                        const size_t off = k0 + size_t(t) * krow + col;
+                        float2 q, k;
+                        q.x = fmaf(c1.inv, ak[n][2 * r], fq[r] * aq[n][2 * r]);
+                        q.y = fmaf(c1.inv, ak[n][2 * r + 1], fq[r] * aq[n][2 * r + 1]);
+                        k.x = fmaf(c2.inv, am[n][2 * r], fmaf(fw[r], aw[n][2 * r], fe[r] * ae[n][2 * r]));
+                        k.y = fmaf(c2.inv, am[n][2 * r + 1], fmaf(fw[r], aw[n][2 * r + 1], fe[r] * ae[n][2 * r + 1]));
+                        float2 *pq = reinterpret_cast<float2 *>(p.part + off);
+                        float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
+                        if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
+                        if (hg + 1 < group) {
+                            *pq = q;
+                            *pk = k;
+                        } else if constexpr (sizeof(Tg) == 4) {
+                            *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
+                            *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
+                        } else {
+                            *reinterpret_cast<unsigned *>(static_cast<Tg *>(p.dq) + off) = pack_bf16x2(q.x, q.y);
+                            *reinterpret_cast<unsigned *>(static_cast<Tg *>(p.dk) + off) = pack_bf16x2(k.x, k.y);
+                        }
+                    }
+            }
+        }
+    }
 }
 
 }  // namespace ssm

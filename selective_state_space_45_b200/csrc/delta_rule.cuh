@@ -56,6 +56,10 @@ struct DeltaArgs {
     float *sum;             // backward: [slices][batch][heads][seqlen] sums over a slice's rows:
                             // dy.y; in the reverse pass e.du (the gradient of beta)
     float *zsum;            // reverse pass: [slices * warps][batch][heads][boundaries] <dS, S>
+    unsigned *smax;         // backward: [batch][heads][boundaries][slices * warps] largest |S| (reverse
+                            // pass: |dS|) of a warp's rows, as bits
+    unsigned *emax, *ymax;  // backward: [batch][heads][chunks][slices * warps] the same of e (reverse
+                            // pass: w) and, in the reverse pass, dy
     int batch, seqlen, heads, qk_heads, P, N, slices;
     float scale;
 };
@@ -763,7 +767,14 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 
         const float *one = vec + kVecScalars * C;
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
-        const Pow2 cS = pow2_for(warp_max_bits(ms));
+        const unsigned msb = warp_max_bits(ms);
+        const Pow2 cS = pow2_for(msb);
+        const size_t part = slice * NW + warp, parts = size_t(p.slices) * NW;
+        if constexpr (MODE == 1)
+            if (c % CS == 0 && lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
+        if constexpr (REV)
+            if ((c % CS == CS - 1 || c == nchunk - 1) && lane == 0)
+                p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
         Tok sk, sq;
         zero_tok(sk); zero_tok(sq);
         unsigned kb[2][KP][4], qb[2][KP][4];
@@ -839,6 +850,11 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
         }
         // The scales of x times a vector over the tokens follow from their largest magnitudes.
         const unsigned mx = max_tok(x);
+        if constexpr (MODE != 0)
+            if (lane == 0) {
+                p.emax[(size_t(bh) * nchunk + c) * parts + part] = mx;
+                if constexpr (REV) p.ymax[(size_t(bh) * nchunk + c) * parts + part] = mv;
+            }
         auto scale_by = [&](unsigned m, float most) {
             const float b = __uint_as_float(m) * most;
             return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
