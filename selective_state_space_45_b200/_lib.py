@@ -314,8 +314,8 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
 
 
 def _require(shapes):
-    """Raise ValueError unless every (name, tensor or None, shape, dtype) is given as asked:
-    the kernels read what the sizes say, so a wrong shape or dtype must not reach them.  All
+    """Raise ValueError unless every (name, tensor or None, shape, dtype) is given as asked and
+    contiguous: the kernels read what the sizes say, so nothing else must reach them.  All
     tensors have to be on one CUDA device, which is returned."""
     device = None
     for name, t, shape, dtype in shapes:
@@ -325,39 +325,47 @@ def _require(shapes):
             raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
         if t.dtype != dtype:
             raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to libssm must be contiguous (%s is not)" % name)
         if device is None:
             device = t.device
+            if device.type != "cuda":
+                raise ValueError("libssm needs CUDA tensors, got %s" % device)
         elif t.device != device:
             raise ValueError("%s is on %s, other tensors on %s" % (name, t.device, device))
-    if device.type != "cuda":
-        raise ValueError("libssm needs CUDA tensors, got %s" % device)
     return device
 
 
-class _Workspace:
-    """Scratch of one call from torch's allocator, on the stream that the call runs on (so the
-    memory is not handed out again before the call's kernels are done with it)."""
+def _dtype_code(name, t):
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be fp32 or bf16, got %s" % (name, t.dtype))
+    return code
 
-    def __init__(self, nbytes, device, stream):
-        if stream is None or stream == torch.cuda.current_stream(device).cuda_stream:
-            self.t = torch.empty(nbytes, device=device, dtype=torch.uint8)
-        else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-                self.t = torch.empty(nbytes, device=device, dtype=torch.uint8)
-        self.args = (self.t.data_ptr() if nbytes else None, nbytes)
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call_on(device, stream, name, *args, workspace=None):
-    """Run a library call with ``device`` current (its kernels and scratch live there)."""
-    if torch.cuda.current_device() != device.index:
+    """Run a library call with ``device`` current (its kernels and scratch live there).  Scratch
+    comes from torch's allocator, on the stream that the call runs on: the memory is not handed
+    out again before the call's kernels are done with it."""
+    index = device.index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(device):
             return _call_on(device, stream, name, *args, workspace=workspace)
-    lib = load_library()
-    stream = (torch.cuda.current_stream(device).cuda_stream if stream is None else
-              stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    lib = _lib or load_library()
+    here = torch._C._cuda_getCurrentRawStream(index)
+    stream = (here if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
     if workspace is not None:
-        ws = _Workspace(getattr(lib, name + "_workspace")(*workspace), device, stream)
-        args += ws.args
+        nbytes = getattr(lib, name + "_workspace")(*workspace)
+        if stream == here:
+            ws = torch.empty(nbytes, device=device, dtype=torch.uint8)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+                ws = torch.empty(nbytes, device=device, dtype=torch.uint8)
+        args += (ws.data_ptr() if nbytes else None, nbytes)
     _check(getattr(lib, name)(*args, stream))
 
 
@@ -379,17 +387,16 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
     st = (lead[0], H, P, N)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
                              ("final_state", final_state, st, torch.float32)])
-    sizes = (lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype])
-    _call_on(dev, stream, "ssm_delta_rule_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta), _ptr(y),
-             _ptr(initial_state), _ptr(final_state), float(scale), *sizes, workspace=sizes)
+    sizes = (lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("y", y))
+    _call_on(dev, stream, "ssm_delta_rule_fwd", _at(q), _at(k), _at(v), _at(a), _at(beta), _at(y),
+             _at(initial_state), _at(final_state), float(scale), *sizes, workspace=sizes)
 
 
 def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0, out_dtype=None, return_final_state=True,
                stream=None):
     """Allocate y (and the final state) with torch and run ``ssm_delta_rule_fwd``."""
-    y = torch.empty(v.shape, device=v.device, dtype=out_dtype or v.dtype)
-    fs = (torch.empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1]), device=v.device, dtype=torch.float32)
-          if return_final_state else None)
+    y = torch.empty_like(v, dtype=out_dtype)
+    fs = a.new_empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1])) if return_final_state else None
     ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state, fs, scale, stream)
     return (y, fs) if return_final_state else y
 
@@ -401,13 +408,13 @@ def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
     lead = tuple(v.shape[:2])
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
-    _call_on(dev, stream, "ssm_delta_rule_step", _ptr(state), _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
-             _ptr(y), float(scale), lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[y.dtype])
+    _call_on(dev, stream, "ssm_delta_rule_step", _at(state), _at(q), _at(k), _at(v), _at(a), _at(beta),
+             _at(y), float(scale), lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("y", y))
 
 
 def delta_rule_step(state, q, k, v, a, beta, scale=1.0, out_dtype=None, stream=None):
     """Allocate y with torch and run ``ssm_delta_rule_step``."""
-    y = torch.empty(v.shape, device=v.device, dtype=out_dtype or v.dtype)
+    y = torch.empty_like(v, dtype=out_dtype)
     ssm_delta_rule_step(state, q, k, v, a, beta, y, scale, stream)
     return y
 
@@ -424,10 +431,10 @@ def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk
         ("dfinal_state", dfinal_state, st, f32), ("dq", dq, q.shape, dy.dtype), ("dk", dk, k.shape, dy.dtype),
         ("dv", dv, v.shape, dy.dtype), ("da", da, a.shape, f32), ("dbeta", dbeta, beta.shape, f32),
         ("dinitial_state", dinitial_state, st, f32)])
-    sizes = (lead[0], lead[1], H, K, P, N, _DTYPE_CODE[v.dtype], _DTYPE_CODE[dy.dtype])
-    _call_on(dev, stream, "ssm_delta_rule_bwd", _ptr(q), _ptr(k), _ptr(v), _ptr(a), _ptr(beta),
-             _ptr(initial_state), _ptr(dy), _ptr(dfinal_state), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(da), _ptr(dbeta),
-             _ptr(dinitial_state), float(scale), *sizes, workspace=sizes)
+    sizes = (lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("dy", dy))
+    _call_on(dev, stream, "ssm_delta_rule_bwd", _at(q), _at(k), _at(v), _at(a), _at(beta),
+             _at(initial_state), _at(dy), _at(dfinal_state), _at(dq), _at(dk), _at(dv), _at(da), _at(dbeta),
+             _at(dinitial_state), float(scale), *sizes, workspace=sizes)
 
 
 def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, scale=1.0, stream=None):
@@ -447,16 +454,18 @@ def ssm_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, strea
     dim, f32 = x.shape[-1], torch.float32
     dev = _require([("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32), ("bias", bias, (dim,), f32),
                     ("y", y, x.shape, y.dtype), ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32)])
-    _call_on(dev, stream, "ssm_layer_norm_fwd", _ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean),
-             _ptr(rstd), float(eps), x.numel() // dim if dim else 0, dim, _DTYPE_CODE[x.dtype], _DTYPE_CODE[y.dtype])
+    _call_on(dev, stream, "ssm_layer_norm_fwd", _at(x), _at(weight), _at(bias), _at(y), _at(mean),
+             _at(rstd), float(eps), x.numel() // dim if dim else 0, dim, _dtype_code("x", x), _dtype_code("y", y))
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats=False, stream=None):
     """Allocate y (and mean, rstd) with torch and run the layer norm; returns y, or (y, mean,
     rstd) for the backward."""
-    y = torch.empty(x.shape, device=x.device, dtype=out_dtype or x.dtype)
-    mean, rstd = ((torch.empty(x.shape[:-1], device=x.device, dtype=torch.float32) for _ in range(2))
-                  if return_stats else (None, None))
+    y = torch.empty_like(x, dtype=out_dtype)
+    mean, rstd = None, None
+    if return_stats:
+        mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     ssm_layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, stream)
     return (y, mean, rstd) if return_stats else y
 
@@ -469,15 +478,15 @@ def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, 
                     ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32),
                     ("dx", dx, x.shape, dy.dtype), ("dweight", dweight, (dim,), f32), ("dbias", dbias, (dim,), f32)])
     rows = x.numel() // dim if dim else 0
-    _call_on(dev, stream, "ssm_layer_norm_bwd", _ptr(dy), _ptr(x), _ptr(weight), _ptr(mean), _ptr(rstd),
-             _ptr(dx), _ptr(dweight), _ptr(dbias), rows, dim, _DTYPE_CODE[x.dtype], _DTYPE_CODE[dy.dtype],
+    _call_on(dev, stream, "ssm_layer_norm_bwd", _at(dy), _at(x), _at(weight), _at(mean), _at(rstd),
+             _at(dx), _at(dweight), _at(dbias), rows, dim, _dtype_code("x", x), _dtype_code("dy", dy),
              workspace=(rows, dim))
 
 
 def layer_norm_bwd(dy, x, weight, mean, rstd, stream=None):
     """Allocate the gradients with torch and run ``ssm_layer_norm_bwd``; returns a dict dx
     (dy's dtype), dweight, dbias (fp32)."""
-    g = dict(dx=torch.empty_like(dy), dweight=torch.empty(x.shape[-1], device=x.device, dtype=torch.float32),
-             dbias=torch.empty(x.shape[-1], device=x.device, dtype=torch.float32))
+    dw = x.new_empty(x.shape[-1:], dtype=torch.float32)
+    g = dict(dx=torch.empty_like(dy), dweight=dw, dbias=torch.empty_like(dw))
     ssm_layer_norm_bwd(dy, x, weight, mean, rstd, g["dx"], g["dweight"], g["dbias"], stream)
     return g

@@ -59,11 +59,12 @@ template <int NP_, int PW_, int KP_, typename Tin_, typename Tg_> struct GradCfg
     static constexpr int OFF_S = OFF_W + PG * TOK, OFF_D = OFF_S + PG * ST;
     static constexpr int OFF_K = OFF_D + PG * ST, OFF_Q = OFF_K + KP * KT;
     static constexpr int OFF_VEC = OFF_Q + KP * KT;
-    static constexpr int SMEM_BYTES = OFF_VEC + 8 * kGradC * 4;
+    static constexpr int SMEM_BYTES = OFF_VEC + 6 * kGradC * 4 + 16;
+    static constexpr int CTAS = PG == 1 ? 3 : 1;      // per SM: more, smaller ones hide the loads better
 };
 
 template <class Cfg>
-__global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) {
+__global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaGradArgs p) {
     using Tin = typename Cfg::Tin;
     using Tg = typename Cfg::Tg;
     constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W;
@@ -72,6 +73,7 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
     unsigned char *smem = delta_smem;
     float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
     float *bend = bet + C, *dtok = bend + C;
+    double *half = reinterpret_cast<double *>(dtok + C);
     const int tid = threadIdx.x, lane = tid & 31, rt = tid >> 5, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
     const int c = int(blockIdx.x % unsigned(nchunk)), bk = int(blockIdx.x / unsigned(nchunk));
@@ -98,17 +100,31 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
         const int h = hk * group + hg;
         const size_t bh = size_t(b) * p.heads + h;
         const size_t v0 = (size_t(b) * p.seqlen + t0) * vrow + size_t(h) * p.P;
-        // scales: the largest magnitudes over the rows' warps (and the chunk's halves)
-        auto most = [&](const unsigned *m, size_t first, int n) {
-            unsigned x = 0;
-            for (int i = lane; i < n; i += 32) x = max(x, m[first + i]);
-            return pow2_for(__reduce_max_sync(0xffffffffu, x));
-        };
-        const Pow2 cS = most(p.smax, (bh * nbound + c) * p.zparts, p.zparts);
-        const Pow2 cD = most(p.dsmax, (bh * nbound + c + 1) * p.zparts, p.zparts);
-        const Pow2 cE = most(p.emax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
-        const Pow2 cW = most(p.wmax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
-        const Pow2 cY = most(p.ymax, (bh * nck + c32) * p.zparts, n32 * p.zparts);
+        // scales: the largest magnitudes over the rows' warps (and the chunk's halves); at most
+        // 8 and 16 values each
+        auto max_at = [&](const unsigned *m, size_t first, int n) { return lane < n ? __ldg(m + first + lane) : 0u; };
+        unsigned big[5] = {max_at(p.smax, (bh * nbound + c) * p.zparts, p.zparts),
+                           max_at(p.dsmax, (bh * nbound + c + 1) * p.zparts, p.zparts),
+                           max_at(p.emax, (bh * nck + c32) * p.zparts, n32 * p.zparts),
+                           max_at(p.wmax, (bh * nck + c32) * p.zparts, n32 * p.zparts),
+                           max_at(p.ymax, (bh * nck + c32) * p.zparts, n32 * p.zparts)};
+        // threads 0..63: their token's gates and sums
+        const size_t gate = (size_t(b) * p.seqlen + t0 + (tid & 63)) * p.heads + h;
+        float av = 0.f, bv = 0.f, dyy = 0.f, db = 0.f, z = 0.f;
+        const bool front = 2 * tid < nt;
+        if (tid < nt) {
+            av = fmaxf(p.a[gate], -1e4f);
+            bv = p.beta[gate];
+            for (int s = 0; s < p.slices; ++s) {
+                const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
+                dyy += p.dyy[x];
+                db += p.edu[x];
+            }
+            for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
+        }
+#pragma unroll
+        for (int x = 0; x < 5; ++x) big[x] = __reduce_max_sync(0xffffffffu, big[x]);
+        const Pow2 cS = pow2_for(big[0]), cD = pow2_for(big[1]), cE = pow2_for(big[2]), cW = pow2_for(big[3]), cY = pow2_for(big[4]);
         __syncthreads();                 // the last head's tiles and vectors are done with
 
         // dy, e and w as operands [token][headdim]; v.w on the way
@@ -124,7 +140,7 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
                 *reinterpret_cast<uint4 *>(at + i * piece) = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
         };
         constexpr int CP = PW / 8;       // lanes per row: 8 or 16, so a row stays within a warp
-#pragma unroll 2
+#pragma unroll (PG == 1 ? 4 : 2)
         for (int i = tid; i < C * CP; i += 128) {
             const int r = i / CP, x = (i % CP) * 8;
             const bool ok = r < nt && x < p.P;
@@ -147,51 +163,28 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
             for (int o = 1; o < CP; o <<= 1) vw += __shfl_xor_sync(0xffffffffu, vw, o);
             if (i % CP == 0) dtok[r] = vw;
         }
-        // decays: prefix sums of a as a pair of floats (a below -1e4 counts as -1e4: its
-        // exponential is 0 either way, and the sums stay finite)
+        // decays: prefix sums of a in 64 bits, kept as pairs of floats (a below -1e4 counts as
+        // -1e4: its exponential is 0 either way, and the sums stay finite)
+        double G = av;
         if (tid < C) {
-            const size_t at = (size_t(b) * p.seqlen + t0 + tid) * p.heads + h;
-            Gh[tid] = tid < nt ? fmaxf(p.a[at], -1e4f) : 0.f;
-            bet[tid] = tid < nt ? p.beta[at] : 0.f;
-        }
-        __syncthreads();
-        double G = 0.0, Gend = 0.0;
-        if (tid < C)
-            for (int x = 0; x < C; ++x) {
-                const double av = Gh[x];
-                Gend += av;
-                if (x <= tid) G += av;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const double u = __shfl_up_sync(0xffffffffu, G, o);
+                if (lane >= o) G += u;
             }
-        float dt = 0.f;
-        if (tid < nt) {
-            const size_t at = (size_t(b) * p.seqlen + t0 + tid) * p.heads + h;
-            float db = 0.f;
-            dt = -dtok[tid];
-            for (int s = 0; s < p.slices; ++s) {
-                const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                dt += p.dyy[x];
-                db += p.edu[x];
-            }
-            p.dbeta[at] = db;
+            if (lane == 31) half[tid >> 5] = G;
         }
         __syncthreads();
         if (tid < C) {
+            const double Gend = half[0] + half[1];
+            if (tid >= 32) G += half[0];
             Gh[tid] = float(G);
             Gl[tid] = float(G - double(float(G)));
             gam[tid] = expf(float(G));
-            bend[tid] = bet[tid] * expf(float(Gend - G));
-            dtok[tid] = dt;
+            bet[tid] = bv;
+            bend[tid] = bv * expf(float(Gend - G));
+            dtok[tid] = dyy - dtok[tid];
         }
-        __syncthreads();
-        if (tid < nt) {
-            float z = 0.f;
-            const bool front = 2 * tid < nt;
-            for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
-            if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
-            else for (int x = nt - 1; x >= tid; --x) z += dtok[x];
-            p.da[(size_t(b) * p.seqlen + t0 + tid) * p.heads + h] = z;
-        }
-
         // The token-by-token matrices of this warp's rows, in four tiles of 16 columns.
         const unsigned sy = smem_u32(smem + Cfg::OFF_Y), se = smem_u32(smem + Cfg::OFF_E), sw = smem_u32(smem + Cfg::OFF_W);
         float x1[4][2][4], x2[4][2][4], x3[4][2][4], x4[2][4];   // dy e^T; e dy^T; w e^T, e w^T past the diagonal; e w^T on it
@@ -237,6 +230,7 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
                 }
             }
         }
+        __syncthreads();
         // times the decays, beta and the scales taken back out: M1 / ck for dq; M1^T scale / cq
         // and -(M2 + M2^T) / ck for dk
         float m1 = 0.f, m2 = 0.f;
@@ -281,7 +275,7 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
             if (n0 > 0) __syncthreads();
             // this pass's columns of the states and of k and q
             constexpr int CN = W / 8;
-#pragma unroll 2
+#pragma unroll (PG == 1 ? 4 : 2)
             for (int i = tid; i < PW * CN; i += 128) {
                 const int r = i / CN, x = (i % CN) * 8;
                 float fs[8] = {}, fd[8] = {};
@@ -293,7 +287,7 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
                 put(at + Cfg::OFF_S, Cfg::ST, fs, cS.c);
                 put(at + Cfg::OFF_D, Cfg::ST, fd, cD.c);
             }
-#pragma unroll 2
+#pragma unroll (PG == 1 ? 4 : 2)
             for (int i = tid; i < C * CN; i += 128) {
                 const int r = i / CN, x = (i % CN) * 8, half = r / kDeltaC;
                 const unsigned char *src = p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + (half < n32 ? half : 0)) * Rows::BYTES +
@@ -390,6 +384,12 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
                         }
                     }
             }
+        }
+        if (tid < nt) {
+            if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
+            else for (int x = nt - 1; x >= tid; --x) z += dtok[x];
+            p.da[gate] = z;
+            p.dbeta[gate] = db;
         }
     }
 }
