@@ -9,6 +9,10 @@ from .oracle import (  # noqa: F401
     build,
     causal_conv1d,
     conv1d_step,
+    delta_rule,
+    delta_rule_bwd,
+    layer_norm,
+    layer_norm_bwd,
     lti_conv,
     lti_kernel,
     scan,

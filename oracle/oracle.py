@@ -31,6 +31,9 @@ Functions and the passages they follow:
 ``causal_conv1d`` / ``conv1d_step``  the causal depthwise convolution with SiLU in front of
                               the scan, and its one-token window form: learnllm "Module 19",
                               "The Causal Convolution"; xmarva lesson 10, sections 4 and 7.
+``delta_rule`` / ``delta_rule_bwd``  the gated delta rule token by token and its adjoint: the
+                              state-space dual's loop with the delta correction.
+``layer_norm`` / ``layer_norm_bwd``  the norm around a mixer, from its definition.
 ``lti_kernel`` / ``lti_conv`` the convolutional face of a time-invariant SSM,
                               K = (C Bbar, C Abar Bbar, C Abar^2 Bbar, ...), y = K * x:
                               learnllm "Two Faces: Recurrent = Convolutional".
@@ -374,3 +377,90 @@ def lti_conv(abar, bbar, c, x):
         for i in range(t + 1):
             y[t] += K[i] * x[t - i]
     return y
+
+
+# ---- gated delta rule ------------------------------------------------------------------
+
+
+def _heads(t, heads):
+    """[..., qk_heads, N] -> [..., heads, N]: head h reads key head h // (heads // qk_heads)."""
+    return np.repeat(t, heads // t.shape[-2], axis=-2)
+
+
+def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0):
+    """The gated delta rule token by token in fp64: per sequence and head
+    S' = exp(a_t) S, e_t = v_t - S' k_t, S = S' + beta_t e_t k_t^T, y_t = scale S q_t.
+    q, k [b, L, qk_heads, N]; v [b, L, heads, P]; a, beta [b, L, heads]; S [b, heads, P, N].
+    Returns y and the final state."""
+    q, k, v, a, beta = (_f64(t) for t in (q, k, v, a, beta))
+    b, L, H, P = v.shape
+    q, k = _heads(q, H), _heads(k, H)
+    S = np.zeros((b, H, P, k.shape[-1])) if initial_state is None else _f64(initial_state).copy()
+    y = np.empty_like(v)
+    for t in range(L):
+        S = S * np.exp(a[:, t])[..., None, None]
+        e = v[:, t] - np.einsum("bhpn,bhn->bhp", S, k[:, t])
+        S = S + (beta[:, t][..., None] * e)[..., None] * k[:, t][..., None, :]
+        y[:, t] = scale * np.einsum("bhpn,bhn->bhp", S, q[:, t])
+    return y, S
+
+
+def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, scale=1.0):
+    """Reverse-mode adjoint of delta_rule for the loss sum dy y + sum dfinal S_L; a dict dq, dk
+    (summed over the heads of a key head), dv, da, dbeta, dinitial_state."""
+    dy, q, k, v, a, beta = (_f64(t) for t in (dy, q, k, v, a, beta))
+    b, L, H, P = v.shape
+    K, N = q.shape[2:]
+    q, k = _heads(q, H), _heads(k, H)
+    S = np.zeros((b, H, P, N)) if initial_state is None else _f64(initial_state).copy()
+    decayed, errors = [], []
+    for t in range(L):
+        S = S * np.exp(a[:, t])[..., None, None]
+        e = v[:, t] - np.einsum("bhpn,bhn->bhp", S, k[:, t])
+        decayed.append(S)
+        errors.append(e)
+        S = S + (beta[:, t][..., None] * e)[..., None] * k[:, t][..., None, :]
+    mu = np.zeros((b, H, P, N)) if dfinal_state is None else _f64(dfinal_state).copy()
+    dq, dk, dv = np.empty((b, L, H, N)), np.empty((b, L, H, N)), np.empty_like(v)
+    da, dbeta = np.empty_like(a), np.empty_like(beta)
+    for t in reversed(range(L)):
+        u = beta[:, t][..., None] * errors[t]
+        St = decayed[t] + u[..., None] * k[:, t][..., None, :]
+        dq[:, t] = scale * np.einsum("bhpn,bhp->bhn", St, dy[:, t])
+        lam = mu + scale * dy[:, t][..., None] * q[:, t][..., None, :]
+        lk = np.einsum("bhpn,bhn->bhp", lam, k[:, t])
+        dbeta[:, t] = (lk * errors[t]).sum(-1)
+        dv[:, t] = beta[:, t][..., None] * lk
+        dk[:, t] = np.einsum("bhpn,bhp->bhn", lam, u) - np.einsum("bhpn,bhp->bhn", decayed[t], dv[:, t])
+        lam = lam - dv[:, t][..., None] * k[:, t][..., None, :]
+        da[:, t] = (lam * decayed[t]).sum((-1, -2))
+        mu = np.exp(a[:, t])[..., None, None] * lam
+    g = H // K
+    return dict(dq=dq.reshape(b, L, K, g, N).sum(3), dk=dk.reshape(b, L, K, g, N).sum(3), dv=dv, da=da, dbeta=dbeta,
+                dinitial_state=mu)
+
+
+# ---- layer norm --------------------------------------------------------------------------
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """Layer norm of the last dimension in fp64: y, mean, rstd."""
+    x = _f64(x)
+    mean = x.mean(-1)
+    rstd = 1 / np.sqrt(((x - mean[..., None]) ** 2).mean(-1) + eps)
+    y = (x - mean[..., None]) * rstd[..., None]
+    if weight is not None:
+        y = y * _f64(weight)
+    if bias is not None:
+        y = y + _f64(bias)
+    return y, mean, rstd
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd):
+    """Gradients of layer_norm with the given statistics: dx, dweight, dbias."""
+    dy, x, mean, rstd = (_f64(t) for t in (dy, x, mean, rstd))
+    h = (x - mean[..., None]) * rstd[..., None]
+    g = dy if weight is None else dy * _f64(weight)
+    dx = rstd[..., None] * (g - g.mean(-1, keepdims=True) - h * (g * h).mean(-1, keepdims=True))
+    rows = tuple(range(x.ndim - 1))
+    return dx, (dy * h).sum(rows), dy.sum(rows)

@@ -369,9 +369,13 @@ def _call_on(device, stream, name, *args, workspace=None):
     _check(getattr(lib, name)(*args, stream))
 
 
-def _delta_shapes(lead, q, k, v, a, beta):
-    if q.dim() != 4 or v.dim() != 4:
+def _delta_dims(q, k, v):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must have four dimensions")
+
+
+def _delta_shapes(lead, q, k, v, a, beta):
+    _delta_dims(q, k, v)
     (H, P), (K, N) = v.shape[2:], q.shape[2:]
     return H, K, P, N, [("q", q, (*lead, K, N), v.dtype), ("k", k, (*lead, K, N), v.dtype),
                         ("v", v, (*lead, H, P), v.dtype), ("a", a, (*lead, H), torch.float32),
@@ -382,7 +386,7 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
     """Gated delta rule over whole sequences (see include/ssm.h): q, k [batch, L, qk_heads, N];
     v, y [batch, L, heads, P]; a, beta [batch, L, heads] fp32; states [batch, heads, P, N] fp32.
     Writes y and final_state in place."""
-    lead = tuple(v.shape[:2])
+    lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     st = (lead[0], H, P, N)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
@@ -395,6 +399,7 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
 def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0, out_dtype=None, return_final_state=True,
                stream=None):
     """Allocate y (and the final state) with torch and run ``ssm_delta_rule_fwd``."""
+    _delta_dims(q, k, v)
     y = torch.empty_like(v, dtype=out_dtype)
     fs = a.new_empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1])) if return_final_state else None
     ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state, fs, scale, stream)
@@ -405,7 +410,7 @@ def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
     """Decode tokens of the gated delta rule (see include/ssm.h): state [batch, heads, P, N]
     fp32 updated in place; q, k [ntok, batch, qk_heads, N]; v, y [ntok, batch, heads, P]; a,
     beta [ntok, batch, heads] fp32."""
-    lead = tuple(v.shape[:2])
+    lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     dev = _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
     _call_on(dev, stream, "ssm_delta_rule_step", _at(state), _at(q), _at(k), _at(v), _at(a), _at(beta),
@@ -423,7 +428,7 @@ def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk
                        dinitial_state=None, scale=1.0, stream=None):
     """Backward of the gated delta rule (see include/ssm.h).  dq, dk, dv share dy's dtype; da,
     dbeta, dinitial_state are fp32.  Writes the gradients in place."""
-    lead = tuple(v.shape[:2])
+    lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     st, f32 = (lead[0], H, P, N), torch.float32
     dev = _require(shapes + [

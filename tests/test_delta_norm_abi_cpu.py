@@ -1,0 +1,161 @@
+"""Host-side checks of the delta rule's and the layer norm's entry points: what is refused,
+with which status, before anything is launched (fake device addresses, no GPU)."""
+import pytest
+import torch
+
+import selective_state_space_45_b200 as ssm
+from selective_state_space_45_b200 import build as ssm_build
+
+INV, UNS, ALI, SCR, OK = (ssm.SSM_ERR_INVALID_ARG, ssm.SSM_ERR_UNSUPPORTED, ssm.SSM_ERR_ALIGNMENT, ssm.SSM_ERR_SCRATCH,
+                          ssm.SSM_OK)
+# distinct fake buffers, 16 MiB apart
+BUF = [0x7F0000000000 + k * (1 << 24) for k in range(20)]
+Q, KK, V, A, B, Y, H0, H1, DY, DF, DQ, DK, DV, DA, DB, DH, WS = BUF[:17]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ssm_build.build()
+    return ssm.load_library()
+
+
+SIZES = dict(batch=2, L=8, H=4, K=2, P=64, N=128, din=ssm.SSM_BF16, dout=ssm.SSM_BF16)
+
+
+def _sizes(a):
+    return [a[n] for n in ("batch", "L", "H", "K", "P", "N", "din", "dout")]
+
+
+def fwd(lib, **kw):
+    a = dict(q=Q, k=KK, v=V, a=A, beta=B, y=Y, h0=H0, h1=H1, ws=WS, nws=1 << 23, **SIZES)
+    a.update(kw)
+    return lib.ssm_delta_rule_fwd(*[a[n] for n in ("q", "k", "v", "a", "beta", "y", "h0", "h1")], 1.0, *_sizes(a),
+                                  a["ws"], a["nws"], None)
+
+
+def step(lib, **kw):
+    a = dict(state=H0, q=Q, k=KK, v=V, a=A, beta=B, y=Y, **SIZES)
+    a.update(kw)
+    s = _sizes(a)
+    return lib.ssm_delta_rule_step(*[a[n] for n in ("state", "q", "k", "v", "a", "beta", "y")], 1.0, s[1], s[0], *s[2:],
+                                   None)
+
+
+def bwd(lib, **kw):
+    a = dict(q=Q, k=KK, v=V, a=A, beta=B, h0=H0, dy=DY, df=DF, dq=DQ, dk=DK, dv=DV, da=DA, db=DB, dh=DH, ws=WS,
+             nws=1 << 23, **SIZES)
+    a.update(kw)
+    return lib.ssm_delta_rule_bwd(*[a[n] for n in ("q", "k", "v", "a", "beta", "h0", "dy", "df", "dq", "dk", "dv", "da",
+                                                   "db", "dh")], 1.0, *_sizes(a), a["ws"], a["nws"], None)
+
+
+SIZE_REFUSALS = [
+    (dict(batch=-1), INV), (dict(L=-1), INV), (dict(H=-4), INV), (dict(K=-2), INV),
+    (dict(H=4, K=3), INV), (dict(H=2, K=4), INV), (dict(K=0), INV),          # key heads that do not divide the heads
+    (dict(P=0), INV), (dict(N=0), INV), (dict(P=12), UNS), (dict(N=20), UNS), (dict(P=136), UNS), (dict(N=256), UNS),
+    (dict(din=2), INV), (dict(dout=-1), INV),
+]
+
+
+@pytest.mark.parametrize("kw,status", SIZE_REFUSALS)
+def test_sizes_are_refused_alike(lib, kw, status):
+    assert fwd(lib, **kw) == status
+    assert step(lib, **kw) == status
+    assert bwd(lib, **kw) == status
+    s = _sizes({**SIZES, **kw})
+    assert lib.ssm_delta_rule_fwd_workspace(*s) == 0 and lib.ssm_delta_rule_bwd_workspace(*s) == 0
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(a=None), INV), (dict(beta=None), INV),
+    (dict(y=None), INV), (dict(q=Q + 8), ALI), (dict(h0=H0 + 4), ALI), (dict(h1=H1 + 8), ALI), (dict(ws=WS + 8), ALI),
+    (dict(y=V), INV), (dict(y=H0), INV), (dict(h1=KK), INV), (dict(h1=H0 + 64), INV),      # overlaps
+    (dict(ws=Y), INV), (dict(ws=Q + 16), INV), (dict(ws=H1), INV),
+    (dict(nws=64), SCR),
+    (dict(batch=0), OK), (dict(H=0, K=0), OK), (dict(L=0, h1=None), OK), (dict(L=0, h0=H1), OK),
+])
+def test_forward_refusals(lib, kw, status):
+    assert fwd(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(state=None), INV), (dict(q=None), INV), (dict(y=None), INV), (dict(state=H0 + 4), ALI), (dict(a=A + 4), ALI),
+    (dict(y=H0), INV), (dict(state=V), INV), (dict(y=B), INV), (dict(L=0, state=None), OK), (dict(batch=0), OK),
+])
+def test_step_refusals(lib, kw, status):
+    assert step(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), INV), (dict(dq=None), INV), (dict(dk=None), INV), (dict(dv=None), INV), (dict(da=None), INV),
+    (dict(db=None), INV), (dict(q=None), INV), (dict(beta=None), INV), (dict(dy=DY + 2), ALI), (dict(dh=DH + 4), ALI),
+    (dict(dv=DY), INV), (dict(dq=DK), INV), (dict(da=DB), INV), (dict(dh=DF), INV), (dict(ws=DQ), INV), (dict(ws=DY), INV),
+    (dict(ws=WS + 8), ALI), (dict(nws=1024), SCR), (dict(batch=0), OK), (dict(L=0, dh=None), OK),
+])
+def test_backward_refusals(lib, kw, status):
+    assert bwd(lib, **kw) == status
+
+
+def ln_fwd(lib, **kw):
+    a = dict(x=Q, w=A, b=B, y=Y, mean=DA, rstd=DB, eps=1e-5, rows=8, dim=64, din=ssm.SSM_BF16, dout=ssm.SSM_F32)
+    a.update(kw)
+    return lib.ssm_layer_norm_fwd(*[a[n] for n in ("x", "w", "b", "y", "mean", "rstd", "eps", "rows", "dim", "din", "dout")],
+                                  None)
+
+
+def ln_bwd(lib, **kw):
+    a = dict(dy=DY, x=Q, w=A, mean=DA, rstd=DB, dx=DQ, dw=DK, db=DV, rows=8, dim=64, din=ssm.SSM_BF16, dout=ssm.SSM_F32,
+             ws=WS, nws=1 << 20)
+    a.update(kw)
+    return lib.ssm_layer_norm_bwd(*[a[n] for n in ("dy", "x", "w", "mean", "rstd", "dx", "dw", "db", "rows", "dim", "din",
+                                                   "dout", "ws", "nws")], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), INV), (dict(dim=0), INV), (dict(dim=8193), UNS), (dict(din=5), INV), (dict(dout=2), INV),
+])
+def test_norm_sizes_are_refused_alike(lib, kw, status):
+    assert ln_fwd(lib, **kw) == status
+    assert ln_bwd(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(x=None), INV), (dict(y=None), INV), (dict(eps=-1e-5), INV), (dict(eps=float("nan")), INV), (dict(x=Q + 2), ALI),
+    (dict(w=A + 4), ALI), (dict(mean=DA + 4), ALI), (dict(y=Q), INV), (dict(mean=DB), INV), (dict(rstd=A), INV),
+    (dict(rows=0, x=None, y=None), OK),
+])
+def test_norm_forward_refusals(lib, kw, status):
+    assert ln_fwd(lib, **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dy=None), INV), (dict(x=None), INV), (dict(mean=None), INV), (dict(rstd=None), INV), (dict(dx=None), INV),
+    (dict(dx=DY), INV), (dict(dw=A), INV), (dict(dw=DV), INV), (dict(ws=DQ), INV), (dict(ws=Q), INV), (dict(dx=DQ + 4), ALI),
+    (dict(ws=WS + 4), ALI), (dict(nws=16), SCR),
+])
+def test_norm_backward_refusals(lib, kw, status):
+    assert ln_bwd(lib, **kw) == status
+
+
+def test_binding_refuses_before_the_library():
+    """Wrong shapes, dtypes, strides and devices raise ValueError in the binding."""
+    def t(*s, dtype=torch.float32):
+        return torch.zeros(s, dtype=dtype)
+
+    good = dict(q=t(1, 4, 2, 8), k=t(1, 4, 2, 8), v=t(1, 4, 2, 8), a=t(1, 4, 2), beta=t(1, 4, 2))
+    for name, bad in (("k", t(1, 4, 2, 16)), ("a", t(1, 4, 2, dtype=torch.bfloat16)), ("beta", t(1, 3, 2)),
+                      ("q", t(1, 4, 2, 8, dtype=torch.bfloat16)), ("v", t(4, 2, 8)), ("k", t(1, 4, 8, 2).transpose(2, 3))):
+        with pytest.raises(ValueError):
+            ssm.delta_rule(**{**good, name: bad})
+    with pytest.raises(ValueError, match="CUDA"):
+        ssm.delta_rule(**good)
+    with pytest.raises(ValueError):
+        ssm.delta_rule_step(t(2, 2, 8, 8), **good)               # a state of another batch
+    with pytest.raises(ValueError):
+        ssm.delta_rule_bwd(t(1, 4, 2, 16), **good)
+    x = t(4, 8)
+    for args in ((x, t(7)), (x, t(8, dtype=torch.bfloat16)), (x.t(), t(4))):
+        with pytest.raises(ValueError):
+            ssm.layer_norm(*args)
+    with pytest.raises(ValueError):
+        ssm.layer_norm_bwd(x, x, None, t(3), t(4))

@@ -1,0 +1,390 @@
+"""GPU parity of the gated delta rule (forward, decode tokens, backward) with the fp64 oracle.
+
+Bounds, derived before the first run (per output tensor, M = max|ref|, u(t) = half a step):
+  * fp32 outputs that follow the state (final state, fp32 y, da, dbeta, start-state and fp32
+    gradients): every product takes operands in two fp16 pieces, off by at most 2^-22 of an
+    element, and sums up to 128 terms in fp32 accumulators that cut off (2^-23 a step).  Cut
+    off sums of n terms are off by at most n 2^-23 of their size, sqrt(n)-like for mixed
+    signs; with the chunk's three chained products (R, T R, update) 3 * 128 * 2^-23 = 2^-14.4
+    at worst.  Relative L2 error <= 2^-15 and |err| <= 2^-13 M.
+  * a bf16 y: u = 2^-8 of the value, and behind it one fp16 piece per operand (2^-12 each, two
+    operands): |err| <= 2^-8 |ref| + 2^-10 M.  bf16 dq, dk chain two such products (four
+    roundings): 2^-8 |ref| + 2^-9 M.  bf16 dv is an fp32 value rounded: 2^-8 |ref| + 2^-13 M.
+  * decode tokens are fp32 arithmetic throughout: sums of 128 terms, 128 * 2^-24 = 2^-17 at
+    worst per token: |err| <= 2^-16 M (+ u |ref|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import selective_state_space_45_b200 as ssm
+from tests.helpers import to64
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def make(b, L, H, K, P, N, dtype=BF16, seed=0, state=True, decay=0.3):
+    g = torch.Generator().manual_seed(seed)
+    q, k = (torch.randn(b, L, K, N, generator=g) for _ in range(2))
+    d = dict(q=(q / q.norm(dim=-1, keepdim=True)).to(dtype), k=(k / k.norm(dim=-1, keepdim=True)).to(dtype),
+             v=torch.randn(b, L, H, P, generator=g).to(dtype), a=-decay * torch.rand(b, L, H, generator=g),
+             beta=torch.rand(b, L, H, generator=g))
+    d["initial_state"] = 0.5 * torch.randn(b, H, P, N, generator=g) if state else None
+    return {n: None if t is None else t.to(DEV) for n, t in d.items()}
+
+
+def close(got, ref, what, elem, of_max, l2=None):
+    g, r = to64(got), np.asarray(ref)
+    assert g.shape == r.shape, what
+    assert np.isfinite(g).all(), what
+    if not r.size:
+        return
+    err, M = np.abs(g - r), np.abs(r).max()
+    assert (err <= elem * np.abs(r) + of_max * M + 1e-30).all(), (what, float(err.max()), float(M))
+    if l2 is not None:
+        assert np.linalg.norm(g - r) <= l2 * np.linalg.norm(r) + 1e-30, (what, np.linalg.norm(g - r) / np.linalg.norm(r))
+
+
+def close_state(got, ref, what):
+    close(got, ref, what, 0, 2.0 ** -13, 2.0 ** -15)
+
+
+def close_y(got, ref, what="y"):
+    if got.dtype == F32:
+        close_state(got, ref, what)
+    else:
+        close(got, ref, what, 2.0 ** -8, 2.0 ** -10)
+
+
+def run_and_check(d, out_dtype, scale=0.7):
+    y, S = ssm.delta_rule(**d, scale=scale, out_dtype=out_dtype)
+    yr, Sr = oracle.delta_rule(**d, scale=scale)
+    close_y(y, yr)
+    close_state(S, Sr, "final state")
+    assert ssm.ssm_device_timeouts() == 0
+    return y, S
+
+
+SHAPES = [  # batch, L, heads, key heads, headdim, dstate
+    (1, 1, 1, 1, 8, 8), (2, 2, 2, 1, 16, 24), (1, 31, 3, 3, 24, 32), (2, 32, 4, 2, 64, 64), (1, 33, 4, 1, 32, 128),
+    (1, 64, 2, 2, 128, 128), (2, 65, 6, 2, 96, 96), (1, 97, 2, 2, 72, 104), (3, 130, 2, 1, 64, 40), (1, 257, 3, 3, 120, 72),
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_forward(cuda_lib, shape, dtype, out):
+    run_and_check(make(*shape, dtype=dtype, seed=sum(shape), state=shape[1] % 2 == 1), out)
+
+
+def test_forward_many_chunks_long_memory(cuda_lib):
+    """1500 tokens whose decay keeps most of the state: errors must not pile up."""
+    run_and_check(make(1, 1500, 2, 1, 32, 64, dtype=F32, seed=4, decay=1e-3), F32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_hard_gates(cuda_lib, dtype):
+    """Full resets (-inf), no decay, growth, steps of 0, 1 and 2, repeated and zero keys."""
+    d = make(2, 75, 3, 3, 40, 48, dtype=dtype, seed=9)
+    d["a"][:, 10] = d["a"][:, 40, 1] = -float("inf")
+    d["a"][:, 20:24] = 0
+    d["a"][:, 50] = 0.4
+    d["a"][:, 60:62] = -1e30
+    d["beta"][:, 5:8] = 0
+    d["beta"][:, 30] = 1
+    d["beta"][:, 33] = 2
+    d["k"][:, 41:46] = d["k"][:, 41:42]
+    d["k"][:, 52] = 0
+    d["q"][:, 53] = 0
+    run_and_check(d, F32)
+
+
+@pytest.mark.parametrize("kv,st", [(1e8, 1e8), (1e-9, 1e-9), (1e-20, 0.0), (3e4, 1.0)])
+def test_forward_any_magnitude(cuda_lib, kv, st):
+    """The fp16 operands are scaled: values far outside fp16's range keep their digits."""
+    d = make(1, 70, 2, 2, 32, 32, dtype=F32, seed=11)
+    d["v"] *= kv
+    d["initial_state"] *= st
+    run_and_check(d, F32)
+
+
+def test_forward_any_key_magnitude(cuda_lib):
+    """Keys of length 1e-6 and 300, the step scaled so that the recurrence stays stable."""
+    for s in (1e-6, 300.0):
+        d = make(1, 70, 2, 2, 32, 32, dtype=F32, seed=12)
+        d["k"] *= s
+        d["q"] *= s
+        d["beta"] = d["beta"] / s ** 2
+        d["initial_state"] = d["initial_state"] / s
+        run_and_check(d, F32, scale=1.0)
+
+
+def test_forward_continues(cuda_lib):
+    """A sequence in two calls is the sequence in one, also with the state carried in place."""
+    d = make(2, 150, 4, 2, 64, 128, seed=5)
+    y, S = ssm.delta_rule(**d, out_dtype=F32)
+    cut = {n: d[n][:, :70].contiguous() for n in ("q", "k", "v", "a", "beta")}
+    rest = {n: d[n][:, 70:].contiguous() for n in ("q", "k", "v", "a", "beta")}
+    state = d["initial_state"].clone()
+    for part, at in ((cut, slice(0, 70)), (rest, slice(70, 150))):
+        yp = torch.empty_like(part["v"], dtype=F32)
+        ssm.ssm_delta_rule_fwd(**part, y=yp, initial_state=state, final_state=state)
+        close_state(yp, to64(y[:, at]), "y of the part")
+    close_state(state, to64(S), "carried state")
+
+
+def test_forward_writes_nothing_else(cuda_lib):
+    """Guards around y and the final state, a ragged length, and a NaN workspace."""
+    d = make(1, 45, 2, 1, 40, 24, seed=6)
+    y = torch.full((45 * 2 * 40 + 256,), 7.0, device=DEV, dtype=BF16)
+    S = torch.full((2 * 40 * 24 + 128,), 7.0, device=DEV)
+    sizes = (1, 45, 2, 1, 40, 24, ssm.SSM_BF16, ssm.SSM_BF16)
+    n = ssm.load_library().ssm_delta_rule_fwd_workspace(*sizes)
+    ws = torch.full((n // 4 + 64,), float("nan"), device=DEV)
+    st = ssm.load_library().ssm_delta_rule_fwd(
+        *[d[x].data_ptr() for x in ("q", "k", "v", "a", "beta")], y.data_ptr(), d["initial_state"].data_ptr(), S.data_ptr(),
+        1.0, *sizes, ws.data_ptr(), n, torch.cuda.current_stream().cuda_stream)
+    assert st == ssm.SSM_OK
+    yr, Sr = oracle.delta_rule(**d)
+    close_y(y[:3600].reshape(yr.shape), yr)
+    close_state(S[:1920].reshape(Sr.shape), Sr, "final state")
+    assert bool((y[3600:] == 7).all()) and bool((S[1920:] == 7).all()) and bool(ws[(n + 3) // 4:].isnan().all())
+
+
+def test_without_workspace_or_final_state(cuda_lib):
+    d = make(1, 40, 2, 2, 16, 16, seed=8)
+    y = torch.empty_like(d["v"])
+    sizes = (1, 40, 2, 2, 16, 16, ssm.SSM_BF16, ssm.SSM_BF16)
+    st = ssm.load_library().ssm_delta_rule_fwd(
+        *[d[x].data_ptr() for x in ("q", "k", "v", "a", "beta")], y.data_ptr(), d["initial_state"].data_ptr(), None, 1.0,
+        *sizes, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == ssm.SSM_OK
+    close_y(y, oracle.delta_rule(**d)[0])
+
+
+def test_no_tokens(cuda_lib):
+    d = make(2, 0, 2, 2, 16, 16)
+    y, S = ssm.delta_rule(**d)
+    assert y.numel() == 0 and torch.equal(S, d["initial_state"])
+    _, S = ssm.delta_rule(**{**d, "initial_state": None})
+    assert not S.any()
+    dS = torch.randn_like(S)
+    g = ssm.delta_rule_bwd(y, **d, dfinal_state=dS)
+    assert torch.equal(g["dinitial_state"], dS)
+
+
+# ---- decode tokens --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 8, 8), (1, 3, 4, 2, 24, 32), (4, 2, 6, 3, 64, 128), (3, 5, 2, 2, 128, 64),
+                                   (7, 33, 3, 1, 40, 96), (2, 2, 2, 2, 16, 104)], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_step(cuda_lib, shape, dtype, out):
+    ntok, batch, H, K, P, N = shape
+    d = make(batch, ntok, H, K, P, N, dtype=dtype, seed=sum(shape))
+    state = d.pop("initial_state")
+    yr, Sr = oracle.delta_rule(**d, initial_state=state, scale=0.3)
+    t = {n: x.transpose(0, 1).contiguous() for n, x in d.items()}
+    one = state.clone()
+    y = ssm.delta_rule_step(state, **t, scale=0.3, out_dtype=out)
+    elem = 2.0 ** -8 if out == BF16 else 0
+    close(y.transpose(0, 1), yr, "y", elem, ntok * 2.0 ** -16)
+    close(state, Sr, "state", 0, ntok * 2.0 ** -16)
+    # token by token: the same bits (copies: a token's slice need not start on 16 bytes)
+    for i in range(ntok):
+        yi = ssm.delta_rule_step(one, **{n: x[i:i + 1].clone() for n, x in t.items()}, scale=0.3, out_dtype=out)
+        assert torch.equal(yi[0], y[i])
+    assert torch.equal(one, state)
+
+
+def test_prefill_then_decode(cuda_lib):
+    """The forward's final state carried through decode tokens is the longer sequence."""
+    d = make(2, 60, 4, 2, 64, 128, seed=3, state=False)
+    yr, Sr = oracle.delta_rule(**d)
+    head = {n: d[n][:, :50].contiguous() for n in ("q", "k", "v", "a", "beta")}
+    _, state = ssm.delta_rule(**head)
+    tail = {n: d[n][:, 50:].transpose(0, 1).contiguous() for n in ("q", "k", "v", "a", "beta")}
+    y = ssm.delta_rule_step(state, **tail, out_dtype=F32)
+    close_state(y.transpose(0, 1), yr[:, 50:], "decoded y")
+    close_state(state, Sr, "state")
+
+
+# ---- backward ---------------------------------------------------------------------------
+
+
+def check_bwd(d, grad_dtype, seed=0, dfinal=True, scale=0.7, of_max=1.0):
+    g = torch.Generator().manual_seed(seed)
+    dy = torch.randn(d["v"].shape, generator=g).to(DEV).to(grad_dtype)
+    b, _, H, P = d["v"].shape
+    dS = torch.randn(b, H, P, d["k"].shape[-1], generator=g).to(DEV) if dfinal else None
+    got = ssm.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=scale)
+    ref = oracle.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=scale)
+    for n in ("da", "dbeta"):
+        close(got[n], ref[n], n, 0, of_max * 2.0 ** -13, 2.0 ** -14)
+    if d["initial_state"] is not None:
+        close_state(got["dinitial_state"], ref["dinitial_state"], "dinitial_state")
+    else:
+        assert got["dinitial_state"] is None
+    for n in ("dq", "dk", "dv"):
+        assert got[n].dtype == grad_dtype
+        if grad_dtype == F32:
+            close(got[n], ref[n], n, 0, 2.0 ** -13, 2.0 ** -14)
+        else:
+            close(got[n], ref[n], n, 2.0 ** -8, 2.0 ** -13 if n == "dv" else 2.0 ** -9)
+    assert ssm.ssm_device_timeouts() == 0
+    return dy, dS, got
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_backward(cuda_lib, shape, dtype, grad):
+    check_bwd(make(*shape, dtype=dtype, seed=sum(shape), state=shape[1] % 2 == 1), grad, seed=1, dfinal=shape[1] % 3 != 0)
+
+
+def test_backward_long_memory(cuda_lib):
+    check_bwd(make(1, 700, 2, 1, 32, 64, dtype=F32, seed=4, decay=1e-3), F32)
+
+
+def test_backward_hard_gates(cuda_lib):
+    """beta = 0 (its gradient still counts what would have been written), -inf resets (nothing
+    flows past them), repeated and zero keys."""
+    d = make(2, 139, 3, 3, 40, 48, dtype=F32, seed=9)
+    d["a"][:, 10] = d["a"][:, 64] = -float("inf")
+    d["a"][:, 100, 1] = -1e30
+    d["a"][:, 20:24] = 0
+    d["beta"][:, 5:8] = 0
+    d["beta"][:, 30] = 1
+    d["k"][:, 41:46] = d["k"][:, 41:42]
+    d["k"][:, 52] = 0
+    _, _, g = check_bwd(d, F32, seed=2)
+    assert float(g["dbeta"][:, 5:8].abs().max()) > 0
+
+
+def test_backward_tiny_gradients(cuda_lib):
+    """Gradients of 1e-9, as behind a mean over a large batch: the scaled operands keep them."""
+    d = make(1, 90, 2, 2, 64, 64, seed=13)
+    dy, _, g = check_bwd(d, BF16, seed=3, dfinal=False)
+    small = ssm.delta_rule_bwd((dy.float() * 2.0 ** -30).to(BF16), **d, scale=0.7)
+    for n in ("dq", "dk", "dv", "da", "dbeta"):
+        assert torch.equal(small[n].float() * 2.0 ** 30, g[n].float()), n    # powers of two: the same digits
+
+
+def test_backward_by_differences(cuda_lib):
+    """Directional derivatives of the GPU's own fp32 forward against its gradients."""
+    d = make(1, 40, 2, 1, 16, 16, dtype=F32, seed=21)
+    dy, dS, g = check_bwd(d, F32, seed=4)
+    w = {n: torch.randn(t.shape, generator=torch.Generator().manual_seed(5)).to(DEV) for n, t in d.items()}
+
+    def loss(h):
+        y, S = ssm.delta_rule(**{n: t + h * w[n] for n, t in d.items()}, scale=0.7)
+        return float((dy.double() * y.double()).sum() + (dS.double() * S.double()).sum())
+
+    want = sum(float((g["d" + n].double() * w[n].double()).sum()) for n in d)
+    # central difference: h^2 f''' / 6 (h = 2^-7: 1e-5 of third derivatives of order 10 want) and
+    # fp32 noise of y, 2^-15 of the summands' size, over 2h
+    h = 2.0 ** -7
+    noise = 2.0 ** -15 * float(dy.double().norm() * 3) / (2 * h)
+    assert abs((loss(h) - loss(-h)) / (2 * h) - want) <= 2e-3 * abs(want) + noise + 0.05
+
+
+def test_results_do_not_vary(cuda_lib):
+    d = make(3, 333, 6, 3, 64, 128, seed=7)
+    dy = torch.randn(d["v"].shape, device=DEV).to(BF16)
+    y, S = ssm.delta_rule(**d)
+    g = ssm.delta_rule_bwd(dy, **d)
+    for _ in range(3):
+        y2, S2 = ssm.delta_rule(**d)
+        g2 = ssm.delta_rule_bwd(dy, **d)
+        assert torch.equal(y, y2) and torch.equal(S, S2)
+        assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
+# ---- streams and graphs --------------------------------------------------------------------
+
+
+def test_two_streams_at_once(cuda_lib):
+    ds = [make(2, 200, 4, 2, 64, 64, seed=30 + i) for i in range(2)]
+    want = [ssm.delta_rule(**d) for d in ds]
+    dy = torch.ones_like(ds[0]["v"])
+    wantg = [ssm.delta_rule_bwd(dy, **d) for d in ds]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((ssm.delta_rule(**ds[i]), ssm.delta_rule_bwd(dy, **ds[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (y, S), g in got[i]:
+            assert torch.equal(y, want[i][0]) and torch.equal(S, want[i][1])
+            assert all(torch.equal(g[n], wantg[i][n]) for n in g)
+
+
+def test_stream_argument(cuda_lib):
+    """The call runs, scratch included, on the stream that it is given."""
+    d = make(1, 120, 2, 2, 64, 64, seed=40)
+    want, _ = ssm.delta_rule(**d)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    y, S = torch.empty_like(d["v"]), torch.empty_like(d["initial_state"])
+    ssm.ssm_delta_rule_fwd(**{n: d[n] for n in ("q", "k", "v", "a", "beta")}, y=y, initial_state=d["initial_state"],
+                           final_state=S, stream=s)
+    s.synchronize()
+    assert torch.equal(y, want)
+
+
+def test_captured_and_replayed(cuda_lib):
+    """Forward, backward and decode tokens in two graphs, replayed in turn on new inputs."""
+    d = make(2, 100, 4, 2, 64, 64, seed=50)
+    dy = torch.randn(d["v"].shape, device=DEV).to(BF16)
+    state = torch.zeros(2, 4, 64, 64, device=DEV)
+    t = {n: d[n][:, :2].transpose(0, 1).contiguous() for n in ("q", "k", "v", "a", "beta")}
+
+    def all_calls():
+        return ssm.delta_rule(**d), ssm.delta_rule_bwd(dy, **d), ssm.delta_rule_step(state, **t)
+
+    all_calls()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(all_calls())
+        graphs.append(g)
+    for i in range(4):
+        new = make(2, 100, 4, 2, 64, 64, seed=60 + i)
+        for n in ("q", "k", "v", "a", "beta", "initial_state"):
+            d[n].copy_(new[n])
+        state.zero_()
+        graphs[i % 2].replay()
+        (y, S), g, ys = (x for x in outs[i % 2])
+        got = [y.clone(), S.clone(), *(g[n].clone() for n in sorted(g)), ys.clone(), state.clone()]
+        state.zero_()
+        (y, S), g, ys = all_calls()
+        want = [y, S, *(g[n] for n in sorted(g)), ys, state]
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del graphs
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """More than 2^31 values (2^32 bytes) before the last sequence's rows."""
+    b, L, H, P, N = 65, 4096, 64, 128, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    v = torch.zeros(b, L, H, P, device=DEV, dtype=BF16)
+    assert v.numel() > 2 ** 31
+    q, k = (torch.zeros(b, L, 1, N, device=DEV, dtype=BF16) for _ in range(2))
+    a, beta = torch.zeros(b, L, H, device=DEV), torch.zeros(b, L, H, device=DEV)
+    last = make(1, 64, H, 1, P, N, seed=2)
+    for t, n in ((v, "v"), (q, "q"), (k, "k"), (a, "a"), (beta, "beta")):
+        t[-1, -64:] = last[n][0]
+    y, S = ssm.delta_rule(q, k, v, a, beta)
+    yr, Sr = oracle.delta_rule(**{n: last[n] for n in ("q", "k", "v", "a", "beta")})
+    close_y(y[-1:, -64:], yr)
+    close_state(S[-1:], Sr, "final state")
+    assert not y[0].any()
+    del g
