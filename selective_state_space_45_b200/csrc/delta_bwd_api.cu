@@ -34,7 +34,7 @@ struct BwdParts {
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
-        const size_t sum = size_t(delta_slices(P)) * tok * 4, state = bh * nbound * P * N * 4;
+        const size_t sum = size_t(delta_slices(P)) * kDeltaWarps * tok * 4, state = bh * nbound * P * N * 4;
         size_t at = 0;
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         add(prep, prep_bytes<Block>(batch, seqlen, heads));
@@ -85,12 +85,11 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
         st = dispatch_chain<KP, Tg, Tg, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
-        const int slices = delta_slices(f.P);
         const ssm::DeltaGradArgs g{v, dy, f.a, f.beta, part(at.e), w, f.rows, f.prep, Block::BYTES, part(at.ck),
                                    part(at.dck), part(at.dyy), part(at.edu), part(at.zsum), bits(at.smax),
                                    bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
-                                   da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N, slices,
-                                   slices * kDeltaWarps, f.scale};
+                                   da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N,
+                                   delta_slices(f.P) * kDeltaWarps, f.scale};
         st = f.P <= 64 ? dispatch_grad<64, Tin, Tg>(g, s) : dispatch_grad<128, Tin, Tg>(g, s);
     }
     return ws.release(st);

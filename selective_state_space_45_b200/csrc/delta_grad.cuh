@@ -34,14 +34,14 @@ struct DeltaGradArgs {
     const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
     size_t block;                      // bytes of a chunk block
     const float *ck, *dck;             // states and their gradients at the boundaries
-    const float *dyy, *edu;            // [slices][batch][heads][seqlen]
+    const float *dyy, *edu;            // [zparts][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
     const unsigned *smax, *dsmax;      // [batch][heads][boundaries][zparts]
     const unsigned *emax, *wmax, *ymax;// [batch][heads][chunks of 32][zparts]
     float *part;                       // heads that share a key head: running sums of dq, dk, [2][tokens][qk_heads][N]
     void *dq, *dk;
     float *da, *dbeta;
-    int batch, seqlen, heads, qk_heads, P, N, slices, zparts;
+    int batch, seqlen, heads, qk_heads, P, N, zparts;
     float scale;
 };
 
@@ -115,11 +115,13 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
         if (tid < nt) {
             av = fmaxf(p.a[gate], -1e4f);
             bv = p.beta[gate];
-            for (int s = 0; s < p.slices; ++s) {
+#pragma unroll 4
+            for (int s = 0; s < p.zparts; ++s) {
                 const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
                 dyy += p.dyy[x];
                 db += p.edu[x];
             }
+#pragma unroll 4
             for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
         }
 #pragma unroll

@@ -14,9 +14,12 @@
 // the state enters each product as a register operand and no step of the chain goes through
 // shared memory or waits for another warp.  What depends on k, q, a and beta alone (T, Pm and
 // the decays) is formed for all chunks in parallel by delta_prep_kernel, one warp per chunk,
-// which also lays the chunk's k and q out as the chains' operands; the chains read both back
-// with two bulk copies a chunk (cp.async.bulk, one chunk ahead).  Copying and converting the
-// rows in the chains instead cost 1100 of 3700 cycles a chunk.
+// which also lays the chunk's k and q out as the chains' operands.  The warps of a CTA take
+// turns at starting the copies of the next chunk (cp.async.bulk, cp.async for the rows of v,
+// which one bulk copy each would take 70 cycles to start; two stages, mbarriers both ways) and
+// otherwise wait for data only, never for each other.  Copying and converting the
+// rows in the chains instead cost 1100 of 3700 cycles a chunk; a fifth warp for the copies
+// costs the others the registers that they need (168 instead of 255: spills).
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
 //     w = T^T (beta (end (dS k) + Pm^T dO)) = dv,  dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
@@ -53,13 +56,13 @@ struct DeltaArgs {
     float *ck;              // backward: the state at every boundary of 64 tokens and at the end,
                             // [batch][heads][boundaries][headdim][dstate]
     float *dck;             // reverse pass: its gradient there
-    float *sum;             // backward: [slices][batch][heads][seqlen] sums over a slice's rows:
-                            // dy.y; in the reverse pass e.du (the gradient of beta)
+    float *sum;             // backward: [slices * warps][batch][heads][seqlen] sums over a warp's
+                            // rows: dy.y; in the reverse pass e.du (the gradient of beta)
     float *zsum;            // reverse pass: [slices * warps][batch][heads][boundaries] <dS, S>
     unsigned *smax;         // backward: [batch][heads][boundaries][slices * warps] largest |S| (reverse
                             // pass: |dS|) of a warp's rows, as bits
-    unsigned *emax, *ymax;  // backward: [batch][heads][chunks][slices * warps] the same of e (reverse
-                            // pass: w) and, in the reverse pass, dy
+    unsigned *emax, *ymax;  // backward: [batch][heads][chunks][slices * warps] bounds of |e| (reverse
+                            // pass: |w|) and, in the reverse pass, the largest |dy|
     int batch, seqlen, heads, qk_heads, P, N, slices;
     float scale;
 };
@@ -110,6 +113,7 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     using Tv2 = Tv2_;      // MODE 1: dy
     using Tout = Tout_;
     static constexpr int C = kDeltaC, NT = 32 * NW;
+    static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
     static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
     static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 2 : 1;         // pieces behind y
     using Block = DeltaBlock<PO, MODE != 0>;
@@ -121,12 +125,11 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int PIECE = Rows::PIECE;
     static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
     static constexpr int OFF_V = OFF_TRI + BLOCK, OFF_V2 = OFF_V + C * VROW;
-    static constexpr int STAGE = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);        // two stages
-    static constexpr int OFF_BAR = 2 * STAGE;                                 // their mbarriers
-    static constexpr int OFF_OUT = OFF_BAR + 16;                              // per-warp output tiles
-    static constexpr int OFF_RED = OFF_OUT + NW * 16 * kOutRow;               // 2 buffers of token sums
-    static constexpr int REDBUF = MODE != 0 ? NW * C * 4 : 0;
-    static constexpr int OFF_ST = OFF_RED + 2 * REDBUF;                       // reverse pass: kept states
+    static constexpr int STAGE = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);
+    static constexpr int STAGES = MODE == 0 && KP == 1 ? 3 : 2;               // three where two CTAs still fit
+    static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
+    static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
+    static constexpr int OFF_ST = OFF_OUT + NW * 16 * kOutRow;                // reverse pass: kept states
     static constexpr int STROW = NP * 4 + 16;
     static constexpr int SMEM_BYTES = OFF_ST + (MODE == 2 ? NW * 16 * STROW : 0);
 };
@@ -557,7 +560,7 @@ __device__ __forceinline__ void scale_tok(Tok &out, const Tok &x, const float *f
 }
 
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p) {
+__global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const DeltaArgs p) {
     using Tv = typename Cfg::Tv;
     using Tv2 = typename Cfg::Tv2;
     using Tout = typename Cfg::Tout;
@@ -574,65 +577,61 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
     // chunk of loop step i: forwards, or backwards in the reverse pass
     auto chunk_of = [&](int i) { return REV ? nchunk - 1 - i : i; };
 
-    // Loop step i's data: two bulk copies by one thread on the stage's mbarrier, and the rows of
-    // v by every thread (cp.async).
     const int hk = h / (p.heads / p.qk_heads), prow = p.P - slice * NW * 16;
     const size_t vrow = size_t(p.heads) * p.P;
-    const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR);
+    const int active = min(NW, (prow + 15) / 16);          // warps with rows
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR), *empty = full + Cfg::STAGES;
     if (tid == 0) {
-        mbar_init(&full[0], 1);
-        mbar_init(&full[1], 1);
+        for (int i = 0; i < Cfg::STAGES; ++i) {
+            mbar_init(&full[i], 1 + 32);                   // the bulk copies, a warp of cp.async
+            mbar_init(&empty[i], active);
+        }
         mbar_fence_init();
     }
     __syncthreads();
-    auto copy_v = [&](unsigned dst, int rowbytes, const auto *src, int left) {
-        using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
-        constexpr int E = 16 / sizeof(T), CR = NW * 16 / E, STEP = Cfg::NT / CR;     // copies per row, rows per round
-        const int r0 = tid / CR, n = (tid % CR) * E, rows = n < prow ? left - r0 : 0;
-        const T *at = src + r0 * vrow + n;
-#pragma unroll
-        for (int i = 0; i < C / STEP; ++i) {
-            cp_async_16z(dst + (r0 + i * STEP) * rowbytes + n * int(sizeof(T)), i * STEP < rows ? at : src, i * STEP < rows);
-            at += STEP * vrow;
-        }
-    };
-    auto issue = [&](int i) {
-        if (i < nchunk) {
-            const int c = chunk_of(i), left = p.seqlen - c * C;
-            unsigned char *st = smem + (i & 1) * Cfg::STAGE;
-            if (tid == 0) {
-                mbar_arrive_expect_tx(&full[i & 1], Cfg::Rows::BYTES + Cfg::BLOCK);
-                bulk_load(st, p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Cfg::Rows::BYTES, Cfg::Rows::BYTES,
-                          &full[i & 1]);
-                bulk_load(st + Cfg::OFF_TRI, p.prep + (size_t(bh) * nchunk + c) * Block::BYTES, Cfg::BLOCK, &full[i & 1]);
-            }
-            const size_t vat = voff + size_t(c) * C * vrow;
-            copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + vat, left);
-            if constexpr (MODE == 1) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + vat, left);
-        }
-        cp_async_commit();
-    };
-    // Step i's data are here, for every thread after the barrier that follows.
+    // a bounded wait; after one that gave up the results are void and nothing waits any more
     bool alive = true;
-    auto arrive = [&](int i) {
-        cp_async_wait<0>();
-        if (alive && !mbar_wait(&full[i & 1], uint32_t(i >> 1) & 1, kDeltaWaitCycles)) {
+    auto wait = [&](uint64_t *bar, int parity) {
+        if (!mbar_test(bar, uint32_t(parity) & 1) && alive && !mbar_wait(bar, uint32_t(parity) & 1, kDeltaWaitCycles)) {
             alive = false;
             atomicAdd(p.timeouts, 1u);
         }
     };
-    // The sums over the warps' rows of loop step i, left in shared memory at its end.
-    auto flush_sums = [&](int i) {
-        const int t = chunk_of(i) * C + lane;
-        if (t >= p.seqlen) return;
-        const float *red = reinterpret_cast<const float *>(smem + Cfg::OFF_RED + (i & 1) * Cfg::REDBUF);
-        float x = 0.f;
+
+    // Start the copies of loop step i into its stage, once the warps are done with what is there:
+    // lane 0 the operands and the block, all lanes the rows of v (of dy too in MODE 1), zeros
+    // past the end and past headdim.
+    const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
+    auto copy_v = [&](unsigned dst, int rowbytes, const auto *src, int ntok) {
+        using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
+        constexpr int E = 16 / sizeof(T), CR = NW * 16 / E, STEP = 32 / CR;          // copies per row, rows per round
+        const int r0 = lane / CR, n = (lane % CR) * E, rows = n < prow ? ntok - r0 : 0;
+        const T *at = src + r0 * vrow + n;
+        dst += r0 * rowbytes + n * int(sizeof(T));
 #pragma unroll
-        for (int w = 0; w < NW; ++w) x += red[w * C + lane];
-        p.sum[(size_t(slice) * p.batch * p.heads + bh) * p.seqlen + t] = x;
+        for (int i = 0; i < C / STEP; ++i) {
+            cp_async_16z(dst + i * STEP * rowbytes, i * STEP < rows ? at : src, i * STEP < rows);
+            at += STEP * vrow;
+        }
     };
-    issue(0);
+    auto issue = [&](int i) {
+        const int c = chunk_of(i), ntok = min(C, p.seqlen - c * C), slot = i % Cfg::STAGES;
+        unsigned char *st = smem + slot * Cfg::STAGE;
+        if (i >= Cfg::STAGES) wait(&empty[slot], i / Cfg::STAGES - 1);
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&full[slot], Cfg::Rows::BYTES + Cfg::BLOCK);
+            bulk_load(st, p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Cfg::Rows::BYTES, Cfg::Rows::BYTES,
+                      &full[slot]);
+            bulk_load(st + Cfg::OFF_TRI, p.prep + (size_t(bh) * nchunk + c) * Block::BYTES, Cfg::BLOCK, &full[slot]);
+        }
+        __syncwarp();
+        const size_t at = voff + size_t(c) * C * vrow;
+        copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + at, ntok);
+        if constexpr (MODE == 1) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
+        mbar_arrive_cp_async(&full[slot]);
+    };
+    if (warp == 0)
+        for (int i = 0; i + 1 < Cfg::STAGES && i < nchunk; ++i) issue(i);
 
     const int g = lane >> 2, t4 = lane & 3;
     const int p0 = slice * NW * 16 + warp * 16;           // the warp's first row
@@ -674,7 +673,9 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             cp_async_16z(smem_u32(strow + r * Cfg::STROW + n * 4), base + (ok ? size_t(p0 + r) * p.N + n : 0), ok);
         }
     };
-    auto dot_state = [&](int x) {                          // after the wait for the fetch
+    auto dot_state = [&](int x) {
+        cp_async_wait<0>();
+        __syncwarp();
         float z0 = 0.f, z1 = 0.f;
 #pragma unroll
         for (int j = 0; j < NP / 8; ++j)
@@ -691,9 +692,9 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = z0;
         __syncwarp();
     };
-    // sums over the warp's 16 rows of f[row][token], for flush_sums to add up
-    auto token_sums = [&](const Tok &f, int buf) {
-        float *red = reinterpret_cast<float *>(smem + Cfg::OFF_RED + buf * Cfg::REDBUF) + warp * C;
+    // sums over the warp's 16 rows of f[row][token], tokens from t0 on
+    auto token_sums = [&](const Tok &f, int t0) {
+        float *out = p.sum + (size_t(slice * NW + warp) * p.batch * p.heads + bh) * p.seqlen;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             float u = f[n][0] + f[n][2], w = f[n][1] + f[n][3];
@@ -702,31 +703,25 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 u += __shfl_xor_sync(0xffffffffu, u, o);
                 w += __shfl_xor_sync(0xffffffffu, w, o);
             }
-            if (g == 0) *reinterpret_cast<float2 *>(red + 8 * n + 2 * t4) = make_float2(u, w);
+            const int t = t0 + 8 * n + 2 * t4;
+            if (g == 0 && t < p.seqlen) out[t] = u;
+            if (g == 0 && t + 1 < p.seqlen) out[t + 1] = w;
         }
     };
-    if (nrow <= 0) {                                       // rows past headdim: only copies and barriers
-        if constexpr (MODE != 0) {
-            const Tok zero = {};
-            token_sums(zero, 0);
-            token_sums(zero, 1);
-        }
+    if (nrow <= 0) {                                       // rows past headdim
+        if constexpr (MODE != 0)
+            for (int t = lane; t < p.seqlen; t += 32)
+                p.sum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
         if constexpr (REV)
             for (int x = lane; x < nbound; x += 32)
                 p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = 0.f;
-        for (int i = 0; i < nchunk; ++i) {
-            arrive(i);
-            __syncthreads();
-            issue(i + 1);
-        }
-        if constexpr (MODE != 0) __syncthreads();
         return;
     }
     if constexpr (REV) {
         fetch_state(nbound - 1);
         cp_async_commit();
     }
-
+    int turn = warp + 1;                                   // loop steps until it is this warp's to start copies
     // the largest magnitude of the state, kept up with its updates
     float ms = 0.f;
 #pragma unroll
@@ -736,13 +731,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 
     for (int i = 0; i < nchunk; ++i) {
         const int c = chunk_of(i);
-        arrive(i);
-        __syncthreads();
         constexpr int CS = kDeltaSave / C;
-        const unsigned char *stage = smem + (i & 1) * Cfg::STAGE;
-        const float *vec = reinterpret_cast<const float *>(stage + Cfg::OFF_TRI + Block::OFF_VEC);
-        const unsigned kbase = smem_u32(stage + Cfg::OFF_K), qbase = smem_u32(stage + Cfg::OFF_Q);
-        const unsigned tbase = smem_u32(stage + Cfg::OFF_TRI) + tr;
         const size_t tok0 = (size_t(b) * p.seqlen + size_t(c) * C) * p.heads + h;
         const int ntok = min(C, p.seqlen - c * C);
         Tok er;
@@ -760,11 +749,18 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 keep_state(p.dck, c / CS + 1);
                 dot_state(c / CS + 1);
             }
-            if (c % CS == 0) fetch_state(c / CS);          // in the commit group of issue()
+            if (c % CS == 0) {
+                fetch_state(c / CS);
+                cp_async_commit();
+            }
         }
-        issue(i + 1);
-        if constexpr (MODE != 0) if (i > 0 && warp == 0) flush_sums(i - 1);
 
+        const int slot = i % Cfg::STAGES;
+        wait(&full[slot], i / Cfg::STAGES);
+        const unsigned char *stage = smem + slot * Cfg::STAGE;
+        const float *vec = reinterpret_cast<const float *>(stage + Cfg::OFF_TRI + Block::OFF_VEC);
+        const unsigned kbase = smem_u32(stage + Cfg::OFF_K), qbase = smem_u32(stage + Cfg::OFF_Q);
+        const unsigned tbase = smem_u32(stage + Cfg::OFF_TRI) + tr;
         const float *one = vec + kVecScalars * C;
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
         const unsigned msb = warp_max_bits(ms);
@@ -808,6 +804,12 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 }
             if (j + 1 < NP / 16) load_kq(j + 1);
         }
+        // By now the other warps have left the stage that comes next (or soon will): the one whose
+        // turn it is starts the copies into it.
+        if (--turn == 0) {
+            turn = active;
+            if (i + Cfg::STAGES - 1 < nchunk) issue(i + Cfg::STAGES - 1);
+        }
         Tok v, x, du;
         load_tok<Tv>(stage + Cfg::OFF_V + warp * 16 * int(sizeof(Tv)), Cfg::VROW, lane, v);
         unsigned mv = 0;                                   // reverse pass: largest |dO|
@@ -835,10 +837,12 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv, sk[n][m], f * lo[n][m]);
             scale_tok(x, du, vec + kVecBeta * C, t4);
         }
+        unsigned mr = 0;
         {   // e = R + (T - I) R, or w with the transpose
             unsigned A[2][2][4];
             Tok d;
-            const Pow2 cx = pow2_for(max_tok(x));
+            mr = max_tok(x);
+            const Pow2 cx = pow2_for(mr);
             split_tok<2>(x, cx.c, A);
             zero_tok(d);
             mma_triangle<2, 2, REV>(d, A, tbase);
@@ -848,8 +852,11 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) x[n][m] = fmaf(f, d[n][m], x[n][m]);
         }
-        // The scales of x times a vector over the tokens follow from their largest magnitudes.
-        const unsigned mx = max_tok(x);
+        // The scales of what x is multiplied with next follow from bounds: x grew by at most 31
+        // entries of T - I, each below 2^14 / its scale (five bits more than it takes, of the 24
+        // and more between fp16's largest and smallest steps).
+        const float grown = __uint_as_float(mr) * fmaf(31.f * 16384.f, one[kInvT], 1.f);
+        const unsigned mx = __float_as_uint(isfinite(grown) ? grown : 0.f);
         if constexpr (MODE != 0)
             if (lane == 0) {
                 p.emax[(size_t(bh) * nchunk + c) * parts + part] = mx;
@@ -933,7 +940,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
-                token_sums(dy, i & 1);
+                token_sums(dy, c * C);
             }
         } else {
             // du = rhs - (n / beta)^T w, the gradient of beta e: with e it gives beta's
@@ -948,15 +955,12 @@ __global__ void __launch_bounds__(Cfg::NT) delta_chain_kernel(const DeltaArgs p)
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] = er[n][m] * fmaf(f, d[n][m], du[n][m]);
-            token_sums(du, i & 1);
+            token_sums(du, c * C);
             if (p.w != nullptr) store_tok<float>(p.w + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
         }
-    }
-    if constexpr (MODE != 0) {
-        cp_async_wait<0>();
-        __syncthreads();
-        if (warp == 0) flush_sums(nchunk - 1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[slot]);         // the stage may be filled again
     }
     if constexpr (MODE == 1) keep_state(p.ck, nbound - 1);
     if constexpr (REV) dot_state(0);
