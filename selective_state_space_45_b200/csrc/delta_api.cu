@@ -22,12 +22,12 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
 
 // Forward: the chunk blocks and operands, then the chains.
 template <typename Tin, typename Tout> size_t fwd_bytes(int batch, int seqlen, int heads, int qk_heads, int N) {
-    return prep_bytes<ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1, false>>(batch, seqlen, heads) +
+    return prep_bytes<ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>>(batch, seqlen, heads) +
            rows_bytes(batch, seqlen, qk_heads, N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
 }
 
 template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *workspace, size_t bytes, cudaStream_t s) {
-    using Block = ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1, false>;
+    using Block = ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>;
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, fwd_bytes<Tin, Tout>(a.batch, a.seqlen, a.heads, a.qk_heads, a.N), s))
         return st;

@@ -26,7 +26,7 @@ template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaG
     }
 }
 
-using Block = ssm::DeltaBlock<2, true>;
+using Block = ssm::DeltaBlock<2>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {

@@ -6,13 +6,13 @@
 // Over a chunk of C tokens with start state S, r(t,s) = exp(a_{s+1} + ... + a_t),
 // gam_t = r(t, before the chunk), end_s = r(last, s):
 //     R_t = v_t - gam_t S k_t
-//     e   = T R,           T = (I + n)^-1,  n(t,s) = r(t,s) (k_t.k_s) beta_s   for s < t
+//     e   = R - G (beta R),   G = (I + A diag(beta))^-1 A,   A(t,s) = r(t,s) (k_t.k_s) for s < t
 //     y_t = scale gam_t S q_t + sum_{s<=t} Pm(t,s) beta_s e_s,  Pm(t,s) = scale r(t,s) (q_t.k_s)
 //     S  <- gam_last S + sum_s (end_s beta_s e_s) k_s^T
-// Every row of S (one value of headdim) goes through this on its own, given k, q, T and Pm,
+// Every row of S (one value of headdim) goes through this on its own, given k, q, G and Pm,
 // so a warp owns 16 rows and keeps them in registers as accumulator tiles [16 x dstate]:
 // the state enters each product as a register operand and no step of the chain goes through
-// shared memory or waits for another warp.  What depends on k, q, a and beta alone (T, Pm and
+// shared memory or waits for another warp.  What depends on k, q, a and beta alone (G, Pm and
 // the decays) is formed for all chunks in parallel by delta_prep_kernel, one warp per chunk,
 // which also lays the chunk's k and q out as the chains' operands.  The warps of a CTA take
 // turns at starting the copies of the next chunk (cp.async.bulk, cp.async for the rows of v,
@@ -22,7 +22,9 @@
 // costs the others the registers that they need (168 instead of 255: spills).
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
-//     w = T^T (beta (end (dS k) + Pm^T dO)) = dv,  dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
+//     rhs = end (dS k) + Pm^T dO,  du = rhs - G^T (beta rhs),  dv = w = beta du,  dbeta = e.du,
+//     dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
+// (G without beta in its columns keeps du, and with it dbeta, exact where beta is small or 0.)
 //
 // Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
 // operand scaled by a power of two (one per chunk for k, q and the triangles, one per warp and
@@ -77,9 +79,9 @@ constexpr int kOutRow = 48;          // bytes per row of a warp's output tile
 __device__ __forceinline__ int tri_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
 
 // What the prep kernel leaves per chunk and head.  A triangle is the three 16 x 16 tiles
-// (0,0), (1,0), (1,1) per fp16 piece, scaled by a power of two: T - I in two pieces, Pm in PP,
-// and for the reverse pass n / beta in two behind the vectors.  Vectors over the chunk's
-// tokens, the scales of k and q (ck, cq) taken back out where a product with them is used:
+// (0,0), (1,0), (1,1) per fp16 piece, scaled by a power of two: G in two pieces, Pm in PP.
+// Vectors over the chunk's tokens, the scales of k and q (ck, cq) taken back out where a
+// product with them is used:
 enum {
     kVecGk,        // gam / ck: S k -> gam S k
     kVecSgq,       // scale gam / cq
@@ -89,12 +91,10 @@ enum {
     kVecScalars,   // then the scalars below
     kVecs
 };
-enum { kGamLast, kCk, kCq, kInvT, kInvP, kInvN, kMaxBeta, kMaxEbk, kMaxGk, kMaxSgq };   // 1 / scales; largest magnitudes
-template <int PP_, bool BWD_> struct DeltaBlock {
+enum { kGamLast, kCk, kCq, kInvG, kInvP, kMaxBeta, kMaxEbk, kMaxGk, kMaxSgq };   // 1 / scales; largest magnitudes
+template <int PP_> struct DeltaBlock {
     static constexpr int PP = PP_;
-    static constexpr bool BWD = BWD_;
-    static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 3 * PP * kTri, OFF_N = OFF_VEC + kVecs * kDeltaC * 4;
-    static constexpr int BYTES = OFF_N + (BWD ? 6 * kTri : 0);
+    static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 3 * PP * kTri, BYTES = OFF_VEC + kVecs * kDeltaC * 4;
 };
 
 // k and q of a chunk as the chains read them: scaled fp16, KP pieces of k, then of q, each 32
@@ -116,15 +116,14 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
     static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
     static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 2 : 1;         // pieces behind y
-    using Block = DeltaBlock<PO, MODE != 0>;
-    static constexpr int BLOCK = MODE == 2 ? Block::BYTES : Block::OFF_N;     // the part that is read
+    using Block = DeltaBlock<PO>;
     using Rows = DeltaRows<NP, KP>;
     static constexpr int KROW = Rows::ROW;
     static constexpr int VROW = NW * 16 * int(sizeof(Tv)) + 16;
     static constexpr int V2ROW = NW * 16 * int(sizeof(Tv2)) + 16;
     static constexpr int PIECE = Rows::PIECE;
     static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
-    static constexpr int OFF_V = OFF_TRI + BLOCK, OFF_V2 = OFF_V + C * VROW;
+    static constexpr int OFF_V = OFF_TRI + Block::BYTES, OFF_V2 = OFF_V + C * VROW;
     static constexpr int STAGE = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);
     static constexpr int STAGES = MODE == 0 && KP == 1 ? 3 : 2;               // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
@@ -152,8 +151,9 @@ template <int NP, typename Tin, class Block> struct PrepScratch {
         unsigned char rows[2][kDeltaC * ROW];                   // k and q as they come
         struct {
             unsigned char block[Block::BYTES];                  // as it goes out
-            float nt[kDeltaC * NROW];                           // nt[s][t] = n(t, s)
-            float rat[kDeltaC * RATROW + 4];                    // rat[t][s + 1] = r(t, s); later T11, T22, Z
+            float at[kDeltaC * NROW];                           // at[s][t] = A(t, s)
+            float rat[kDeltaC * RATROW + 4];                    // rat[t][s + 1] = r(t, s); later parts of G
+            float beta[kDeltaC];
         };
     };
 };
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
         }
     }
     __syncwarp();                   // the rows' memory is the scratch of what follows
-    float *rat = sc.rat, *nt = sc.nt;
+    float *rat = sc.rat, *at = sc.at;
     // r(t, s): lane s + 1 adds up a from token s + 1 on (no differences of long sums, so
     // a = -inf, a full reset, is exact); lane 0 is the chunk's start
     float acc = 0.f;
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
         vec[kVecGk * C + lane] = gk;
         vec[kVecSgq * C + lane] = sgq;
         vec[kVecBeta * C + lane] = beta;
+        sc.beta[lane] = beta;
         vec[kVecEk * C + lane] = end * cs[0].inv;
         vec[kVecEbk * C + lane] = ebk;
         const float mb = max_of(beta), me = max_of(ebk), mg = max_of(gk), ms = max_of(sgq);
@@ -308,8 +309,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
             one[kMaxBeta] = mb; one[kMaxEbk] = me; one[kMaxGk] = mg; one[kMaxSgq] = ms;
         }
     }
-    // n, Pm and n / beta: the products times their decays, in place of kk (n / beta) and qk
-    float mp = 0.f, mn = 0.f;
+    // A and Pm: the products times their decays
+    float mp = 0.f;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -317,24 +318,21 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int s0 = 16 * n + 8 * i + 2 * t4;
-                const float b0 = __shfl_sync(0xffffffffu, beta, s0), b1 = __shfl_sync(0xffffffffu, beta, s0 + 1);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int t = 16 * m + 8 * r + g;
-                    float *ck = kk[2 * (m + n) + i] + 2 * r, *cq = qk[2 * (m + n) + i] + 2 * r;
+                    const float *ck = kk[2 * (m + n) + i] + 2 * r;
+                    float *cq = qk[2 * (m + n) + i] + 2 * r;
                     const float r0 = rat[t * RATROW + s0 + 1], r1 = rat[t * RATROW + s0 + 2];
-                    ck[0] = s0 < t ? ck[0] * r0 : 0.f;
-                    ck[1] = s0 + 1 < t ? ck[1] * r1 : 0.f;
-                    nt[s0 * NROW + t] = s0 < t ? ck[0] * b0 : 0.f;
-                    nt[(s0 + 1) * NROW + t] = s0 + 1 < t ? ck[1] * b1 : 0.f;
+                    at[s0 * NROW + t] = s0 < t ? ck[0] * r0 : 0.f;
+                    at[(s0 + 1) * NROW + t] = s0 + 1 < t ? ck[1] * r1 : 0.f;
                     cq[0] = s0 <= t ? cq[0] * r0 * p.scale : 0.f;
                     cq[1] = s0 + 1 <= t ? cq[1] * r1 * p.scale : 0.f;
                     mp = fmaxf(mp, fmaxf(fabsf(cq[0]), fabsf(cq[1])));
-                    mn = fmaxf(mn, fmaxf(fabsf(ck[0]), fabsf(ck[1])));
                 }
             }
-    const Pow2 sp = pow2_for(warp_max_bits(mp)), sn = pow2_for(warp_max_bits(mn));
-    if (lane == 0) { one[kInvP] = sp.inv; one[kInvN] = sn.inv; }
+    const Pow2 sp = pow2_for(warp_max_bits(mp));
+    if (lane == 0) one[kInvP] = sp.inv;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -343,88 +341,90 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float *ck = kk[2 * (m + n) + i] + 2 * r, *cq = qk[2 * (m + n) + i] + 2 * r;
-                    unsigned char *at = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
+                    const float *cq = qk[2 * (m + n) + i] + 2 * r;
+                    unsigned char *to = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
                     unsigned w[Block::PP];
                     split_f16<Block::PP>(f2(cq[0], cq[1]), sp.c, w);
 #pragma unroll
-                    for (int y = 0; y < Block::PP; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_P + 3 * y * kTri) = w[y];
-                    if constexpr (Block::BWD) {
-                        unsigned x[2];
-                        split_f16<2>(f2(ck[0], ck[1]), sn.c, x);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) *reinterpret_cast<unsigned *>(at + Block::OFF_N + 3 * y * kTri) = x[y];
-                    }
+                    for (int y = 0; y < Block::PP; ++y) *reinterpret_cast<unsigned *>(to + Block::OFF_P + 3 * y * kTri) = w[y];
                 }
     __syncwarp();
-    // T of the two diagonal tiles: lane t solves row t of T (I + n) = I from the diagonal
-    // leftwards within its tile
+    // G of the two diagonal tiles, G (I + diag(beta) A) = A: lane t solves its row from the
+    // diagonal leftwards, G(t,s) = A(t,s) - sum_{s<r<t} G(t,r) beta_r A(r,s)
     const int blk = lane >> 4, tl = lane & 15;
-    float T[16];
+    float G[16], Gb[16];                                        // G(t, .) and G(t, .) beta
     {
-        const float *nb = nt + 16 * blk * NROW + 16 * blk;
+        const float *ab = at + 16 * blk * NROW + 16 * blk;
 #pragma unroll
         for (int s = 15; s >= 0; --s) {
-            float x0 = 0.f, x1 = 0.f;
+            float x0 = ab[s * NROW + tl], x1 = 0.f;             // 0 for s >= t
 #pragma unroll
             for (int r4 = (s + 1) / 4; r4 < 4; ++r4) {
-                const float4 n4 = *reinterpret_cast<const float4 *>(nb + s * NROW + 4 * r4);
-                const float nv[4] = {n4.x, n4.y, n4.z, n4.w};
+                const float4 a4 = *reinterpret_cast<const float4 *>(ab + s * NROW + 4 * r4);
+                const float av[4] = {a4.x, a4.y, a4.z, a4.w};
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                     if (4 * r4 + m > s) {
-                        if (m & 1) x1 = fmaf(-T[4 * r4 + m], nv[m], x1);
-                        else x0 = fmaf(-T[4 * r4 + m], nv[m], x0);
+                        if (m & 1) x1 = fmaf(-Gb[4 * r4 + m], av[m], x1);
+                        else x0 = fmaf(-Gb[4 * r4 + m], av[m], x0);
                     }
             }
-            T[s] = s == tl ? 1.f : (s < tl ? x0 + x1 : 0.f);
+            G[s] = s < tl ? x0 + x1 : 0.f;
+            Gb[s] = G[s] * sc.beta[16 * blk + s];
         }
     }
-    float *Td = rat, *Z = rat + 2 * 16 * 20;                    // T11 and T22, then Z, rows of 20
+    // rows of 20: G11, then G22 beta2, then Z beta1
+    float *G1 = rat, *G2 = rat + 16 * 20, *Z = rat + 2 * 16 * 20;
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-        *reinterpret_cast<float4 *>(Td + (blk * 16 + tl) * 20 + 4 * x) = make_float4(T[4 * x], T[4 * x + 1], T[4 * x + 2], T[4 * x + 3]);
-#pragma unroll
-    for (int s = 0; s < 16; ++s) T[s] = s == tl ? 0.f : T[s];
-    __syncwarp();
-    // T21 = -T22 (n21 T11): a lane forms 8 values of row tl, columns 8 blk on
-    float z[8] = {};
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        const float n = nt[r * NROW + 16 + tl];
-        const float *tr = Td + r * 20 + 8 * blk;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) z[x] = fmaf(n, tr[x], z[x]);
+    for (int x = 0; x < 4; ++x) {
+        const float *f = blk ? Gb : G;
+        *reinterpret_cast<float4 *>((blk ? G2 : G1) + tl * 20 + 4 * x) = make_float4(f[4 * x], f[4 * x + 1], f[4 * x + 2], f[4 * x + 3]);
     }
+    __syncwarp();
+    // G21 = Z - (Z beta1) G11, Z = A21 - (G22 beta2) A21: a lane forms 8 values of row tl, columns
+    // 8 blk on
+    float z[8], y[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) z[x] = at[(8 * blk + x) * NROW + 16 + tl];
+#pragma unroll
+    for (int r4 = 0; r4 < 4; ++r4) {
+        const float4 gr = *reinterpret_cast<const float4 *>(G2 + tl * 20 + 4 * r4);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float4 a4 = *reinterpret_cast<const float4 *>(at + (8 * blk + x) * NROW + 16 + 4 * r4);
+            z[x] = fmaf(-gr.x, a4.x, fmaf(-gr.y, a4.y, fmaf(-gr.z, a4.z, fmaf(-gr.w, a4.w, z[x]))));
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) { y[x] = z[x]; z[x] *= sc.beta[8 * blk + x]; }
     *reinterpret_cast<float4 *>(Z + tl * 20 + 8 * blk) = make_float4(z[0], z[1], z[2], z[3]);
     *reinterpret_cast<float4 *>(Z + tl * 20 + 8 * blk + 4) = make_float4(z[4], z[5], z[6], z[7]);
     __syncwarp();
 #pragma unroll
-    for (int x = 0; x < 8; ++x) z[x] = 0.f;
-#pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const float t = -Td[(16 + tl) * 20 + r];
-        const float *zr = Z + r * 20 + 8 * blk;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) z[x] = fmaf(t, zr[x], z[x]);
+        const float t = -Z[tl * 20 + r];
+        const float4 lo = *reinterpret_cast<const float4 *>(G1 + r * 20 + 8 * blk);
+        const float4 hi = *reinterpret_cast<const float4 *>(G1 + r * 20 + 8 * blk + 4);
+        y[0] = fmaf(t, lo.x, y[0]); y[1] = fmaf(t, lo.y, y[1]); y[2] = fmaf(t, lo.z, y[2]); y[3] = fmaf(t, lo.w, y[3]);
+        y[4] = fmaf(t, hi.x, y[4]); y[5] = fmaf(t, hi.y, y[5]); y[6] = fmaf(t, hi.z, y[6]); y[7] = fmaf(t, hi.w, y[7]);
     }
     float mt = 0.f;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) mt = fmaxf(mt, fmaxf(fabsf(T[x]), fabsf(z[x & 7])));
+    for (int x = 0; x < 16; ++x) mt = fmaxf(mt, fmaxf(fabsf(G[x]), fabsf(y[x & 7])));
     const Pow2 st = pow2_for(warp_max_bits(mt));
-    if (lane == 0) one[kInvT] = st.inv;
-    auto put = [&](int tile, int row, int half, const float *f) {     // 8 values of a row of T's tile
+    if (lane == 0) one[kInvG] = st.inv;
+    auto put = [&](int tile, int row, int half, const float *f) {     // 8 values of a row of G's tile
         unsigned x[4][2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) split_f16<2>(f2(f[2 * y], f[2 * y + 1]), st.c, x[y]);
+        for (int i = 0; i < 4; ++i) split_f16<2>(f2(f[2 * i], f[2 * i + 1]), st.c, x[i]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-            *reinterpret_cast<uint4 *>(sc.block + (3 * y + tile) * kTri + tri_at(row, half)) =
-                make_uint4(x[0][y], x[1][y], x[2][y], x[3][y]);
+        for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<uint4 *>(sc.block + (3 * i + tile) * kTri + tri_at(row, half)) =
+                make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
     };
-    put(2 * blk, tl, 0, T);
-    put(2 * blk, tl, 1, T + 8);
-    put(1, tl, blk, z);
+    put(2 * blk, tl, 0, G);
+    put(2 * blk, tl, 1, G + 8);
+    put(1, tl, blk, y);
     // the block to global memory, one bulk copy
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -619,10 +619,10 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         unsigned char *st = smem + slot * Cfg::STAGE;
         if (i >= Cfg::STAGES) wait(&empty[slot], i / Cfg::STAGES - 1);
         if (lane == 0) {
-            mbar_arrive_expect_tx(&full[slot], Cfg::Rows::BYTES + Cfg::BLOCK);
+            mbar_arrive_expect_tx(&full[slot], Cfg::Rows::BYTES + Block::BYTES);
             bulk_load(st, p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Cfg::Rows::BYTES, Cfg::Rows::BYTES,
                       &full[slot]);
-            bulk_load(st + Cfg::OFF_TRI, p.prep + (size_t(bh) * nchunk + c) * Block::BYTES, Cfg::BLOCK, &full[slot]);
+            bulk_load(st + Cfg::OFF_TRI, p.prep + (size_t(bh) * nchunk + c) * Block::BYTES, Block::BYTES, &full[slot]);
         }
         __syncwarp();
         const size_t at = voff + size_t(c) * C * vrow;
@@ -835,37 +835,41 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv, sk[n][m], f * lo[n][m]);
-            scale_tok(x, du, vec + kVecBeta * C, t4);
         }
-        unsigned mr = 0;
-        {   // e = R + (T - I) R, or w with the transpose
+        auto scale_by = [&](unsigned m, float most) {
+            const float b = __uint_as_float(m) * most;
+            return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
+        };
+        // e = R - G (beta R), or du = rhs - G^T (beta rhs) and w = beta du.  Scales of what follows
+        // come from bounds: at most 31 entries of G, each below 2^14 / its scale, times beta's
+        // largest (a few bits more than it takes, of the 24 and more between fp16's largest and
+        // smallest steps).
+        float grown;
+        {
             unsigned A[2][2][4];
             Tok d;
-            mr = max_tok(x);
-            const Pow2 cx = pow2_for(mr);
-            split_tok<2>(x, cx.c, A);
+            const unsigned mr = max_tok(REV ? du : x);
+            const Pow2 cx = scale_by(mr, one[kMaxBeta]);
+            scale_tok(d, REV ? du : x, vec + kVecBeta * C, t4);
+            split_tok<2>(d, cx.c, A);
             zero_tok(d);
             mma_triangle<2, 2, REV>(d, A, tbase);
-            const float f = one[kInvT] * cx.inv;
+            const float f = -one[kInvG] * cx.inv;
+            grown = __uint_as_float(mr) * fmaf(31.f * 16384.f * one[kInvG], one[kMaxBeta], 1.f);
+            if constexpr (REV) grown *= one[kMaxBeta];
+            Tok &to = REV ? du : x;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) x[n][m] = fmaf(f, d[n][m], x[n][m]);
+                for (int m = 0; m < 4; ++m) to[n][m] = fmaf(f, d[n][m], to[n][m]);
+            if constexpr (REV) scale_tok(x, du, vec + kVecBeta * C, t4);
         }
-        // The scales of what x is multiplied with next follow from bounds: x grew by at most 31
-        // entries of T - I, each below 2^14 / its scale (five bits more than it takes, of the 24
-        // and more between fp16's largest and smallest steps).
-        const float grown = __uint_as_float(mr) * fmaf(31.f * 16384.f, one[kInvT], 1.f);
         const unsigned mx = __float_as_uint(isfinite(grown) ? grown : 0.f);
         if constexpr (MODE != 0)
             if (lane == 0) {
                 p.emax[(size_t(bh) * nchunk + c) * parts + part] = mx;
                 if constexpr (REV) p.ymax[(size_t(bh) * nchunk + c) * parts + part] = mv;
             }
-        auto scale_by = [&](unsigned m, float most) {
-            const float b = __uint_as_float(m) * most;
-            return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
-        };
         Tok o;
         if constexpr (!REV) {
             // y = scale gam S q + Pm (beta e)
@@ -881,6 +885,27 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f, o[n][m], cS.inv * sq[n][m]);
+        }
+        if constexpr (!REV) {
+            if constexpr (MODE == 1) {
+                store_tok<float>(p.e + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
+                Tok dy;
+                load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
+                token_sums(dy, c * C);
+            }
+        } else {
+            // the gradient of beta
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) du[n][m] *= er[n][m];
+            token_sums(du, c * C);
+            if (p.w != nullptr) store_tok<float>(p.w + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
+            store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
         }
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
         const float glast = one[kGamLast];
@@ -929,36 +954,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                     }
             }
         }
-        if constexpr (!REV) {
-            if constexpr (MODE == 0) {
-                store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, o);
-            } else {
-                store_tok<float>(p.e + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
-                Tok dy;
-                load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
-                token_sums(dy, c * C);
-            }
-        } else {
-            // du = rhs - (n / beta)^T w, the gradient of beta e: with e it gives beta's
-            unsigned A[2][2][4];
-            Tok d;
-            const Pow2 cx = pow2_for(mx);
-            split_tok<2>(x, cx.c, A);
-            zero_tok(d);
-            mma_triangle<2, 2, true>(d, A, tbase + Block::OFF_N);
-            const float f = -one[kInvN] * cx.inv;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] = er[n][m] * fmaf(f, d[n][m], du[n][m]);
-            token_sums(du, c * C);
-            if (p.w != nullptr) store_tok<float>(p.w + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
-            store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
-        }
+        if constexpr (MODE == 0)
+            store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, o);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);         // the stage may be filled again
     }
