@@ -30,28 +30,30 @@ using Block = ssm::DeltaBlock<2>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, w, ck, dck, dyy, edu, zsum, smax, dsmax, emax, wmax, ymax, part, all;
+    size_t prep, rows, e, w, ck, dck, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, all;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
-        const size_t sum = size_t(delta_slices(P)) * kDeltaWarps * tok * 4, state = bh * nbound * P * N * 4;
+        const size_t parts = size_t(delta_slices(P)) * kDeltaWarps;       // of 16 rows
+        const size_t sum = parts * tok * 4, state = bh * nbound * parts * 16 * padded_state(N) * 4;
+        const size_t rows16 = bh * delta_chunks(seqlen) * parts * 512 * 4;
         size_t at = 0;
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         add(prep, prep_bytes<Block>(batch, seqlen, heads));
         add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
-        add(e, tok * P * 4);
-        add(w, grad_dtype == SSM_F32 ? 0 : tok * P * 4);       // fp32 gradients: w is dv itself
+        add(e, rows16);
+        add(w, rows16);
         add(ck, state);
         add(dck, state);
         add(dyy, sum);
         add(edu, sum);
-        const size_t parts = size_t(delta_slices(P)) * kDeltaWarps * 4;
-        add(zsum, parts * bh * nbound);
-        add(smax, parts * bh * nbound);             // these five together: zeroed
-        add(dsmax, parts * bh * nbound);
-        add(emax, parts * bh * delta_chunks(seqlen));
-        add(wmax, parts * bh * delta_chunks(seqlen));
-        add(ymax, parts * bh * delta_chunks(seqlen));
+        add(vw, sum);
+        add(zsum, 4 * parts * bh * nbound);
+        add(smax, 4 * parts * bh * nbound);             // these five together: zeroed
+        add(dsmax, 4 * parts * bh * nbound);
+        add(emax, 4 * parts * bh * delta_chunks(seqlen));
+        add(wmax, 4 * parts * bh * delta_chunks(seqlen));
+        add(ymax, 4 * parts * bh * delta_chunks(seqlen));
         add(part, heads > qk_heads ? 2 * size_t(batch) * seqlen * qk_heads * N * 4 : 0);
         all = at;
     }
@@ -66,7 +68,6 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, at.all, s)) return st;
     auto part = [&](size_t off) { return reinterpret_cast<float *>(ws.p + off); };
-    float *w = sizeof(Tg) == 4 ? static_cast<float *>(dv) : part(at.w);
     constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
     f.prep = ws.p + at.prep;
     f.rows = ws.p + at.rows;
@@ -75,18 +76,18 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     int st = f.timeouts ? dispatch_prep<Tin, Block>(f, s) : int(SSM_ERR_CUDA);
     if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
     f.smax = bits(at.smax); f.emax = bits(at.emax);
-    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
+    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy); f.w = part(at.w);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
-        r.v = dy; r.y = dv; r.h0 = dfinal; r.hN = dh0; r.w = sizeof(Tg) == 4 ? nullptr : w;
-        r.dck = part(at.dck); r.sum = part(at.edu); r.zsum = part(at.zsum);
+        r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
+        r.dck = part(at.dck); r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
-        st = dispatch_chain<KP, Tg, Tg, Tg, 2>(r, s);
+        st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
-        const ssm::DeltaGradArgs g{v, dy, f.a, f.beta, part(at.e), w, f.rows, f.prep, Block::BYTES, part(at.ck),
-                                   part(at.dck), part(at.dyy), part(at.edu), part(at.zsum), bits(at.smax),
+        const ssm::DeltaGradArgs g{dy, f.a, f.beta, part(at.e), part(at.w), f.rows, f.prep, Block::BYTES, part(at.ck),
+                                   part(at.dck), part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
                                    bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
                                    da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N,
                                    delta_slices(f.P) * kDeltaWarps, f.scale};

@@ -29,12 +29,12 @@
 namespace ssm {
 
 struct DeltaGradArgs {
-    const void *v, *dy;
-    const float *a, *beta, *e, *w;
+    const void *dy;
+    const float *a, *beta, *e, *w;     // e, w and the states as the passes leave them
     const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
     size_t block;                      // bytes of a chunk block
     const float *ck, *dck;             // states and their gradients at the boundaries
-    const float *dyy, *edu;            // [zparts][batch][heads][seqlen]
+    const float *dyy, *edu, *vw;       // [zparts][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
     const unsigned *smax, *dsmax;      // [batch][heads][boundaries][zparts]
     const unsigned *emax, *wmax, *ymax;// [batch][heads][chunks of 32][zparts]
@@ -53,19 +53,18 @@ template <int NP_, int PW_, int KP_, typename Tin_, typename Tg_> struct GradCfg
     using Tin = Tin_;
     using Tg = Tg_;
     static constexpr int W = NP < kGradN ? NP : kGradN;
-    static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16;                // padded rows (bytes)
-    static constexpr int TOK = kGradC * PROW, ST = PW * NROW, KT = kGradC * NROW;
-    static constexpr int OFF_Y = 0, OFF_E = OFF_Y + PG * TOK, OFF_W = OFF_E + PG * TOK;
-    static constexpr int OFF_S = OFF_W + PG * TOK, OFF_D = OFF_S + PG * ST;
+    static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16, TROW = kGradC * 2 + 16;      // padded rows (bytes)
+    static constexpr int TOK = kGradC * PROW, TT = PW * TROW, ST = PW * NROW, KT = kGradC * NROW;
+    static constexpr int OFF_Y = 0, OFF_E = OFF_Y + PG * TOK, OFF_W = OFF_E + PG * TT;
+    static constexpr int OFF_S = OFF_W + PG * TT, OFF_D = OFF_S + PG * ST;
     static constexpr int OFF_K = OFF_D + PG * ST, OFF_Q = OFF_K + KP * KT;
     static constexpr int OFF_VEC = OFF_Q + KP * KT;
     static constexpr int SMEM_BYTES = OFF_VEC + 6 * kGradC * 4 + 16;
-    static constexpr int CTAS = PG == 1 ? 3 : 1;      // per SM: more, smaller ones hide the loads better
+    static constexpr int CTAS = PG == 1 ? (PW == 64 && NP > 64 ? 3 : 2) : 1;      // per SM, by shared memory and registers
 };
 
 template <class Cfg>
 __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaGradArgs p) {
-    using Tin = typename Cfg::Tin;
     using Tg = typename Cfg::Tg;
     constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W;
     using Rows = DeltaRows<NP, KP>;
@@ -95,6 +94,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
     }
     const unsigned an = unsigned((16 * rt + (lane & 15)) * Cfg::PROW + (lane >> 4) * 16);      // A: this warp's rows
     const unsigned bp = b_rows_n(lane, Cfg::PROW), bn = b_rows_k(lane, Cfg::NROW);
+    const unsigned at_ = b_rows_n(lane, Cfg::TROW) + 32 * rt, bt = b_rows_k(lane, Cfg::TROW);     // e, w: [headdim][token]
 
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
 #pragma unroll 4
             for (int s = 0; s < p.zparts; ++s) {
                 const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                dyy += p.dyy[x];
+                dyy += p.dyy[x] - p.vw[x];
                 db += p.edu[x];
             }
 #pragma unroll 4
@@ -129,41 +129,44 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
         const Pow2 cS = pow2_for(big[0]), cD = pow2_for(big[1]), cE = pow2_for(big[2]), cW = pow2_for(big[3]), cY = pow2_for(big[4]);
         __syncthreads();                 // the last head's tiles and vectors are done with
 
-        // dy, e and w as operands [token][headdim]; v.w on the way
+        // dy as an operand [token][headdim], e and w as [headdim][token]
         const Tg *dyp = static_cast<const Tg *>(p.dy) + v0;
-        const Tin *vp = static_cast<const Tin *>(p.v) + v0;
-        const float *ep = p.e + v0, *wp = p.w + v0;
-        auto put = [&](unsigned char *at, int piece, const float (&f)[8], float scale) {
-            unsigned x[4][PG];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) split_f16<PG>(f2(f[2 * y], f[2 * y + 1]), scale, x[y]);
-#pragma unroll
-            for (int i = 0; i < PG; ++i)
-                *reinterpret_cast<uint4 *>(at + i * piece) = make_uint4(x[0][i], x[1][i], x[2][i], x[3][i]);
-        };
-        constexpr int CP = PW / 8;       // lanes per row: 8 or 16, so a row stays within a warp
+        constexpr int CP = PW / 8;
 #pragma unroll (PG == 1 ? 4 : 2)
         for (int i = tid; i < C * CP; i += 128) {
             const int r = i / CP, x = (i % CP) * 8;
-            const bool ok = r < nt && x < p.P;
-            float fy[8] = {}, fe[8] = {}, fw[8] = {}, fv[8] = {};
-            if (ok) {
-                const size_t off = size_t(r) * vrow + x;
-                load8(dyp + off, fy);
-                load8(ep + off, fe);
-                load8(wp + off, fw);
-                load8(vp + off, fv);
+            float f[8] = {};
+            if (r < nt && x < p.P) load8(dyp + size_t(r) * vrow + x, f);
+            unsigned u[4][PG];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) split_f16<PG>(f2(f[2 * y], f[2 * y + 1]), cY.c, u[y]);
+#pragma unroll
+            for (int y = 0; y < PG; ++y)
+                *reinterpret_cast<uint4 *>(smem + Cfg::OFF_Y + y * Cfg::TOK + r * Cfg::PROW + x * 2) =
+                    make_uint4(u[0][y], u[1][y], u[2][y], u[3][y]);
+        }
+        // what a lane of the passes held, two rows of two neighbouring columns, into a tile of rows
+        auto put = [&](unsigned char *to, int piece, int rowbytes, float4 f, float scale) {
+            unsigned x[PG], y[PG];
+            split_f16<PG>(f2(f.x, f.y), scale, x);
+            split_f16<PG>(f2(f.z, f.w), scale, y);
+#pragma unroll
+            for (int i = 0; i < PG; ++i) {
+                *reinterpret_cast<unsigned *>(to + i * piece + g * rowbytes + 4 * t4) = x[i];
+                *reinterpret_cast<unsigned *>(to + i * piece + (g + 8) * rowbytes + 4 * t4) = y[i];
             }
-            unsigned char *at = smem + r * Cfg::PROW + x * 2;
-            put(at + Cfg::OFF_Y, Cfg::TOK, fy, cY.c);
-            put(at + Cfg::OFF_E, Cfg::TOK, fe, cE.c);
-            put(at + Cfg::OFF_W, Cfg::TOK, fw, cW.c);
-            float vw = 0.f;
-#pragma unroll
-            for (int y = 0; y < 8; ++y) vw = fmaf(fv[y], fw[y], vw);
-#pragma unroll
-            for (int o = 1; o < CP; o <<= 1) vw += __shfl_xor_sync(0xffffffffu, vw, o);
-            if (i % CP == 0) dtok[r] = vw;
+        };
+        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll (PG == 1 ? 4 : 2)
+        for (int i = rt; i < 2 * (PW / 16) * 4; i += 4) {      // (half, 16 rows, 8 tokens)
+            const int n = i & 3, rb = (i >> 2) % (PW / 16), hf = i / (PW / 4);
+            const bool ok = hf < n32 && 16 * rb < p.P;
+            const size_t from = ((((bh * nck + c32 + hf) * p.zparts + rb) * 4 + n) * 32 + lane) * 4;
+            const float4 fe = ok ? __ldg(reinterpret_cast<const float4 *>(p.e + from)) : none;
+            const float4 fw = ok ? __ldg(reinterpret_cast<const float4 *>(p.w + from)) : none;
+            unsigned char *to = smem + 16 * rb * Cfg::TROW + 64 * hf + 16 * n;
+            put(to + Cfg::OFF_E, Cfg::TT, Cfg::TROW, fe, cE.c);
+            put(to + Cfg::OFF_W, Cfg::TT, Cfg::TROW, fw, cW.c);
         }
         // decays: prefix sums of a in 64 bits, kept as pairs of floats (a below -1e4 counts as
         // -1e4: its exponential is 0 either way, and the sums stay finite)
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
             gam[tid] = expf(float(G));
             bet[tid] = bv;
             bend[tid] = bv * expf(float(Gend - G));
-            dtok[tid] = dyy - dtok[tid];
+            dtok[tid] = dyy;
         }
         // The token-by-token matrices of this warp's rows, in four tiles of 16 columns.
         const unsigned sy = smem_u32(smem + Cfg::OFF_Y), se = smem_u32(smem + Cfg::OFF_E), sw = smem_u32(smem + Cfg::OFF_W);
@@ -201,16 +204,16 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
 #pragma unroll
             for (int i = 0; i < PG; ++i) {
                 ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
-                ldsm4(ae[i], se + i * Cfg::TOK + an + k * 32);
-                ldsm4(aw[i], sw + i * Cfg::TOK + an + k * 32);
+                ldsm4_t(ae[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
+                ldsm4_t(aw[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 unsigned be[PG][4], by[PG][4], bw[PG][4];
-                const unsigned at = 16 * u * Cfg::PROW + bp + k * 32;
+                const unsigned at = 16 * u * Cfg::PROW + bp + k * 32, tt = 16 * k * Cfg::TROW + bt + 32 * u;
                 if (u <= rt) {
 #pragma unroll
-                    for (int i = 0; i < PG; ++i) ldsm4(be[i], se + i * Cfg::TOK + at);
+                    for (int i = 0; i < PG; ++i) ldsm4_t(be[i], se + i * Cfg::TT + tt);
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         mma_pieces<PG, PG>(x1[u][n], ay, be, n);
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
 #pragma unroll
                     for (int i = 0; i < PG; ++i) {
                         ldsm4(by[i], sy + i * Cfg::TOK + at);
-                        ldsm4(bw[i], sw + i * Cfg::TOK + at);
+                        ldsm4_t(bw[i], sw + i * Cfg::TT + tt);
                     }
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
@@ -272,22 +275,22 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
             fe[r] = bend[t] * (cE.inv * cD.inv);
         }
 
-        const float *S0 = p.ck + (bh * nbound + c) * p.P * p.N, *dE = p.dck + (bh * nbound + c + 1) * p.P * p.N;
+        const float *S0 = p.ck + (bh * nbound + c) * p.zparts * (NP * 16);
+        const float *dE = p.dck + (bh * nbound + c + 1) * p.zparts * (NP * 16);
         for (int n0 = 0; n0 < NP; n0 += W) {
             if (n0 > 0) __syncthreads();
             // this pass's columns of the states and of k and q
             constexpr int CN = W / 8;
 #pragma unroll (PG == 1 ? 4 : 2)
-            for (int i = tid; i < PW * CN; i += 128) {
-                const int r = i / CN, x = (i % CN) * 8;
-                float fs[8] = {}, fd[8] = {};
-                if (r < p.P && n0 + x < p.N) {
-                    load8(S0 + size_t(r) * p.N + n0 + x, fs);
-                    load8(dE + size_t(r) * p.N + n0 + x, fd);
-                }
-                unsigned char *at = smem + r * Cfg::NROW + x * 2;
-                put(at + Cfg::OFF_S, Cfg::ST, fs, cS.c);
-                put(at + Cfg::OFF_D, Cfg::ST, fd, cD.c);
+            for (int i = rt; i < (PW / 16) * CN; i += 4) {     // (16 rows, 8 columns)
+                const int j = i % CN, rb = i / CN;
+                const bool ok = 16 * rb < p.P && n0 + 8 * j < NP;
+                const size_t from = ((size_t(rb) * (NP / 8) + n0 / 8 + j) * 32 + lane) * 4;
+                const float4 fs = ok ? __ldg(reinterpret_cast<const float4 *>(S0 + from)) : none;
+                const float4 fd = ok ? __ldg(reinterpret_cast<const float4 *>(dE + from)) : none;
+                unsigned char *to = smem + 16 * rb * Cfg::NROW + 16 * j;
+                put(to + Cfg::OFF_S, Cfg::ST, Cfg::NROW, fs, cS.c);
+                put(to + Cfg::OFF_D, Cfg::ST, Cfg::NROW, fd, cD.c);
             }
 #pragma unroll (PG == 1 ? 4 : 2)
             for (int i = tid; i < C * CN; i += 128) {
@@ -319,8 +322,8 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
 #pragma unroll
                     for (int i = 0; i < PG; ++i) {
                         ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
-                        ldsm4(aE[i], se + i * Cfg::TOK + an + k * 32);
-                        ldsm4(aW[i], sw + i * Cfg::TOK + an + k * 32);
+                        ldsm4_t(aE[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
+                        ldsm4_t(aW[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {

@@ -48,23 +48,23 @@ struct DeltaArgs {
     unsigned char *rows;    // [batch][qk_heads][chunks] k and q as operands, from the prep kernel
     unsigned *timeouts;     // counts waits that gave up
     const void *v;          // [batch][seqlen][heads][headdim]; the reverse pass: dy
-    const void *v2;         // forward of the backward pass: dy
+    const void *v2;         // backward: dy in the forward pass, v in the reverse pass
     const float *a, *beta;  // [batch][seqlen][heads]
     void *y;                // forward: y; reverse pass: dv
     const float *h0;        // start state (reverse pass: the final state's gradient) or NULL
     float *hN;              // end state (reverse pass: the start state's gradient) or NULL
-    float *e;               // backward: [batch][seqlen][heads][headdim], e written, then read
-    float *w;               // reverse pass: the same of w, or NULL (w is then dv itself)
-    float *ck;              // backward: the state at every boundary of 64 tokens and at the end,
-                            // [batch][heads][boundaries][headdim][dstate]
-    float *dck;             // reverse pass: its gradient there
-    float *sum;             // backward: [slices * warps][batch][heads][seqlen] sums over a warp's
-                            // rows: dy.y; in the reverse pass e.du (the gradient of beta)
-    float *zsum;            // reverse pass: [slices * warps][batch][heads][boundaries] <dS, S>
-    unsigned *smax;         // backward: [batch][heads][boundaries][slices * warps] largest |S| (reverse
-                            // pass: |dS|) of a warp's rows, as bits
-    unsigned *emax, *ymax;  // backward: [batch][heads][chunks][slices * warps] bounds of |e| (reverse
-                            // pass: |w|) and, in the reverse pass, the largest |dy|
+    // The backward's scratch.  A "part" is a warp's 16 rows: part = slice * warps + warp.  What one
+    // pass leaves for the next is laid out as the warps hold it (accumulator tiles, four values a
+    // lane), so that every access is a whole 16 bytes a lane in order.
+    float *e, *w;           // [batch][heads][chunks][parts][4 tiles of 8 tokens][lane][4]: e, w
+    float *ck, *dck;        // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
+                            // and its gradient at every boundary of 64 tokens and at the end
+    float *sum, *sum2;      // [parts][batch][heads][seqlen] sums over a part's rows: dy.y; in the
+                            // reverse pass e.du (the gradient of beta) and v.w
+    float *zsum;            // [parts][batch][heads][boundaries] <dS, S>
+    unsigned *smax;         // [batch][heads][boundaries][parts] largest |S| (reverse pass: |dS|), as bits
+    unsigned *emax, *ymax;  // [batch][heads][chunks][parts] bounds of |e| (reverse pass: |w|) and, in the
+                            // reverse pass, the largest |dy|
     int batch, seqlen, heads, qk_heads, P, N, slices;
     float scale;
 };
@@ -110,7 +110,7 @@ constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's 
 template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
     using Tv = Tv_;        // v, or dy in the reverse pass
-    using Tv2 = Tv2_;      // MODE 1: dy
+    using Tv2 = Tv2_;      // MODE 1: dy; MODE 2: v
     using Tout = Tout_;
     static constexpr int C = kDeltaC, NT = 32 * NW;
     static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
@@ -124,13 +124,13 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int PIECE = Rows::PIECE;
     static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
     static constexpr int OFF_V = OFF_TRI + Block::BYTES, OFF_V2 = OFF_V + C * VROW;
-    static constexpr int STAGE = OFF_V2 + (MODE == 1 ? C * V2ROW : 0);
+    static constexpr int STAGE = OFF_V2 + (MODE != 0 ? C * V2ROW : 0);
     static constexpr int STAGES = MODE == 0 && KP == 1 ? 3 : 2;               // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
     static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
     static constexpr int OFF_ST = OFF_OUT + NW * 16 * kOutRow;                // reverse pass: kept states
-    static constexpr int STROW = NP * 4 + 16;
-    static constexpr int SMEM_BYTES = OFF_ST + (MODE == 2 ? NW * 16 * STROW : 0);
+    static constexpr int STATE = NP * 16 * 4;                                 // bytes of a part's state
+    static constexpr int SMEM_BYTES = OFF_ST + (MODE == 2 ? NW * STATE : 0);
 };
 
 // acc += A B of operands in KP bf16 pieces (1: exact, 3: all bits of fp32), the products of
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     };
 
     // Start the copies of loop step i into its stage, once the warps are done with what is there:
-    // lane 0 the operands and the block, all lanes the rows of v (of dy too in MODE 1), zeros
+    // lane 0 the operands and the block, all lanes the rows of v (and of v2), zeros
     // past the end and past headdim.
     const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
     auto copy_v = [&](unsigned dst, int rowbytes, const auto *src, int ntok) {
@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         __syncwarp();
         const size_t at = voff + size_t(c) * C * vrow;
         copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + at, ntok);
-        if constexpr (MODE == 1) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
+        if constexpr (MODE != 0) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
         mbar_arrive_cp_async(&full[slot]);
     };
     if (warp == 0)
@@ -658,69 +658,69 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     const unsigned bn = b_rows_n(lane, Cfg::KROW), bk = b_rows_k(lane, Cfg::KROW);
     const unsigned tr = REV ? tri_rows_k(lane) : tri_rows_n(lane);
     const int nbound = (p.seqlen + kDeltaSave - 1) / kDeltaSave + 1;       // boundaries, the end among them
+    const size_t part = slice * NW + warp, parts = size_t(p.slices) * NW;
     auto keep_state = [&](float *ck, int x) {
-        float *base = ck + (size_t(bh) * nbound + x) * p.P * p.N;
-        state_io([&](float &u, float &v, size_t off) { *reinterpret_cast<float2 *>(base + off) = make_float2(u, v); });
+        float4 *to = reinterpret_cast<float4 *>(ck + ((size_t(bh) * nbound + x) * parts + part) * (NP * 16)) + lane;
+#pragma unroll
+        for (int j = 0; j < NP / 8; ++j) to[32 * j] = make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
     };
-    // reverse pass: the kept state of boundary x into the warp's rows of shared memory, and
-    // its inner product with the gradient
-    unsigned char *strow = smem + Cfg::OFF_ST + warp * 16 * Cfg::STROW;
+    // reverse pass: the kept state of boundary x into the warp's shared memory, and its inner
+    // product with the gradient
+    unsigned char *strow = smem + Cfg::OFF_ST + warp * Cfg::STATE + lane * 16;
     auto fetch_state = [&](int x) {
-        const float *base = p.ck + (size_t(bh) * nbound + x) * p.P * p.N;
-        for (int y = lane; y < 16 * (NP / 4); y += 32) {
-            const int r = y / (NP / 4), n = (y % (NP / 4)) * 4;
-            const bool ok = r < nrow && n < p.N;
-            cp_async_16z(smem_u32(strow + r * Cfg::STROW + n * 4), base + (ok ? size_t(p0 + r) * p.N + n : 0), ok);
-        }
+        const float4 *from = reinterpret_cast<const float4 *>(p.ck + ((size_t(bh) * nbound + x) * parts + part) * (NP * 16)) + lane;
+#pragma unroll
+        for (int j = 0; j < NP / 8; ++j) cp_async_16(strow + 512 * j, from + 32 * j);
+        cp_async_commit();
     };
     auto dot_state = [&](int x) {
-        cp_async_wait<0>();
-        __syncwarp();
+        cp_async_wait<0>();                                // this lane's own copies
         float z0 = 0.f, z1 = 0.f;
 #pragma unroll
-        for (int j = 0; j < NP / 8; ++j)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const float2 f = *reinterpret_cast<const float2 *>(strow + (g + 8 * r) * Cfg::STROW + (8 * j + 2 * t4) * 4);
-                z0 = fmaf(f.x, s[j][2 * r], z0);
-                z1 = fmaf(f.y, s[j][2 * r + 1], z1);
-            }
+        for (int j = 0; j < NP / 8; ++j) {
+            const float4 f = *reinterpret_cast<const float4 *>(strow + 512 * j);
+            z0 = fmaf(f.x, s[j][0], fmaf(f.z, s[j][2], z0));
+            z1 = fmaf(f.y, s[j][1], fmaf(f.w, s[j][3], z1));
+        }
         z0 += z1;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z0 += __shfl_xor_sync(0xffffffffu, z0, o);
-        if (lane == 0)
-            p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = z0;
-        __syncwarp();
+        if (lane == 0) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = z0;
     };
-    // sums over the warp's 16 rows of f[row][token], tokens from t0 on
-    auto token_sums = [&](const Tok &f, int t0) {
-        float *out = p.sum + (size_t(slice * NW + warp) * p.batch * p.heads + bh) * p.seqlen;
+    // sums over the part's 16 rows of f[row][token], tokens from t0 on: the eight values a lane
+    // has are halved in three exchanges, after which it holds one token's sum
+    auto token_sums = [&](float *sum, const Tok &f, int t0) {
+        float v[8];
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            float u = f[n][0] + f[n][2], w = f[n][1] + f[n][3];
+        for (int n = 0; n < 4; ++n) { v[2 * n] = f[n][0] + f[n][2]; v[2 * n + 1] = f[n][1] + f[n][3]; }
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                u += __shfl_xor_sync(0xffffffffu, u, o);
-                w += __shfl_xor_sync(0xffffffffu, w, o);
+        for (int o = 16, h = 4; h > 0; o >>= 1, h >>= 1)
+#pragma unroll
+            for (int k = 0; k < h; ++k) {
+                const bool up = lane & o;
+                const float got = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + h], o);
+                v[k] = (up ? v[k + h] : v[k]) + got;
             }
-            const int t = t0 + 8 * n + 2 * t4;
-            if (g == 0 && t < p.seqlen) out[t] = u;
-            if (g == 0 && t + 1 < p.seqlen) out[t + 1] = w;
-        }
+        const int t = t0 + 8 * (g >> 1) + 2 * t4 + (g & 1);
+        if (t < p.seqlen) sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = v[0];
+    };
+    // a Tok as the next pass reads it
+    auto keep_tok = [&](float *to, const Tok &f, int c) {
+        float4 *at = reinterpret_cast<float4 *>(to + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) at[32 * n] = make_float4(f[n][0], f[n][1], f[n][2], f[n][3]);
     };
     if (nrow <= 0) {                                       // rows past headdim
         if constexpr (MODE != 0)
-            for (int t = lane; t < p.seqlen; t += 32)
-                p.sum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
+            for (int t = lane; t < p.seqlen; t += 32) {
+                p.sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
+                if constexpr (REV) p.sum2[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
+            }
         if constexpr (REV)
-            for (int x = lane; x < nbound; x += 32)
-                p.zsum[(size_t(slice * NW + warp) * p.batch * p.heads + bh) * nbound + x] = 0.f;
+            for (int x = lane; x < nbound; x += 32) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = 0.f;
         return;
     }
-    if constexpr (REV) {
-        fetch_state(nbound - 1);
-        cp_async_commit();
-    }
+    if constexpr (REV) fetch_state(nbound - 1);
     int turn = warp + 1;                                   // loop steps until it is this warp's to start copies
     // the largest magnitude of the state, kept up with its updates
     float ms = 0.f;
@@ -737,22 +737,17 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         Tok er;
         if constexpr (MODE == 1) if (c % CS == 0) keep_state(p.ck, c / CS);
         if constexpr (REV) {
-            const float *ep = p.e + tok0 * p.P + p0;
+            const float4 *ep = reinterpret_cast<const float4 *>(p.e + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int tok = 8 * n + 2 * t4 + (m & 1), row = g + 8 * (m >> 1);
-                    er[n][m] = tok < ntok && row < nrow ? ep[size_t(tok) * vrow + row] : 0.f;
-                }
+            for (int n = 0; n < 4; ++n) {
+                const float4 f = __ldg(ep + 32 * n);
+                er[n][0] = f.x; er[n][1] = f.y; er[n][2] = f.z; er[n][3] = f.w;
+            }
             if (c % CS == CS - 1 || c == nchunk - 1) {
                 keep_state(p.dck, c / CS + 1);
                 dot_state(c / CS + 1);
             }
-            if (c % CS == 0) {
-                fetch_state(c / CS);
-                cp_async_commit();
-            }
+            if (c % CS == 0) fetch_state(c / CS);
         }
 
         const int slot = i % Cfg::STAGES;
@@ -765,7 +760,6 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
         const unsigned msb = warp_max_bits(ms);
         const Pow2 cS = pow2_for(msb);
-        const size_t part = slice * NW + warp, parts = size_t(p.slices) * NW;
         if constexpr (MODE == 1)
             if (c % CS == 0 && lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
         if constexpr (REV)
@@ -888,14 +882,14 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         }
         if constexpr (!REV) {
             if constexpr (MODE == 1) {
-                store_tok<float>(p.e + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
+                keep_tok(p.e, x, c);
                 Tok dy;
                 load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
-                token_sums(dy, c * C);
+                token_sums(p.sum, dy, c * C);
             }
         } else {
             // the gradient of beta
@@ -903,8 +897,14 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] *= er[n][m];
-            token_sums(du, c * C);
-            if (p.w != nullptr) store_tok<float>(p.w + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
+            token_sums(p.sum, du, c * C);
+            load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, du);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int m = 0; m < 4; ++m) du[n][m] *= x[n][m];
+            token_sums(p.sum2, du, c * C);
+            keep_tok(p.w, x, c);
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
         }
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
