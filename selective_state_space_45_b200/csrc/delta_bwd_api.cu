@@ -2,7 +2,7 @@
 // forward pass again (e and the states every 64 tokens), the reverse pass (dv, the state's
 // gradient at the same places), then the chunks' gradients in parallel.  One stream-ordered
 // scratch buffer per call.
-#include "delta_grad.cuh"
+#include "delta_grad16.cuh"
 #include "delta_host.cuh"
 
 using namespace ssm_host;
@@ -10,11 +10,18 @@ using namespace ssm_host;
 namespace {
 
 template <int NP, int PW, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
-    using Cfg = ssm::GradCfg<NP, PW, sizeof(Tin) == 4 ? 2 : 1, Tin, Tg>;
     const long long ctas = (long long)a.batch * a.qk_heads * ((a.seqlen + ssm::kGradC - 1) / ssm::kGradC);
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
-    ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
+    constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
+    if constexpr (sizeof(Tg) == 2) {
+        using Cfg = ssm::Grad16Cfg<NP, PW, KP>;
+        if (const int st = set_smem(ssm::delta_grad16_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
+        ssm::delta_grad16_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
+    } else {
+        using Cfg = ssm::GradCfg<NP, PW, KP, Tin, Tg>;
+        if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
+        ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
+    }
     return status_of(cudaGetLastError());
 }
 template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
@@ -30,7 +37,7 @@ using Block = ssm::DeltaBlock<2>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, w, ck, dck, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, all;
+    size_t prep, rows, e, w, ck, dck, y16, e16, s16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, all;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
@@ -41,10 +48,17 @@ struct BwdParts {
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         add(prep, prep_bytes<Block>(batch, seqlen, heads));
         add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
+        // bf16 gradients: w and the state's gradient as fp16 tiles alone, dy, e and the state beside
+        const bool g16 = grad_dtype == SSM_BF16;
+        const size_t tok16 = g16 ? bh * delta_chunks(seqlen) * parts * ssm::kTok16 : 0;
+        const size_t state16 = g16 ? bh * nbound * parts * 16 * (padded_state(N) > 64 ? 256 : 2 * padded_state(N)) : 0;
         add(e, rows16);
-        add(w, rows16);
+        add(w, g16 ? tok16 : rows16);
         add(ck, state);
-        add(dck, state);
+        add(dck, g16 ? state16 : state);
+        add(y16, tok16);
+        add(e16, tok16);
+        add(s16, state16);
         add(dyy, sum);
         add(edu, sum);
         add(vw, sum);
@@ -76,18 +90,20 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     int st = f.timeouts ? dispatch_prep<Tin, Block>(f, s) : int(SSM_ERR_CUDA);
     if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
     f.smax = bits(at.smax); f.emax = bits(at.emax);
-    f.v = v; f.v2 = dy; f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy); f.w = part(at.w);
+    f.v = v; f.v2 = dy; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;
+    f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy); f.w = part(at.w);
     if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
         r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
-        r.dck = part(at.dck); r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
+        r.dck = part(at.dck); r.d16 = ws.p + at.dck; r.w16 = ws.p + at.w; r.y16 = ws.p + at.y16; r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
         st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
     }
     if (st == SSM_OK) {
         const ssm::DeltaGradArgs g{dy, f.a, f.beta, part(at.e), part(at.w), f.rows, f.prep, Block::BYTES, part(at.ck),
-                                   part(at.dck), part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
+                                   part(at.dck), ws.p + at.e16, ws.p + at.w, ws.p + at.y16, ws.p + at.s16,
+                                   ws.p + at.dck, f.timeouts, part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
                                    bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
                                    da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N,
                                    delta_slices(f.P) * kDeltaWarps, f.scale};

@@ -34,6 +34,8 @@ struct DeltaGradArgs {
     const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
     size_t block;                      // bytes of a chunk block
     const float *ck, *dck;             // states and their gradients at the boundaries
+    const unsigned char *e16, *w16, *y16, *s16, *d16;      // bf16 gradients: the same as fp16 tiles
+    unsigned *timeouts;
     const float *dyy, *edu, *vw;       // [zparts][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
     const unsigned *smax, *dsmax;      // [batch][heads][boundaries][zparts]

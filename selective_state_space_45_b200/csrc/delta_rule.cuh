@@ -59,6 +59,10 @@ struct DeltaArgs {
     float *e, *w;           // [batch][heads][chunks][parts][4 tiles of 8 tokens][lane][4]: e, w
     float *ck, *dck;        // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
                             // and its gradient at every boundary of 64 tokens and at the end
+    // For bf16 gradients the last kernel takes scaled fp16 operands, tiles of its shared memory
+    // as they stand (stm16 writes them): e, w and dy of a part and chunk, S and dS of a part.
+    unsigned char *e16, *w16, *y16;     // [batch][heads][chunks][parts] 16 rows of 32 tokens
+    unsigned char *s16, *d16;           // [batch][heads][boundaries][parts] 16 rows of dstate
     float *sum, *sum2;      // [parts][batch][heads][seqlen] sums over a part's rows: dy.y; in the
                             // reverse pass e.du (the gradient of beta) and v.w
     float *zsum;            // [parts][batch][heads][boundaries] <dS, S>
@@ -103,6 +107,17 @@ template <int NP, int KP> struct DeltaRows {
     static constexpr int ROW = NP * 2 + 16, PIECE = kDeltaC * ROW, BYTES = 2 * KP * PIECE;
 };
 
+// Rows of a 16-bit tile of a part: 64 bytes (32 tokens), or dstate padded to a power of two.
+// The 16-byte pieces of a row change places with the row, so that eight rows' pieces of one
+// column are eight bank groups (ldmatrix).
+constexpr int kTok16 = 1024;
+__device__ __forceinline__ int tok16_at(int r, int n) { return r * 64 + ((n ^ (r >> 1)) & 3) * 16; }
+template <int NP> struct State16 {
+    static constexpr int ROW = NP > 64 ? 256 : NP * 2, BYTES = 16 * ROW;
+    __device__ static __forceinline__ int flip(int r) { return (NP > 32 ? r & 7 : (r >> 1) & 3) * 16; }
+    __device__ static __forceinline__ int at(int r, int n) { return r * ROW + ((n * 16) ^ flip(r)); }
+};
+
 constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's limit, about a second
 
 // NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k.  MODE 0:
@@ -128,9 +143,13 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int STAGES = MODE == 0 && KP == 1 ? 3 : 2;               // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
     static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
-    static constexpr int OFF_ST = OFF_OUT + NW * 16 * kOutRow;                // reverse pass: kept states
+    static constexpr bool G16 = MODE == 1 ? sizeof(Tv2) == 2 : MODE == 2 && sizeof(Tv) == 2;      // bf16 gradients
+    static constexpr int OUT = 1024;                                          // bytes of a warp's tile
+    static constexpr int OFF_ST = OFF_OUT + NW * OUT;                         // kept states on their way
     static constexpr int STATE = NP * 16 * 4;                                 // bytes of a part's state
-    static constexpr int SMEM_BYTES = OFF_ST + (MODE == 2 ? NW * STATE : 0);
+    static constexpr int ST = MODE == 2 ? STATE : MODE == 1 && G16 ? State16<NP>::BYTES : 0;
+    static constexpr int SMEM_BYTES = OFF_ST + NW * ST;
+    static_assert(MODE != 2 || STATE >= State16<NP>::BYTES);
 };
 
 // acc += A B of operands in KP bf16 pieces (1: exact, 3: all bits of fp32), the products of
@@ -654,7 +673,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             const float2 f = *reinterpret_cast<const float2 *>(p.h0 + sbase + off);
             x = f.x; y = f.y;
         });
-    unsigned char *tile = smem + Cfg::OFF_OUT + warp * 16 * kOutRow;
+    unsigned char *tile = smem + Cfg::OFF_OUT + warp * Cfg::OUT;
     const unsigned bn = b_rows_n(lane, Cfg::KROW), bk = b_rows_k(lane, Cfg::KROW);
     const unsigned tr = REV ? tri_rows_k(lane) : tri_rows_n(lane);
     const int nbound = (p.seqlen + kDeltaSave - 1) / kDeltaSave + 1;       // boundaries, the end among them
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     };
     // reverse pass: the kept state of boundary x into the warp's shared memory, and its inner
     // product with the gradient
-    unsigned char *strow = smem + Cfg::OFF_ST + warp * Cfg::STATE + lane * 16;
+    unsigned char *strow = smem + Cfg::OFF_ST + warp * Cfg::ST + lane * 16;
     auto fetch_state = [&](int x) {
         const float4 *from = reinterpret_cast<const float4 *>(p.ck + ((size_t(bh) * nbound + x) * parts + part) * (NP * 16)) + lane;
 #pragma unroll
@@ -686,6 +705,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) z0 += __shfl_xor_sync(0xffffffffu, z0, o);
         if (lane == 0) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = z0;
+        __syncwarp();                                      // the memory may be used again
     };
     // sums over the part's 16 rows of f[row][token], tokens from t0 on: the eight values a lane
     // has are halved in three exchanges, after which it holds one token's sum
@@ -703,6 +723,42 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             }
         const int t = t0 + 8 * (g >> 1) + 2 * t4 + (g & 1);
         if (t < p.seqlen) sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = v[0];
+    };
+    // a shared tile to global memory, as it stands
+    auto copy_out = [&](unsigned char *to, const unsigned char *from, auto bytes) {
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < decltype(bytes)::value / 512; ++x)
+            *reinterpret_cast<uint4 *>(to + 512 * x + 16 * lane) = *reinterpret_cast<const uint4 *>(from + 512 * x + 16 * lane);
+        __syncwarp();
+    };
+    const int srow = (lane >> 3 & 1) * 8 + (lane & 7), spiece = lane >> 4;       // stmatrix: row and piece of the lane
+    // a Tok times c as the last kernel reads it
+    auto keep_tok16 = [&](unsigned char *to, const Tok &f, float k, int c) {
+#pragma unroll
+        for (int h2 = 0; h2 < 2; ++h2) {
+            unsigned r[4], x[1];
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float *v = f[2 * h2 + (m >> 1)] + 2 * (m & 1);
+                split_f16<1>(f2(v[0], v[1]), k, x);
+                r[m] = x[0];
+            }
+            stsm4(smem_u32(tile) + tok16_at(srow, 2 * h2 + spiece), r);
+        }
+        copy_out(to + ((size_t(bh) * nchunk + c) * parts + part) * kTok16, tile, std::integral_constant<int, kTok16>());
+    };
+    // the state times c
+    auto keep_state16 = [&](unsigned char *to, float k, int x) {
+        unsigned char *st = smem + Cfg::OFF_ST + warp * Cfg::ST;
+        using S16 = State16<NP>;
+#pragma unroll
+        for (int j = 0; j < NP / 16; ++j) {
+            unsigned A[1][4];
+            split_tiles<1>(s[2 * j], s[2 * j + 1], k, A);
+            stsm4(smem_u32(st) + S16::at(srow, 2 * j + spiece), A[0]);
+        }
+        copy_out(to + ((size_t(bh) * nbound + x) * parts + part) * S16::BYTES, st, std::integral_constant<int, S16::BYTES>());
     };
     // a Tok as the next pass reads it
     auto keep_tok = [&](float *to, const Tok &f, int c) {
@@ -734,8 +790,15 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         constexpr int CS = kDeltaSave / C;
         const size_t tok0 = (size_t(b) * p.seqlen + size_t(c) * C) * p.heads + h;
         const int ntok = min(C, p.seqlen - c * C);
+        const unsigned msb = warp_max_bits(ms);
+        const Pow2 cS = pow2_for(msb);
         Tok er;
-        if constexpr (MODE == 1) if (c % CS == 0) keep_state(p.ck, c / CS);
+        if constexpr (MODE == 1)
+            if (c % CS == 0) {
+                keep_state(p.ck, c / CS);
+                if constexpr (Cfg::G16) keep_state16(p.s16, cS.c, c / CS);
+                if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
+            }
         if constexpr (REV) {
             const float4 *ep = reinterpret_cast<const float4 *>(p.e + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
 #pragma unroll
@@ -744,8 +807,10 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                 er[n][0] = f.x; er[n][1] = f.y; er[n][2] = f.z; er[n][3] = f.w;
             }
             if (c % CS == CS - 1 || c == nchunk - 1) {
-                keep_state(p.dck, c / CS + 1);
                 dot_state(c / CS + 1);
+                if constexpr (Cfg::G16) keep_state16(p.d16, cS.c, c / CS + 1);
+                else keep_state(p.dck, c / CS + 1);
+                if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
             }
             if (c % CS == 0) fetch_state(c / CS);
         }
@@ -758,13 +823,6 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         const unsigned tbase = smem_u32(stage + Cfg::OFF_TRI) + tr;
         const float *one = vec + kVecScalars * C;
         // S k, and S q for y; the next step's operands are loaded ahead of this one's products
-        const unsigned msb = warp_max_bits(ms);
-        const Pow2 cS = pow2_for(msb);
-        if constexpr (MODE == 1)
-            if (c % CS == 0 && lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
-        if constexpr (REV)
-            if ((c % CS == CS - 1 || c == nchunk - 1) && lane == 0)
-                p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
         Tok sk, sq;
         zero_tok(sk); zero_tok(sq);
         unsigned kb[2][KP][4], qb[2][KP][4];
@@ -883,6 +941,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         if constexpr (!REV) {
             if constexpr (MODE == 1) {
                 keep_tok(p.e, x, c);
+                if constexpr (Cfg::G16) keep_tok16(p.e16, x, pow2_for(mx).c, c);
                 Tok dy;
                 load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
 #pragma unroll
@@ -904,7 +963,12 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] *= x[n][m];
             token_sums(p.sum2, du, c * C);
-            keep_tok(p.w, x, c);
+            if constexpr (Cfg::G16) {
+                keep_tok16(p.w16, x, pow2_for(mx).c, c);
+                keep_tok16(p.y16, v, pow2_for(mv).c, c);
+            } else {
+                keep_tok(p.w, x, c);
+            }
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
         }
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
