@@ -24,7 +24,8 @@ template <int NP_, int PW_, int KP_> struct Grad16Cfg {
     static constexpr int OFF_S = 3 * TOK, OFF_D = OFF_S + PARTS * S16::BYTES;
     static constexpr int OFF_KQ = OFF_D + PARTS * S16::BYTES;                 // [half] k and q
     static constexpr int OFF_VEC = OFF_KQ + 2 * Rows::BYTES;
-    static constexpr int SMEM_BYTES = OFF_VEC + 6 * kGradC * 4 + 32;
+    static constexpr int OFF_OUT = OFF_VEC + 6 * kGradC * 4 + 32;             // per-warp output tiles
+    static constexpr int SMEM_BYTES = OFF_OUT + 4 * kTok16;
     static constexpr int CTAS = SMEM_BYTES <= 113 * 1024 ? 2 : 1;
 };
 
@@ -65,15 +66,25 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
         mbar_init(bar, 1);
         mbar_fence_init();
     }
+    auto zero = [&](int off, int bytes) {
+        for (int x = tid; x < bytes / 16; x += 128) *reinterpret_cast<uint4 *>(smem + off + 16 * x) = make_uint4(0, 0, 0, 0);
+    };
     // a chunk whose second half is past the end: that half is zeros
     if (n32 == 1) {
-        auto zero = [&](int off, int bytes) {
-            for (int x = tid; x < bytes / 16; x += 128) *reinterpret_cast<uint4 *>(smem + off + 16 * x) = make_uint4(0, 0, 0, 0);
-        };
         zero(Cfg::OFF_E + Cfg::TOK / 2, Cfg::TOK / 2);
         zero(Cfg::OFF_W + Cfg::TOK / 2, Cfg::TOK / 2);
         zero(Cfg::OFF_Y + Cfg::TOK / 2, Cfg::TOK / 2);
         zero(Cfg::OFF_KQ + Rows::BYTES, Rows::BYTES);
+    }
+    if (kp < Cfg::PARTS) {               // parts past headdim: zeros
+        const int n = Cfg::PARTS - kp;
+        for (int hf = 0; hf < 2; ++hf) {
+            zero(Cfg::OFF_E + hf * (Cfg::TOK / 2) + kp * kTok16, n * kTok16);
+            zero(Cfg::OFF_W + hf * (Cfg::TOK / 2) + kp * kTok16, n * kTok16);
+            zero(Cfg::OFF_Y + hf * (Cfg::TOK / 2) + kp * kTok16, n * kTok16);
+        }
+        zero(Cfg::OFF_S + kp * S16::BYTES, n * S16::BYTES);
+        zero(Cfg::OFF_D + kp * S16::BYTES, n * S16::BYTES);
     }
     __syncthreads();
     auto copies = [&](int hg) {          // by one thread
@@ -95,16 +106,6 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
     };
     if (tid == 0) copies(0);
 
-    // 1 / scales of k and q in the chunk's halves
-    float ick[2], icq[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int cc = c32 + (x < n32 ? x : 0);
-        const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * p.block +
-                                                           DeltaBlock<2>::OFF_VEC) + kVecScalars * kDeltaC;
-        ick[x] = 1.f / one[kCk];         // powers of two: exact
-        icq[x] = 1.f / one[kCq];
-    }
     // ldmatrix offsets.  e, w, dy tiles are [headdim][token], states [headdim][dstate]: both take
     // the transposing load.  A: this warp's 16 tokens; B: 16 tokens of a half, or 16 columns.
     const int ra = (lane >> 4) * 8 + (lane & 7), rb = (lane >> 3 & 1) * 8 + (lane & 7);
@@ -115,40 +116,62 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
     const unsigned sbase = smem_u32(smem);
 
     bool alive = true;
+    float ick[2], icq[2];                // 1 / scales of k and q in the chunk's halves
     for (int hg = 0; hg < group; ++hg) {
         const int h = hk * group + hg;
         const size_t bh = size_t(b) * p.heads + h;
-        // threads 0..63: their token's gates and sums
+        // Everything small at once: scales, and for threads 0..63 their token's gates and sums.
+        if (hg == 0)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int cc = c32 + (x < n32 ? x : 0);
+                const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + h) * nck + cc) * p.block +
+                                                                   DeltaBlock<2>::OFF_VEC) + kVecScalars * kDeltaC;
+                ick[x] = __ldg(one + kCk);
+                icq[x] = __ldg(one + kCq);
+            }
+        unsigned bits[8];                                 // lane k: part k's largest magnitudes
+        auto max_at = [&](const unsigned *m, size_t first) { return lane < kp ? __ldg(m + first + lane) : 0u; };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const size_t at = (bh * nck + c32 + (x < n32 ? x : 0)) * p.zparts;
+            bits[x] = max_at(p.ymax, at);
+            bits[2 + x] = max_at(p.emax, at);
+            bits[4 + x] = max_at(p.wmax, at);
+        }
+        bits[6] = max_at(p.smax, (bh * nbound + c) * p.zparts);
+        bits[7] = max_at(p.dsmax, (bh * nbound + c + 1) * p.zparts);
         const size_t gate = (size_t(b) * p.seqlen + t0 + (tid & 63)) * p.heads + h;
         float av = 0.f, bv = 0.f, dyy = 0.f, db = 0.f, z = 0.f;
         const bool front = 2 * tid < nt;
         if (tid < nt) {
-            av = fmaxf(p.a[gate], -1e4f);
-            bv = p.beta[gate];
-#pragma unroll 4
-            for (int s = 0; s < p.zparts; ++s) {
-                const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                dyy += p.dyy[x] - p.vw[x];
-                db += p.edu[x];
-            }
-#pragma unroll 4
-            for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
-        }
-        // Scales as powers of two: lane k has those of part k; per product the smallest over the
-        // parts (the products come out times 2^it) and each part's distance to it.
-        int ly[2], le[2], lw[2], ls, ld;
-        auto log_scale = [&](const unsigned *m, size_t first) {
-            return int(__float_as_uint(pow2_for(lane < kp ? __ldg(m + first + lane) : 0u).c) >> 23) - 127;
-        };
+            av = __ldg(p.a + gate);
+            bv = __ldg(p.beta + gate);
+            float v[4][4];
+            for (int s0 = 0; s0 < p.zparts; s0 += 4) {    // zparts is a multiple of 4
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const size_t at = (bh * nck + c32 + (x < n32 ? x : 0)) * p.zparts;
-            ly[x] = log_scale(p.ymax, at);
-            le[x] = log_scale(p.emax, at);
-            lw[x] = log_scale(p.wmax, at);
+                for (int s = 0; s < 4; ++s) {
+                    const size_t x = ((s0 + s) * all + bh) * p.seqlen + t0 + tid;
+                    v[s][0] = __ldg(p.dyy + x);
+                    v[s][1] = __ldg(p.vw + x);
+                    v[s][2] = __ldg(p.edu + x);
+                    v[s][3] = __ldg(p.zsum + ((s0 + s) * all + bh) * nbound + c + (front ? 0 : 1));
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s) { dyy += v[s][0] - v[s][1]; db += v[s][2]; z += v[s][3]; }
+            }
+            av = fmaxf(av, -1e4f);
         }
-        ls = log_scale(p.smax, (bh * nbound + c) * p.zparts);
-        ld = log_scale(p.dsmax, (bh * nbound + c + 1) * p.zparts);
+        if (hg == 0)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) { ick[x] = 1.f / ick[x]; icq[x] = 1.f / icq[x]; }       // powers of two: exact
+        // Scales as powers of two: per product the smallest over the parts (the products come out
+        // times 2^it) and each part's distance to it.
+        int ly[2], le[2], lw[2];
+        auto log_scale = [&](unsigned m) { return int(__float_as_uint(pow2_for(m).c) >> 23) - 127; };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) { ly[x] = log_scale(bits[x]); le[x] = log_scale(bits[2 + x]); lw[x] = log_scale(bits[4 + x]); }
+        const int ls = log_scale(bits[6]), ld = log_scale(bits[7]);
         auto common = [&](int l, float &inv) {
             const int least = __reduce_min_sync(0xffffffffu, lane < kp ? l : 1 << 20);
             inv = exp2_int(-(least >> 1)) * exp2_int((least >> 1) - least);       // 0 when too small for a float
@@ -200,7 +223,8 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
 #pragma unroll
             for (int n = 0; n < 2; ++n) { zero4(x1[u][n]); zero4(x2[u][n]); zero4(x3[u][n]); }
         zero4(x4[0]); zero4(x4[1]);
-        for (int k = 0; k < kp; ++k) {
+#pragma unroll 4
+        for (int k = 0; k < Cfg::PARTS; ++k) {
             unsigned ay[1][4], ae[1][4], aw[1][4];
             const unsigned kt = sbase + k * kTok16;
             ldsm4_t(ay[0], kt + Cfg::OFF_Y + a_tok);
@@ -262,15 +286,36 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
                 const int q0 = 16 * u + 8 * n + 2 * t4;
                 const float2 gh = *reinterpret_cast<const float2 *>(Gh + q0), gl = *reinterpret_cast<const float2 *>(Gl + q0);
                 const float2 bq = *reinterpret_cast<const float2 *>(bet + q0);
+                // f(m, exponent to take, beta of the column): tiles off the diagonal need one side only
+                auto each = [&](auto f) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        f(m, ((grh[m >> 1] - (m & 1 ? gh.y : gh.x)) + (grl[m >> 1] - (m & 1 ? gl.y : gl.x))) * kLog2e,
+                          m & 1 ? bq.y : bq.x);
+                };
+                if (u < rt) {
+                    each([&](int m, float gd, float bc) {
+                        const float d = ex2_approx(gd) * bc;
+                        x1[u][n][m] *= d * e1;
+                        x3[u][n][m] *= d * e3;
+                    });
+                } else if (u > rt) {
+                    each([&](int m, float gd, float) {
+                        const float d = ex2_approx(-gd) * br[m >> 1];
+                        x2[u][n][m] *= d * e2;
+                        x3[u][n][m] *= d * e4;
+                    });
+                } else {
+                    each([&](int m, float gd, float bc) {
+                        const int r = g + 8 * (m >> 1), q = 8 * n + 2 * t4 + (m & 1);
+                        const float d = ex2_approx(q <= r ? gd : -gd) * (q < r ? bc : br[m >> 1]);       // r(the later, the earlier)
+                        x1[u][n][m] = q <= r ? x1[u][n][m] * (d * e1) : 0.f;
+                        x2[u][n][m] = q >= r ? x2[u][n][m] * (d * e2) : 0.f;
+                        x3[u][n][m] = q < r ? x3[u][n][m] * (d * e3) : q > r ? x4[n][m] * (d * e4) : 0.f;
+                    });
+                }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) {
-                    const int r = 16 * rt + g + 8 * (m >> 1), q = q0 + (m & 1);
-                    const float gd = (grh[m >> 1] - (m & 1 ? gh.y : gh.x)) + (grl[m >> 1] - (m & 1 ? gl.y : gl.x));
-                    const float d = ex2_approx((q <= r ? gd : -gd) * kLog2e) *           // r(the later, the earlier)
-                                    (q < r ? (m & 1 ? bq.y : bq.x) : br[m >> 1]);
-                    x1[u][n][m] = q <= r ? x1[u][n][m] * (d * e1) : 0.f;
-                    x2[u][n][m] = q >= r ? x2[u][n][m] * (d * e2) : 0.f;
-                    x3[u][n][m] = q < r ? x3[u][n][m] * (d * e3) : q > r ? (u == rt ? x4[n][m] : x3[u][n][m]) * (d * e4) : 0.f;
                     m1 = fmaxf(m1, fabsf(x1[u][n][m]));
                     m2 = fmaxf(m2, fmaxf(fabsf(x2[u][n][m]), fabsf(x3[u][n][m])));
                 }
@@ -292,21 +337,36 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
             fw[r] = -gam[t] * i6;
             fe[r] = bend[t] * i7;
         }
+        // the A operands of the products with the states, at their common scales; kept for all
+        // columns where they fit
+        constexpr bool HOLD = Cfg::PARTS == 4;
+        unsigned hy[HOLD ? 4 : 1][1][4], hw[HOLD ? 4 : 1][1][4], he[HOLD ? 4 : 1][1][4];
+        auto load_a = [&](int k, unsigned (&sy)[1][4], unsigned (&sw)[1][4], unsigned (&se)[1][4]) {
+            unsigned r[4];
+            const unsigned kt = sbase + k * kTok16 + a_tok;
+            ldsm4_t(r, kt + Cfg::OFF_Y);
+            mul_f16x2(sy[0], r, __shfl_sync(0xffffffffu, f5, k));
+            ldsm4_t(r, kt + Cfg::OFF_W);
+            mul_f16x2(sw[0], r, __shfl_sync(0xffffffffu, f6, k));
+            ldsm4_t(r, kt + Cfg::OFF_E);
+            mul_f16x2(se[0], r, __shfl_sync(0xffffffffu, f7, k));
+        };
+        if constexpr (HOLD)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) load_a(k, hy[k], hw[k], he[k]);
         // 32 columns at a time
 #pragma unroll 1
         for (int j0 = 0; j0 < NP / 32; ++j0) {
             float aq[4][4], ak[4][4], aw[4][4], ae[4][4], am[4][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) { zero4(aq[n]); zero4(ak[n]); zero4(aw[n]); zero4(ae[n]); zero4(am[n]); }
-            for (int k = 0; k < kp; ++k) {
-                unsigned r[4], sy[1][4], sw[1][4], se[1][4];
-                const unsigned kt = sbase + k * kTok16 + a_tok;
-                ldsm4_t(r, kt + Cfg::OFF_Y);
-                mul_f16x2(sy[0], r, __shfl_sync(0xffffffffu, f5, k));
-                ldsm4_t(r, kt + Cfg::OFF_W);
-                mul_f16x2(sw[0], r, __shfl_sync(0xffffffffu, f6, k));
-                ldsm4_t(r, kt + Cfg::OFF_E);
-                mul_f16x2(se[0], r, __shfl_sync(0xffffffffu, f7, k));
+#pragma unroll 4
+            for (int k = 0; k < Cfg::PARTS; ++k) {
+                unsigned ty[1][4], tw[1][4], te[1][4];
+                if constexpr (!HOLD) load_a(k, ty, tw, te);
+                const unsigned (&sy)[1][4] = HOLD ? hy[HOLD ? k : 0] : ty;
+                const unsigned (&sw)[1][4] = HOLD ? hw[HOLD ? k : 0] : tw;
+                const unsigned (&se)[1][4] = HOLD ? he[HOLD ? k : 0] : te;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     unsigned bS[1][4], bD[1][4];
@@ -341,31 +401,55 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
                         for (int n = 0; n < 2; ++n) mma_pieces<1, KP>(am[2 * j + n], a2[u], bQ, n);
                     }
                 }
+            // dq into aq, dk into am; sums over the heads of a key head so far from scratch
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int t = 16 * rt + g + 8 * r, col = 32 * j0 + 8 * n + 2 * t4;
-                    if (t >= nt || col >= p.N) continue;
-                    const size_t off = k0 + size_t(t) * krow + col;
-                    float2 q, k;
-                    q.x = fmaf(c1.inv, ak[n][2 * r], fq[r] * aq[n][2 * r]);
-                    q.y = fmaf(c1.inv, ak[n][2 * r + 1], fq[r] * aq[n][2 * r + 1]);
-                    k.x = fmaf(c2.inv, am[n][2 * r], fmaf(fw[r], aw[n][2 * r], fe[r] * ae[n][2 * r]));
-                    k.y = fmaf(c2.inv, am[n][2 * r + 1], fmaf(fw[r], aw[n][2 * r + 1], fe[r] * ae[n][2 * r + 1]));
-                    if (group > 1) {
+                for (int m = 0; m < 4; ++m) {
+                    aq[n][m] = fmaf(c1.inv, ak[n][m], fq[m >> 1] * aq[n][m]);
+                    am[n][m] = fmaf(c2.inv, am[n][m], fmaf(fw[m >> 1], aw[n][m], fe[m >> 1] * ae[n][m]));
+                }
+            if (group > 1) {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const int t = 16 * rt + g + 8 * r, col = 32 * j0 + 8 * n + 2 * t4;
+                        if (t >= nt || col >= p.N) continue;
+                        const size_t off = k0 + size_t(t) * krow + col;
                         float2 *pq = reinterpret_cast<float2 *>(p.part + off);
                         float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
+                        float2 q = f2(aq[n][2 * r], aq[n][2 * r + 1]), k = f2(am[n][2 * r], am[n][2 * r + 1]);
                         if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
-                        if (hg + 1 < group) {
-                            *pq = q;
-                            *pk = k;
-                            continue;
-                        }
+                        if (hg + 1 < group) { *pq = q; *pk = k; }
+                        aq[n][2 * r] = q.x; aq[n][2 * r + 1] = q.y;
+                        am[n][2 * r] = k.x; am[n][2 * r + 1] = k.y;
                     }
-                    *reinterpret_cast<unsigned *>(static_cast<__nv_bfloat16 *>(p.dq) + off) = pack_bf16x2(q.x, q.y);
-                    *reinterpret_cast<unsigned *>(static_cast<__nv_bfloat16 *>(p.dk) + off) = pack_bf16x2(k.x, k.y);
+            }
+            if (hg + 1 == group) {       // 16 rows of 32 columns through the warp's tile: whole 16-byte stores
+                unsigned char *tile = smem + Cfg::OFF_OUT + rt * kTok16;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float (&f)[4][4] = x ? am : aq;
+#pragma unroll
+                    for (int h2 = 0; h2 < 2; ++h2) {
+                        unsigned r[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) r[m] = pack_bf16x2(f[2 * h2 + (m >> 1)][2 * (m & 1)], f[2 * h2 + (m >> 1)][2 * (m & 1) + 1]);
+                        stsm4(smem_u32(tile) + tok16_at(rb, 2 * h2 + (lane >> 4)), r);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const int r = 8 * y + (lane >> 2), col = 32 * j0 + 8 * (lane & 3);
+                        const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok16_at(r, lane & 3));
+                        if (16 * rt + r < nt && col < p.N)
+                            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(x ? p.dk : p.dq) + k0 +
+                                                       size_t(16 * rt + r) * krow + col) = w;
+                    }
+                    __syncwarp();
                 }
+            }
         }
         if (tid < nt) {
             if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
