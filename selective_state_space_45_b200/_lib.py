@@ -316,24 +316,20 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
 def _require(shapes):
     """Raise ValueError unless every (name, tensor or None, shape, dtype) is given as asked and
     contiguous: the kernels read what the sizes say, so nothing else must reach them.  All
-    tensors have to be on one CUDA device, which is returned."""
+    tensors have to be on one CUDA device."""
     device = None
     for name, t, shape, dtype in shapes:
         if t is None:
             continue
-        if t.shape != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-        if t.dtype != dtype:
-            raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if not t.is_contiguous():
-            raise ValueError("tensors passed to libssm must be contiguous (%s is not)" % name)
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError("%s must be a contiguous %s tensor of shape %s, got %s of shape %s and strides %s" % (
+                name, dtype, tuple(shape), t.dtype, tuple(t.shape), t.stride()))
         if device is None:
             device = t.device
             if device.type != "cuda":
                 raise ValueError("libssm needs CUDA tensors, got %s" % device)
         elif t.device != device:
             raise ValueError("%s is on %s, other tensors on %s" % (name, t.device, device))
-    return device
 
 
 def _dtype_code(name, t):
@@ -347,24 +343,24 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _call_on(device, stream, name, *args, workspace=None):
-    """Run a library call with ``device`` current (its kernels and scratch live there).  Scratch
+def _call_on(like, stream, name, *args, workspace=None):
+    """Run a library call with ``like``'s device current (its kernels and scratch live there).  Scratch
     comes from torch's allocator, on the stream that the call runs on: the memory is not handed
     out again before the call's kernels are done with it."""
-    index = device.index
+    index = like.device.index
     if torch.cuda.current_device() != index:
-        with torch.cuda.device(device):
-            return _call_on(device, stream, name, *args, workspace=workspace)
+        with torch.cuda.device(index):
+            return _call_on(like, stream, name, *args, workspace=workspace)
     lib = _lib or load_library()
     here = torch._C._cuda_getCurrentRawStream(index)
     stream = (here if stream is None else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
     if workspace is not None:
         nbytes = getattr(lib, name + "_workspace")(*workspace)
         if stream == here:
-            ws = torch.empty(nbytes, device=device, dtype=torch.uint8)
+            ws = like.new_empty(nbytes, dtype=torch.uint8)
         else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-                ws = torch.empty(nbytes, device=device, dtype=torch.uint8)
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device)):
+                ws = like.new_empty(nbytes, dtype=torch.uint8)
         args += (ws.data_ptr() if nbytes else None, nbytes)
     _check(getattr(lib, name)(*args, stream))
 
@@ -389,10 +385,10 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
     lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     st = (lead[0], H, P, N)
-    dev = _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
+    _require(shapes + [("y", y, v.shape, y.dtype), ("initial_state", initial_state, st, torch.float32),
                              ("final_state", final_state, st, torch.float32)])
     sizes = (lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("y", y))
-    _call_on(dev, stream, "ssm_delta_rule_fwd", _at(q), _at(k), _at(v), _at(a), _at(beta), _at(y),
+    _call_on(v, stream, "ssm_delta_rule_fwd", _at(q), _at(k), _at(v), _at(a), _at(beta), _at(y),
              _at(initial_state), _at(final_state), float(scale), *sizes, workspace=sizes)
 
 
@@ -412,8 +408,8 @@ def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
     beta [ntok, batch, heads] fp32."""
     lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
-    dev = _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
-    _call_on(dev, stream, "ssm_delta_rule_step", _at(state), _at(q), _at(k), _at(v), _at(a), _at(beta),
+    _require(shapes + [("y", y, v.shape, y.dtype), ("state", state, (lead[1], H, P, N), torch.float32)])
+    _call_on(v, stream, "ssm_delta_rule_step", _at(state), _at(q), _at(k), _at(v), _at(a), _at(beta),
              _at(y), float(scale), lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("y", y))
 
 
@@ -431,13 +427,13 @@ def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk
     lead = v.shape[:2]
     H, K, P, N, shapes = _delta_shapes(lead, q, k, v, a, beta)
     st, f32 = (lead[0], H, P, N), torch.float32
-    dev = _require(shapes + [
+    _require(shapes + [
         ("initial_state", initial_state, st, f32), ("dy", dy, v.shape, dy.dtype),
         ("dfinal_state", dfinal_state, st, f32), ("dq", dq, q.shape, dy.dtype), ("dk", dk, k.shape, dy.dtype),
         ("dv", dv, v.shape, dy.dtype), ("da", da, a.shape, f32), ("dbeta", dbeta, beta.shape, f32),
         ("dinitial_state", dinitial_state, st, f32)])
     sizes = (lead[0], lead[1], H, K, P, N, _dtype_code("v", v), _dtype_code("dy", dy))
-    _call_on(dev, stream, "ssm_delta_rule_bwd", _at(q), _at(k), _at(v), _at(a), _at(beta),
+    _call_on(v, stream, "ssm_delta_rule_bwd", _at(q), _at(k), _at(v), _at(a), _at(beta),
              _at(initial_state), _at(dy), _at(dfinal_state), _at(dq), _at(dk), _at(dv), _at(da), _at(dbeta),
              _at(dinitial_state), float(scale), *sizes, workspace=sizes)
 
@@ -456,10 +452,15 @@ def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, 
 def ssm_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, stream=None):
     """Layer norm over the last dimension (see include/ssm.h): x, y [..., dim]; weight, bias
     [dim] fp32 or None; mean, rstd fp32, one value per row, or None.  Writes in place."""
-    dim, f32 = x.shape[-1], torch.float32
-    dev = _require([("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32), ("bias", bias, (dim,), f32),
-                    ("y", y, x.shape, y.dtype), ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32)])
-    _call_on(dev, stream, "ssm_layer_norm_fwd", _at(x), _at(weight), _at(bias), _at(y), _at(mean),
+    shape, f32 = x.shape, torch.float32
+    dim = shape[-1]
+    _require((("x", x, shape, x.dtype), ("weight", weight, shape[-1:], f32), ("bias", bias, shape[-1:], f32),
+                    ("y", y, shape, y.dtype), ("mean", mean, shape[:-1], f32), ("rstd", rstd, shape[:-1], f32)))
+    _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, dim, stream)
+
+
+def _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, dim, stream):
+    _call_on(x, stream, "ssm_layer_norm_fwd", _at(x), _at(weight), _at(bias), _at(y), _at(mean),
              _at(rstd), float(eps), x.numel() // dim if dim else 0, dim, _dtype_code("x", x), _dtype_code("y", y))
 
 
@@ -471,7 +472,10 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats
     if return_stats:
         mean = x.new_empty(x.shape[:-1], dtype=torch.float32)
         rstd = torch.empty_like(mean)
-    ssm_layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, stream)
+    shape = x.shape
+    _require((("x", x, shape, x.dtype), ("weight", weight, shape[-1:], torch.float32),
+                    ("bias", bias, shape[-1:], torch.float32)))
+    _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, shape[-1], stream)
     return (y, mean, rstd) if return_stats else y
 
 
@@ -479,11 +483,11 @@ def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, 
     """Backward of the layer norm (see include/ssm.h): dx in dy's dtype; dweight, dbias [dim]
     fp32 or None.  Writes the gradients in place."""
     dim, f32 = x.shape[-1], torch.float32
-    dev = _require([("dy", dy, x.shape, dy.dtype), ("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32),
+    _require([("dy", dy, x.shape, dy.dtype), ("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32),
                     ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32),
                     ("dx", dx, x.shape, dy.dtype), ("dweight", dweight, (dim,), f32), ("dbias", dbias, (dim,), f32)])
     rows = x.numel() // dim if dim else 0
-    _call_on(dev, stream, "ssm_layer_norm_bwd", _at(dy), _at(x), _at(weight), _at(mean), _at(rstd),
+    _call_on(x, stream, "ssm_layer_norm_bwd", _at(dy), _at(x), _at(weight), _at(mean), _at(rstd),
              _at(dx), _at(dweight), _at(dbias), rows, dim, _dtype_code("x", x), _dtype_code("dy", dy),
              workspace=(rows, dim))
 

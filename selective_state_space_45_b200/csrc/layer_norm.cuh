@@ -112,22 +112,24 @@ template <int V, bool VEC, typename T> struct RawRow {
     }
 };
 
-// Sums of two values over a group, to all of its lanes.  LANES = 8 or 32: shuffles; 0: the
-// CTA, through shared memory, with two buffers in turn so that one barrier per sum is enough.
-template <int LANES> __device__ __forceinline__ float2 group_sum(float2 v, float2 *sm, int &turn) {
+// The sum of a value, or of a pair, over a group, to all of its lanes.  LANES = 8 or 32:
+// shuffles; 0: the CTA, through shared memory, with two buffers in turn so that one barrier per
+// sum is enough.
+__device__ __forceinline__ float add_up(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add_up(float2 a, float2 b) { return fadd2(a, b); }
+__device__ __forceinline__ float shfl_xor(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ float2 shfl_xor(float2 v, int o) { return f2(shfl_xor(v.x, o), shfl_xor(v.y, o)); }
+template <int LANES, typename T> __device__ __forceinline__ T group_sum(T v, float2 *sm, int &turn) {
 #pragma unroll
-    for (int o = (LANES == 8 ? 4 : 16); o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    for (int o = (LANES == 8 ? 4 : 16); o > 0; o >>= 1) v = add_up(v, shfl_xor(v, o));
     if constexpr (LANES == 0) {
-        float2 *buf = sm + (turn & 1) * 32;
+        T *buf = reinterpret_cast<T *>(sm + (turn & 1) * 32);
         ++turn;
         if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
         __syncthreads();
         const int nw = blockDim.x >> 5;
-        v = f2(0.f, 0.f);
-        for (int w = 0; w < nw; ++w) v = fadd2(v, buf[w]);
+        v = T{};
+        for (int w = 0; w < nw; ++w) v = add_up(v, buf[w]);
     }
     return v;
 }
@@ -147,60 +149,96 @@ template <int LANES> struct NormGroups {
     }
 };
 
-template <int LANES, int V, bool VEC, typename Tin, typename Tout>
+// R rows per group and step (narrow rows: more bytes in flight).  The arithmetic runs on packed
+// pairs: with one value an instruction, rows of 64 were bound by issue (24.5 us for 393216).
+template <int LANES, int V, int R, bool VEC, typename Tin, typename Tout>
 __global__ void __launch_bounds__(LANES ? 256 : 512) layer_norm_fwd_kernel(const NormArgs p) {
     __shared__ float2 sm[64];
     const NormGroups<LANES> gr;
     const RowLanes<V, VEC> r{gr.l, gr.G, p.dim};
     const Tin *x = static_cast<const Tin *>(p.x);
     Tout *y = static_cast<Tout *>(p.out);
-    RawRow<V, VEC, Tin> next;
+    RawRow<V, VEC, Tin> next[R];
     // whole warps walk the same number of steps (a narrow group past the end repeats row 0)
-    const long long steps = (p.rows - gr.first + gr.stride - 1) / gr.stride;
+    const long long steps = (p.rows - gr.first + gr.stride * R - 1) / (gr.stride * R);
     const long long all = LANES == 8 ? (long long)__reduce_max_sync(0xffffffffu, unsigned(steps > 0 ? steps : 0))
                                      : (steps > 0 ? steps : 0);
     if (all == 0) return;
-    auto row_of = [&](long long i) { const long long n = gr.first + i * gr.stride; return n < p.rows ? n : 0; };
-    next.fetch(x + size_t(row_of(0)) * p.dim, r);
+    auto fetch = [&](long long i) {
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            const long long n = gr.first + (i * R + m) * gr.stride;
+            next[m].fetch(x + size_t(n < p.rows ? n : 0) * p.dim, r);
+        }
+    };
+    fetch(0);
     float w[V][8], b[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) { w[v][k] = 1.f; b[v][k] = 0.f; }
     if (p.w != nullptr) r.load(p.w, w, 0.f);
     if (p.b != nullptr) r.load(p.b, b, 0.f);
     const float inv = 1.f / float(p.dim);
     int turn = 0;
     for (long long i = 0; i < all; ++i) {
-        float f[V][8];
-        next.widen(f);
-        const long long row = row_of(i);
-        if (i + 1 < all) next.fetch(x + size_t(row_of(i + 1)) * p.dim, r);
-        float s = 0.f;
+        float f[R][V][8];
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int m = 0; m < R; ++m) next[m].widen(f[m]);
+        if (i + 1 < all) fetch(i + 1);
+        float mean[R], rstd[R];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s += f[v][k];
-        const float mean = group_sum<LANES>(f2(s, 0.f), sm, turn).x * inv;
-        float q = 0.f;
+        for (int m = 0; m < R; ++m) {
+            float2 s = f2(0.f, 0.f);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                f[v][k] = r.has(v, k) ? f[v][k] - mean : 0.f;
-                q = fmaf(f[v][k], f[v][k], q);
+                for (int k = 0; k < 8; k += 2) s = fadd2(s, f2(f[m][v][k], f[m][v][k + 1]));
+            mean[m] = s.x + s.y;
+        }
+#pragma unroll
+        for (int m = 0; m < R; ++m) mean[m] = group_sum<LANES>(mean[m], sm, turn) * inv;
+#pragma unroll
+        for (int m = 0; m < R; ++m) {
+            float2 q = f2(0.f, 0.f);
+            const float2 mm = f2(-mean[m], -mean[m]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                float2 qv = f2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    float2 c = fadd2(f2(f[m][v][k], f[m][v][k + 1]), mm);
+                    if constexpr (!VEC) {               // values past the row: nothing
+                        if (!r.has(v, k)) c.x = 0.f;
+                        if (!r.has(v, k + 1)) c.y = 0.f;
+                    }
+                    f[m][v][k] = c.x; f[m][v][k + 1] = c.y;
+                    qv = ffma2(c, c, qv);
+                }
+                if (!VEC || r.has(v, 0)) q = fadd2(q, qv);
             }
-        const float var = group_sum<LANES>(f2(q, 0.f), sm, turn).x * inv;
-        const float rstd = 1.f / sqrtf(var + p.eps);
+            rstd[m] = q.x + q.y;
+        }
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int m = 0; m < R; ++m) rstd[m] = 1.f / sqrtf(group_sum<LANES>(rstd[m], sm, turn) * inv + p.eps);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                f[v][k] *= rstd;
-                if (p.w != nullptr) f[v][k] *= w[v][k];
-                if (p.b != nullptr) f[v][k] += b[v][k];
-            }
-        if (gr.first + i * gr.stride < p.rows) {
-            r.store(y + size_t(row) * p.dim, f);
-            if (r.l == 0) {
-                if (p.mean != nullptr) p.mean[row] = mean;
-                if (p.rstd != nullptr) p.rstd[row] = rstd;
+        for (int m = 0; m < R; ++m) {
+            const long long row = gr.first + (i * R + m) * gr.stride;
+            const float2 rr = f2(rstd[m], rstd[m]);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int k = 0; k < 8; k += 2) {
+                    const float2 o = ffma2(fmul2(f2(f[m][v][k], f[m][v][k + 1]), rr), f2(w[v][k], w[v][k + 1]),
+                                           f2(b[v][k], b[v][k + 1]));
+                    f[m][v][k] = o.x; f[m][v][k + 1] = o.y;
+                }
+            if (row < p.rows) {
+                r.store(y + size_t(row) * p.dim, f[m]);
+                if (r.l == 0) {
+                    if (p.mean != nullptr) p.mean[row] = mean[m];
+                    if (p.rstd != nullptr) p.rstd[row] = rstd[m];
+                }
             }
         }
     }
@@ -305,22 +343,24 @@ __global__ void __launch_bounds__(LANES ? 256 : 512) layer_norm_bwd_kernel(const
     }
 }
 
-// out[c] = sum over n parts of part[i][c], c < cols: 32 columns x 8 interleaved sums per CTA,
+// out[c] = sum over n parts of part[i][c], c < cols: 32 columns x 32 interleaved sums per CTA,
 // added in a fixed order.  Columns below `dim` go to dw, the others to db.
-__global__ void __launch_bounds__(256) layer_norm_cols_kernel(const float *part, int n, int dim, float *dw, float *db) {
-    __shared__ float sm[8][33];
+__global__ void __launch_bounds__(1024) layer_norm_cols_kernel(const float *part, int n, int dim, float *dw, float *db) {
+    __shared__ float sm[32][33];
     const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5, c = blockIdx.x * 32 + cx;
     float s = 0.f;
     if (c < 2 * dim)
 #pragma unroll 8
-        for (int i = ry; i < n; i += 8) s += part[size_t(i) * 2 * dim + c];
+        for (int i = ry; i < n; i += 32) s += part[size_t(i) * 2 * dim + c];
     sm[ry][cx] = s;
     __syncthreads();
-    if (ry == 0 && c < 2 * dim) {
+    s = sm[cx][ry];                      // column ry's sums, one per lane
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += sm[i][cx];
-        if (c < dim) { if (dw != nullptr) dw[c] = s; }
-        else if (db != nullptr) db[c - dim] = s;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int out = blockIdx.x * 32 + ry;
+    if (cx == 0 && out < 2 * dim) {
+        if (out < dim) { if (dw != nullptr) dw[out] = s; }
+        else if (db != nullptr) db[out - dim] = s;
     }
 }
 

@@ -34,10 +34,19 @@ int grid_of(int lanes, int threads, int per_sm, int rows) {
     return std::min((rows - 1) / per_cta + 1, kSMs * std::max(1, per_sm / threads));
 }
 
+// Threads of a kernel that an SM's registers hold at once.
+template <typename K> int resident(K kernel) {
+    cudaFuncAttributes at{};
+    if (cudaFuncGetAttributes(&at, kernel) != cudaSuccess) { cudaGetLastError(); return 512; }
+    return std::min(2048, 65536 / ((std::max(at.numRegs, 32) + 7) / 8 * 8) / 32 * 32);
+}
+
 template <bool VEC, typename Tin, typename Tout> int run_fwd(const ssm::NormArgs &a, cudaStream_t s) {
     return by_width<false>(a.dim, [&](auto lanes, auto v, int threads) {
-        auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), VEC, Tin, Tout>;
-        kernel<<<grid_of(lanes(), threads, 1024, int(a.rows)), threads, 0, s>>>(a);
+        constexpr int R = lanes() == 8 && v() == 1 ? 4 : lanes() == 8 || (lanes() == 32 && v() == 1) ? 2 : 1;
+        auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), R, VEC, Tin, Tout>;
+        static const int per_sm = resident(kernel);
+        kernel<<<grid_of(lanes(), threads, per_sm, int(a.rows)), threads, 0, s>>>(a);
         return status_of(cudaGetLastError());
     });
 }
@@ -58,7 +67,7 @@ int run_bwd(ssm::NormArgs a, float *dw, float *db, void *workspace, size_t bytes
         return status_of(cudaGetLastError());
     });
     if (st == SSM_OK && (dw != nullptr || db != nullptr)) {
-        ssm::layer_norm_cols_kernel<<<(2 * a.dim + 31) / 32, 256, 0, s>>>(a.part, grid, a.dim, dw, db);
+        ssm::layer_norm_cols_kernel<<<(2 * a.dim + 31) / 32, 1024, 0, s>>>(a.part, grid, a.dim, dw, db);
         st = status_of(cudaGetLastError());
     }
     return ws.release(st);
