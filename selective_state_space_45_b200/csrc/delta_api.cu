@@ -2,6 +2,9 @@
 // over decode tokens (ssm_delta_rule_step).  Arguments are checked on the host before
 // anything is launched.  The forward takes scratch (the caller's workspace or a stream-ordered
 // buffer), the step none.
+#include <algorithm>
+#include <cmath>
+
 #include "delta_host.cuh"
 #include "delta_step.cuh"
 
@@ -20,22 +23,83 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
     return status_of(cudaGetLastError());
 }
 
-// Forward: the chunk blocks and operands, then the chains.
-template <typename Tin, typename Tout> size_t fwd_bytes(int batch, int seqlen, int heads, int qk_heads, int N) {
-    return prep_bytes<ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>>(batch, seqlen, heads) +
-           rows_bytes(batch, seqlen, qk_heads, N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
+// How many segments a sequence is cut into.  A chain's chunks follow one another, so with few
+// heads most of the GPU is idle.  Segments run at once: first every segment's end state from a
+// zero start and its map (dstate more rows), then, from the folded start states, the outputs.
+// In units of a chunk's time in a CTA (1.5 us; 0.9 of it without outputs): two CTAs on an SM take
+// 1.9, more share it; fp32 inputs leave room for one CTA.  Folding costs about four units a
+// segment.  Segments have at least 16 chunks, and what they save must be a tenth.  32749 tokens
+// of 16 heads of 128 x 128: one piece 1565 us, five 1044 us, nine 850 us (and 94 us for the
+// chunk blocks).
+int segments(int batch, int seqlen, int heads, int P, int N, bool one_per_sm) {
+    const long long chunks = (long long)delta_chunks(seqlen), all = (long long)batch * heads;
+    auto cost = [&](double ctas) {
+        const double r = ctas / 148;
+        return r <= 1 ? 1.0 : one_per_sm ? std::ceil(r) : r <= 2 ? 1.9 : r;
+    };
+    const double rows = double(all) * delta_slices(P), maps = double(all) * delta_slices(N);
+    int best = 1;
+    double least = chunks * cost(rows);
+    const double bar = 0.9 * least;
+    for (int n = 2; n <= 64 && chunks / n >= 16; ++n) {
+        const double t = double((chunks + n - 1) / n) * (0.9 * cost((n - 1) * rows + (n - 2) * maps) + cost(n * rows)) + 4 * n;
+        if (t < bar && t < least) { least = t; best = n; }
+    }
+    return best;
 }
 
+struct FwdPlan {
+    int nseg;
+    size_t prep, rows, seg_state, seg_map, all;      // offsets, and the bytes
+    FwdPlan(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int out_dtype) {
+        const size_t blocks = out_dtype == SSM_F32 ? prep_bytes<ssm::DeltaBlock<2>>(batch, seqlen, heads)
+                                                   : prep_bytes<ssm::DeltaBlock<1>>(batch, seqlen, heads);
+        nseg = segments(batch, seqlen, heads, P, N, in_dtype == SSM_F32);
+        const size_t seg = nseg > 1 ? size_t(batch) * heads * nseg * N * 4 : 0;
+        prep = 0;
+        rows = prep + round16(blocks);
+        seg_state = rows + round16(rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
+        seg_map = seg_state + seg * P;
+        all = seg_map + seg * N;
+    }
+};
+
+// Forward: the chunk blocks and operands, then the chains, in segments where that pays.
 template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *workspace, size_t bytes, cudaStream_t s) {
-    using Block = ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>;
+    const FwdPlan at(a.batch, a.seqlen, a.heads, a.qk_heads, a.P, a.N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16,
+                     sizeof(Tout) == 4 ? SSM_F32 : SSM_BF16);
+    constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
     Scratch ws;
-    if (const int st = ws.take(workspace, bytes, fwd_bytes<Tin, Tout>(a.batch, a.seqlen, a.heads, a.qk_heads, a.N), s))
-        return st;
-    a.prep = ws.p;
-    a.rows = ws.p + prep_bytes<Block>(a.batch, a.seqlen, a.heads);
+    if (const int st = ws.take(workspace, bytes, at.all, s)) return st;
+    a.prep = ws.p + at.prep;
+    a.rows = ws.p + at.rows;
+    a.seg_state = reinterpret_cast<float *>(ws.p + at.seg_state);
+    a.seg_map = reinterpret_cast<float *>(ws.p + at.seg_map);
     a.timeouts = wait_counter();
-    int st = a.timeouts ? dispatch_prep<Tin, Block>(a, s) : int(SSM_ERR_CUDA);
-    if (st == SSM_OK) st = dispatch_chain<sizeof(Tin) == 4 ? 2 : 1, Tin, Tin, Tout, 0>(a, s);
+    int st = a.timeouts ? dispatch_prep<Tin, ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>>(a, s) : int(SSM_ERR_CUDA);
+    if (at.nseg > 1) {
+        const long long chunks = (long long)delta_chunks(a.seqlen);
+        a.seg_chunks = int((chunks + at.nseg - 1) / at.nseg);
+        const int nseg = int((chunks + a.seg_chunks - 1) / a.seg_chunks);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, Tout, 3>(a, s, nseg);
+        if (st == SSM_OK) {
+            const unsigned ctas = unsigned(a.batch) * unsigned(a.heads) * unsigned((a.P + 7) / 8);
+            ssm::delta_fold_kernel<8><<<ctas, 128, 0, s>>>(a, nseg);
+            st = status_of(cudaGetLastError());
+        }
+        // a state carried in place: the last segment's end must not be written before the first
+        // segment has read its start, so it goes by the slot that the last segment leaves unused
+        float *const end = a.hN;
+        const size_t state = size_t(a.P) * a.N * 4;
+        const bool in_place = end != nullptr && end == a.h0;
+        a.end_slot = in_place;
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, Tout, 0>(a, s, nseg);
+        if (st == SSM_OK && in_place)
+            st = status_of(cudaMemcpy2DAsync(end, state, ws.p + at.seg_state + (nseg - 1) * state, nseg * state, state,
+                                             size_t(a.batch) * a.heads, cudaMemcpyDeviceToDevice, s));
+    } else if (st == SSM_OK) {
+        st = dispatch_chain<KP, Tin, Tin, Tout, 0>(a, s);
+    }
     return ws.release(st);
 }
 
@@ -47,12 +111,8 @@ size_t ssm_delta_rule_fwd_workspace(int batch, int seqlen, int heads, int qk_hea
                                     int in_dtype, int out_dtype) {
     if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return 0;
     if (delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate) != SSM_OK) return 0;
-    using bf16 = __nv_bfloat16;
-    if (in_dtype == SSM_BF16)
-        return out_dtype == SSM_BF16 ? fwd_bytes<bf16, bf16>(batch, seqlen, heads, qk_heads, dstate)
-                                     : fwd_bytes<bf16, float>(batch, seqlen, heads, qk_heads, dstate);
-    return out_dtype == SSM_BF16 ? fwd_bytes<float, bf16>(batch, seqlen, heads, qk_heads, dstate)
-                                 : fwd_bytes<float, float>(batch, seqlen, heads, qk_heads, dstate);
+    if (batch == 0 || heads == 0 || seqlen == 0) return 0;
+    return FwdPlan(batch, seqlen, heads, qk_heads, headdim, dstate, in_dtype, out_dtype).all;
 }
 
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

@@ -3,7 +3,7 @@
 
 #include <climits>
 
-#include "api_host.cuh"
+#include "api_scratch.cuh"
 #include "delta_rule.cuh"
 
 namespace ssm_host {
@@ -64,23 +64,25 @@ constexpr int kDeltaWarps = 4;
 inline int delta_slices(int P) { return (P + 16 * kDeltaWarps - 1) / (16 * kDeltaWarps); }
 
 template <int NP, int KP, typename Tv, typename Tv2, typename Tout, int MODE>
-int launch_chain(ssm::DeltaArgs a, cudaStream_t s) {
+int launch_chain(ssm::DeltaArgs a, int nseg, cudaStream_t s) {
     using Cfg = ssm::DeltaCfg<NP, kDeltaWarps, KP, Tv, Tv2, Tout, MODE>;
     a.slices = delta_slices(a.P);
-    const long long ctas = (long long)a.batch * a.heads * a.slices;
+    if (nseg == 1) a.seg_chunks = int(delta_chunks(a.seqlen));
+    // MODE 3 has the identity's rows beside those of headdim
+    const long long ctas = (long long)a.batch * a.heads * (a.slices + (MODE == 3 ? delta_slices(a.N) : 0));
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
     if (const int st = set_smem(ssm::delta_chain_kernel<Cfg>, int(Cfg::SMEM_BYTES))) return st;
-    ssm::delta_chain_kernel<Cfg><<<unsigned(ctas), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
+    ssm::delta_chain_kernel<Cfg><<<dim3(unsigned(ctas), unsigned(nseg)), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
     return status_of(cudaGetLastError());
 }
 
 template <int KP, typename Tv, typename Tv2, typename Tout, int MODE>
-int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s) {
+int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s, int nseg = 1) {
     switch (padded_state(a.N)) {
-    case 32: return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, s);
-    case 64: return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, s);
-    case 96: return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, s);
-    default: return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, s);
+    case 32: return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
+    case 64: return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
+    case 96: return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
+    default: return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
     }
 }
 

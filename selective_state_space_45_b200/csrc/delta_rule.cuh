@@ -69,6 +69,12 @@ struct DeltaArgs {
     unsigned *smax;         // [batch][heads][boundaries][parts] largest |S| (reverse pass: |dS|), as bits
     unsigned *emax, *ymax;  // [batch][heads][chunks][parts] bounds of |e| (reverse pass: |w|) and, in the
                             // reverse pass, the largest |dy|
+    // Segments of a long sequence with few heads (forward only): chunks per segment, and per segment
+    // [batch][heads][segments] the end state from a zero start (the first: from h0), later the next
+    // one's start state, and the map that takes a start state's rows to their part of the end state.
+    int seg_chunks;
+    float *seg_state, *seg_map;     // [headdim][dstate], [dstate][dstate]
+    bool end_slot;                  // the end state goes to the last segment's slot of seg_state, not hN
     int batch, seqlen, heads, qk_heads, P, N, slices;
     float scale;
 };
@@ -121,7 +127,8 @@ template <int NP> struct State16 {
 constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's limit, about a second
 
 // NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k.  MODE 0:
-// forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass.
+// forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass; 3:
+// a segment's end state and map (the recurrence of the identity's rows with v = 0).
 template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
     using Tv = Tv_;        // v, or dy in the reverse pass
@@ -130,7 +137,7 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int C = kDeltaC, NT = 32 * NW;
     static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
     static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
-    static constexpr int PO = MODE != 0 || sizeof(Tout) == 4 ? 2 : 1;         // pieces behind y
+    static constexpr int PO = MODE == 1 || MODE == 2 || sizeof(Tout) == 4 ? 2 : 1;       // pieces behind y
     using Block = DeltaBlock<PO>;
     using Rows = DeltaRows<NP, KP>;
     static constexpr int KROW = Rows::ROW;
@@ -139,8 +146,9 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int PIECE = Rows::PIECE;
     static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
     static constexpr int OFF_V = OFF_TRI + Block::BYTES, OFF_V2 = OFF_V + C * VROW;
-    static constexpr int STAGE = OFF_V2 + (MODE != 0 ? C * V2ROW : 0);
-    static constexpr int STAGES = MODE == 0 && KP == 1 ? 3 : 2;               // three where two CTAs still fit
+    static constexpr bool BWD = MODE == 1 || MODE == 2;
+    static constexpr int STAGE = OFF_V2 + (BWD ? C * V2ROW : 0);
+    static constexpr int STAGES = !BWD && KP == 1 ? 3 : 2;                // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
     static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
     static constexpr bool G16 = MODE == 1 ? sizeof(Tv2) == 2 : MODE == 2 && sizeof(Tv) == 2;      // bf16 gradients
@@ -585,18 +593,25 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     using Tout = typename Cfg::Tout;
     using Block = typename Cfg::Block;
     constexpr int C = Cfg::C, NP = Cfg::NP, NW = Cfg::NW, MODE = Cfg::MODE, KP = Cfg::KP, PO = Cfg::PO, PV = Cfg::PV;
-    constexpr bool REV = MODE == 2;
+    constexpr bool REV = MODE == 2, BWD = Cfg::BWD, STATE = MODE == 3;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = int(blockIdx.x % unsigned(p.slices));
-    const int bh = int(blockIdx.x / unsigned(p.slices));
+    // STATE: after the slices of headdim come those of the identity's rows (dstate of them)
+    const int nslice = STATE ? p.slices + (p.N + 16 * NW - 1) / (16 * NW) : p.slices;
+    const int slice0 = int(blockIdx.x % unsigned(nslice)), bh = int(blockIdx.x / unsigned(nslice));
+    const bool ident = STATE && slice0 >= p.slices;
+    const int slice = ident ? slice0 - p.slices : slice0, rows = ident ? p.N : p.P;
+    const int seg = int(blockIdx.y);
+    // the first segment starts from h0 itself; nothing starts from the last one's end
+    if (STATE && (seg + 1 == int(gridDim.y) || (ident && seg == 0))) return;
     const int b = bh / p.heads, h = bh - b * p.heads;
     const int nchunk = (p.seqlen + C - 1) / C;
-    // chunk of loop step i: forwards, or backwards in the reverse pass
-    auto chunk_of = [&](int i) { return REV ? nchunk - 1 - i : i; };
+    // this segment's steps; chunk of loop step i: forwards, or backwards in the reverse pass
+    const int first = seg * p.seg_chunks, count = min(p.seg_chunks, nchunk - first);
+    auto chunk_of = [&](int i) { return REV ? nchunk - 1 - i : first + i; };
 
-    const int hk = h / (p.heads / p.qk_heads), prow = p.P - slice * NW * 16;
+    const int hk = h / (p.heads / p.qk_heads), prow = rows - slice * NW * 16;
     const size_t vrow = size_t(p.heads) * p.P;
     const int active = min(NW, (prow + 15) / 16);          // warps with rows
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::OFF_BAR), *empty = full + Cfg::STAGES;
@@ -645,16 +660,16 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         }
         __syncwarp();
         const size_t at = voff + size_t(c) * C * vrow;
-        copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + at, ntok);
-        if constexpr (MODE != 0) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
+        if (!ident) copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + at, ntok);
+        if constexpr (BWD) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
         mbar_arrive_cp_async(&full[slot]);
     };
     if (warp == 0)
-        for (int i = 0; i + 1 < Cfg::STAGES && i < nchunk; ++i) issue(i);
+        for (int i = 0; i + 1 < Cfg::STAGES && i < count; ++i) issue(i);
 
     const int g = lane >> 2, t4 = lane & 3;
     const int p0 = slice * NW * 16 + warp * 16;           // the warp's first row
-    const int nrow = p.P - p0;                             // its rows (<= 0: none, may exceed 16)
+    const int nrow = rows - p0;                            // its rows (<= 0: none, may exceed 16)
     float s[NP / 8][4];
     const size_t sbase = size_t(bh) * p.P * p.N;
     auto state_io = [&](auto f) {                          // f(accumulator pair, offset) of each pair held
@@ -668,11 +683,26 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     };
 #pragma unroll
     for (int j = 0; j < NP / 8; ++j) zero4(s[j]);
-    if (p.h0 != nullptr)
+    const int nseg = int(gridDim.y);
+    const float *start = ident || (STATE && seg > 0) ? nullptr
+                         : seg > 0 ? p.seg_state + (size_t(bh) * nseg + seg - 1) * p.P * p.N
+                         : p.h0 ? p.h0 + sbase : nullptr;
+    if (start != nullptr)
         state_io([&](float &x, float &y, size_t off) {
-            const float2 f = *reinterpret_cast<const float2 *>(p.h0 + sbase + off);
+            const float2 f = *reinterpret_cast<const float2 *>(start + off);
             x = f.x; y = f.y;
         });
+    if (ident) {                                           // rows of the identity, and no v
+#pragma unroll
+        for (int j = 0; j < NP / 8; ++j)
+#pragma unroll
+            for (int m = 0; m < 4; ++m) s[j][m] = p0 + g + 8 * (m >> 1) == 8 * j + 2 * t4 + (m & 1) ? 1.f : 0.f;
+        for (int i = 0; i < Cfg::STAGES; ++i)              // each warp its own columns of the staged rows
+            for (int x = lane; x < C * sizeof(Tv); x += 32)
+                *reinterpret_cast<uint4 *>(smem + i * Cfg::STAGE + Cfg::OFF_V + (x / sizeof(Tv)) * Cfg::VROW +
+                                           warp * 16 * sizeof(Tv) + (x % sizeof(Tv)) * 16) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+    }
     unsigned char *tile = smem + Cfg::OFF_OUT + warp * Cfg::OUT;
     const unsigned bn = b_rows_n(lane, Cfg::KROW), bk = b_rows_k(lane, Cfg::KROW);
     const unsigned tr = REV ? tri_rows_k(lane) : tri_rows_n(lane);
@@ -767,7 +797,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         for (int n = 0; n < 4; ++n) at[32 * n] = make_float4(f[n][0], f[n][1], f[n][2], f[n][3]);
     };
     if (nrow <= 0) {                                       // rows past headdim
-        if constexpr (MODE != 0)
+        if constexpr (BWD)
             for (int t = lane; t < p.seqlen; t += 32) {
                 p.sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
                 if constexpr (REV) p.sum2[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
@@ -785,7 +815,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
         for (int m = 0; m < 4; ++m) ms = fmaxf(ms, fabsf(s[j][m]));
 
-    for (int i = 0; i < nchunk; ++i) {
+    for (int i = 0; i < count; ++i) {
         const int c = chunk_of(i);
         constexpr int CS = kDeltaSave / C;
         const size_t tok0 = (size_t(b) * p.seqlen + size_t(c) * C) * p.heads + h;
@@ -832,7 +862,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < KP; ++m) {
                     ldsm4(kb[h2][m], kbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
-                    if constexpr (MODE != 2) ldsm4(qb[h2][m], qbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
+                    if constexpr (!REV && !STATE) ldsm4(qb[h2][m], qbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
                 }
         };
         load_kq(0);
@@ -845,7 +875,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     mma_pieces<2, KP>(sk[2 * h2 + n], A, kb[h2], n);
-                    if constexpr (MODE != 2) {
+                    if constexpr (!REV && !STATE) {
                         unsigned Ao[PO][4];
 #pragma unroll
                         for (int m = 0; m < PO; ++m)
@@ -860,7 +890,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         // turn it is starts the copies into it.
         if (--turn == 0) {
             turn = active;
-            if (i + Cfg::STAGES - 1 < nchunk) issue(i + Cfg::STAGES - 1);
+            if (i + Cfg::STAGES - 1 < count) issue(i + Cfg::STAGES - 1);
         }
         Tok v, x, du;
         load_tok<Tv>(stage + Cfg::OFF_V + warp * 16 * int(sizeof(Tv)), Cfg::VROW, lane, v);
@@ -917,13 +947,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             if constexpr (REV) scale_tok(x, du, vec + kVecBeta * C, t4);
         }
         const unsigned mx = __float_as_uint(isfinite(grown) ? grown : 0.f);
-        if constexpr (MODE != 0)
+        if constexpr (BWD)
             if (lane == 0) {
                 p.emax[(size_t(bh) * nchunk + c) * parts + part] = mx;
                 if constexpr (REV) p.ymax[(size_t(bh) * nchunk + c) * parts + part] = mv;
             }
         Tok o;
-        if constexpr (!REV) {
+        if constexpr (!REV && !STATE) {
             // y = scale gam S q + Pm (beta e)
             unsigned A[2][PO][4];
             const Pow2 cu = scale_by(mx, one[kMaxBeta]);
@@ -1025,10 +1055,54 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     }
     if constexpr (MODE == 1) keep_state(p.ck, nbound - 1);
     if constexpr (REV) dot_state(0);
-    if (p.hN != nullptr)
-        state_io([&](float &x, float &y, size_t off) {
-            *reinterpret_cast<float2 *>(p.hN + sbase + off) = make_float2(x, y);
-        });
+    float *end = ident ? p.seg_map + (size_t(bh) * nseg + seg) * p.N * p.N
+                 : STATE ? p.seg_state + (size_t(bh) * nseg + seg) * p.P * p.N
+                 : !p.hN || first + count < nchunk ? nullptr
+                 : p.end_slot ? p.seg_state + (size_t(bh) * nseg + seg) * p.P * p.N : p.hN + sbase;
+    if (end != nullptr)
+        state_io([&](float &x, float &y, size_t off) { *reinterpret_cast<float2 *>(end + off) = make_float2(x, y); });
+}
+
+// The segments' start states: behind segment 0 the state that it ended with, then
+//     start(i + 1) = start(i) map(i) + end(i)
+// in place of end(i).  A CTA takes R rows of one head through the segments, thread j column j.
+template <int R>
+__global__ void __launch_bounds__(128) delta_fold_kernel(const DeltaArgs p, int nseg) {
+    __shared__ __align__(16) float row[R][128];
+    const int tiles = (p.P + R - 1) / R, bh = int(blockIdx.x) / tiles, r0 = (int(blockIdx.x) % tiles) * R, j = threadIdx.x;
+    const int nr = min(R, p.P - r0);
+    float *st = p.seg_state + (size_t(bh) * nseg * p.P + r0) * p.N;
+    const float *map = p.seg_map + size_t(bh) * nseg * p.N * p.N;
+    float x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = r < nr && j < p.N ? st[size_t(r) * p.N + j] : 0.f;
+    for (int i = 1; i + 1 < nseg; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r][j] = x[r];
+        __syncthreads();
+        float *end = st + size_t(i) * p.P * p.N;
+#pragma unroll
+        for (int r = 0; r < R; ++r) x[r] = r < nr && j < p.N ? end[size_t(r) * p.N + j] : 0.f;
+        if (j < p.N) {
+            const float *m = map + size_t(i) * p.N * p.N + j;
+            for (int n0 = 0; n0 < p.N; n0 += 32) {         // 32 loads on their way at once
+                float f[32];
+#pragma unroll
+                for (int n = 0; n < 32; ++n) f[n] = n0 + n < p.N ? __ldg(m + size_t(n0 + n) * p.N) : 0.f;
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int n = 0; n < 32; n += 4) {
+                        const float4 u = *reinterpret_cast<const float4 *>(&row[r][n0 + n]);
+                        x[r] = fmaf(u.x, f[n], fmaf(u.y, f[n + 1], fmaf(u.z, f[n + 2], fmaf(u.w, f[n + 3], x[r]))));
+                    }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                if (r < nr) end[size_t(r) * p.N + j] = x[r];
+        }
+    }
 }
 
 }  // namespace ssm

@@ -2,7 +2,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "api_host.cuh"
+#include "api_scratch.cuh"
 #include "layer_norm.cuh"
 
 using namespace ssm_host;

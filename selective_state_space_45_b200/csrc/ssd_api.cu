@@ -5,7 +5,7 @@
 // per call (cuTensorMapEncodeTiled, reached through the runtime's driver entry point).
 #include <climits>
 
-#include "api_host.cuh"
+#include "api_scratch.cuh"
 #include "ssd_tc.cuh"
 
 using namespace ssm_host;

@@ -86,6 +86,28 @@ def test_forward_many_chunks_long_memory(cuda_lib):
     run_and_check(make(1, 1500, 2, 1, 32, 64, dtype=F32, seed=4, decay=1e-3), F32)
 
 
+@pytest.mark.parametrize("shape", [(1, 2048, 1, 1, 16, 32), (1, 2101, 2, 1, 32, 64), (2, 3000, 3, 3, 72, 40),
+                                   (1, 4255, 2, 2, 128, 128)], ids=str)
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F32, F32)])
+def test_forward_in_segments(cuda_lib, shape, dtype, out):
+    """Long sequences of few heads are cut into segments that run at once; the state is also
+    carried in place, which the segments must not race on."""
+    d = make(*shape, dtype=dtype, seed=sum(shape), decay=0.02)
+    d["a"][:, 700] = -float("inf")
+    y, S = run_and_check(d, out)
+    state = d["initial_state"].clone()
+    y2 = torch.empty_like(y)
+    for _ in range(2):
+        state.copy_(d["initial_state"])
+        ssm.ssm_delta_rule_fwd(**{n: d[n] for n in ("q", "k", "v", "a", "beta")}, y=y2, initial_state=state, final_state=state,
+                               scale=0.7)
+        assert torch.equal(y2, y) and torch.equal(state, S)
+    y0, S0 = ssm.delta_rule(**{**d, "initial_state": None}, scale=0.7, out_dtype=out)
+    yr, Sr = oracle.delta_rule(**{**d, "initial_state": None}, scale=0.7)
+    close_y(y0, yr)
+    close_state(S0, Sr, "final state from zero")
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_forward_hard_gates(cuda_lib, dtype):
     """Full resets (-inf), no decay, growth, steps of 0, 1 and 2, repeated and zero keys."""
