@@ -316,7 +316,7 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * per head with the delta correction (what the state already answers for the key is taken
  * off the value before it is written).  Per sequence and head,
  *     S' = exp(a_t) S,   e_t = v_t - S' k_t,   S = S' + beta_t e_t k_t^T,   y_t = scale S q_t
- * computed by chunks of 16 tokens: inside a chunk the corrections e solve a triangular
+ * computed by chunks of 32 tokens: inside a chunk the corrections e solve a triangular
  * system, between chunks the state stays in registers.
  *
  *   q, k          : [batch][seqlen][qk_heads][dstate], in_dtype.  qk_heads divides heads:
@@ -327,12 +327,15 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  *   initial_state : [batch][heads][headdim][dstate] fp32 or NULL (zero).
  *   final_state   : the same, or NULL (not written).  May be initial_state itself.
  * headdim and dstate must be multiples of 8 and at most 128
- * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on bf16 pieces of the
- * fp32 operands with fp32 accumulation: the final state and an fp32 y are good to a few
- * 2^-20 of their size (normwise), a bf16 y to its own rounding and 2^-16.  A value that is
- * not finite spreads over the rest of its chunk, earlier tokens included.
- * seqlen = 0 copies the start state through.  Takes scratch (about 150 bytes per token and
- * head, and the keys and queries again when they are fp32): see the conventions above.
+ * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on scaled fp16 operands,
+ * two for each fp32 value, with fp32 accumulation: the final state and an fp32 y come out as
+ * from fp32 arithmetic (about 2^-21 of their size), a bf16 y within its own rounding and 2^-11.
+ * A value that is not finite spreads over the rest of its chunk of 32 tokens, earlier ones
+ * included.  Long sequences of few heads are cut into segments that run at once (the sizes alone
+ * decide); a segment's map of start states must then be finite too.
+ * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
+ * 175 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
+ * segments 8 * (headdim + dstate) * dstate bytes or less per segment and head.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        void *y, const float *initial_state, float *final_state, float scale,
@@ -374,8 +377,9 @@ int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *
  *   da, dbeta     : [batch][seqlen][heads] fp32, written.
  *   dinitial_state: [batch][heads][headdim][dstate] fp32 or NULL.
  * Every sum has a fixed order: results are deterministic.  Takes scratch (see the
- * conventions above) of about 8 * batch * heads * headdim * (seqlen + dstate * (seqlen / 64 + 2))
- * bytes, mostly the state and its gradient every 64 tokens.
+ * conventions above) of about 8 * batch * heads * headdim' * (seqlen + dstate * (seqlen / 64 + 2))
+ * bytes, headdim' = headdim rounded up to 64: mostly e, w and the state and its gradient every
+ * 64 tokens.
  * seqlen = 0 writes dinitial_state = dfinal_state.
  */
 int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

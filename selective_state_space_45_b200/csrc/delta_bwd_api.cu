@@ -1,7 +1,7 @@
 // delta_bwd_api.cu -- C ABI of the gated delta rule's backward (ssm_delta_rule_bwd): the
 // forward pass again (e and the states every 64 tokens), the reverse pass (dv, the state's
-// gradient at the same places), then the chunks' gradients in parallel.  One stream-ordered
-// scratch buffer per call.
+// gradient at the same places), then the chunks' gradients in parallel.  Scratch: the caller's
+// workspace or a stream-ordered buffer.
 #include "delta_grad16.cuh"
 #include "delta_host.cuh"
 
@@ -18,7 +18,7 @@ template <int NP, int PW, typename Tin, typename Tg> int launch_grad(const ssm::
         if (const int st = set_smem(ssm::delta_grad16_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
         ssm::delta_grad16_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
     } else {
-        using Cfg = ssm::GradCfg<NP, PW, KP, Tin, Tg>;
+        using Cfg = ssm::GradCfg<NP, PW, KP>;
         if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
         ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
     }
@@ -96,7 +96,8 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
         r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
-        r.dck = part(at.dck); r.d16 = ws.p + at.dck; r.w16 = ws.p + at.w; r.y16 = ws.p + at.y16; r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
+        r.dck = part(at.dck); r.d16 = ws.p + at.dck; r.w16 = ws.p + at.w; r.y16 = ws.p + at.y16;
+        r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
         st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
     }

@@ -16,7 +16,8 @@
 // with the inner products taken afresh every 64 tokens: at most 32 terms are summed.
 //
 // Four warps with 16 tokens (rows) each; every product on the tensor cores with scaled fp16
-// operands: one piece behind bf16 gradients (2^-12 against their 2^-9), two behind fp32 ones.
+// operands, here two pieces of each for fp32 gradients; delta_grad16.cuh is the form for bf16
+// gradients (one piece: 2^-12 against their 2^-9).
 // The token-by-token matrices never leave the registers: each is formed in the layout of an
 // accumulator whose rows are the rows it is then used with (dy e^T for dq, e dy^T, e w^T and
 // w e^T for dk), so that it becomes the next product's A operand as it stands, and tiles off
@@ -50,10 +51,8 @@ struct DeltaGradArgs {
 constexpr int kGradC = 64, kGradN = 64;        // tokens per CTA, state columns per pass
 
 // PW: headdim padded to 64 or 128; NP: dstate padded; KP: pieces of k and q; PG: of the others.
-template <int NP_, int PW_, int KP_, typename Tin_, typename Tg_> struct GradCfg {
-    static constexpr int NP = NP_, PW = PW_, KP = KP_, PG = sizeof(Tg_) == 4 ? 2 : 1;
-    using Tin = Tin_;
-    using Tg = Tg_;
+template <int NP_, int PW_, int KP_> struct GradCfg {
+    static constexpr int NP = NP_, PW = PW_, KP = KP_, PG = 2;
     static constexpr int W = NP < kGradN ? NP : kGradN;
     static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16, TROW = kGradC * 2 + 16;      // padded rows (bytes)
     static constexpr int TOK = kGradC * PROW, TT = PW * TROW, ST = PW * NROW, KT = kGradC * NROW;
@@ -62,12 +61,10 @@ template <int NP_, int PW_, int KP_, typename Tin_, typename Tg_> struct GradCfg
     static constexpr int OFF_K = OFF_D + PG * ST, OFF_Q = OFF_K + KP * KT;
     static constexpr int OFF_VEC = OFF_Q + KP * KT;
     static constexpr int SMEM_BYTES = OFF_VEC + 6 * kGradC * 4 + 16;
-    static constexpr int CTAS = PG == 1 ? (PW == 64 && NP > 64 ? 3 : 2) : 1;      // per SM, by shared memory and registers
 };
 
 template <class Cfg>
-__global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaGradArgs p) {
-    using Tg = typename Cfg::Tg;
+__global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) {
     constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W;
     using Rows = DeltaRows<NP, KP>;
     extern __shared__ __align__(128) unsigned char delta_smem[];
@@ -132,9 +129,9 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
         __syncthreads();                 // the last head's tiles and vectors are done with
 
         // dy as an operand [token][headdim], e and w as [headdim][token]
-        const Tg *dyp = static_cast<const Tg *>(p.dy) + v0;
+        const float *dyp = static_cast<const float *>(p.dy) + v0;
         constexpr int CP = PW / 8;
-#pragma unroll (PG == 1 ? 4 : 2)
+#pragma unroll 2
         for (int i = tid; i < C * CP; i += 128) {
             const int r = i / CP, x = (i % CP) * 8;
             float f[8] = {};
@@ -159,7 +156,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
             }
         };
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll (PG == 1 ? 4 : 2)
+#pragma unroll 2
         for (int i = rt; i < 2 * (PW / 16) * 4; i += 4) {      // (half, 16 rows, 8 tokens)
             const int n = i & 3, rb = (i >> 2) % (PW / 16), hf = i / (PW / 4);
             const bool ok = hf < n32 && 16 * rb < p.P;
@@ -283,7 +280,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
             if (n0 > 0) __syncthreads();
             // this pass's columns of the states and of k and q
             constexpr int CN = W / 8;
-#pragma unroll (PG == 1 ? 4 : 2)
+#pragma unroll 2
             for (int i = rt; i < (PW / 16) * CN; i += 4) {     // (16 rows, 8 columns)
                 const int j = i % CN, rb = i / CN;
                 const bool ok = 16 * rb < p.P && n0 + 8 * j < NP;
@@ -294,7 +291,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
                 put(to + Cfg::OFF_S, Cfg::ST, Cfg::NROW, fs, cS.c);
                 put(to + Cfg::OFF_D, Cfg::ST, Cfg::NROW, fd, cD.c);
             }
-#pragma unroll (PG == 1 ? 4 : 2)
+#pragma unroll 2
             for (int i = tid; i < C * CN; i += 128) {
                 const int r = i / CN, x = (i % CN) * 8, half = r / kDeltaC;
                 const unsigned char *src = p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + (half < n32 ? half : 0)) * Rows::BYTES +
@@ -382,12 +379,9 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad_kernel(const DeltaG
                         if (hg + 1 < group) {
                             *pq = q;
                             *pk = k;
-                        } else if constexpr (sizeof(Tg) == 4) {
+                        } else {
                             *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
                             *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
-                        } else {
-                            *reinterpret_cast<unsigned *>(static_cast<Tg *>(p.dq) + off) = pack_bf16x2(q.x, q.y);
-                            *reinterpret_cast<unsigned *>(static_cast<Tg *>(p.dk) + off) = pack_bf16x2(k.x, k.y);
                         }
                     }
             }

@@ -12,6 +12,7 @@ namespace ssm_host {
 inline int delta_sizes(int batch, int tokens, int heads, int qk_heads, int headdim, int dstate) {
     if (batch < 0 || tokens < 0 || heads < 0 || qk_heads < 0 || headdim < 1 || dstate < 1) return SSM_ERR_INVALID_ARG;
     if (heads > 0 && (qk_heads == 0 || heads % qk_heads != 0)) return SSM_ERR_INVALID_ARG;
+    if (tokens > INT_MAX - 128) return SSM_ERR_UNSUPPORTED;
     if (headdim % 8 != 0 || dstate % 8 != 0 || headdim > 128 || dstate > 128) return SSM_ERR_UNSUPPORTED;
     return SSM_OK;
 }

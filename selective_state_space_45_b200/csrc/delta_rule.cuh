@@ -15,11 +15,19 @@
 // shared memory or waits for another warp.  What depends on k, q, a and beta alone (G, Pm and
 // the decays) is formed for all chunks in parallel by delta_prep_kernel, one warp per chunk,
 // which also lays the chunk's k and q out as the chains' operands.  The warps of a CTA take
-// turns at starting the copies of the next chunk (cp.async.bulk, cp.async for the rows of v,
-// which one bulk copy each would take 70 cycles to start; two stages, mbarriers both ways) and
-// otherwise wait for data only, never for each other.  Copying and converting the
+// turns at starting the copies of a later chunk (cp.async.bulk, cp.async for the rows of v,
+// which one bulk copy each would take 70 cycles to start; two or three stages, mbarriers both
+// ways) and otherwise wait for data only, never for each other.  Copying and converting the
 // rows in the chains instead cost 1100 of 3700 cycles a chunk; a fifth warp for the copies
 // costs the others the registers that they need (168 instead of 255: spills).
+//
+// What bounds it: the chain of dependent products of a chunk, not HBM and not the rate of the
+// tensor cores.  bf16, dstate 128: a chunk takes 1.5 us in a CTA that has its SM to itself
+// and 2.9 us where two share one; 8 x 2048 tokens x 24 heads of 64 x 128 (192 CTAs) 185 us, and
+// the prep kernel 99 us (74% of HBM's copy rate: it writes the blocks and the operands).
+// mma.sync rather than tcgen05: the state and its products stay in registers with the warp that
+// needs them next, where tensor memory would put a round trip behind each of the four products
+// of a chunk, and one warp's tiles are 16 rows.
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
 //     rhs = end (dS k) + Pm^T dO,  du = rhs - G^T (beta rhs),  dv = w = beta du,  dbeta = e.du,
@@ -60,7 +68,7 @@ struct DeltaArgs {
     float *ck, *dck;        // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
                             // and its gradient at every boundary of 64 tokens and at the end
     // For bf16 gradients the last kernel takes scaled fp16 operands, tiles of its shared memory
-    // as they stand (stm16 writes them): e, w and dy of a part and chunk, S and dS of a part.
+    // as they stand: e, w and dy of a part and chunk, S and dS of a part.
     unsigned char *e16, *w16, *y16;     // [batch][heads][chunks][parts] 16 rows of 32 tokens
     unsigned char *s16, *d16;           // [batch][heads][boundaries][parts] 16 rows of dstate
     float *sum, *sum2;      // [parts][batch][heads][seqlen] sums over a part's rows: dy.y; in the
@@ -81,7 +89,7 @@ struct DeltaArgs {
 
 constexpr int kDeltaC = 32;          // tokens per chunk
 constexpr int kDeltaSave = 64;       // tokens between the states kept for the backward
-constexpr int kTri = 512;            // bytes of a 16 x 16 bf16 tile, rows of 32
+constexpr int kTri = 512;            // bytes of a 16 x 16 tile of 16-bit values, rows of 32
 constexpr int kOutRow = 48;          // bytes per row of a warp's output tile
 
 // Byte offset of the 16-byte half `c` of row r in such a tile: the halves change places every
@@ -1053,6 +1061,9 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[slot]);         // the stage may be filled again
     }
+    if (!alive)                                            // copies may still be on their way: wait (bounded) for them
+        for (int i = max(0, count - Cfg::STAGES); i < count; ++i)
+            mbar_wait(&full[i % Cfg::STAGES], uint32_t(i / Cfg::STAGES) & 1, kDeltaWaitCycles);
     if constexpr (MODE == 1) keep_state(p.ck, nbound - 1);
     if constexpr (REV) dot_state(0);
     float *end = ident ? p.seg_map + (size_t(bh) * nseg + seg) * p.N * p.N

@@ -53,7 +53,7 @@ SIZE_REFUSALS = [
     (dict(batch=-1), INV), (dict(L=-1), INV), (dict(H=-4), INV), (dict(K=-2), INV),
     (dict(H=4, K=3), INV), (dict(H=2, K=4), INV), (dict(K=0), INV),          # key heads that do not divide the heads
     (dict(P=0), INV), (dict(N=0), INV), (dict(P=12), UNS), (dict(N=20), UNS), (dict(P=136), UNS), (dict(N=256), UNS),
-    (dict(din=2), INV), (dict(dout=-1), INV),
+    (dict(din=2), INV), (dict(dout=-1), INV), (dict(L=2 ** 31 - 1), UNS),
 ]
 
 
