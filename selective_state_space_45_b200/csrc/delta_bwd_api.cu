@@ -20,7 +20,7 @@ template <int NP, int PW, typename Tin, typename Tg> int launch_grad(const ssm::
     } else {
         using Cfg = ssm::GradCfg<NP, PW, KP>;
         if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
-        ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
+        ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
     }
     return status_of(cudaGetLastError());
 }

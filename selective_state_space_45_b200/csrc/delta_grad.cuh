@@ -15,7 +15,8 @@
 //          = <dS, S>(chunk's start) - sum_{t'<t} (dy.y - v.w)_t'
 // with the inner products taken afresh every 64 tokens: at most 32 terms are summed.
 //
-// Four warps with 16 tokens (rows) each; every product on the tensor cores with scaled fp16
+// Four warps with 16 tokens (rows) each, and with 64 columns of the state in shared memory four
+// more that take the upper 32 of them: every product on the tensor cores with scaled fp16
 // operands, here two pieces of each for fp32 gradients; delta_grad16.cuh is the form for bf16
 // gradients (one piece: 2^-12 against their 2^-9).
 // The token-by-token matrices never leave the registers: each is formed in the layout of an
@@ -53,7 +54,7 @@ constexpr int kGradC = 64, kGradN = 64;        // tokens per CTA, state columns 
 // PW: headdim padded to 64 or 128; NP: dstate padded; KP: pieces of k and q; PG: of the others.
 template <int NP_, int PW_, int KP_> struct GradCfg {
     static constexpr int NP = NP_, PW = PW_, KP = KP_, PG = 2;
-    static constexpr int W = NP < kGradN ? NP : kGradN;
+    static constexpr int W = NP < kGradN ? NP : kGradN, NT = 128 * (W / 32);
     static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16, TROW = kGradC * 2 + 16;      // padded rows (bytes)
     static constexpr int TOK = kGradC * PROW, TT = PW * TROW, ST = PW * NROW, KT = kGradC * NROW;
     static constexpr int OFF_Y = 0, OFF_E = OFF_Y + PG * TOK, OFF_W = OFF_E + PG * TT;
@@ -64,15 +65,15 @@ template <int NP_, int PW_, int KP_> struct GradCfg {
 };
 
 template <class Cfg>
-__global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) {
-    constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W;
+__global__ void __launch_bounds__(Cfg::NT) delta_grad_kernel(const DeltaGradArgs p) {
+    constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W, NT = Cfg::NT;
     using Rows = DeltaRows<NP, KP>;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
     float *bend = bet + C, *dtok = bend + C;
     double *half = reinterpret_cast<double *>(dtok + C);
-    const int tid = threadIdx.x, lane = tid & 31, rt = tid >> 5, g = lane >> 2, t4 = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, rt = (tid >> 5) & 3, j0 = tid >> 7, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
     const int c = int(blockIdx.x % unsigned(nchunk)), bk = int(blockIdx.x / unsigned(nchunk));
     const int b = bk / p.qk_heads, hk = bk - b * p.qk_heads;
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
         // dy as an operand [token][headdim], e and w as [headdim][token]
         const float *dyp = static_cast<const float *>(p.dy) + v0;
         constexpr int CP = PW / 8;
-#pragma unroll 2
-        for (int i = tid; i < C * CP; i += 128) {
+#pragma unroll 4
+        for (int i = tid; i < C * CP; i += NT) {
             const int r = i / CP, x = (i % CP) * 8;
             float f[8] = {};
             if (r < nt && x < p.P) load8(dyp + size_t(r) * vrow + x, f);
@@ -156,8 +157,8 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
             }
         };
         const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int i = rt; i < 2 * (PW / 16) * 4; i += 4) {      // (half, 16 rows, 8 tokens)
+#pragma unroll 4
+        for (int i = tid >> 5; i < 2 * (PW / 16) * 4; i += NT / 32) {      // (half, 16 rows, 8 tokens)
             const int n = i & 3, rb = (i >> 2) % (PW / 16), hf = i / (PW / 4);
             const bool ok = hf < n32 && 16 * rb < p.P;
             const size_t from = ((((bh * nck + c32 + hf) * p.zparts + rb) * 4 + n) * 32 + lane) * 4;
@@ -280,8 +281,8 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
             if (n0 > 0) __syncthreads();
             // this pass's columns of the states and of k and q
             constexpr int CN = W / 8;
-#pragma unroll 2
-            for (int i = rt; i < (PW / 16) * CN; i += 4) {     // (16 rows, 8 columns)
+#pragma unroll 4
+            for (int i = tid >> 5; i < (PW / 16) * CN; i += NT / 32) {     // (16 rows, 8 columns)
                 const int j = i % CN, rb = i / CN;
                 const bool ok = 16 * rb < p.P && n0 + 8 * j < NP;
                 const size_t from = ((size_t(rb) * (NP / 8) + n0 / 8 + j) * 32 + lane) * 4;
@@ -291,8 +292,8 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
                 put(to + Cfg::OFF_S, Cfg::ST, Cfg::NROW, fs, cS.c);
                 put(to + Cfg::OFF_D, Cfg::ST, Cfg::NROW, fd, cD.c);
             }
-#pragma unroll 2
-            for (int i = tid; i < C * CN; i += 128) {
+#pragma unroll 4
+            for (int i = tid; i < C * CN; i += NT) {
                 const int r = i / CN, x = (i % CN) * 8, half = r / kDeltaC;
                 const unsigned char *src = p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + (half < n32 ? half : 0)) * Rows::BYTES +
                                            (r % kDeltaC) * Rows::ROW + (n0 + x) * 2;
@@ -309,82 +310,79 @@ __global__ void __launch_bounds__(128) delta_grad_kernel(const DeltaGradArgs p) 
             __syncthreads();
             const unsigned sS = smem_u32(smem + Cfg::OFF_S), sD = smem_u32(smem + Cfg::OFF_D);
             const unsigned sk = smem_u32(smem + Cfg::OFF_K), sq = smem_u32(smem + Cfg::OFF_Q);
-            // 32 columns at a time
-#pragma unroll 1
-            for (int j0 = 0; j0 < W / 32; ++j0) {
-                float aq[4][4], ak[4][4], aw[4][4], ae[4][4], am[4][4];
+            // 32 columns per group of four warps
+            float aq[4][4], ak[4][4], aw[4][4], ae[4][4], am[4][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) { zero4(aq[n]); zero4(ak[n]); zero4(aw[n]); zero4(ae[n]); zero4(am[n]); }
+            for (int n = 0; n < 4; ++n) { zero4(aq[n]); zero4(ak[n]); zero4(aw[n]); zero4(ae[n]); zero4(am[n]); }
 #pragma unroll
-                for (int k = 0; k < PW / 16; ++k) {
-                    unsigned ay[PG][4], aE[PG][4], aW[PG][4];
+            for (int k = 0; k < PW / 16; ++k) {
+                unsigned ay[PG][4], aE[PG][4], aW[PG][4];
+#pragma unroll
+                for (int i = 0; i < PG; ++i) {
+                    ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
+                    ldsm4_t(aE[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
+                    ldsm4_t(aW[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    unsigned bS[PG][4], bD[PG][4];
+                    const unsigned at = 16 * k * Cfg::NROW + bn + j0 * 64 + j * 32;
 #pragma unroll
                     for (int i = 0; i < PG; ++i) {
-                        ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
-                        ldsm4_t(aE[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
-                        ldsm4_t(aW[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
+                        ldsm4_t(bS[i], sS + i * Cfg::ST + at);
+                        ldsm4_t(bD[i], sD + i * Cfg::ST + at);
                     }
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        unsigned bS[PG][4], bD[PG][4];
-                        const unsigned at = 16 * k * Cfg::NROW + bn + j0 * 64 + j * 32;
+                    for (int n = 0; n < 2; ++n) {
+                        mma_pieces<PG, PG>(aq[2 * j + n], ay, bS, n);
+                        mma_pieces<PG, PG>(aw[2 * j + n], aW, bS, n);
+                        mma_pieces<PG, PG>(ae[2 * j + n], aE, bD, n);
+                    }
+                }
+            }
 #pragma unroll
-                        for (int i = 0; i < PG; ++i) {
-                            ldsm4_t(bS[i], sS + i * Cfg::ST + at);
-                            ldsm4_t(bD[i], sD + i * Cfg::ST + at);
-                        }
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            mma_pieces<PG, PG>(aq[2 * j + n], ay, bS, n);
-                            mma_pieces<PG, PG>(aw[2 * j + n], aW, bS, n);
-                            mma_pieces<PG, PG>(ae[2 * j + n], aE, bD, n);
-                        }
+                for (int j = 0; j < 2; ++j) {
+                    unsigned bK[KP][4], bQ[KP][4];
+                    const unsigned at = 16 * u * Cfg::NROW + bn + j0 * 64 + j * 32;
+#pragma unroll
+                    for (int i = 0; i < KP; ++i) ldsm4_t(bK[i], sk + i * Cfg::KT + at);
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        if (u <= rt) mma_pieces<PG, KP>(ak[2 * j + n], a1[u], bK, n);
+                        mma_pieces<PG, KP>(am[2 * j + n], a3[u], bK, n);
+                    }
+                    if (u >= rt) {
+#pragma unroll
+                        for (int i = 0; i < KP; ++i) ldsm4_t(bQ[i], sq + i * Cfg::KT + at);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) mma_pieces<PG, KP>(am[2 * j + n], a2[u], bQ, n);
                     }
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        unsigned bK[KP][4], bQ[KP][4];
-                        const unsigned at = 16 * u * Cfg::NROW + bn + j0 * 64 + j * 32;
-#pragma unroll
-                        for (int i = 0; i < KP; ++i) ldsm4_t(bK[i], sk + i * Cfg::KT + at);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            if (u <= rt) mma_pieces<PG, KP>(ak[2 * j + n], a1[u], bK, n);
-                            mma_pieces<PG, KP>(am[2 * j + n], a3[u], bK, n);
-                        }
-                        if (u >= rt) {
-#pragma unroll
-                            for (int i = 0; i < KP; ++i) ldsm4_t(bQ[i], sq + i * Cfg::KT + at);
-#pragma unroll
-                            for (int n = 0; n < 2; ++n) mma_pieces<PG, KP>(am[2 * j + n], a2[u], bQ, n);
-                        }
+                for (int r = 0; r < 2; ++r) {
+                    const int t = 16 * rt + g + 8 * r, col = n0 + 32 * j0 + 8 * n + 2 * t4;
+                    if (t >= nt || col >= p.N) continue;
+                    const size_t off = k0 + size_t(t) * krow + col;
+                    float2 q, k;
+                    q.x = fmaf(c1.inv, ak[n][2 * r], fq[r] * aq[n][2 * r]);
+                    q.y = fmaf(c1.inv, ak[n][2 * r + 1], fq[r] * aq[n][2 * r + 1]);
+                    k.x = fmaf(c2.inv, am[n][2 * r], fmaf(fw[r], aw[n][2 * r], fe[r] * ae[n][2 * r]));
+                    k.y = fmaf(c2.inv, am[n][2 * r + 1], fmaf(fw[r], aw[n][2 * r + 1], fe[r] * ae[n][2 * r + 1]));
+                    float2 *pq = reinterpret_cast<float2 *>(p.part + off);
+                    float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
+                    if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
+                    if (hg + 1 < group) {
+                        *pq = q;
+                        *pk = k;
+                    } else {
+                        *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
+                        *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
                     }
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int t = 16 * rt + g + 8 * r, col = n0 + 32 * j0 + 8 * n + 2 * t4;
-                        if (t >= nt || col >= p.N) continue;
-                        const size_t off = k0 + size_t(t) * krow + col;
-                        float2 q, k;
-                        q.x = fmaf(c1.inv, ak[n][2 * r], fq[r] * aq[n][2 * r]);
-                        q.y = fmaf(c1.inv, ak[n][2 * r + 1], fq[r] * aq[n][2 * r + 1]);
-                        k.x = fmaf(c2.inv, am[n][2 * r], fmaf(fw[r], aw[n][2 * r], fe[r] * ae[n][2 * r]));
-                        k.y = fmaf(c2.inv, am[n][2 * r + 1], fmaf(fw[r], aw[n][2 * r + 1], fe[r] * ae[n][2 * r + 1]));
-                        float2 *pq = reinterpret_cast<float2 *>(p.part + off);
-                        float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
-                        if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
-                        if (hg + 1 < group) {
-                            *pq = q;
-                            *pk = k;
-                        } else {
-                            *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
-                            *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
-                        }
-                    }
-            }
+                }
         }
         if (tid < nt) {
             if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];

@@ -214,10 +214,6 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
             alive = false;
             atomicAdd(p.timeouts, 1u);
         }
-        if (__syncthreads_and(alive) == 0) {              // results are void: one more bounded wait for the copies, and out
-            mbar_wait(bar, hg & 1, kDeltaWaitCycles);
-            return;
-        }
 
         // The token-by-token matrices of this warp's rows, in four tiles of 16 columns: dy e^T;
         // e dy^T; w e^T up to the diagonal and e w^T past it; e w^T on it.
@@ -461,10 +457,14 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
             p.da[gate] = z;
             p.dbeta[gate] = db;
         }
-        if (hg + 1 < group) {
-            __syncthreads();             // the tiles and vectors are done with
+        if (hg + 1 < group) {            // the tiles and vectors are done with
+            if (!__syncthreads_and(alive)) { alive = false; break; }
             if (tid == 0) copies(hg + 1);
         }
+    }
+    if (!alive) {                        // results are void; copies may still be on their way: wait (bounded) for them
+        mbar_wait(bar, 0, kDeltaWaitCycles);
+        mbar_wait(bar, 1, kDeltaWaitCycles);
     }
 }
 
