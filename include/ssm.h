@@ -335,7 +335,7 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * decide); a segment's map of start states must then be finite too.
  * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
  * 175 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
- * segments 8 * (headdim + dstate) * dstate bytes or less per segment and head.
+ * each segment and head 4 * (headdim + dstate) * dstate bytes.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        void *y, const float *initial_state, float *final_state, float scale,
@@ -379,7 +379,8 @@ int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *
  * Every sum has a fixed order: results are deterministic.  Takes scratch (see the
  * conventions above) of about 8 * batch * heads * headdim' * (seqlen + dstate * (seqlen / 64 + 2))
  * bytes, headdim' = headdim rounded up to 64: mostly e, w and the state and its gradient every
- * 64 tokens.
+ * 64 tokens; and what the forward takes for segments, into which long sequences of few heads
+ * are cut here too.
  * seqlen = 0 writes dinitial_state = dfinal_state.
  */
 int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

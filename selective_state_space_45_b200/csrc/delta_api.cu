@@ -3,7 +3,6 @@
 // anything is launched.  The forward takes scratch (the caller's workspace or a stream-ordered
 // buffer), the step none.
 #include <algorithm>
-#include <cmath>
 
 #include "delta_host.cuh"
 #include "delta_step.cuh"
@@ -23,38 +22,13 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
     return status_of(cudaGetLastError());
 }
 
-// How many segments a sequence is cut into.  A chain's chunks follow one another, so with few
-// heads most of the GPU is idle.  Segments run at once: first every segment's end state from a
-// zero start and its map (dstate more rows), then, from the folded start states, the outputs.
-// In units of a chunk's time in a CTA (1.5 us; 0.9 of it without outputs): two CTAs on an SM take
-// 1.9, more share it; fp32 inputs leave room for one CTA.  Folding costs about four units a
-// segment.  Segments have at least 16 chunks, and what they save must be a tenth.  32749 tokens
-// of 16 heads of 128 x 128: one piece 1565 us, five 1044 us, nine 850 us (and 94 us for the
-// chunk blocks).
-int segments(int batch, int seqlen, int heads, int P, int N, bool one_per_sm) {
-    const long long chunks = (long long)delta_chunks(seqlen), all = (long long)batch * heads;
-    auto cost = [&](double ctas) {
-        const double r = ctas / 148;
-        return r <= 1 ? 1.0 : one_per_sm ? std::ceil(r) : r <= 2 ? 1.9 : r;
-    };
-    const double rows = double(all) * delta_slices(P), maps = double(all) * delta_slices(N);
-    int best = 1;
-    double least = chunks * cost(rows);
-    const double bar = 0.9 * least;
-    for (int n = 2; n <= 64 && chunks / n >= 16; ++n) {
-        const double t = double((chunks + n - 1) / n) * (0.9 * cost((n - 1) * rows + (n - 2) * maps) + cost(n * rows)) + 4 * n;
-        if (t < bar && t < least) { least = t; best = n; }
-    }
-    return best;
-}
-
 struct FwdPlan {
     int nseg;
     size_t prep, rows, seg_state, seg_map, all;      // offsets, and the bytes
     FwdPlan(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int out_dtype) {
         const size_t blocks = out_dtype == SSM_F32 ? prep_bytes<ssm::DeltaBlock<2>>(batch, seqlen, heads)
                                                    : prep_bytes<ssm::DeltaBlock<1>>(batch, seqlen, heads);
-        nseg = segments(batch, seqlen, heads, P, N, in_dtype == SSM_F32);
+        nseg = segments(batch, seqlen, heads, P, N, in_dtype == SSM_F32, false);
         const size_t seg = nseg > 1 ? size_t(batch) * heads * nseg * N * 4 : 0;
         prep = 0;
         rows = prep + round16(blocks);
@@ -82,11 +56,7 @@ template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *works
         a.seg_chunks = int((chunks + at.nseg - 1) / at.nseg);
         const int nseg = int((chunks + a.seg_chunks - 1) / a.seg_chunks);
         if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, Tout, 3>(a, s, nseg);
-        if (st == SSM_OK) {
-            const unsigned ctas = unsigned(a.batch) * unsigned(a.heads) * unsigned((a.P + 7) / 8);
-            ssm::delta_fold_kernel<8><<<ctas, 128, 0, s>>>(a, nseg);
-            st = status_of(cudaGetLastError());
-        }
+        if (st == SSM_OK) st = launch_fold<false>(a, nseg, s);
         // a state carried in place: the last segment's end must not be written before the first
         // segment has read its start, so it goes by the slot that the last segment leaves unused
         float *const end = a.hN;

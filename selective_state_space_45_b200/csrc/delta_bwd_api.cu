@@ -1,7 +1,8 @@
 // delta_bwd_api.cu -- C ABI of the gated delta rule's backward (ssm_delta_rule_bwd): the
 // forward pass again (e and the states every 64 tokens), the reverse pass (dv, the state's
-// gradient at the same places), then the chunks' gradients in parallel.  Scratch: the caller's
-// workspace or a stream-ordered buffer.
+// gradient at the same places), then the chunks' gradients in parallel.  Long sequences of few
+// heads go through the two passes in segments that run at once, as in the forward.  Scratch: the
+// caller's workspace or a stream-ordered buffer.
 #include "delta_grad16.cuh"
 #include "delta_host.cuh"
 
@@ -37,7 +38,8 @@ using Block = ssm::DeltaBlock<2>;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, w, ck, dck, y16, e16, s16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, all;
+    size_t prep, rows, e, w, ck, dck, y16, e16, s16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, seg_state, seg_map, all;
+    int nseg;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
@@ -69,6 +71,9 @@ struct BwdParts {
         add(wmax, 4 * parts * bh * delta_chunks(seqlen));
         add(ymax, 4 * parts * bh * delta_chunks(seqlen));
         add(part, heads > qk_heads ? 2 * size_t(batch) * seqlen * qk_heads * N * 4 : 0);
+        nseg = segments(batch, seqlen, heads, P, N, in_dtype == SSM_F32 || grad_dtype == SSM_F32, true);
+        add(seg_state, nseg > 1 ? bh * nseg * P * N * 4 : 0);
+        add(seg_map, nseg > 1 ? bh * nseg * N * N * 4 : 0);
         all = at;
     }
 };
@@ -92,14 +97,29 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     f.smax = bits(at.smax); f.emax = bits(at.emax);
     f.v = v; f.v2 = dy; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;
     f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy); f.w = part(at.w);
-    if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s);
+    // segments: whole spans of the kept states
+    int nseg = 1;
+    if (at.nseg > 1) {
+        constexpr int span = ssm::kDeltaSave / ssm::kDeltaC;
+        const int chunks = int(delta_chunks(f.seqlen));
+        f.seg_chunks = ((chunks + at.nseg - 1) / at.nseg + span - 1) / span * span;
+        nseg = (chunks + f.seg_chunks - 1) / f.seg_chunks;
+        f.seg_state = part(at.seg_state); f.seg_map = part(at.seg_map);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, float, 3>(f, s, nseg);
+        if (st == SSM_OK) st = launch_fold<false>(f, nseg, s);
+    }
+    if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s, nseg);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
         r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
         r.dck = part(at.dck); r.d16 = ws.p + at.dck; r.w16 = ws.p + at.w; r.y16 = ws.p + at.y16;
         r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
-        st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s);
+        if (nseg > 1) {
+            st = dispatch_chain<KP, Tg, Tg, float, 4>(r, s, nseg);
+            if (st == SSM_OK) st = launch_fold<true>(r, nseg, s);
+        }
+        if (st == SSM_OK) st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s, nseg);
     }
     if (st == SSM_OK) {
         const ssm::DeltaGradArgs g{dy, f.a, f.beta, part(at.e), part(at.w), f.rows, f.prep, Block::BYTES, part(at.ck),

@@ -77,9 +77,10 @@ struct DeltaArgs {
     unsigned *smax;         // [batch][heads][boundaries][parts] largest |S| (reverse pass: |dS|), as bits
     unsigned *emax, *ymax;  // [batch][heads][chunks][parts] bounds of |e| (reverse pass: |w|) and, in the
                             // reverse pass, the largest |dy|
-    // Segments of a long sequence with few heads (forward only): chunks per segment, and per segment
+    // Segments of a long sequence with few heads: chunks per segment, and per segment
     // [batch][heads][segments] the end state from a zero start (the first: from h0), later the next
     // one's start state, and the map that takes a start state's rows to their part of the end state.
+    // Reverse passes: the same from the other end, gradients of start states.
     int seg_chunks;
     float *seg_state, *seg_map;     // [headdim][dstate], [dstate][dstate]
     bool end_slot;                  // the end state goes to the last segment's slot of seg_state, not hN
@@ -136,7 +137,8 @@ constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's 
 
 // NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k.  MODE 0:
 // forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass; 3:
-// a segment's end state and map (the recurrence of the identity's rows with v = 0).
+// a segment's end state and map (the recurrence of the identity's rows with v = 0); 4: the
+// reverse of 3, a segment's gradient of its start state (its map is the forward's, transposed).
 template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
     using Tv = Tv_;        // v, or dy in the reverse pass
@@ -601,23 +603,26 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     using Tout = typename Cfg::Tout;
     using Block = typename Cfg::Block;
     constexpr int C = Cfg::C, NP = Cfg::NP, NW = Cfg::NW, MODE = Cfg::MODE, KP = Cfg::KP, PO = Cfg::PO, PV = Cfg::PV;
-    constexpr bool REV = MODE == 2, BWD = Cfg::BWD, STATE = MODE == 3;
+    constexpr bool REV = MODE == 2 || MODE == 4, BWD = Cfg::BWD, STATE = MODE == 3 || MODE == 4, MAP = MODE == 3;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // STATE: after the slices of headdim come those of the identity's rows (dstate of them)
-    const int nslice = STATE ? p.slices + (p.N + 16 * NW - 1) / (16 * NW) : p.slices;
+    // MAP: after the slices of headdim come those of the identity's rows (dstate of them)
+    const int nslice = MAP ? p.slices + (p.N + 16 * NW - 1) / (16 * NW) : p.slices;
     const int slice0 = int(blockIdx.x % unsigned(nslice)), bh = int(blockIdx.x / unsigned(nslice));
-    const bool ident = STATE && slice0 >= p.slices;
+    const bool ident = MAP && slice0 >= p.slices;
     const int slice = ident ? slice0 - p.slices : slice0, rows = ident ? p.N : p.P;
     const int seg = int(blockIdx.y);
-    // the first segment starts from h0 itself; nothing starts from the last one's end
-    if (STATE && (seg + 1 == int(gridDim.y) || (ident && seg == 0))) return;
+    // the first segment starts from h0 itself; nothing starts from the last one's end (reverse
+    // passes: from the other end)
+    const int nseg = int(gridDim.y);
+    const bool inner = REV ? seg + 1 < nseg : seg > 0;     // not the segment that starts from h0
+    if (STATE && (seg == (REV ? 0 : nseg - 1) || (ident && seg == 0))) return;
     const int b = bh / p.heads, h = bh - b * p.heads;
     const int nchunk = (p.seqlen + C - 1) / C;
     // this segment's steps; chunk of loop step i: forwards, or backwards in the reverse pass
     const int first = seg * p.seg_chunks, count = min(p.seg_chunks, nchunk - first);
-    auto chunk_of = [&](int i) { return REV ? nchunk - 1 - i : first + i; };
+    auto chunk_of = [&](int i) { return REV ? first + count - 1 - i : first + i; };
 
     const int hk = h / (p.heads / p.qk_heads), prow = rows - slice * NW * 16;
     const size_t vrow = size_t(p.heads) * p.P;
@@ -691,9 +696,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     };
 #pragma unroll
     for (int j = 0; j < NP / 8; ++j) zero4(s[j]);
-    const int nseg = int(gridDim.y);
-    const float *start = ident || (STATE && seg > 0) ? nullptr
-                         : seg > 0 ? p.seg_state + (size_t(bh) * nseg + seg - 1) * p.P * p.N
+    const float *start = ident || (STATE && inner) ? nullptr
+                         : inner ? p.seg_state + (size_t(bh) * nseg + (REV ? seg + 1 : seg - 1)) * p.P * p.N
                          : p.h0 ? p.h0 + sbase : nullptr;
     if (start != nullptr)
         state_io([&](float &x, float &y, size_t off) {
@@ -808,13 +812,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         if constexpr (BWD)
             for (int t = lane; t < p.seqlen; t += 32) {
                 p.sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
-                if constexpr (REV) p.sum2[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
+                if constexpr (MODE == 2) p.sum2[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
             }
-        if constexpr (REV)
+        if constexpr (MODE == 2)
             for (int x = lane; x < nbound; x += 32) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = 0.f;
         return;
     }
-    if constexpr (REV) fetch_state(nbound - 1);
+    if constexpr (MODE == 2) fetch_state(inner ? (first + count) / (kDeltaSave / C) : nbound - 1);
     int turn = warp + 1;                                   // loop steps until it is this warp's to start copies
     // the largest magnitude of the state, kept up with its updates
     float ms = 0.f;
@@ -837,7 +841,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                 if constexpr (Cfg::G16) keep_state16(p.s16, cS.c, c / CS);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
             }
-        if constexpr (REV) {
+        if constexpr (MODE == 2) {
             const float4 *ep = reinterpret_cast<const float4 *>(p.e + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -988,7 +992,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                     for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
                 token_sums(p.sum, dy, c * C);
             }
-        } else {
+        } else if constexpr (MODE == 2) {
             // the gradient of beta
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -1064,11 +1068,15 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     if (!alive)                                            // copies may still be on their way: wait (bounded) for them
         for (int i = max(0, count - Cfg::STAGES); i < count; ++i)
             mbar_wait(&full[i % Cfg::STAGES], uint32_t(i / Cfg::STAGES) & 1, kDeltaWaitCycles);
-    if constexpr (MODE == 1) keep_state(p.ck, nbound - 1);
-    if constexpr (REV) dot_state(0);
+    if constexpr (MODE == 1)
+        if (seg + 1 == nseg) keep_state(p.ck, nbound - 1);
+    if constexpr (MODE == 2) {
+        if (seg == 0) dot_state(0);
+        else cp_async_wait<0>();
+    }
     float *end = ident ? p.seg_map + (size_t(bh) * nseg + seg) * p.N * p.N
                  : STATE ? p.seg_state + (size_t(bh) * nseg + seg) * p.P * p.N
-                 : !p.hN || first + count < nchunk ? nullptr
+                 : !p.hN || seg != (REV ? 0 : nseg - 1) ? nullptr
                  : p.end_slot ? p.seg_state + (size_t(bh) * nseg + seg) * p.P * p.N : p.hN + sbase;
     if (end != nullptr)
         state_io([&](float &x, float &y, size_t off) { *reinterpret_cast<float2 *>(end + off) = make_float2(x, y); });
@@ -1076,8 +1084,9 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 
 // The segments' start states: behind segment 0 the state that it ended with, then
 //     start(i + 1) = start(i) map(i) + end(i)
-// in place of end(i).  A CTA takes R rows of one head through the segments, thread j column j.
-template <int R>
+// in place of end(i); reverse passes from the last segment down, with map(i) transposed.  A CTA
+// takes R rows of one head through the segments, thread j column j.
+template <int R, bool REV>
 __global__ void __launch_bounds__(128) delta_fold_kernel(const DeltaArgs p, int nseg) {
     __shared__ __align__(16) float row[R][128];
     const int tiles = (p.P + R - 1) / R, bh = int(blockIdx.x) / tiles, r0 = (int(blockIdx.x) % tiles) * R, j = threadIdx.x;
@@ -1086,8 +1095,9 @@ __global__ void __launch_bounds__(128) delta_fold_kernel(const DeltaArgs p, int 
     const float *map = p.seg_map + size_t(bh) * nseg * p.N * p.N;
     float x[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) x[r] = r < nr && j < p.N ? st[size_t(r) * p.N + j] : 0.f;
-    for (int i = 1; i + 1 < nseg; ++i) {
+    for (int r = 0; r < R; ++r) x[r] = r < nr && j < p.N ? st[(REV ? size_t(nseg - 1) * p.P * p.N : 0) + size_t(r) * p.N + j] : 0.f;
+    for (int step = 1; step + 1 < nseg; ++step) {
+        const int i = REV ? nseg - 1 - step : step;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < R; ++r) row[r][j] = x[r];
@@ -1096,11 +1106,11 @@ __global__ void __launch_bounds__(128) delta_fold_kernel(const DeltaArgs p, int 
 #pragma unroll
         for (int r = 0; r < R; ++r) x[r] = r < nr && j < p.N ? end[size_t(r) * p.N + j] : 0.f;
         if (j < p.N) {
-            const float *m = map + size_t(i) * p.N * p.N + j;
+            const float *m = map + size_t(i) * p.N * p.N + (REV ? size_t(j) * p.N : size_t(j));
             for (int n0 = 0; n0 < p.N; n0 += 32) {         // 32 loads on their way at once
                 float f[32];
 #pragma unroll
-                for (int n = 0; n < 32; ++n) f[n] = n0 + n < p.N ? __ldg(m + size_t(n0 + n) * p.N) : 0.f;
+                for (int n = 0; n < 32; ++n) f[n] = n0 + n < p.N ? __ldg(m + size_t(n0 + n) * (REV ? 1 : p.N)) : 0.f;
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll

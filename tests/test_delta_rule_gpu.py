@@ -272,6 +272,18 @@ def test_backward_long_memory(cuda_lib):
     check_bwd(make(1, 700, 2, 1, 32, 64, dtype=F32, seed=4, decay=1e-3), F32)
 
 
+@pytest.mark.parametrize("shape", [(1, 2048, 1, 1, 16, 32), (1, 2101, 2, 1, 32, 64), (2, 3000, 3, 3, 72, 40),
+                                   (1, 2500, 2, 2, 128, 128)], ids=str)
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32), (BF16, F32), (F32, BF16)])
+def test_backward_in_segments(cuda_lib, shape, dtype, grad):
+    """Long sequences of few heads: both passes are cut into segments that run at once."""
+    d = make(*shape, dtype=dtype, seed=sum(shape), decay=0.02, state=shape[2] > 1)
+    d["a"][:, 700] = -float("inf")
+    dy, dS, got = check_bwd(d, grad, seed=2, dfinal=shape[1] != 2101)
+    again = ssm.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=0.7)
+    assert all(got[n] is None or torch.equal(got[n], again[n]) for n in got)
+
+
 def test_backward_hard_gates(cuda_lib):
     """beta = 0 (its gradient still counts what would have been written), -inf resets (nothing
     flows past them), repeated and zero keys."""
