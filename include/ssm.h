@@ -322,14 +322,17 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  *   q, k          : [batch][seqlen][qk_heads][dstate], in_dtype.  qk_heads divides heads:
  *                   head h reads key head h / (heads / qk_heads).
  *   v, y          : [batch][seqlen][heads][headdim], in_dtype / out_dtype (y written).
- *   a, beta       : [batch][seqlen][heads] fp32.  a is the log decay (any value, -inf forgets
- *                   everything before the token); beta any value, 0 writes nothing.
+ *   a, beta       : [batch][seqlen][heads] fp32.  a is the log decay (at most 0; -inf forgets
+ *                   everything before the token; see below for growth); beta 0 writes nothing.
  *   initial_state : [batch][heads][headdim][dstate] fp32 or NULL (zero).
  *   final_state   : the same, or NULL (not written).  May be initial_state itself.
  * headdim and dstate must be multiples of 8 and at most 128
  * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on scaled fp16 operands,
  * two for each fp32 value, with fp32 accumulation: the final state and an fp32 y come out as
  * from fp32 arithmetic (about 2^-21 of their size), a bf16 y within its own rounding and 2^-11.
+ * This holds for states that do not grow: a <= 0 and beta k.k in [0, 2].  Growth by up to 2^16
+ * within a chunk costs nothing; by 2^g the terms of the chunk's first tokens keep about 38 - g
+ * bits.
  * A value that is not finite spreads over the rest of its chunk of 32 tokens, earlier ones
  * included.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.

@@ -152,7 +152,7 @@ template <int LANES> struct NormGroups {
     }
 };
 
-// R rows per group and step (narrow rows: more bytes in flight).  The arithmetic runs on packed
+// R rows per group and step (many narrow rows: more bytes in flight).  The arithmetic runs on packed
 // pairs: with one value an instruction, rows of 64 were bound by issue (24.5 us for 393216).
 template <int LANES, int V, int R, bool VEC, typename Tin, typename Tout>
 __global__ void __launch_bounds__(LANES ? 256 : 512) layer_norm_fwd_kernel(const NormArgs p) {

@@ -13,7 +13,8 @@ constexpr int kSMs = 148, kMaxDim = 8192;
 
 // The group that owns a row and its vectors per lane, by the row's width: f(lanes, V, threads)
 // with `lanes` 8 or 32 within a warp (CTAs of 256 threads), or 0 for one CTA per row.  A
-// backward lane carries 16 V column sums beside the row, so its warps stop at V = 2.
+// backward lane carries 16 V column sums beside the row, so its warps stop at V = 2.  A warp per
+// row where it can be: 16384 rows of 768 take 16.4 us with the call and 22.5 with a CTA per row.
 template <bool BWD, typename F> int by_width(int dim, F f) {
     using std::integral_constant;
     if (dim <= 64) return f(integral_constant<int, 8>(), integral_constant<int, 1>(), 256);
@@ -41,10 +42,23 @@ template <typename K> int resident(K kernel) {
     return std::min(2048, 65536 / ((std::max(at.numRegs, 32) + 7) / 8 * 8) / 32 * 32);
 }
 
+// Narrow rows go several a step once the whole grid has that many for every group: 393216 rows
+// of 64 took 26.6 us so and 28.7 one by one, 98304 rows of 256 26.7 and 28.7 (bf16, from HBM); with
+// fewer the idle places cost more than they bring (1000 rows of 64: 8.2 and 6.1 us), and so they
+// do where a lane's values are loaded one by one (393219 rows of 63: 47 and 43 us).
 template <bool VEC, typename Tin, typename Tout> int run_fwd(const ssm::NormArgs &a, cudaStream_t s) {
     return by_width<false>(a.dim, [&](auto lanes, auto v, int threads) {
-        constexpr int R = lanes() == 8 && v() == 1 ? 4 : lanes() == 8 || (lanes() == 32 && v() == 1) ? 2 : 1;
-        auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), R, VEC, Tin, Tout>;
+        constexpr int R = !VEC ? 1 : lanes() == 8 && v() == 1 ? 4 : lanes() == 8 || (lanes() == 32 && v() == 1) ? 2 : 1;
+        if constexpr (R > 1) {
+            auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), R, VEC, Tin, Tout>;
+            static const int per_sm = resident(kernel);
+            const int grid = kSMs * std::max(1, per_sm / threads);
+            if (a.rows >= (long long)grid * (threads / lanes()) * R) {
+                kernel<<<grid, threads, 0, s>>>(a);
+                return status_of(cudaGetLastError());
+            }
+        }
+        auto kernel = ssm::layer_norm_fwd_kernel<lanes(), v(), 1, VEC, Tin, Tout>;
         static const int per_sm = resident(kernel);
         kernel<<<grid_of(lanes(), threads, per_sm, int(a.rows)), threads, 0, s>>>(a);
         return status_of(cudaGetLastError());

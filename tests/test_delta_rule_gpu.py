@@ -299,6 +299,20 @@ def test_backward_hard_gates(cuda_lib):
     assert float(g["dbeta"][:, 5:8].abs().max()) > 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_growing_states(cuda_lib, dtype):
+    """Gates above 0 and corrections that overshoot: growth by up to 2^14 within a chunk stays
+    within the operands' range, and the bounds are the same."""
+    d = make(1, 75, 2, 1, 32, 64, dtype=dtype, seed=21)
+    d["a"] = d["a"].abs()                                  # 0 to 0.3: e^4.8 = 2^7 a chunk on average
+    run_and_check(d, F32)
+    check_bwd(d, F32, seed=4)
+    d["a"] = -d["a"]
+    d["beta"] = d["beta"] * 2.2
+    run_and_check(d, F32)
+    check_bwd(d, F32, seed=5)
+
+
 def test_backward_tiny_gradients(cuda_lib):
     """Gradients of 1e-9, as behind a mean over a large batch: the scaled operands keep them."""
     d = make(1, 90, 2, 2, 64, 64, seed=13)

@@ -75,6 +75,14 @@ def test_many_rows(cuda_lib, rows, dim):
     check_bwd(x, w, dy.to(BF16).to(DEV), mean, rstd)
 
 
+@pytest.mark.parametrize("rows,dim,dtype", [(160001, 64, BF16), (310003, 40, BF16), (170005, 32, F32), (80001, 128, BF16),
+                                            (60007, 120, F32), (40011, 200, BF16)])
+def test_more_rows_than_steps_of_the_whole_grid(cuda_lib, rows, dim, dtype):
+    """Enough narrow rows that a group takes several a step, the last step partly past the end."""
+    x, w, b, _ = make(rows, dim, dtype, seed=rows)
+    check_fwd(x, w, b)
+
+
 @pytest.mark.parametrize("dim", [64, 100, 1024, 3000])
 def test_without_weight_or_bias(cuda_lib, dim):
     x, w, b, dy = make(9, dim, F32, seed=dim)
