@@ -5,9 +5,11 @@
 // A CTA (a chunk of 64 tokens of one key head) starts ten bulk copies per value head and waits
 // once: nothing is loaded, converted or stored by its threads on the way.  Converting fp32
 // operands here instead took 4000 of 6100 instructions a warp, and 446 us where this takes 296
-// (batch 8 x 2048 tokens x 24 heads over 24 key heads, headdim 64, dstate 128).  A tile's scale is that of its part, 16 rows of headdim, which are one step of a
-// product's inner index: before a step its A operand is multiplied with the power of two (at
-// most 1) that brings the step's product to the smallest of the parts' scales.
+// (8 x 2048 tokens, 24 heads over 24 key heads, headdim 64, dstate 128).  What is left is the
+// latency of the copies and of dependent products, at two CTAs an SM.  A tile's scale is that of
+// its part, 16 rows of headdim, which are one step of a product's inner index: before a step its
+// A operand is multiplied with the power of two (at most 1) that brings the step's product to
+// the smallest of the parts' scales.
 #pragma once
 
 #include "delta_grad.cuh"
