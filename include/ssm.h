@@ -328,8 +328,8 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  *   final_state   : the same, or NULL (not written).  May be initial_state itself.
  * headdim and dstate must be multiples of 8 and at most 128
  * (SSM_ERR_UNSUPPORTED otherwise).  Products run on the tensor cores on scaled fp16 operands,
- * two for each fp32 value, with fp32 accumulation: the final state and an fp32 y come out as
- * from fp32 arithmetic (about 2^-21 of their size), a bf16 y within its own rounding and 2^-11.
+ * two for each fp32 value, with fp32 accumulation: the final state and y come out as from fp32
+ * arithmetic (about 2^-21 of their size), a bf16 y rounded once from that.
  * This holds for states that do not grow: a <= 0 and beta k.k in [0, 2].  Growth by up to 2^16
  * within a chunk costs nothing; by 2^g the terms of the chunk's first tokens keep about 38 - g
  * bits.
@@ -337,7 +337,7 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * included.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.
  * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
- * 175 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
+ * 216 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
  * each segment and head 4 * (headdim + dstate) * dstate bytes.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

@@ -25,13 +25,11 @@ template <typename Tin, typename Tout> int launch_step(const ssm::DeltaStepArgs 
 struct FwdPlan {
     int nseg;
     size_t prep, rows, seg_state, seg_map, all;      // offsets, and the bytes
-    FwdPlan(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int out_dtype) {
-        const size_t blocks = out_dtype == SSM_F32 ? prep_bytes<ssm::DeltaBlock<2>>(batch, seqlen, heads)
-                                                   : prep_bytes<ssm::DeltaBlock<1>>(batch, seqlen, heads);
+    FwdPlan(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype) {
         nseg = segments(batch, seqlen, heads, P, N, in_dtype == SSM_F32, false);
         const size_t seg = nseg > 1 ? size_t(batch) * heads * nseg * N * 4 : 0;
         prep = 0;
-        rows = prep + round16(blocks);
+        rows = prep + round16(prep_bytes(batch, seqlen, heads));
         seg_state = rows + round16(rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
         seg_map = seg_state + seg * P;
         all = seg_map + seg * N;
@@ -40,8 +38,7 @@ struct FwdPlan {
 
 // Forward: the chunk blocks and operands, then the chains, in segments where that pays.
 template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *workspace, size_t bytes, cudaStream_t s) {
-    const FwdPlan at(a.batch, a.seqlen, a.heads, a.qk_heads, a.P, a.N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16,
-                     sizeof(Tout) == 4 ? SSM_F32 : SSM_BF16);
+    const FwdPlan at(a.batch, a.seqlen, a.heads, a.qk_heads, a.P, a.N, sizeof(Tin) == 4 ? SSM_F32 : SSM_BF16);
     constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, at.all, s)) return st;
@@ -50,7 +47,7 @@ template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *works
     a.seg_state = reinterpret_cast<float *>(ws.p + at.seg_state);
     a.seg_map = reinterpret_cast<float *>(ws.p + at.seg_map);
     a.timeouts = wait_counter();
-    int st = a.timeouts ? dispatch_prep<Tin, ssm::DeltaBlock<sizeof(Tout) == 4 ? 2 : 1>>(a, s) : int(SSM_ERR_CUDA);
+    int st = a.timeouts ? dispatch_prep<Tin>(a, s) : int(SSM_ERR_CUDA);
     if (at.nseg > 1) {
         const long long chunks = (long long)delta_chunks(a.seqlen);
         a.seg_chunks = int((chunks + at.nseg - 1) / at.nseg);
@@ -82,7 +79,7 @@ size_t ssm_delta_rule_fwd_workspace(int batch, int seqlen, int heads, int qk_hea
     if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return 0;
     if (delta_sizes(batch, seqlen, heads, qk_heads, headdim, dstate) != SSM_OK) return 0;
     if (batch == 0 || heads == 0 || seqlen == 0) return 0;
-    return FwdPlan(batch, seqlen, heads, qk_heads, headdim, dstate, in_dtype, out_dtype).all;
+    return FwdPlan(batch, seqlen, heads, qk_heads, headdim, dstate, in_dtype).all;
 }
 
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

@@ -34,7 +34,7 @@ template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaG
     }
 }
 
-using Block = ssm::DeltaBlock<2>;
+using Block = ssm::DeltaBlock;
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
@@ -48,7 +48,7 @@ struct BwdParts {
         const size_t rows16 = bh * delta_chunks(seqlen) * parts * 512 * 4;
         size_t at = 0;
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
-        add(prep, prep_bytes<Block>(batch, seqlen, heads));
+        add(prep, prep_bytes(batch, seqlen, heads));
         add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
         // bf16 gradients: w and the state's gradient as fp16 tiles alone, dy, e and the state beside
         const bool g16 = grad_dtype == SSM_BF16;
@@ -92,7 +92,7 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     f.rows = ws.p + at.rows;
     f.timeouts = wait_counter();
     auto bits = [&](size_t off) { return reinterpret_cast<unsigned *>(ws.p + off); };
-    int st = f.timeouts ? dispatch_prep<Tin, Block>(f, s) : int(SSM_ERR_CUDA);
+    int st = f.timeouts ? dispatch_prep<Tin>(f, s) : int(SSM_ERR_CUDA);
     if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
     f.smax = bits(at.smax); f.emax = bits(at.emax);
     f.v = v; f.v2 = dy; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;

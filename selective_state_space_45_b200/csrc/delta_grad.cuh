@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(Cfg::NT) delta_grad_kernel(const DeltaGradArgs
     for (int x = 0; x < 2; ++x) {
         const int cc = c32 + (x < n32 ? x : 0);
         const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * p.block +
-                                                           DeltaBlock<2>::OFF_VEC) + kVecScalars * kDeltaC;
+                                                           DeltaBlock::OFF_VEC) + kVecScalars * kDeltaC;
         ick[x] = 1.f / one[kCk];         // powers of two: exact
         icq[x] = 1.f / one[kCq];
     }

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(128, Cfg::CTAS) delta_grad16_kernel(const Delt
             for (int x = 0; x < 2; ++x) {
                 const int cc = c32 + (x < n32 ? x : 0);
                 const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + h) * nck + cc) * p.block +
-                                                                   DeltaBlock<2>::OFF_VEC) + kVecScalars * kDeltaC;
+                                                                   DeltaBlock::OFF_VEC) + kVecScalars * kDeltaC;
                 ick[x] = __ldg(one + kCk);
                 icq[x] = __ldg(one + kCq);
             }

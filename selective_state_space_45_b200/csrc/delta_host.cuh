@@ -21,8 +21,8 @@ inline int delta_sizes(int batch, int tokens, int heads, int qk_heads, int headd
 inline size_t delta_chunks(int seqlen) { return (size_t(seqlen) + ssm::kDeltaC - 1) / ssm::kDeltaC; }
 
 // Bytes of the prep kernel's blocks.
-template <class Block> size_t prep_bytes(int batch, int seqlen, int heads) {
-    return size_t(batch) * heads * delta_chunks(seqlen) * Block::BYTES;
+inline size_t prep_bytes(int batch, int seqlen, int heads) {
+    return size_t(batch) * heads * delta_chunks(seqlen) * ssm::DeltaBlock::BYTES;
 }
 // dstate padded to the next multiple of 32 (zero columns): the products' inner length.
 inline int padded_state(int N) { return (N + 31) / 32 * 32; }
@@ -44,20 +44,20 @@ template <typename K> int set_smem(K kernel, int bytes) {
 }
 
 // The chunk blocks into a.prep, k and q as operands into a.rows.
-template <int NP, typename Tin, class Block> int launch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
+template <int NP, typename Tin> int launch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
     const long long blocks = ((long long)a.batch * a.heads * (long long)delta_chunks(a.seqlen) + 3) / 4;
     if (blocks > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    constexpr int smem = 4 * int(sizeof(ssm::PrepScratch<NP, Tin, Block>));
-    if (const int st = set_smem(ssm::delta_prep_kernel<NP, Tin, Block>, smem)) return st;
-    ssm::delta_prep_kernel<NP, Tin, Block><<<unsigned(blocks), 128, smem, s>>>(a);
+    constexpr int smem = 4 * int(sizeof(ssm::PrepScratch<NP, Tin>));
+    if (const int st = set_smem(ssm::delta_prep_kernel<NP, Tin>, smem)) return st;
+    ssm::delta_prep_kernel<NP, Tin><<<unsigned(blocks), 128, smem, s>>>(a);
     return status_of(cudaGetLastError());
 }
-template <typename Tin, class Block> int dispatch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
+template <typename Tin> int dispatch_prep(const ssm::DeltaArgs &a, cudaStream_t s) {
     switch (padded_state(a.N)) {
-    case 32: return launch_prep<32, Tin, Block>(a, s);
-    case 64: return launch_prep<64, Tin, Block>(a, s);
-    case 96: return launch_prep<96, Tin, Block>(a, s);
-    default: return launch_prep<128, Tin, Block>(a, s);
+    case 32: return launch_prep<32, Tin>(a, s);
+    case 64: return launch_prep<64, Tin>(a, s);
+    case 96: return launch_prep<96, Tin>(a, s);
+    default: return launch_prep<128, Tin>(a, s);
     }
 }
 

@@ -37,10 +37,10 @@
 // Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
 // operand scaled by a power of two (one per chunk for k, q and the triangles, one per warp and
 // chunk for the state and what follows from it) so that its range does not matter.  bf16
-// inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), those
-// behind a bf16 y as one.  Against the definition in 64 bits the state comes out at 2e-7, as
-// from fp32 arithmetic.  Three bf16 pieces hold the same bits but cost half as many products
-// again; two bf16 pieces gave 6e-6.
+// inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), whatever
+// the type of y: one behind a bf16 y made 11% of its values round the other way (8 x 2048
+// tokens x 24 heads of 64 x 128: 280 us with the call, 312 with two).  Three bf16 pieces hold
+// the same bits but cost half as many products again; two bf16 pieces gave 6e-6.
 #pragma once
 
 #include <type_traits>
@@ -98,7 +98,7 @@ constexpr int kOutRow = 48;          // bytes per row of a warp's output tile
 __device__ __forceinline__ int tri_at(int r, int c) { return r * 32 + ((c ^ (r >> 2)) & 1) * 16; }
 
 // What the prep kernel leaves per chunk and head.  A triangle is the three 16 x 16 tiles
-// (0,0), (1,0), (1,1) per fp16 piece, scaled by a power of two: G in two pieces, Pm in PP.
+// (0,0), (1,0), (1,1) per fp16 piece, scaled by a power of two: G and Pm, two pieces each.
 // Vectors over the chunk's tokens, the scales of k and q (ck, cq) taken back out where a
 // product with them is used:
 enum {
@@ -111,9 +111,8 @@ enum {
     kVecs
 };
 enum { kGamLast, kCk, kCq, kInvG, kInvP, kMaxBeta, kMaxEbk, kMaxGk, kMaxSgq };   // 1 / scales; largest magnitudes
-template <int PP_> struct DeltaBlock {
-    static constexpr int PP = PP_;
-    static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 3 * PP * kTri, BYTES = OFF_VEC + kVecs * kDeltaC * 4;
+struct DeltaBlock {
+    static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 6 * kTri, BYTES = OFF_VEC + kVecs * kDeltaC * 4;
 };
 
 // k and q of a chunk as the chains read them: scaled fp16, KP pieces of k, then of q, each 32
@@ -147,8 +146,7 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int C = kDeltaC, NT = 32 * NW;
     static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
     static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
-    static constexpr int PO = MODE == 1 || MODE == 2 || sizeof(Tout) == 4 ? 2 : 1;       // pieces behind y
-    using Block = DeltaBlock<PO>;
+    using Block = DeltaBlock;
     using Rows = DeltaRows<NP, KP>;
     static constexpr int KROW = Rows::ROW;
     static constexpr int VROW = NW * 16 * int(sizeof(Tv)) + 16;
@@ -182,12 +180,12 @@ __device__ __forceinline__ void mma_exact(float (&acc)[4], const unsigned (&a)[K
 
 // One warp per chunk and head forms the chunk's block; the first head of each key head also
 // writes the chunk's k and q as operands.  Four warps per CTA, each with its own scratch.
-template <int NP, typename Tin, class Block> struct PrepScratch {
+template <int NP, typename Tin> struct PrepScratch {
     static constexpr int RATROW = 33, NROW = 36, ROW = NP * int(sizeof(Tin)) + 16;
     union {
         unsigned char rows[2][kDeltaC * ROW];                   // k and q as they come
         struct {
-            unsigned char block[Block::BYTES];                  // as it goes out
+            unsigned char block[DeltaBlock::BYTES];               // as it goes out
             float at[kDeltaC * NROW];                           // at[s][t] = A(t, s)
             float rat[kDeltaC * RATROW + 4];                    // rat[t][s + 1] = r(t, s); later parts of G
             float beta[kDeltaC];
@@ -195,9 +193,10 @@ template <int NP, typename Tin, class Block> struct PrepScratch {
     };
 };
 
-template <int NP, typename Tin, class Block>
+template <int NP, typename Tin>
 __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
-    using Scratch = PrepScratch<NP, Tin, Block>;
+    using Block = DeltaBlock;
+    using Scratch = PrepScratch<NP, Tin>;
     constexpr int C = kDeltaC, RATROW = Scratch::RATROW, NROW = Scratch::NROW, ROW = Scratch::ROW;
     constexpr int KP = sizeof(Tin) == 4 ? 3 : 1, OP = sizeof(Tin) == 4 ? 2 : 1;      // pieces here, and as operands
     using Rows = DeltaRows<NP, OP>;
@@ -380,10 +379,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
                 for (int r = 0; r < 2; ++r) {
                     const float *cq = qk[2 * (m + n) + i] + 2 * r;
                     unsigned char *to = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
-                    unsigned w[Block::PP];
-                    split_f16<Block::PP>(f2(cq[0], cq[1]), sp.c, w);
+                    unsigned w[2];
+                    split_f16<2>(f2(cq[0], cq[1]), sp.c, w);
 #pragma unroll
-                    for (int y = 0; y < Block::PP; ++y) *reinterpret_cast<unsigned *>(to + Block::OFF_P + 3 * y * kTri) = w[y];
+                    for (int y = 0; y < 2; ++y) *reinterpret_cast<unsigned *>(to + Block::OFF_P + 3 * y * kTri) = w[y];
                 }
     __syncwarp();
     // G of the two diagonal tiles, G (I + diag(beta) A) = A: lane t solves its row from the
@@ -602,7 +601,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     using Tv2 = typename Cfg::Tv2;
     using Tout = typename Cfg::Tout;
     using Block = typename Cfg::Block;
-    constexpr int C = Cfg::C, NP = Cfg::NP, NW = Cfg::NW, MODE = Cfg::MODE, KP = Cfg::KP, PO = Cfg::PO, PV = Cfg::PV;
+    constexpr int C = Cfg::C, NP = Cfg::NP, NW = Cfg::NW, MODE = Cfg::MODE, KP = Cfg::KP, PV = Cfg::PV;
     constexpr bool REV = MODE == 2 || MODE == 4, BWD = Cfg::BWD, STATE = MODE == 3 || MODE == 4, MAP = MODE == 3;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
@@ -887,14 +886,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     mma_pieces<2, KP>(sk[2 * h2 + n], A, kb[h2], n);
-                    if constexpr (!REV && !STATE) {
-                        unsigned Ao[PO][4];
-#pragma unroll
-                        for (int m = 0; m < PO; ++m)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) Ao[m][r] = A[m][r];
-                        mma_pieces<PO, KP>(sq[2 * h2 + n], Ao, qb[h2], n);
-                    }
+                    if constexpr (!REV && !STATE) mma_pieces<2, KP>(sq[2 * h2 + n], A, qb[h2], n);
                 }
             if (j + 1 < NP / 16) load_kq(j + 1);
         }
@@ -967,12 +959,12 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         Tok o;
         if constexpr (!REV && !STATE) {
             // y = scale gam S q + Pm (beta e)
-            unsigned A[2][PO][4];
+            unsigned A[2][2][4];
             const Pow2 cu = scale_by(mx, one[kMaxBeta]);
             scale_tok(o, x, vec + kVecBeta * C, t4);
-            split_tok<PO>(o, cu.c, A);
+            split_tok<2>(o, cu.c, A);
             zero_tok(o);
-            mma_triangle<PO, PO, false>(o, A, tbase + Block::OFF_P);
+            mma_triangle<2, 2, false>(o, A, tbase + Block::OFF_P);
             scale_tok(sq, sq, vec + kVecSgq * C, t4);
             const float f = one[kInvP] * cu.inv;
 #pragma unroll

@@ -81,6 +81,26 @@ def test_forward(cuda_lib, shape, dtype, out):
     run_and_check(make(*shape, dtype=dtype, seed=sum(shape), state=shape[1] % 2 == 1), out)
 
 
+def share_misrounded(got, ref):
+    """The share of bf16 values that are not the reference's, rounded."""
+    return float((got.cpu() != torch.from_numpy(np.ascontiguousarray(ref)).to(BF16)).float().mean())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_bf16_y_is_the_fp32_result_rounded(cuda_lib, dtype):
+    """A bf16 y holds what an fp32 y would, rounded once.  Before the rounding it is off by at
+    most d = 2^-15 of its size (relative L2, as an fp32 y).  A value x then rounds the other way
+    only where it lies within its error of a border between two steps, which are 2^-8 |x| apart
+    or more: a share of at most 2 d |y| / (2^-8 |x|) of the values near x.  Over values spread
+    like a normal distribution, E[min(1, 2^-6 / |x|)] with d |y| = 2^-15: 2^-6 0.8 (1 + ln 2^6)
+    = 6.4%, and a sixteenth of that at the errors that fp32 sums have.  Operands of 11 bits
+    gave 11%."""
+    for shape in ((2, 130, 4, 2, 64, 128), (1, 257, 2, 2, 128, 64)):
+        d = make(*shape, dtype=dtype, seed=17)
+        y, _ = ssm.delta_rule(**d, scale=0.7, out_dtype=BF16)
+        assert share_misrounded(y, oracle.delta_rule(**d, scale=0.7)[0]) <= 0.064
+
+
 def test_forward_many_chunks_long_memory(cuda_lib):
     """1500 tokens whose decay keeps most of the state: errors must not pile up."""
     run_and_check(make(1, 1500, 2, 1, 32, 64, dtype=F32, seed=4, decay=1e-3), F32)
