@@ -3,7 +3,7 @@
 // gradient at the same places), then the chunks' gradients in parallel.  Long sequences of few
 // heads go through the two passes in segments that run at once, as in the forward.  Scratch: the
 // caller's workspace or a stream-ordered buffer.
-#include "delta_grad16.cuh"
+#include "delta_grad.cuh"
 #include "delta_host.cuh"
 
 using namespace ssm_host;
@@ -13,16 +13,9 @@ namespace {
 template <int NP, int PW, typename Tin, typename Tg> int launch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
     const long long ctas = (long long)a.batch * a.qk_heads * ((a.seqlen + ssm::kGradC - 1) / ssm::kGradC);
     if (ctas > INT_MAX) return SSM_ERR_UNSUPPORTED;
-    constexpr int KP = sizeof(Tin) == 4 ? 2 : 1;
-    if constexpr (sizeof(Tg) == 2) {
-        using Cfg = ssm::Grad16Cfg<NP, PW, KP>;
-        if (const int st = set_smem(ssm::delta_grad16_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
-        ssm::delta_grad16_kernel<Cfg><<<unsigned(ctas), 128, Cfg::SMEM_BYTES, s>>>(a);
-    } else {
-        using Cfg = ssm::GradCfg<NP, PW, KP>;
-        if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
-        ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
-    }
+    using Cfg = ssm::GradCfg<NP, PW, (sizeof(Tin) == 4 ? 2 : 1), Tg>;
+    if (const int st = set_smem(ssm::delta_grad_kernel<Cfg>, Cfg::SMEM_BYTES)) return st;
+    ssm::delta_grad_kernel<Cfg><<<unsigned(ctas), Cfg::NT, Cfg::SMEM_BYTES, s>>>(a);
     return status_of(cudaGetLastError());
 }
 template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaGradArgs &a, cudaStream_t s) {
@@ -34,33 +27,27 @@ template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaG
     }
 }
 
-using Block = ssm::DeltaBlock;
-
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, w, ck, dck, y16, e16, s16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, seg_state, seg_map, all;
+    size_t prep, rows, e, ck, e16, w16, y16, s16, d16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, seg_state, seg_map, all;
     int nseg;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
         const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
         const size_t parts = size_t(delta_slices(P)) * kDeltaWarps;       // of 16 rows
         const size_t sum = parts * tok * 4, state = bh * nbound * parts * 16 * padded_state(N) * 4;
-        const size_t rows16 = bh * delta_chunks(seqlen) * parts * 512 * 4;
+        const size_t tok16 = bh * delta_chunks(seqlen) * parts * ssm::kTok16;       // a piece of e, w or dy
         size_t at = 0;
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         add(prep, prep_bytes(batch, seqlen, heads));
         add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
-        // bf16 gradients: w and the state's gradient as fp16 tiles alone, dy, e and the state beside
-        const bool g16 = grad_dtype == SSM_BF16;
-        const size_t tok16 = g16 ? bh * delta_chunks(seqlen) * parts * ssm::kTok16 : 0;
-        const size_t state16 = g16 ? bh * nbound * parts * 16 * (padded_state(N) > 64 ? 256 : 2 * padded_state(N)) : 0;
-        add(e, rows16);
-        add(w, g16 ? tok16 : rows16);
+        add(e, 2 * tok16);                              // as fp32
         add(ck, state);
-        add(dck, g16 ? state16 : state);
-        add(y16, tok16);
-        add(e16, tok16);
-        add(s16, state16);
+        add(e16, 2 * tok16);
+        add(w16, 2 * tok16);
+        add(y16, grad_dtype == SSM_BF16 ? tok16 : 2 * tok16);
+        add(s16, state);
+        add(d16, state);
         add(dyy, sum);
         add(edu, sum);
         add(vw, sum);
@@ -96,7 +83,7 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
     f.smax = bits(at.smax); f.emax = bits(at.emax);
     f.v = v; f.v2 = dy; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;
-    f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy); f.w = part(at.w);
+    f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
     // segments: whole spans of the kept states
     int nseg = 1;
     if (at.nseg > 1) {
@@ -112,7 +99,7 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
         r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
-        r.dck = part(at.dck); r.d16 = ws.p + at.dck; r.w16 = ws.p + at.w; r.y16 = ws.p + at.y16;
+        r.d16 = ws.p + at.d16; r.w16 = ws.p + at.w16; r.y16 = ws.p + at.y16;
         r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
         if (nseg > 1) {
@@ -122,9 +109,8 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
         if (st == SSM_OK) st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s, nseg);
     }
     if (st == SSM_OK) {
-        const ssm::DeltaGradArgs g{dy, f.a, f.beta, part(at.e), part(at.w), f.rows, f.prep, Block::BYTES, part(at.ck),
-                                   part(at.dck), ws.p + at.e16, ws.p + at.w, ws.p + at.y16, ws.p + at.s16,
-                                   ws.p + at.dck, f.timeouts, part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
+        const ssm::DeltaGradArgs g{f.a, f.beta, f.rows, f.prep, ws.p + at.e16, ws.p + at.w16, ws.p + at.y16,
+                                   ws.p + at.s16, ws.p + at.d16, f.timeouts, part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
                                    bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
                                    da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N,
                                    delta_slices(f.P) * kDeltaWarps, f.scale};

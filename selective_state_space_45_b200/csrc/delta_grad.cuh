@@ -15,17 +15,21 @@
 //          = <dS, S>(chunk's start) - sum_{t'<t} (dy.y - v.w)_t'
 // with the inner products taken afresh every 64 tokens: at most 32 terms are summed.
 //
-// Four warps with 16 tokens (rows) each, and with 64 columns of the state in shared memory four
-// more that take the upper 32 of them: every product on the tensor cores with scaled fp16
-// operands, here two pieces of each for fp32 gradients; delta_grad16.cuh is the form for bf16
-// gradients (one piece: 2^-12 against their 2^-9).  Bound by the loads' latency and the
-// conversions: 3 x 1021 tokens, 8 heads of 128 x 64 took 161 us with four warps and batches of
-// two loads, about 130 so (one CTA per SM by shared memory either way).
-// The token-by-token matrices never leave the registers: each is formed in the layout of an
-// accumulator whose rows are the rows it is then used with (dy e^T for dq, e dy^T, e w^T and
-// w e^T for dk), so that it becomes the next product's A operand as it stands, and tiles off
-// the triangle are skipped; every warp has ten of them.  The largest magnitudes that set the
-// scales come from the passes.
+// Operands.  Every product runs on the tensor cores with scaled fp16 operands, two pieces for
+// each value (one for dy, q and k where they come as bf16), as in the passes; the passes leave
+// them as tiles of this kernel's shared memory, and bulk copies bring them in: nothing is loaded
+// or converted by its threads on the way.  One piece behind bf16 gradients made 13% of them
+// round the other way.  A tile's scale is that of its part, 16 rows of headdim, which are one
+// step of a product's inner index: before a step its A operand is multiplied with the power of
+// two (at most 1) that brings the step's product to the smallest of the parts' scales.
+//
+// Four warps with 16 tokens (rows) each; where shared memory leaves room for one CTA only, four
+// more that take the other half of the state's columns.  The columns go by in slices of 32, the
+// next ones on their way as far as the memory reaches.  The token-by-token matrices never leave
+// the registers: each is formed in the layout of an accumulator whose rows are the rows it is
+// then used with (dy e^T for dq, e dy^T, e w^T and w e^T for dk), so that it becomes the next
+// product's A operand as it stands, and tiles off the triangle are skipped; every warp has ten
+// of them.  The largest magnitudes that set the scales come from the passes.
 #pragma once
 
 #include "delta_rule.cuh"
@@ -33,12 +37,9 @@
 namespace ssm {
 
 struct DeltaGradArgs {
-    const void *dy;
-    const float *a, *beta, *e, *w;     // e, w and the states as the passes leave them
+    const float *a, *beta;
     const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
-    size_t block;                      // bytes of a chunk block
-    const float *ck, *dck;             // states and their gradients at the boundaries
-    const unsigned char *e16, *w16, *y16, *s16, *d16;      // bf16 gradients: the same as fp16 tiles
+    const unsigned char *e16, *w16, *y16, *s16, *d16;      // the passes' tiles
     unsigned *timeouts;
     const float *dyy, *edu, *vw;       // [zparts][batch][heads][seqlen]
     const float *zsum;                 // [zparts][batch][heads][boundaries]
@@ -51,125 +52,219 @@ struct DeltaGradArgs {
     float scale;
 };
 
-constexpr int kGradC = 64, kGradN = 64;        // tokens per CTA, state columns per pass
+constexpr int kGradC = 64;                     // tokens per CTA
 
-// PW: headdim padded to 64 or 128; NP: dstate padded; KP: pieces of k and q; PG: of the others.
-template <int NP_, int PW_, int KP_> struct GradCfg {
-    static constexpr int NP = NP_, PW = PW_, KP = KP_, PG = 2;
-    static constexpr int W = NP < kGradN ? NP : kGradN, NT = 128 * (W / 32);
-    static constexpr int PROW = PW * 2 + 16, NROW = W * 2 + 16, TROW = kGradC * 2 + 16;      // padded rows (bytes)
-    static constexpr int TOK = kGradC * PROW, TT = PW * TROW, ST = PW * NROW, KT = kGradC * NROW;
-    static constexpr int OFF_Y = 0, OFF_E = OFF_Y + PG * TOK, OFF_W = OFF_E + PG * TT;
-    static constexpr int OFF_S = OFF_W + PG * TT, OFF_D = OFF_S + PG * ST;
-    static constexpr int OFF_K = OFF_D + PG * ST, OFF_Q = OFF_K + KP * KT;
-    static constexpr int OFF_VEC = OFF_Q + KP * KT;
-    static constexpr int SMEM_BYTES = OFF_VEC + 6 * kGradC * 4 + 16;
+// NP: dstate padded; PW: headdim padded to 64 or 128; KP: pieces of k and q; Tg: the gradients' type.
+template <int NP_, int PW_, int KP_, typename Tg_> struct GradCfg {
+    using Tg = Tg_;
+    static constexpr int NP = NP_, PW = PW_, KP = KP_, PARTS = PW / 16, PY = sizeof(Tg) == 2 ? 1 : 2;
+    using Rows = DeltaRows<NP, KP>;
+    static constexpr int TOK = 2 * PARTS * kTok16;         // bytes of a piece of e, w or dy: [half][part][piece]
+    static constexpr int OFF_E = 0, OFF_W = 2 * TOK, OFF_Y = 4 * TOK;
+    static constexpr int OFF_KQ = OFF_Y + PY * TOK;                           // [half] k and q
+    static constexpr int OFF_VEC = OFF_KQ + 2 * Rows::BYTES;
+    static constexpr int OFF_OUT = OFF_VEC + 6 * kGradC * 4 + 64;             // per-warp output tiles
+    static constexpr int OUT = sizeof(Tg) == 2 ? kTok16 : 0;
+    static constexpr int SLICE = 4 * PARTS * kTok16;                          // S and dE, 32 columns: [S, dE][part][piece]
+    static constexpr int HALF = 113 * 1024, WHOLE = 227 * 1024;               // shared memory for two CTAs on an SM, or one
+    static constexpr int fixed(int groups) { return OFF_OUT + 4 * groups * OUT; }
+    static constexpr int CTAS = fixed(1) + SLICE <= HALF ? 2 : 1;
+    static constexpr int NG = CTAS == 2 ? 1 : 2, NT = 128 * NG;               // groups of four warps
+    static constexpr int CW = NG == 2 && (NP == 32 || fixed(2) + 2 * SLICE > WHOLE) ? 16 : 32;       // a group's columns in a step
+    static constexpr int COLS = NG * CW, SL = COLS / 32, STEPS = (NP + COLS - 1) / COLS;
+    static constexpr int ROOM = ((CTAS == 2 ? HALF : WHOLE) - fixed(NG)) / (SL * SLICE);
+    static constexpr int STAGES = ROOM < STEPS ? ROOM : STEPS;
+    static constexpr int OFF_ST = fixed(NG);
+    static constexpr int SMEM_BYTES = OFF_ST + STAGES * SL * SLICE;
+    static_assert(STAGES >= 1 && STAGES <= 4);
 };
 
+// 2^e as a float and, for e <= 0, as a pair of halves (0 below the smallest).
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float(unsigned(min(max(e, -126), 127) + 127) << 23); }
+__device__ __forceinline__ unsigned half2_exp2(int e) {
+    const __half2 h = __float2half2_rn(exp2_int(e));
+    return *reinterpret_cast<const unsigned *>(&h);
+}
+template <int P> __device__ __forceinline__ void mul_f16x2(unsigned (&o)[P][4], const unsigned (&a)[P][4], unsigned f) {
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&a[p][i]), *reinterpret_cast<const __half2 *>(&f));
+            o[p][i] = *reinterpret_cast<const unsigned *>(&h);
+        }
+}
+// The pieces of a tile, 1 KB apart, as they are or transposed.
+template <int P> __device__ __forceinline__ void ldsm4_t_pieces(unsigned (&r)[P][4], unsigned at) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) ldsm4_t(r[i], at + i * kTok16);
+}
+
 template <class Cfg>
-__global__ void __launch_bounds__(Cfg::NT) delta_grad_kernel(const DeltaGradArgs p) {
-    constexpr int C = kGradC, NP = Cfg::NP, PW = Cfg::PW, KP = Cfg::KP, PG = Cfg::PG, W = Cfg::W, NT = Cfg::NT;
-    using Rows = DeltaRows<NP, KP>;
+__global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const DeltaGradArgs p) {
+    using Rows = typename Cfg::Rows;
+    using Tg = typename Cfg::Tg;
+    constexpr int C = kGradC, NP = Cfg::NP, KP = Cfg::KP, PY = Cfg::PY, PARTS = Cfg::PARTS, NT = Cfg::NT;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
     float *bend = bet + C, *dtok = bend + C;
     double *half = reinterpret_cast<double *>(dtok + C);
-    const int tid = threadIdx.x, lane = tid & 31, rt = (tid >> 5) & 3, j0 = tid >> 7, g = lane >> 2, t4 = lane & 3;
+    uint64_t *tokbar = reinterpret_cast<uint64_t *>(half + 2), *stbar = tokbar + 1;
+    const int tid = threadIdx.x, lane = tid & 31, rt = (tid >> 5) & 3, gr = tid >> 7, ht = rt >> 1, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
     const int c = int(blockIdx.x % unsigned(nchunk)), bk = int(blockIdx.x / unsigned(nchunk));
     const int b = bk / p.qk_heads, hk = bk - b * p.qk_heads;
     const int t0 = c * C, nt = min(C, p.seqlen - t0), group = p.heads / p.qk_heads;
-    const int c32 = 2 * c, n32 = min(2, nck - c32);
-    const size_t all = size_t(p.batch) * p.heads, krow = size_t(p.qk_heads) * p.N, vrow = size_t(p.heads) * p.P;
+    const int c32 = 2 * c, n32 = min(2, nck - c32), kp = (p.P + 15) / 16;
+    const size_t all = size_t(p.batch) * p.heads, krow = size_t(p.qk_heads) * p.N;
     const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
+    const int total = group * Cfg::STEPS;
+    if (tid == 0) {
+        mbar_init(tokbar, 1);
+        for (int i = 0; i < Cfg::STAGES; ++i) mbar_init(&stbar[i], 1);
+        mbar_fence_init();
+    }
+    auto zero = [&](int off, int bytes) {
+        for (int x = tid; x < bytes / 16; x += NT) *reinterpret_cast<uint4 *>(smem + off + 16 * x) = make_uint4(0, 0, 0, 0);
+    };
+    // a chunk whose second half is past the end: that half is zeros
+    if (n32 == 1) {
+        zero(Cfg::OFF_E + Cfg::TOK, Cfg::TOK);
+        zero(Cfg::OFF_W + Cfg::TOK, Cfg::TOK);
+        zero(Cfg::OFF_Y + PY * Cfg::TOK / 2, PY * Cfg::TOK / 2);
+        zero(Cfg::OFF_KQ + Rows::BYTES, Rows::BYTES);
+    }
+    if (kp < PARTS) {                    // parts past headdim: zeros
+        const int n = PARTS - kp;
+        for (int hf = 0; hf < 2; ++hf) {
+            zero(Cfg::OFF_E + hf * Cfg::TOK + kp * 2 * kTok16, n * 2 * kTok16);
+            zero(Cfg::OFF_W + hf * Cfg::TOK + kp * 2 * kTok16, n * 2 * kTok16);
+            zero(Cfg::OFF_Y + hf * (PY * Cfg::TOK / 2) + kp * PY * kTok16, n * PY * kTok16);
+        }
+        for (int i = 0; i < 2 * Cfg::SL * Cfg::STAGES; ++i)
+            zero(Cfg::OFF_ST + i * (Cfg::SLICE / 2) + kp * 2 * kTok16, n * 2 * kTok16);
+    }
+    __syncthreads();
+    // by one thread: a head's tokens; a step's slices of its states
+    auto copy_tokens = [&](int hg) {
+        const size_t bh = size_t(b) * p.heads + hk * group + hg;
+        const uint32_t tok = kp * kTok16;
+        mbar_arrive_expect_tx(tokbar, n32 * ((4 + PY) * tok + (hg == 0 ? Rows::BYTES : 0)));
+        for (int hf = 0; hf < n32; ++hf) {
+            const size_t at = (bh * nck + c32 + hf) * p.zparts * kTok16;
+            bulk_load(smem + Cfg::OFF_E + hf * Cfg::TOK, p.e16 + 2 * at, 2 * tok, tokbar);
+            bulk_load(smem + Cfg::OFF_W + hf * Cfg::TOK, p.w16 + 2 * at, 2 * tok, tokbar);
+            bulk_load(smem + Cfg::OFF_Y + hf * (PY * Cfg::TOK / 2), p.y16 + PY * at, PY * tok, tokbar);
+            if (hg == 0)
+                bulk_load(smem + Cfg::OFF_KQ + hf * Rows::BYTES,
+                          p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + hf) * Rows::BYTES, Rows::BYTES, tokbar);
+        }
+    };
+    auto copy_states = [&](int it) {
+        const int hg = it / Cfg::STEPS, s0 = (it % Cfg::STEPS) * Cfg::SL, ns = min(Cfg::SL, NP / 32 - s0);
+        const size_t bh = size_t(b) * p.heads + hk * group + hg;
+        const uint32_t bytes = kp * 2 * kTok16;
+        unsigned char *to = smem + Cfg::OFF_ST + (it % Cfg::STAGES) * (Cfg::SL * Cfg::SLICE);
+        uint64_t *bar = &stbar[it % Cfg::STAGES];
+        mbar_arrive_expect_tx(bar, ns * 2 * bytes);
+        for (int s = 0; s < ns; ++s) {
+            const size_t at = (bh * nbound + c) * (NP / 32) + s0 + s;
+            bulk_load(to + s * Cfg::SLICE, p.s16 + at * p.zparts * (2 * kTok16), bytes, bar);
+            bulk_load(to + s * Cfg::SLICE + Cfg::SLICE / 2, p.d16 + (at + NP / 32) * p.zparts * (2 * kTok16), bytes, bar);
+        }
+    };
+    if (tid == 0) {
+        copy_tokens(0);
+        for (int it = 0; it < Cfg::STAGES; ++it) copy_states(it);
+    }
+    // a bounded wait; after one that gave up the results are void and this thread waits no more
+    bool alive = true;
+    auto wait = [&](uint64_t *bar, int parity) {
+        if (!mbar_test(bar, parity & 1) && alive && !mbar_wait(bar, parity & 1, kDeltaWaitCycles)) {
+            alive = false;
+            atomicAdd(p.timeouts, 1u);
+        }
+    };
 
-    // 1 / scales of k and q in the chunk's halves
-    float ick[2], icq[2];
+    // ldmatrix offsets.  e, w, dy tiles are [headdim][token], states [headdim][dstate]: both take
+    // the transposing load.  A: this warp's 16 tokens; B: 16 tokens of a half, or 16 columns.
+    const int ra = (lane >> 4) * 8 + (lane & 7), rb = (lane >> 3 & 1) * 8 + (lane & 7);
+    const unsigned a_tok = tok16_at(ra, (rt & 1) * 2 + (lane >> 3 & 1));
+    const unsigned b_tok[2] = {unsigned(tok16_at(rb, lane >> 4)), unsigned(tok16_at(rb, 2 + (lane >> 4)))};
+    const unsigned b_kq = b_rows_k(lane, Rows::ROW);
+    const unsigned sbase = smem_u32(smem);
+    const unsigned aE = sbase + Cfg::OFF_E + ht * Cfg::TOK + a_tok, aW = aE + (Cfg::OFF_W - Cfg::OFF_E);
+    const unsigned aY = sbase + Cfg::OFF_Y + ht * (PY * Cfg::TOK / 2) + a_tok;
+
+    float ick[2], icq[2];                // 1 / scales of k and q in the chunk's halves
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
         const int cc = c32 + (x < n32 ? x : 0);
-        const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * p.block +
+        const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * DeltaBlock::BYTES +
                                                            DeltaBlock::OFF_VEC) + kVecScalars * kDeltaC;
-        ick[x] = 1.f / one[kCk];         // powers of two: exact
-        icq[x] = 1.f / one[kCq];
+        ick[x] = 1.f / __ldg(one + kCk);          // powers of two: exact
+        icq[x] = 1.f / __ldg(one + kCq);
     }
-    const unsigned an = unsigned((16 * rt + (lane & 15)) * Cfg::PROW + (lane >> 4) * 16);      // A: this warp's rows
-    const unsigned bp = b_rows_n(lane, Cfg::PROW), bn = b_rows_k(lane, Cfg::NROW);
-    const unsigned at_ = b_rows_n(lane, Cfg::TROW) + 32 * rt, bt = b_rows_k(lane, Cfg::TROW);     // e, w: [headdim][token]
-
-    for (int hg = 0; hg < group; ++hg) {
+    bool dead = false;
+    for (int hg = 0; hg < group && !dead; ++hg) {
         const int h = hk * group + hg;
         const size_t bh = size_t(b) * p.heads + h;
-        const size_t v0 = (size_t(b) * p.seqlen + t0) * vrow + size_t(h) * p.P;
-        // scales: the largest magnitudes over the rows' warps (and the chunk's halves); at most
-        // 8 and 16 values each
-        auto max_at = [&](const unsigned *m, size_t first, int n) { return lane < n ? __ldg(m + first + lane) : 0u; };
-        unsigned big[5] = {max_at(p.smax, (bh * nbound + c) * p.zparts, p.zparts),
-                           max_at(p.dsmax, (bh * nbound + c + 1) * p.zparts, p.zparts),
-                           max_at(p.emax, (bh * nck + c32) * p.zparts, n32 * p.zparts),
-                           max_at(p.wmax, (bh * nck + c32) * p.zparts, n32 * p.zparts),
-                           max_at(p.ymax, (bh * nck + c32) * p.zparts, n32 * p.zparts)};
-        // threads 0..63: their token's gates and sums
+        // Everything small at once: scales, and for threads 0..63 their token's gates and sums.
+        unsigned bits[8];                                 // lane k: part k's largest magnitudes
+        auto max_at = [&](const unsigned *m, size_t first) { return lane < kp ? __ldg(m + first + lane) : 0u; };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const size_t at = (bh * nck + c32 + (x < n32 ? x : 0)) * p.zparts;
+            bits[x] = max_at(p.ymax, at);
+            bits[2 + x] = max_at(p.emax, at);
+            bits[4 + x] = max_at(p.wmax, at);
+        }
+        bits[6] = max_at(p.smax, (bh * nbound + c) * p.zparts);
+        bits[7] = max_at(p.dsmax, (bh * nbound + c + 1) * p.zparts);
         const size_t gate = (size_t(b) * p.seqlen + t0 + (tid & 63)) * p.heads + h;
         float av = 0.f, bv = 0.f, dyy = 0.f, db = 0.f, z = 0.f;
         const bool front = 2 * tid < nt;
         if (tid < nt) {
-            av = fmaxf(p.a[gate], -1e4f);
-            bv = p.beta[gate];
-#pragma unroll 4
-            for (int s = 0; s < p.zparts; ++s) {
-                const size_t x = (s * all + bh) * p.seqlen + t0 + tid;
-                dyy += p.dyy[x] - p.vw[x];
-                db += p.edu[x];
+            av = __ldg(p.a + gate);
+            bv = __ldg(p.beta + gate);
+            float v[4][4];
+            for (int s0 = 0; s0 < p.zparts; s0 += 4) {    // zparts is a multiple of 4
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const size_t x = ((s0 + s) * all + bh) * p.seqlen + t0 + tid;
+                    v[s][0] = __ldg(p.dyy + x);
+                    v[s][1] = __ldg(p.vw + x);
+                    v[s][2] = __ldg(p.edu + x);
+                    v[s][3] = __ldg(p.zsum + ((s0 + s) * all + bh) * nbound + c + (front ? 0 : 1));
+                }
+#pragma unroll
+                for (int s = 0; s < 4; ++s) { dyy += v[s][0] - v[s][1]; db += v[s][2]; z += v[s][3]; }
             }
-#pragma unroll 4
-            for (int s = 0; s < p.zparts; ++s) z += p.zsum[(s * all + bh) * nbound + c + (front ? 0 : 1)];
+            av = fmaxf(av, -1e4f);
         }
+        // Scales as powers of two: per product the smallest over the parts (the products come out
+        // times 2^it) and each part's distance to it.
+        int ly[2], le[2], lw[2];
+        auto log_scale = [&](unsigned m) { return int(__float_as_uint(pow2_for(m).c) >> 23) - 127; };
 #pragma unroll
-        for (int x = 0; x < 5; ++x) big[x] = __reduce_max_sync(0xffffffffu, big[x]);
-        const Pow2 cS = pow2_for(big[0]), cD = pow2_for(big[1]), cE = pow2_for(big[2]), cW = pow2_for(big[3]), cY = pow2_for(big[4]);
-        __syncthreads();                 // the last head's tiles and vectors are done with
-
-        // dy as an operand [token][headdim], e and w as [headdim][token]
-        const float *dyp = static_cast<const float *>(p.dy) + v0;
-        constexpr int CP = PW / 8;
-#pragma unroll 4
-        for (int i = tid; i < C * CP; i += NT) {
-            const int r = i / CP, x = (i % CP) * 8;
-            float f[8] = {};
-            if (r < nt && x < p.P) load8(dyp + size_t(r) * vrow + x, f);
-            unsigned u[4][PG];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) split_f16<PG>(f2(f[2 * y], f[2 * y + 1]), cY.c, u[y]);
-#pragma unroll
-            for (int y = 0; y < PG; ++y)
-                *reinterpret_cast<uint4 *>(smem + Cfg::OFF_Y + y * Cfg::TOK + r * Cfg::PROW + x * 2) =
-                    make_uint4(u[0][y], u[1][y], u[2][y], u[3][y]);
-        }
-        // what a lane of the passes held, two rows of two neighbouring columns, into a tile of rows
-        auto put = [&](unsigned char *to, int piece, int rowbytes, float4 f, float scale) {
-            unsigned x[PG], y[PG];
-            split_f16<PG>(f2(f.x, f.y), scale, x);
-            split_f16<PG>(f2(f.z, f.w), scale, y);
-#pragma unroll
-            for (int i = 0; i < PG; ++i) {
-                *reinterpret_cast<unsigned *>(to + i * piece + g * rowbytes + 4 * t4) = x[i];
-                *reinterpret_cast<unsigned *>(to + i * piece + (g + 8) * rowbytes + 4 * t4) = y[i];
-            }
+        for (int x = 0; x < 2; ++x) { ly[x] = log_scale(bits[x]); le[x] = log_scale(bits[2 + x]); lw[x] = log_scale(bits[4 + x]); }
+        const int ls = log_scale(bits[6]), ld = log_scale(bits[7]);
+        auto common = [&](int l, float &inv) {
+            const int least = __reduce_min_sync(0xffffffffu, lane < kp ? l : 1 << 20);
+            inv = exp2_int(-(least >> 1)) * exp2_int((least >> 1) - least);       // 0 when too small for a float
+            return lane < kp ? half2_exp2(least - l) : 0u;
         };
-        const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = tid >> 5; i < 2 * (PW / 16) * 4; i += NT / 32) {      // (half, 16 rows, 8 tokens)
-            const int n = i & 3, rb = (i >> 2) % (PW / 16), hf = i / (PW / 4);
-            const bool ok = hf < n32 && 16 * rb < p.P;
-            const size_t from = ((((bh * nck + c32 + hf) * p.zparts + rb) * 4 + n) * 32 + lane) * 4;
-            const float4 fe = ok ? __ldg(reinterpret_cast<const float4 *>(p.e + from)) : none;
-            const float4 fw = ok ? __ldg(reinterpret_cast<const float4 *>(p.w + from)) : none;
-            unsigned char *to = smem + 16 * rb * Cfg::TROW + 64 * hf + 16 * n;
-            put(to + Cfg::OFF_E, Cfg::TT, Cfg::TROW, fe, cE.c);
-            put(to + Cfg::OFF_W, Cfg::TT, Cfg::TROW, fw, cW.c);
+        float i1[2], i2[2], i3[2], i4[2], i5, i6, i7;
+        unsigned f1[2], f2x[2], f3[2], f4[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            f1[x] = common(ly[ht] + le[x], i1[x]);        // dy e^T
+            f2x[x] = common(le[ht] + ly[x], i2[x]);       // e dy^T
+            f3[x] = common(lw[ht] + le[x], i3[x]);        // w e^T
+            f4[x] = common(le[ht] + lw[x], i4[x]);        // e w^T
         }
+        const unsigned f5 = common(ly[ht] + ls, i5), f6 = common(lw[ht] + ls, i6), f7 = common(le[ht] + ld, i7);
         // decays: prefix sums of a in 64 bits, kept as pairs of floats (a below -1e4 counts as
         // -1e4: its exponential is 0 either way, and the sums stay finite)
         double G = av;
@@ -192,207 +287,278 @@ __global__ void __launch_bounds__(Cfg::NT) delta_grad_kernel(const DeltaGradArgs
             bend[tid] = bv * expf(float(Gend - G));
             dtok[tid] = dyy;
         }
-        // The token-by-token matrices of this warp's rows, in four tiles of 16 columns.
-        const unsigned sy = smem_u32(smem + Cfg::OFF_Y), se = smem_u32(smem + Cfg::OFF_E), sw = smem_u32(smem + Cfg::OFF_W);
-        float x1[4][2][4], x2[4][2][4], x3[4][2][4], x4[2][4];   // dy e^T; e dy^T; w e^T, e w^T past the diagonal; e w^T on it
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int n = 0; n < 2; ++n) { zero4(x1[u][n]); zero4(x2[u][n]); zero4(x3[u][n]); }
-        zero4(x4[0]); zero4(x4[1]);
-#pragma unroll
-        for (int k = 0; k < PW / 16; ++k) {
-            unsigned ay[PG][4], ae[PG][4], aw[PG][4];
-#pragma unroll
-            for (int i = 0; i < PG; ++i) {
-                ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
-                ldsm4_t(ae[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
-                ldsm4_t(aw[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                unsigned be[PG][4], by[PG][4], bw[PG][4];
-                const unsigned at = 16 * u * Cfg::PROW + bp + k * 32, tt = 16 * k * Cfg::TROW + bt + 32 * u;
-                if (u <= rt) {
-#pragma unroll
-                    for (int i = 0; i < PG; ++i) ldsm4_t(be[i], se + i * Cfg::TT + tt);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma_pieces<PG, PG>(x1[u][n], ay, be, n);
-                        mma_pieces<PG, PG>(x3[u][n], aw, be, n);
-                    }
-                }
-                if (u >= rt) {
-#pragma unroll
-                    for (int i = 0; i < PG; ++i) {
-                        ldsm4(by[i], sy + i * Cfg::TOK + at);
-                        ldsm4_t(bw[i], sw + i * Cfg::TT + tt);
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma_pieces<PG, PG>(x2[u][n], ae, by, n);
-                        if (u == rt) mma_pieces<PG, PG>(x4[n], ae, bw, n);
-                        else mma_pieces<PG, PG>(x3[u][n], ae, bw, n);
-                    }
-                }
-            }
-        }
         __syncthreads();
-        // times the decays, beta and the scales taken back out: M1 / ck for dq; M1^T scale / cq
-        // and -(M2 + M2^T) / ck for dk
-        float m1 = 0.f, m2 = 0.f;
-        const float fye = cY.inv * cE.inv, fwe = cW.inv * cE.inv;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    const int r = 16 * rt + g + 8 * (m >> 1), q = 16 * u + 8 * n + 2 * t4 + (m & 1);
-                    const float gd = (Gh[r] - Gh[q]) + (Gl[r] - Gl[q]);
-                    const float up = ex2_approx((q <= r ? gd : -gd) * kLog2e);     // r(the later, the earlier)
-                    const float b0 = bet[q < r ? q : r], back = u < 2 ? ick[0] : ick[1], backq = u < 2 ? icq[0] : icq[1];
-                    const float d = up * b0;
-                    x1[u][n][m] = q <= r ? x1[u][n][m] * (d * p.scale * fye * back) : 0.f;
-                    x2[u][n][m] = q >= r ? x2[u][n][m] * (d * p.scale * fye * backq) : 0.f;
-                    const float w3 = (u == rt && q > r) ? x4[n][m] : x3[u][n][m];
-                    x3[u][n][m] = q != r ? -w3 * (d * fwe * back) : 0.f;
-                    m1 = fmaxf(m1, fabsf(x1[u][n][m]));
-                    m2 = fmaxf(m2, fmaxf(fabsf(x2[u][n][m]), fabsf(x3[u][n][m])));
-                }
-        const Pow2 c1 = pow2_for(warp_max_bits(m1)), c2 = pow2_for(warp_max_bits(m2));
-        unsigned a1[4][PG][4], a2[4][PG][4], a3[4][PG][4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            split_tiles<PG>(x1[u][0], x1[u][1], c1.c, a1[u]);
-            split_tiles<PG>(x2[u][0], x2[u][1], c2.c, a2[u]);
-            split_tiles<PG>(x3[u][0], x3[u][1], c2.c, a3[u]);
-        }
-        float fq[2], fw[2], fe[2];       // row factors of the products with the states
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int t = 16 * rt + g + 8 * r;
-            fq[r] = p.scale * gam[t] * (cY.inv * cS.inv);
-            fw[r] = -gam[t] * (cW.inv * cS.inv);
-            fe[r] = bend[t] * (cE.inv * cD.inv);
-        }
-
-        const float *S0 = p.ck + (bh * nbound + c) * p.zparts * (NP * 16);
-        const float *dE = p.dck + (bh * nbound + c + 1) * p.zparts * (NP * 16);
-        for (int n0 = 0; n0 < NP; n0 += W) {
-            if (n0 > 0) __syncthreads();
-            // this pass's columns of the states and of k and q
-            constexpr int CN = W / 8;
-#pragma unroll 4
-            for (int i = tid >> 5; i < (PW / 16) * CN; i += NT / 32) {     // (16 rows, 8 columns)
-                const int j = i % CN, rb = i / CN;
-                const bool ok = 16 * rb < p.P && n0 + 8 * j < NP;
-                const size_t from = ((size_t(rb) * (NP / 8) + n0 / 8 + j) * 32 + lane) * 4;
-                const float4 fs = ok ? __ldg(reinterpret_cast<const float4 *>(S0 + from)) : none;
-                const float4 fd = ok ? __ldg(reinterpret_cast<const float4 *>(dE + from)) : none;
-                unsigned char *to = smem + 16 * rb * Cfg::NROW + 16 * j;
-                put(to + Cfg::OFF_S, Cfg::ST, Cfg::NROW, fs, cS.c);
-                put(to + Cfg::OFF_D, Cfg::ST, Cfg::NROW, fd, cD.c);
-            }
-#pragma unroll 4
-            for (int i = tid; i < C * CN; i += NT) {
-                const int r = i / CN, x = (i % CN) * 8, half = r / kDeltaC;
-                const unsigned char *src = p.rows + ((size_t(b) * p.qk_heads + hk) * nck + c32 + (half < n32 ? half : 0)) * Rows::BYTES +
-                                           (r % kDeltaC) * Rows::ROW + (n0 + x) * 2;
-#pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int y = 0; y < KP; ++y) {
-                        const uint4 w = half < n32 && n0 + x < NP
-                                            ? __ldg(reinterpret_cast<const uint4 *>(src + (m * KP + y) * Rows::PIECE))
-                                            : make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(smem + (m ? Cfg::OFF_Q : Cfg::OFF_K) + y * Cfg::KT + r * Cfg::NROW + x * 2) = w;
-                    }
-            }
-            __syncthreads();
-            const unsigned sS = smem_u32(smem + Cfg::OFF_S), sD = smem_u32(smem + Cfg::OFF_D);
-            const unsigned sk = smem_u32(smem + Cfg::OFF_K), sq = smem_u32(smem + Cfg::OFF_Q);
-            // 32 columns per group of four warps
-            float aq[4][4], ak[4][4], aw[4][4], ae[4][4], am[4][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) { zero4(aq[n]); zero4(ak[n]); zero4(aw[n]); zero4(ae[n]); zero4(am[n]); }
-#pragma unroll
-            for (int k = 0; k < PW / 16; ++k) {
-                unsigned ay[PG][4], aE[PG][4], aW[PG][4];
-#pragma unroll
-                for (int i = 0; i < PG; ++i) {
-                    ldsm4(ay[i], sy + i * Cfg::TOK + an + k * 32);
-                    ldsm4_t(aE[i], se + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
-                    ldsm4_t(aW[i], sw + i * Cfg::TT + at_ + 16 * k * Cfg::TROW);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    unsigned bS[PG][4], bD[PG][4];
-                    const unsigned at = 16 * k * Cfg::NROW + bn + j0 * 64 + j * 32;
-#pragma unroll
-                    for (int i = 0; i < PG; ++i) {
-                        ldsm4_t(bS[i], sS + i * Cfg::ST + at);
-                        ldsm4_t(bD[i], sD + i * Cfg::ST + at);
-                    }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        mma_pieces<PG, PG>(aq[2 * j + n], ay, bS, n);
-                        mma_pieces<PG, PG>(aw[2 * j + n], aW, bS, n);
-                        mma_pieces<PG, PG>(ae[2 * j + n], aE, bD, n);
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    unsigned bK[KP][4], bQ[KP][4];
-                    const unsigned at = 16 * u * Cfg::NROW + bn + j0 * 64 + j * 32;
-#pragma unroll
-                    for (int i = 0; i < KP; ++i) ldsm4_t(bK[i], sk + i * Cfg::KT + at);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        if (u <= rt) mma_pieces<PG, KP>(ak[2 * j + n], a1[u], bK, n);
-                        mma_pieces<PG, KP>(am[2 * j + n], a3[u], bK, n);
-                    }
-                    if (u >= rt) {
-#pragma unroll
-                        for (int i = 0; i < KP; ++i) ldsm4_t(bQ[i], sq + i * Cfg::KT + at);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) mma_pieces<PG, KP>(am[2 * j + n], a2[u], bQ, n);
-                    }
-                }
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int t = 16 * rt + g + 8 * r, col = n0 + 32 * j0 + 8 * n + 2 * t4;
-                    if (t >= nt || col >= p.N) continue;
-                    const size_t off = k0 + size_t(t) * krow + col;
-                    float2 q, k;
-                    q.x = fmaf(c1.inv, ak[n][2 * r], fq[r] * aq[n][2 * r]);
-                    q.y = fmaf(c1.inv, ak[n][2 * r + 1], fq[r] * aq[n][2 * r + 1]);
-                    k.x = fmaf(c2.inv, am[n][2 * r], fmaf(fw[r], aw[n][2 * r], fe[r] * ae[n][2 * r]));
-                    k.y = fmaf(c2.inv, am[n][2 * r + 1], fmaf(fw[r], aw[n][2 * r + 1], fe[r] * ae[n][2 * r + 1]));
-                    float2 *pq = reinterpret_cast<float2 *>(p.part + off);
-                    float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
-                    if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
-                    if (hg + 1 < group) {
-                        *pq = q;
-                        *pk = k;
-                    } else {
-                        *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
-                        *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
-                    }
-                }
-        }
         if (tid < nt) {
             if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
             else for (int x = nt - 1; x >= tid; --x) z += dtok[x];
             p.da[gate] = z;
             p.dbeta[gate] = db;
         }
+        wait(tokbar, hg);
+
+        // The token-by-token matrices of this warp's rows, in four tiles of 16 columns: dy e^T;
+        // e dy^T; w e^T up to the diagonal and e w^T past it; e w^T on it.
+        float x1[4][2][4], x2[4][2][4], x3[4][2][4], x4[2][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) { zero4(x1[u][n]); zero4(x2[u][n]); zero4(x3[u][n]); }
+        zero4(x4[0]); zero4(x4[1]);
+#pragma unroll 2
+        for (int k = 0; k < PARTS; ++k) {
+            unsigned ay[PY][4], ae[2][4], aw[2][4];
+            ldsm4_t_pieces(ay, aY + k * (PY * kTok16));
+            ldsm4_t_pieces(ae, aE + k * (2 * kTok16));
+            ldsm4_t_pieces(aw, aW + k * (2 * kTok16));
+#pragma unroll
+            for (int hu = 0; hu < 2; ++hu) {
+                unsigned sy[PY][4], se[2][4], sw[2][4], ew[2][4];
+                if (hu <= ht) {
+                    mul_f16x2(sy, ay, __shfl_sync(0xffffffffu, f1[hu], k));
+                    mul_f16x2(sw, aw, __shfl_sync(0xffffffffu, f3[hu], k));
+                }
+                if (hu >= ht) {
+                    mul_f16x2(se, ae, __shfl_sync(0xffffffffu, f2x[hu], k));
+                    mul_f16x2(ew, ae, __shfl_sync(0xffffffffu, f4[hu], k));
+                }
+                const unsigned bE = sbase + Cfg::OFF_E + hu * Cfg::TOK + k * (2 * kTok16), bW = bE + (Cfg::OFF_W - Cfg::OFF_E);
+                const unsigned bY = sbase + Cfg::OFF_Y + hu * (PY * Cfg::TOK / 2) + k * (PY * kTok16);
+#pragma unroll
+                for (int uu = 0; uu < 2; ++uu) {
+                    const int u = 2 * hu + uu;
+                    if (u <= rt) {
+                        unsigned be[2][4];
+                        ldsm4_t_pieces(be, bE + b_tok[uu]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma_pieces<PY, 2>(x1[u][n], sy, be, n);
+                            mma_pieces<2, 2>(x3[u][n], sw, be, n);
+                        }
+                    }
+                    if (u >= rt) {
+                        unsigned by[PY][4], bw[2][4];
+                        ldsm4_t_pieces(by, bY + b_tok[uu]);
+                        ldsm4_t_pieces(bw, bW + b_tok[uu]);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            mma_pieces<2, PY>(x2[u][n], se, by, n);
+                            if (u == rt) mma_pieces<2, 2>(x4[n], ew, bw, n);
+                            else mma_pieces<2, 2>(x3[u][n], ew, bw, n);
+                        }
+                    }
+                }
+            }
+        }
+        // times the decays, beta and the scales taken back out: M1 / ck for dq; M1^T scale / cq
+        // and -(M2 + M2^T) / ck for dk
+        float m1 = 0.f, m2 = 0.f;
+        float grh[2], grl[2], br[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = 16 * rt + g + 8 * r;
+            grh[r] = Gh[t]; grl[r] = Gl[t]; br[r] = bet[t];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float e1 = i1[u >> 1] * p.scale * ick[u >> 1], e2 = i2[u >> 1] * p.scale * icq[u >> 1];
+            const float e3 = -i3[u >> 1] * ick[u >> 1], e4 = -i4[u >> 1] * ick[u >> 1];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int q0 = 16 * u + 8 * n + 2 * t4;
+                const float2 gh = *reinterpret_cast<const float2 *>(Gh + q0), gl = *reinterpret_cast<const float2 *>(Gl + q0);
+                const float2 bq = *reinterpret_cast<const float2 *>(bet + q0);
+                // f(m, exponent to take, beta of the column): tiles off the diagonal need one side only
+                auto each = [&](auto f) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+                        f(m, ((grh[m >> 1] - (m & 1 ? gh.y : gh.x)) + (grl[m >> 1] - (m & 1 ? gl.y : gl.x))) * kLog2e,
+                          m & 1 ? bq.y : bq.x);
+                };
+                if (u < rt) {
+                    each([&](int m, float gd, float bc) {
+                        const float d = ex2_approx(gd) * bc;
+                        x1[u][n][m] *= d * e1;
+                        x3[u][n][m] *= d * e3;
+                    });
+                } else if (u > rt) {
+                    each([&](int m, float gd, float) {
+                        const float d = ex2_approx(-gd) * br[m >> 1];
+                        x2[u][n][m] *= d * e2;
+                        x3[u][n][m] *= d * e4;
+                    });
+                } else {
+                    each([&](int m, float gd, float bc) {
+                        const int r = g + 8 * (m >> 1), q = 8 * n + 2 * t4 + (m & 1);
+                        const float d = ex2_approx(q <= r ? gd : -gd) * (q < r ? bc : br[m >> 1]);       // r(the later, the earlier)
+                        x1[u][n][m] = q <= r ? x1[u][n][m] * (d * e1) : 0.f;
+                        x2[u][n][m] = q >= r ? x2[u][n][m] * (d * e2) : 0.f;
+                        x3[u][n][m] = q < r ? x3[u][n][m] * (d * e3) : q > r ? x4[n][m] * (d * e4) : 0.f;
+                    });
+                }
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    m1 = fmaxf(m1, fabsf(x1[u][n][m]));
+                    m2 = fmaxf(m2, fmaxf(fabsf(x2[u][n][m]), fabsf(x3[u][n][m])));
+                }
+            }
+        }
+        const Pow2 c1 = pow2_for(warp_max_bits(m1)), c2 = pow2_for(warp_max_bits(m2));
+        unsigned a1[4][2][4], a2[4][2][4], a3[4][2][4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            split_tiles<2>(x1[u][0], x1[u][1], c1.c, a1[u]);
+            split_tiles<2>(x2[u][0], x2[u][1], c2.c, a2[u]);
+            split_tiles<2>(x3[u][0], x3[u][1], c2.c, a3[u]);
+        }
+        float fq[2], fw[2], fe[2];       // row factors of the products with the states
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = 16 * rt + g + 8 * r;
+            fq[r] = p.scale * gam[t] * i5;
+            fw[r] = -gam[t] * i6;
+            fe[r] = bend[t] * i7;
+        }
+        // CW columns a step and group
+        constexpr int NJ = Cfg::CW / 16;
+#pragma unroll 1
+        for (int i = 0; i < Cfg::STEPS; ++i) {
+            const int it = hg * Cfg::STEPS + i, col0 = i * Cfg::COLS + gr * Cfg::CW;
+            wait(&stbar[it % Cfg::STAGES], it / Cfg::STAGES);
+            if (col0 < NP) {
+                float aq[2 * NJ][4], am[2 * NJ][4];       // dq, dk
+                {
+                    // the products with the states
+                    const unsigned st = sbase + Cfg::OFF_ST + (it % Cfg::STAGES) * (Cfg::SL * Cfg::SLICE) +
+                                        (gr * Cfg::CW / 32) * Cfg::SLICE;
+                    const int piece0 = (gr * Cfg::CW % 32) / 8;
+                    float aw[2 * NJ][4], ae[2 * NJ][4];
+#pragma unroll
+                    for (int n = 0; n < 2 * NJ; ++n) { zero4(aq[n]); zero4(aw[n]); zero4(ae[n]); }
+#pragma unroll 2
+                    for (int k = 0; k < PARTS; ++k) {
+                        unsigned sy[PY][4], sw[2][4], se[2][4];
+                        ldsm4_t_pieces(sy, aY + k * (PY * kTok16));
+                        mul_f16x2(sy, sy, __shfl_sync(0xffffffffu, f5, k));
+                        ldsm4_t_pieces(sw, aW + k * (2 * kTok16));
+                        mul_f16x2(sw, sw, __shfl_sync(0xffffffffu, f6, k));
+                        ldsm4_t_pieces(se, aE + k * (2 * kTok16));
+                        mul_f16x2(se, se, __shfl_sync(0xffffffffu, f7, k));
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            unsigned bS[2][4], bD[2][4];
+                            const unsigned at = st + k * (2 * kTok16) + tok16_at(rb, piece0 + 2 * j + (lane >> 4));
+                            ldsm4_t_pieces(bS, at);
+                            ldsm4_t_pieces(bD, at + Cfg::SLICE / 2);
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) {
+                                mma_pieces<PY, 2>(aq[2 * j + n], sy, bS, n);
+                                mma_pieces<2, 2>(aw[2 * j + n], sw, bS, n);
+                                mma_pieces<2, 2>(ae[2 * j + n], se, bD, n);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            aq[n][m] *= fq[m >> 1];
+                            am[n][m] = fmaf(fw[m >> 1], aw[n][m], fe[m >> 1] * ae[n][m]);
+                        }
+                }
+                // and with the other tokens' k and q
+                float bq[2 * NJ][4], bm[2 * NJ][4];
+#pragma unroll
+                for (int n = 0; n < 2 * NJ; ++n) { zero4(bq[n]); zero4(bm[n]); }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        unsigned bK[KP][4], bQ[KP][4];
+                        const unsigned at = sbase + Cfg::OFF_KQ + (u >> 1) * Rows::BYTES + (u & 1) * 16 * Rows::ROW + b_kq + col0 * 2 + j * 32;
+#pragma unroll
+                        for (int x = 0; x < KP; ++x) ldsm4_t(bK[x], at + x * Rows::PIECE);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            if (u <= rt) mma_pieces<2, KP>(bq[2 * j + n], a1[u], bK, n);
+                            mma_pieces<2, KP>(bm[2 * j + n], a3[u], bK, n);
+                        }
+                        if (u >= rt) {
+#pragma unroll
+                            for (int x = 0; x < KP; ++x) ldsm4_t(bQ[x], at + (KP + x) * Rows::PIECE);
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) mma_pieces<2, KP>(bm[2 * j + n], a2[u], bQ, n);
+                        }
+                    }
+#pragma unroll
+                for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        aq[n][m] = fmaf(c1.inv, bq[n][m], aq[n][m]);
+                        am[n][m] = fmaf(c2.inv, bm[n][m], am[n][m]);
+                    }
+                // sums over the heads of a key head so far from scratch; fp32 gradients straight out
+                if (group > 1 || sizeof(Tg) == 4) {
+#pragma unroll
+                    for (int n = 0; n < 2 * NJ; ++n)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int t = 16 * rt + g + 8 * r, col = col0 + 8 * n + 2 * t4;
+                            if (t >= nt || col >= p.N) continue;
+                            const size_t off = k0 + size_t(t) * krow + col;
+                            float2 *pq = reinterpret_cast<float2 *>(p.part + off);
+                            float2 *pk = reinterpret_cast<float2 *>(p.part + size_t(p.batch) * p.seqlen * krow + off);
+                            float2 q = f2(aq[n][2 * r], aq[n][2 * r + 1]), k = f2(am[n][2 * r], am[n][2 * r + 1]);
+                            if (hg > 0) { q = fadd2(*pq, q); k = fadd2(*pk, k); }
+                            if (hg + 1 < group) {
+                                *pq = q; *pk = k;
+                            } else if constexpr (sizeof(Tg) == 4) {
+                                *reinterpret_cast<float2 *>(static_cast<float *>(p.dq) + off) = q;
+                                *reinterpret_cast<float2 *>(static_cast<float *>(p.dk) + off) = k;
+                            }
+                            aq[n][2 * r] = q.x; aq[n][2 * r + 1] = q.y;
+                            am[n][2 * r] = k.x; am[n][2 * r + 1] = k.y;
+                        }
+                }
+                if constexpr (sizeof(Tg) == 2)
+                    if (hg + 1 == group) {       // 16 rows through the warp's tile: whole 16-byte stores
+                        unsigned char *tile = smem + Cfg::OFF_OUT + (tid >> 5) * Cfg::OUT;
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float (&f)[2 * NJ][4] = x ? am : aq;
+#pragma unroll
+                            for (int h2 = 0; h2 < NJ; ++h2) {
+                                unsigned r[4];
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) r[m] = pack_bf16x2(f[2 * h2 + (m >> 1)][2 * (m & 1)], f[2 * h2 + (m >> 1)][2 * (m & 1) + 1]);
+                                stsm4(smem_u32(tile) + tok16_at(rb, 2 * h2 + (lane >> 4)), r);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int y = 0; y < NJ; ++y) {
+                                const int r = (16 / NJ) * y + lane / (2 * NJ), pc = lane % (2 * NJ), col = col0 + 8 * pc;
+                                const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok16_at(r, pc));
+                                if (16 * rt + r < nt && col < p.N)
+                                    *reinterpret_cast<uint4 *>(static_cast<Tg *>(x ? p.dk : p.dq) + k0 + size_t(16 * rt + r) * krow + col) = w;
+                            }
+                            __syncwarp();
+                        }
+                    }
+            }
+            const bool more = it + Cfg::STAGES < total, next = i + 1 == Cfg::STEPS && hg + 1 < group;
+            if (more || next) {              // this step's memory (at a head's end its tokens' too) is done with
+                if (!__syncthreads_and(alive)) { alive = false; dead = true; break; }
+                if (tid == 0) {
+                    if (next) copy_tokens(hg + 1);
+                    if (more) copy_states(it + Cfg::STAGES);
+                }
+            }
+        }
     }
+    if (!alive)                          // results are void; copies may still be on their way: wait (bounded) for them
+        for (int x = 0; x < 2; ++x) {
+            mbar_wait(tokbar, x, kDeltaWaitCycles);
+            for (int i = 0; i < Cfg::STAGES; ++i) mbar_wait(&stbar[i], x, kDeltaWaitCycles);
+        }
 }
 
 }  // namespace ssm

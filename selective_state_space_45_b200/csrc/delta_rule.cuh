@@ -64,13 +64,13 @@ struct DeltaArgs {
     // The backward's scratch.  A "part" is a warp's 16 rows: part = slice * warps + warp.  What one
     // pass leaves for the next is laid out as the warps hold it (accumulator tiles, four values a
     // lane), so that every access is a whole 16 bytes a lane in order.
-    float *e, *w;           // [batch][heads][chunks][parts][4 tiles of 8 tokens][lane][4]: e, w
-    float *ck, *dck;        // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
-                            // and its gradient at every boundary of 64 tokens and at the end
-    // For bf16 gradients the last kernel takes scaled fp16 operands, tiles of its shared memory
-    // as they stand: e, w and dy of a part and chunk, S and dS of a part.
-    unsigned char *e16, *w16, *y16;     // [batch][heads][chunks][parts] 16 rows of 32 tokens
-    unsigned char *s16, *d16;           // [batch][heads][boundaries][parts] 16 rows of dstate
+    float *e;               // [batch][heads][chunks][parts][4 tiles of 8 tokens][lane][4]
+    float *ck;              // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
+                            // at every boundary of 64 tokens and at the end
+    // The last kernel takes scaled fp16 operands, tiles of its shared memory as they stand, in two
+    // pieces (one of a bf16 dy): e, w and dy of a part and chunk, S and dS of a part and 32 columns.
+    unsigned char *e16, *w16, *y16;     // [batch][heads][chunks][parts][pieces] 16 rows of 32 tokens
+    unsigned char *s16, *d16;           // [batch][heads][boundaries][dstate / 32][parts][pieces] 16 rows of 32 columns
     float *sum, *sum2;      // [parts][batch][heads][seqlen] sums over a part's rows: dy.y; in the
                             // reverse pass e.du (the gradient of beta) and v.w
     float *zsum;            // [parts][batch][heads][boundaries] <dS, S>
@@ -121,16 +121,11 @@ template <int NP, int KP> struct DeltaRows {
     static constexpr int ROW = NP * 2 + 16, PIECE = kDeltaC * ROW, BYTES = 2 * KP * PIECE;
 };
 
-// Rows of a 16-bit tile of a part: 64 bytes (32 tokens), or dstate padded to a power of two.
-// The 16-byte pieces of a row change places with the row, so that eight rows' pieces of one
+// A 16-bit tile of a part: 16 rows of 64 bytes (32 tokens, or 32 columns of the state).  The
+// 16-byte quarters of a row change places with the row, so that eight rows' quarters of one
 // column are eight bank groups (ldmatrix).
 constexpr int kTok16 = 1024;
 __device__ __forceinline__ int tok16_at(int r, int n) { return r * 64 + ((n ^ (r >> 1)) & 3) * 16; }
-template <int NP> struct State16 {
-    static constexpr int ROW = NP > 64 ? 256 : NP * 2, BYTES = 16 * ROW;
-    __device__ static __forceinline__ int flip(int r) { return (NP > 32 ? r & 7 : (r >> 1) & 3) * 16; }
-    __device__ static __forceinline__ int at(int r, int n) { return r * ROW + ((n * 16) ^ flip(r)); }
-};
 
 constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's limit, about a second
 
@@ -159,13 +154,10 @@ template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_
     static constexpr int STAGES = !BWD && KP == 1 ? 3 : 2;                // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
     static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
-    static constexpr bool G16 = MODE == 1 ? sizeof(Tv2) == 2 : MODE == 2 && sizeof(Tv) == 2;      // bf16 gradients
-    static constexpr int OUT = 1024;                                          // bytes of a warp's tile
+    static constexpr int OUT = BWD ? 2 * kTok16 : 1024;                       // bytes of a warp's tile
     static constexpr int OFF_ST = OFF_OUT + NW * OUT;                         // kept states on their way
-    static constexpr int STATE = NP * 16 * 4;                                 // bytes of a part's state
-    static constexpr int ST = MODE == 2 ? STATE : MODE == 1 && G16 ? State16<NP>::BYTES : 0;
+    static constexpr int ST = MODE == 2 ? NP * 16 * 4 : 0;                    // bytes of a part's state
     static constexpr int SMEM_BYTES = OFF_ST + NW * ST;
-    static_assert(MODE != 2 || STATE >= State16<NP>::BYTES);
 };
 
 // acc += A B of operands in KP bf16 pieces (1: exact, 3: all bits of fp32), the products of
@@ -774,33 +766,34 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         __syncwarp();
     };
     const int srow = (lane >> 3 & 1) * 8 + (lane & 7), spiece = lane >> 4;       // stmatrix: row and piece of the lane
-    // a Tok times c as the last kernel reads it
-    auto keep_tok16 = [&](unsigned char *to, const Tok &f, float k, int c) {
+    // a Tok times c as the last kernel reads it, in `pieces` pieces
+    auto keep_tok16 = [&](auto pieces, unsigned char *to, const Tok &f, float k, int c) {
+        constexpr int NPC = decltype(pieces)::value;
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
-            unsigned r[4], x[1];
+            unsigned r[NPC][4];
+            split_tiles<NPC>(f[2 * h2], f[2 * h2 + 1], k, r);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const float *v = f[2 * h2 + (m >> 1)] + 2 * (m & 1);
-                split_f16<1>(f2(v[0], v[1]), k, x);
-                r[m] = x[0];
-            }
-            stsm4(smem_u32(tile) + tok16_at(srow, 2 * h2 + spiece), r);
+            for (int i = 0; i < NPC; ++i) stsm4(smem_u32(tile) + i * kTok16 + tok16_at(srow, 2 * h2 + spiece), r[i]);
         }
-        copy_out(to + ((size_t(bh) * nchunk + c) * parts + part) * kTok16, tile, std::integral_constant<int, kTok16>());
+        copy_out(to + ((size_t(bh) * nchunk + c) * parts + part) * (NPC * kTok16), tile, std::integral_constant<int, NPC * kTok16>());
     };
-    // the state times c
+    // the state times c, in two pieces
     auto keep_state16 = [&](unsigned char *to, float k, int x) {
-        unsigned char *st = smem + Cfg::OFF_ST + warp * Cfg::ST;
-        using S16 = State16<NP>;
 #pragma unroll
-        for (int j = 0; j < NP / 16; ++j) {
-            unsigned A[1][4];
-            split_tiles<1>(s[2 * j], s[2 * j + 1], k, A);
-            stsm4(smem_u32(st) + S16::at(srow, 2 * j + spiece), A[0]);
+        for (int n = 0; n < NP / 32; ++n) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                unsigned A[2][4];
+                split_tiles<2>(s[4 * n + 2 * j], s[4 * n + 2 * j + 1], k, A);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) stsm4(smem_u32(tile) + i * kTok16 + tok16_at(srow, 2 * j + spiece), A[i]);
+            }
+            copy_out(to + (((size_t(bh) * nbound + x) * (NP / 32) + n) * parts + part) * (2 * kTok16), tile,
+                     std::integral_constant<int, 2 * kTok16>());
         }
-        copy_out(to + ((size_t(bh) * nbound + x) * parts + part) * S16::BYTES, st, std::integral_constant<int, S16::BYTES>());
     };
+    using std::integral_constant;
     // a Tok as the next pass reads it
     auto keep_tok = [&](float *to, const Tok &f, int c) {
         float4 *at = reinterpret_cast<float4 *>(to + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
@@ -837,7 +830,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         if constexpr (MODE == 1)
             if (c % CS == 0) {
                 keep_state(p.ck, c / CS);
-                if constexpr (Cfg::G16) keep_state16(p.s16, cS.c, c / CS);
+                keep_state16(p.s16, cS.c, c / CS);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
             }
         if constexpr (MODE == 2) {
@@ -849,8 +842,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             }
             if (c % CS == CS - 1 || c == nchunk - 1) {
                 dot_state(c / CS + 1);
-                if constexpr (Cfg::G16) keep_state16(p.d16, cS.c, c / CS + 1);
-                else keep_state(p.dck, c / CS + 1);
+                keep_state16(p.d16, cS.c, c / CS + 1);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
             }
             if (c % CS == 0) fetch_state(c / CS);
@@ -975,7 +967,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         if constexpr (!REV) {
             if constexpr (MODE == 1) {
                 keep_tok(p.e, x, c);
-                if constexpr (Cfg::G16) keep_tok16(p.e16, x, pow2_for(mx).c, c);
+                keep_tok16(integral_constant<int, 2>(), p.e16, x, pow2_for(mx).c, c);
                 Tok dy;
                 load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
 #pragma unroll
@@ -997,12 +989,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] *= x[n][m];
             token_sums(p.sum2, du, c * C);
-            if constexpr (Cfg::G16) {
-                keep_tok16(p.w16, x, pow2_for(mx).c, c);
-                keep_tok16(p.y16, v, pow2_for(mv).c, c);
-            } else {
-                keep_tok(p.w, x, c);
-            }
+            keep_tok16(integral_constant<int, 2>(), p.w16, x, pow2_for(mx).c, c);
+            keep_tok16(integral_constant<int, PV>(), p.y16, v, pow2_for(mv).c, c);
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
         }
         // the state's update: operand A1 against k (and in the reverse pass A2 against q)
