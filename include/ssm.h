@@ -337,7 +337,7 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * included.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.
  * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
- * 216 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
+ * 224 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
  * each segment and head 4 * (headdim + dstate) * dstate bytes.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

@@ -63,7 +63,7 @@ template <int NP_, int PW_, int KP_, typename Tg_> struct GradCfg {
     static constexpr int OFF_E = 0, OFF_W = 2 * TOK, OFF_Y = 4 * TOK;
     static constexpr int OFF_KQ = OFF_Y + PY * TOK;                           // [half] k and q
     static constexpr int OFF_VEC = OFF_KQ + 2 * Rows::BYTES;
-    static constexpr int OFF_OUT = OFF_VEC + 6 * kGradC * 4 + 64;             // per-warp output tiles
+    static constexpr int OFF_OUT = OFF_VEC + 7 * kGradC * 4 + 64;             // per-warp output tiles
     static constexpr int OUT = sizeof(Tg) == 2 ? kTok16 : 0;
     static constexpr int SLICE = 4 * PARTS * kTok16;                          // S and dE, 32 columns: [S, dE][part][piece]
     static constexpr int HALF = 113 * 1024, WHOLE = 227 * 1024;               // shared memory for two CTAs on an SM, or one
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
-    float *bend = bet + C, *dtok = bend + C;
-    double *half = reinterpret_cast<double *>(dtok + C);
+    float *bend = bet + C, *dtok = bend + C, *ick = dtok + C;       // ick: 1 / scales of the keys
+    double *half = reinterpret_cast<double *>(ick + C);
     uint64_t *tokbar = reinterpret_cast<uint64_t *>(half + 2), *stbar = tokbar + 1;
     const int tid = threadIdx.x, lane = tid & 31, rt = (tid >> 5) & 3, gr = tid >> 7, ht = rt >> 1, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
@@ -197,15 +197,14 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
     const unsigned aE = sbase + Cfg::OFF_E + ht * Cfg::TOK + a_tok, aW = aE + (Cfg::OFF_W - Cfg::OFF_E);
     const unsigned aY = sbase + Cfg::OFF_Y + ht * (PY * Cfg::TOK / 2) + a_tok;
 
-    float ick[2], icq[2];                // 1 / scales of k and q in the chunk's halves
+    auto vec_of = [&](int x) {           // the chunk block's vectors of half x
+        return reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + c32 + (x < n32 ? x : 0)) *
+                                                            DeltaBlock::BYTES + DeltaBlock::OFF_VEC);
+    };
+    float icq[2];                        // 1 / scales of q in the chunk's halves (powers of two: exact)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int cc = c32 + (x < n32 ? x : 0);
-        const float *one = reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + cc) * DeltaBlock::BYTES +
-                                                           DeltaBlock::OFF_VEC) + kVecScalars * kDeltaC;
-        ick[x] = 1.f / __ldg(one + kCk);          // powers of two: exact
-        icq[x] = 1.f / __ldg(one + kCq);
-    }
+    for (int x = 0; x < 2; ++x) icq[x] = 1.f / __ldg(vec_of(x) + kVecScalars * kDeltaC + kCq);
+    if (tid < C) ick[tid] = __ldg(vec_of(tid >> 5) + kVecL * kDeltaC + (tid & 31)) * (1.f / 8192.f);
     bool dead = false;
     for (int hg = 0; hg < group && !dead; ++hg) {
         const int h = hk * group + hg;
@@ -360,39 +359,39 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const float e1 = i1[u >> 1] * p.scale * ick[u >> 1], e2 = i2[u >> 1] * p.scale * icq[u >> 1];
-            const float e3 = -i3[u >> 1] * ick[u >> 1], e4 = -i4[u >> 1] * ick[u >> 1];
+            const float e1 = i1[u >> 1] * p.scale, e2 = i2[u >> 1] * p.scale * icq[u >> 1];
+            const float e3 = -i3[u >> 1], e4 = -i4[u >> 1];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int q0 = 16 * u + 8 * n + 2 * t4;
                 const float2 gh = *reinterpret_cast<const float2 *>(Gh + q0), gl = *reinterpret_cast<const float2 *>(Gl + q0);
-                const float2 bq = *reinterpret_cast<const float2 *>(bet + q0);
-                // f(m, exponent to take, beta of the column): tiles off the diagonal need one side only
+                const float2 bq = *reinterpret_cast<const float2 *>(bet + q0), kq = *reinterpret_cast<const float2 *>(ick + q0);
+                // f(m, exponent to take, beta of the column, 1 / its key's scale): tiles off the diagonal need one side only
                 auto each = [&](auto f) {
 #pragma unroll
                     for (int m = 0; m < 4; ++m)
                         f(m, ((grh[m >> 1] - (m & 1 ? gh.y : gh.x)) + (grl[m >> 1] - (m & 1 ? gl.y : gl.x))) * kLog2e,
-                          m & 1 ? bq.y : bq.x);
+                          m & 1 ? bq.y : bq.x, m & 1 ? kq.y : kq.x);
                 };
                 if (u < rt) {
-                    each([&](int m, float gd, float bc) {
-                        const float d = ex2_approx(gd) * bc;
+                    each([&](int m, float gd, float bc, float kc) {
+                        const float d = ex2_approx(gd) * bc * kc;
                         x1[u][n][m] *= d * e1;
                         x3[u][n][m] *= d * e3;
                     });
                 } else if (u > rt) {
-                    each([&](int m, float gd, float) {
+                    each([&](int m, float gd, float, float kc) {
                         const float d = ex2_approx(-gd) * br[m >> 1];
                         x2[u][n][m] *= d * e2;
-                        x3[u][n][m] *= d * e4;
+                        x3[u][n][m] *= d * kc * e4;
                     });
                 } else {
-                    each([&](int m, float gd, float bc) {
+                    each([&](int m, float gd, float bc, float kc) {
                         const int r = g + 8 * (m >> 1), q = 8 * n + 2 * t4 + (m & 1);
                         const float d = ex2_approx(q <= r ? gd : -gd) * (q < r ? bc : br[m >> 1]);       // r(the later, the earlier)
-                        x1[u][n][m] = q <= r ? x1[u][n][m] * (d * e1) : 0.f;
+                        x1[u][n][m] = q <= r ? x1[u][n][m] * (d * kc * e1) : 0.f;
                         x2[u][n][m] = q >= r ? x2[u][n][m] * (d * e2) : 0.f;
-                        x3[u][n][m] = q < r ? x3[u][n][m] * (d * e3) : q > r ? x4[n][m] * (d * e4) : 0.f;
+                        x3[u][n][m] = q < r ? x3[u][n][m] * (d * kc * e3) : q > r ? x4[n][m] * (d * kc * e4) : 0.f;
                     });
                 }
 #pragma unroll

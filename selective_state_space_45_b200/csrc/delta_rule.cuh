@@ -35,8 +35,13 @@
 // (G without beta in its columns keeps du, and with it dbeta, exact where beta is small or 0.)
 //
 // Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
-// operand scaled by a power of two (one per chunk for k, q and the triangles, one per warp and
-// chunk for the state and what follows from it) so that its range does not matter.  bf16
+// operand scaled by a power of two: one per token for k, one per chunk for q and the triangles,
+// one per warp and chunk for the state and what follows from it, each from the operand's own
+// largest value.  With l_t the power of two that key t is scaled by, the triangles are those of
+// the keys k_t / l_t with steps beta_t l_t^2, which no ratio of lengths spreads; l_t goes onto
+// the tokens' vectors on either side of them.  (Bounds from the factors' largest values in
+// place of the operands' own left 2e-2 of the state at keys 300 times as long as their
+// neighbours, one scale for a chunk's keys 1e-3 at lengths spread over 10^6.)  bf16
 // inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), whatever
 // the type of y: one behind a bf16 y made 11% of its values round the other way (8 x 2048
 // tokens x 24 heads of 64 x 128: 280 us with the call, 312 with two).  Three bf16 pieces hold
@@ -75,8 +80,8 @@ struct DeltaArgs {
                             // reverse pass e.du (the gradient of beta) and v.w
     float *zsum;            // [parts][batch][heads][boundaries] <dS, S>
     unsigned *smax;         // [batch][heads][boundaries][parts] largest |S| (reverse pass: |dS|), as bits
-    unsigned *emax, *ymax;  // [batch][heads][chunks][parts] bounds of |e| (reverse pass: |w|) and, in the
-                            // reverse pass, the largest |dy|
+    unsigned *emax, *ymax;  // [batch][heads][chunks][parts] largest |e| (reverse pass: |w|) and, in the
+                            // reverse pass, |dy|
     // Segments of a long sequence with few heads: chunks per segment, and per segment
     // [batch][heads][segments] the end state from a zero start (the first: from h0), later the next
     // one's start state, and the map that takes a start state's rows to their part of the end state.
@@ -107,10 +112,12 @@ enum {
     kVecBeta,
     kVecEk,        // end / ck
     kVecEbk,       // end beta / ck
+    kVecBl,        // beta l
+    kVecL,         // l = 2^13 / ck
     kVecScalars,   // then the scalars below
     kVecs
 };
-enum { kGamLast, kCk, kCq, kInvG, kInvP, kMaxBeta, kMaxEbk, kMaxGk, kMaxSgq };   // 1 / scales; largest magnitudes
+enum { kGamLast, kCq, kInvG, kInvP };             // the chunk's decay, the scale of q, 1 / scales of G and Pm
 struct DeltaBlock {
     static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 6 * kTri, BYTES = OFF_VEC + kVecs * kDeltaC * 4;
 };
@@ -174,13 +181,14 @@ __device__ __forceinline__ void mma_exact(float (&acc)[4], const unsigned (&a)[K
 // writes the chunk's k and q as operands.  Four warps per CTA, each with its own scratch.
 template <int NP, typename Tin> struct PrepScratch {
     static constexpr int RATROW = 33, NROW = 36, ROW = NP * int(sizeof(Tin)) + 16;
+    float ck[kDeltaC];                                          // the keys' scales
     union {
         unsigned char rows[2][kDeltaC * ROW];                   // k and q as they come
         struct {
             unsigned char block[DeltaBlock::BYTES];               // as it goes out
             float at[kDeltaC * NROW];                           // at[s][t] = A(t, s)
             float rat[kDeltaC * RATROW + 4];                    // rat[t][s + 1] = r(t, s); later parts of G
-            float beta[kDeltaC];
+            float beta[kDeltaC];                                // beta l^2
         };
     };
 };
@@ -234,7 +242,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
     float kk[6][4], qk[6][4];
 #pragma unroll
     for (int i = 0; i < 6; ++i) { zero4(kk[i]); zero4(qk[i]); }
-    unsigned big[2] = {0, 0};                                   // largest |k|, |q| of the lane (bits; bf16: packed pairs)
+    // largest |k| of the lane in rows g, g + 8, g + 16, g + 24, and |q| (bits; bf16: packed pairs)
+    unsigned bigk[4] = {0, 0, 0, 0}, bigq = 0;
 #pragma unroll
     for (int j = 0; j < NP / 16; ++j) {
         unsigned ka[2][KP][4], qa[2][KP][4];                    // A operands of rows 0-15 and 16-31
@@ -246,8 +255,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
                 ldsm4(qa[m][0], at + C * ROW);
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    big[0] = __vmaxu2(big[0], ka[m][0][y] & 0x7fff7fffu);
-                    big[1] = __vmaxu2(big[1], qa[m][0][y] & 0x7fff7fffu);
+                    bigk[2 * m + (y & 1)] = __vmaxu2(bigk[2 * m + (y & 1)], ka[m][0][y] & 0x7fff7fffu);
+                    bigq = __vmaxu2(bigq, qa[m][0][y] & 0x7fff7fffu);
                 }
             } else {
 #pragma unroll
@@ -260,7 +269,8 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
                         split_bf16(f.x, f.y, x);
 #pragma unroll
                         for (int i = 0; i < 3; ++i) (z ? qa : ka)[m][i][y] = x[i];
-                        big[z] = max(big[z], max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
+                        unsigned &big = z ? bigq : bigk[2 * m + (y & 1)];
+                        big = max(big, max(__float_as_uint(fabsf(f.x)), __float_as_uint(fabsf(f.y))));
                     }
             }
         }
@@ -280,25 +290,31 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
                 }
         }
     }
-    Pow2 cs[2];
+    auto whole = [](unsigned b) { return KP == 1 ? max(b << 16, b & 0xffff0000u) : b; };
+    const Pow2 cq = pow2_for(__reduce_max_sync(0xffffffffu, whole(bigq)));
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        if constexpr (KP == 1) big[m] = max(big[m] << 16, big[m] & 0xffff0000u);
-        cs[m] = pow2_for(__reduce_max_sync(0xffffffffu, big[m]));
+    for (int m = 0; m < 4; ++m) {
+        unsigned b = whole(bigk[m]);
+        b = max(b, __shfl_xor_sync(0xffffffffu, b, 1));
+        b = max(b, __shfl_xor_sync(0xffffffffu, b, 2));
+        if (t4 == 0) sc.ck[8 * m + g] = pow2_for(b).c;
     }
+    __syncwarp();
+    const float ck = sc.ck[lane], ick = 1.f / ck, len = ick * 8192.f;      // of token `lane` (powers of two: exact)
     if (h == hk * group) {          // the rows as operands
         unsigned char *out = p.rows + ((size_t(b) * p.qk_heads + hk) * nchunk + c) * Rows::BYTES;
         constexpr int CR = NP / 8;
 #pragma unroll 4
         for (int x = lane; x < C * CR; x += 32) {
             const int r = x / CR, n = (x % CR) * 8;
+            const float cr = sc.ck[r];
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 float f[8];
                 load8<Tin>(reinterpret_cast<const Tin *>(sc.rows[m] + r * ROW) + n, f);
                 unsigned w[4][OP];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) split_f16<OP>(f2(f[2 * y], f[2 * y + 1]), cs[m].c, w[y]);
+                for (int y = 0; y < 4; ++y) split_f16<OP>(f2(f[2 * y], f[2 * y + 1]), m ? cq.c : cr, w[y]);
 #pragma unroll
                 for (int i = 0; i < OP; ++i)
                     *reinterpret_cast<uint4 *>(out + (m * OP + i) * Rows::PIECE + r * Rows::ROW + n * 2) =
@@ -320,24 +336,23 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
     rat[lane * RATROW + C] = lane == C - 1 ? 1.f : 0.f;
     __syncwarp();
     float *vec = reinterpret_cast<float *>(sc.block + Block::OFF_VEC), *one = vec + kVecScalars * C;
-    auto max_of = [&](float x) { return __uint_as_float(warp_max_bits(fabsf(x))); };
     {
         const float gam = rat[lane * RATROW], end = rat[(C - 1) * RATROW + lane + 1];
-        const float gk = gam * cs[0].inv, sgq = p.scale * gam * cs[1].inv, ebk = end * beta * cs[0].inv;
-        vec[kVecGk * C + lane] = gk;
-        vec[kVecSgq * C + lane] = sgq;
+        vec[kVecGk * C + lane] = gam * ick;
+        vec[kVecSgq * C + lane] = p.scale * gam * cq.inv;
         vec[kVecBeta * C + lane] = beta;
-        sc.beta[lane] = beta;
-        vec[kVecEk * C + lane] = end * cs[0].inv;
-        vec[kVecEbk * C + lane] = ebk;
-        const float mb = max_of(beta), me = max_of(ebk), mg = max_of(gk), ms = max_of(sgq);
+        vec[kVecEk * C + lane] = end * ick;
+        vec[kVecEbk * C + lane] = end * beta * ick;
+        vec[kVecBl * C + lane] = beta * len;
+        vec[kVecL * C + lane] = len;
+        sc.beta[lane] = beta * len * len;
         if (lane == 0) {
             one[kGamLast] = rat[(C - 1) * RATROW];
-            one[kCk] = cs[0].c; one[kCq] = cs[1].c;
-            one[kMaxBeta] = mb; one[kMaxEbk] = me; one[kMaxGk] = mg; one[kMaxSgq] = ms;
+            one[kCq] = cq.c;
         }
     }
-    // A and Pm: the products times their decays
+    // A and Pm: the products times their decays, over the keys' lengths
+    constexpr float kOne = 1.f / 8192.f;                        // 1 / l = ck 2^-13
     float mp = 0.f;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
@@ -346,17 +361,18 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int s0 = 16 * n + 8 * i + 2 * t4;
+                const float l0 = sc.ck[s0] * kOne, l1 = sc.ck[s0 + 1] * kOne;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int t = 16 * m + 8 * r + g;
-                    const float *ck = kk[2 * (m + n) + i] + 2 * r;
-                    float *cq = qk[2 * (m + n) + i] + 2 * r;
-                    const float r0 = rat[t * RATROW + s0 + 1], r1 = rat[t * RATROW + s0 + 2];
-                    at[s0 * NROW + t] = s0 < t ? ck[0] * r0 : 0.f;
-                    at[(s0 + 1) * NROW + t] = s0 + 1 < t ? ck[1] * r1 : 0.f;
-                    cq[0] = s0 <= t ? cq[0] * r0 * p.scale : 0.f;
-                    cq[1] = s0 + 1 <= t ? cq[1] * r1 * p.scale : 0.f;
-                    mp = fmaxf(mp, fmaxf(fabsf(cq[0]), fabsf(cq[1])));
+                    const float *ak = kk[2 * (m + n) + i] + 2 * r;
+                    float *pq = qk[2 * (m + n) + i] + 2 * r;
+                    const float r0 = rat[t * RATROW + s0 + 1], r1 = rat[t * RATROW + s0 + 2], lt = sc.ck[t] * kOne;
+                    at[s0 * NROW + t] = s0 < t ? ak[0] * lt * l0 * r0 : 0.f;
+                    at[(s0 + 1) * NROW + t] = s0 + 1 < t ? ak[1] * lt * l1 * r1 : 0.f;
+                    pq[0] = s0 <= t ? pq[0] * l0 * r0 * p.scale : 0.f;
+                    pq[1] = s0 + 1 <= t ? pq[1] * l1 * r1 * p.scale : 0.f;
+                    mp = fmaxf(mp, fmaxf(fabsf(pq[0]), fabsf(pq[1])));
                 }
             }
     const Pow2 sp = pow2_for(warp_max_bits(mp));
@@ -369,10 +385,10 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float *cq = qk[2 * (m + n) + i] + 2 * r;
+                    const float *pq = qk[2 * (m + n) + i] + 2 * r;
                     unsigned char *to = sc.block + (m + n) * kTri + tri_at(8 * r + g, i) + t4 * 4;
                     unsigned w[2];
-                    split_f16<2>(f2(cq[0], cq[1]), sp.c, w);
+                    split_f16<2>(f2(pq[0], pq[1]), sp.c, w);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) *reinterpret_cast<unsigned *>(to + Block::OFF_P + 3 * y * kTri) = w[y];
                 }
@@ -891,6 +907,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         Tok v, x, du;
         load_tok<Tv>(stage + Cfg::OFF_V + warp * 16 * int(sizeof(Tv)), Cfg::VROW, lane, v);
         unsigned mv = 0;                                   // reverse pass: largest |dO|
+        (void)mv;
         if constexpr (!REV) {
             // R = v - gam S k
             scale_tok(sk, sk, vec + kVecGk * C, t4);
@@ -907,6 +924,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             split_tok<PV>(v, cv.c, A);
             zero_tok(lo);
             mma_triangle<PV, 2, true>(lo, A, tbase + Block::OFF_P);
+            scale_tok(lo, lo, vec + kVecL * C, t4);
             scale_tok(sk, sk, vec + kVecEk * C, t4);
             const float f = one[kInvP] * cv.inv;
 #pragma unroll
@@ -914,27 +932,18 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv, sk[n][m], f * lo[n][m]);
         }
-        auto scale_by = [&](unsigned m, float most) {
-            const float b = __uint_as_float(m) * most;
-            return pow2_for(__float_as_uint(isfinite(b) ? b : 0.f));
-        };
-        // e = R - G (beta R), or du = rhs - G^T (beta rhs) and w = beta du.  Scales of what follows
-        // come from bounds: at most 31 entries of G, each below 2^14 / its scale, times beta's
-        // largest (a few bits more than it takes, of the 24 and more between fp16's largest and
-        // smallest steps).
-        float grown;
+        // e = R - G (beta R), or du = rhs - G^T (beta rhs) and w = beta du.  Every operand's scale
+        // comes from its own largest value.
         {
             unsigned A[2][2][4];
             Tok d;
-            const unsigned mr = max_tok(REV ? du : x);
-            const Pow2 cx = scale_by(mr, one[kMaxBeta]);
-            scale_tok(d, REV ? du : x, vec + kVecBeta * C, t4);
+            scale_tok(d, REV ? du : x, vec + kVecBl * C, t4);
+            const Pow2 cx = pow2_for(max_tok(d));
             split_tok<2>(d, cx.c, A);
             zero_tok(d);
             mma_triangle<2, 2, REV>(d, A, tbase);
+            scale_tok(d, d, vec + kVecL * C, t4);
             const float f = -one[kInvG] * cx.inv;
-            grown = __uint_as_float(mr) * fmaf(31.f * 16384.f * one[kInvG], one[kMaxBeta], 1.f);
-            if constexpr (REV) grown *= one[kMaxBeta];
             Tok &to = REV ? du : x;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
@@ -942,18 +951,21 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                 for (int m = 0; m < 4; ++m) to[n][m] = fmaf(f, d[n][m], to[n][m]);
             if constexpr (REV) scale_tok(x, du, vec + kVecBeta * C, t4);
         }
-        const unsigned mx = __float_as_uint(isfinite(grown) ? grown : 0.f);
-        if constexpr (BWD)
+        unsigned mx = 0;                                   // backward: largest |e|, or |w|
+        (void)mx;
+        if constexpr (BWD) {
+            mx = max_tok(x);
             if (lane == 0) {
                 p.emax[(size_t(bh) * nchunk + c) * parts + part] = mx;
                 if constexpr (REV) p.ymax[(size_t(bh) * nchunk + c) * parts + part] = mv;
             }
+        }
         Tok o;
         if constexpr (!REV && !STATE) {
             // y = scale gam S q + Pm (beta e)
             unsigned A[2][2][4];
-            const Pow2 cu = scale_by(mx, one[kMaxBeta]);
-            scale_tok(o, x, vec + kVecBeta * C, t4);
+            scale_tok(o, x, vec + kVecBl * C, t4);
+            const Pow2 cu = pow2_for(max_tok(o));
             split_tok<2>(o, cu.c, A);
             zero_tok(o);
             mma_triangle<2, 2, false>(o, A, tbase + Block::OFF_P);
@@ -998,11 +1010,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         {
             unsigned A1[2][2][4], A2[2][REV ? 2 : 1][4];
             Tok w;
-            const Pow2 c1 = scale_by(mx, one[REV ? kMaxGk : kMaxEbk]), c2 = REV ? scale_by(mv, one[kMaxSgq]) : Pow2{0.f, 0.f};
             scale_tok(w, x, vec + (REV ? kVecGk : kVecEbk) * C, t4);
+            const Pow2 c1 = pow2_for(max_tok(w));
             split_tok<2>(w, c1.c, A1);
+            Pow2 c2{0.f, 0.f};
             if constexpr (REV) {
                 scale_tok(w, v, vec + kVecSgq * C, t4);
+                c2 = pow2_for(max_tok(w));
                 split_tok<2>(w, c2.c, A2);
             }
             auto load_t = [&](unsigned (&f)[KP][4], unsigned base, int h2, int j) {

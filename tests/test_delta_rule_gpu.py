@@ -165,6 +165,33 @@ def test_forward_any_key_magnitude(cuda_lib):
         run_and_check(d, F32, scale=1.0)
 
 
+def unlike_keys(kind, ratio, dtype, seed=14):
+    """Keys whose lengths differ inside a chunk, beta k.k in (0, 1), values of one size.  A
+    state that holds what a short key wrote is long / short larger across it: queries are
+    unit."""
+    d = make(1, 70, 2, 2, 32, 32, dtype=F32, seed=seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    if kind == "some":
+        length = torch.ones(1, 70, 2)
+        length[:, ::4] = ratio
+    else:
+        length = torch.exp(np.log(ratio) / 2 * torch.randn(1, 70, 2, generator=g))
+    d["k"] = (d["k"] * length[..., None].to(DEV)).to(dtype)
+    d["q"], d["v"] = d["q"].to(dtype), d["v"].to(dtype)
+    d["beta"] = (0.1 + 0.8 * torch.rand(1, 70, 2, generator=g)).to(DEV) / (d["k"].float() ** 2).sum(-1)
+    return d
+
+
+UNLIKE = [("some", 30), ("some", 100), ("some", 300), ("lognormal", 30), ("lognormal", 300)]
+
+
+@pytest.mark.parametrize("kind,ratio", UNLIKE)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_keys_of_unlike_lengths(cuda_lib, kind, ratio, dtype):
+    """Lengths that differ inside a chunk, the step making up for them: the same bounds."""
+    run_and_check(unlike_keys(kind, ratio, dtype), F32)
+
+
 def test_forward_continues(cuda_lib):
     """A sequence in two calls is the sequence in one, also with the state carried in place."""
     d = make(2, 150, 4, 2, 64, 128, seed=5)
@@ -344,6 +371,12 @@ def test_growing_states(cuda_lib, dtype):
     d["beta"] = d["beta"] * 2.2
     run_and_check(d, F32)
     check_bwd(d, F32, seed=5)
+
+
+@pytest.mark.parametrize("kind,ratio", UNLIKE)
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_backward_keys_of_unlike_lengths(cuda_lib, kind, ratio, dtype, grad):
+    check_bwd(unlike_keys(kind, ratio, dtype), grad, seed=6)
 
 
 def test_backward_tiny_gradients(cuda_lib):
