@@ -333,8 +333,9 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * This holds for states that do not grow: a <= 0 and beta k.k in [0, 2].  Growth by up to 2^16
  * within a chunk costs nothing; by 2^g the terms of the chunk's first tokens keep about 38 - g
  * bits.
- * A value that is not finite spreads over the rest of its chunk of 32 tokens, earlier ones
- * included.  Long sequences of few heads are cut into segments that run at once (the sizes alone
+ * Rows of headdim are independent, whatever their sizes.  A value of v or of a state that is not
+ * finite stays in its row and spreads there to the sequence's end and over its chunk of 32
+ * tokens, earlier ones included; one of q, k, a or beta spreads over all rows.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.
  * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
  * 224 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for

@@ -36,12 +36,13 @@
 //
 // Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
 // operand scaled by a power of two: one per token for k, one per chunk for q and the triangles,
-// one per warp and chunk for the state and what follows from it, each from the operand's own
+// one per row and chunk for the state and what follows from it, each from the operand's own
 // largest value.  With l_t the power of two that key t is scaled by, the triangles are those of
 // the keys k_t / l_t with steps beta_t l_t^2, which no ratio of lengths spreads; l_t goes onto
 // the tokens' vectors on either side of them.  (Bounds from the factors' largest values in
 // place of the operands' own left 2e-2 of the state at keys 300 times as long as their
-// neighbours, one scale for a chunk's keys 1e-3 at lengths spread over 10^6.)  bf16
+// neighbours, one scale for a chunk's keys 1e-3 at lengths spread over 10^6.)  Rows of headdim
+// never meet, in range no more than in value: a row's inf or NaN stays in its row.  bf16
 // inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), whatever
 // the type of y: one behind a bf16 y made 11% of its values round the other way (8 x 2048
 // tokens x 24 heads of 64 x 128: 280 us with the call, 312 with two).  Three bf16 pieces hold
@@ -554,17 +555,48 @@ __device__ __forceinline__ void store_tok(T *out, size_t stride, int ntok, int n
     }
 }
 
-// A Tok times c as the pieces of two A operands (tokens 0-15 and 16-31 as the inner index).
-template <int NP> __device__ __forceinline__ void split_tok(const Tok &x, float c, unsigned (&a)[2][NP][4]) {
-    split_tiles<NP>(x[0], x[1], c, a[0]);
-    split_tiles<NP>(x[2], x[3], c, a[1]);
+// The scales of a lane's two rows, g and g + 8: of values whose largest magnitudes in the lane are
+// m0 and m1 (the four lanes of a row join theirs).
+struct RowScale {
+    Pow2 r[2];
+    __device__ __forceinline__ void set(float m0, float m1) {
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+        }
+        r[0] = pow2_for(__float_as_uint(m0));
+        r[1] = pow2_for(__float_as_uint(m1));
+    }
+    __device__ __forceinline__ float inv(int m) const { return r[m >> 1].inv; }      // of accumulator value m
+};
+
+// The largest magnitudes of a Tok in a lane's rows g and g + 8.
+__device__ __forceinline__ float2 max_rows(const Tok &x) {
+    float2 m = f2(0.f, 0.f);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+        m.x = fmaxf(m.x, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
+        m.y = fmaxf(m.y, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+    }
+    return m;
+}
+__device__ __forceinline__ RowScale scale_of(const Tok &x) {
+    const float2 m = max_rows(x);
+    RowScale c;
+    c.set(m.x, m.y);
+    return c;
+}
+__device__ __forceinline__ unsigned max_tok(const Tok &x) {        // over the warp, as bits
+    const float2 m = max_rows(x);
+    return warp_max_bits(fmaxf(m.x, m.y));
 }
 
-__device__ __forceinline__ unsigned max_tok(const Tok &x) {        // over the warp, as bits
-    float m = 0.f;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) m = fmaxf(fmaxf(m, fmaxf(fabsf(x[n][0]), fabsf(x[n][1]))), fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
-    return warp_max_bits(m);
+// A Tok times its rows' scales as the pieces of two A operands (tokens 0-15 and 16-31 as the inner
+// index).
+template <int NP> __device__ __forceinline__ void split_tok(const Tok &x, const RowScale &c, unsigned (&a)[2][NP][4]) {
+    split_tiles<NP>(x[0], x[1], c.r[0].c, c.r[1].c, a[0]);
+    split_tiles<NP>(x[2], x[3], c.r[0].c, c.r[1].c, a[1]);
 }
 
 // d += x M^T (d[., t] = sum_s x[., s] M(t, s)), or with REV x M, for a lower triangle M at
@@ -828,25 +860,26 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     }
     if constexpr (MODE == 2) fetch_state(inner ? (first + count) / (kDeltaSave / C) : nbound - 1);
     int turn = warp + 1;                                   // loop steps until it is this warp's to start copies
-    // the largest magnitude of the state, kept up with its updates
-    float ms = 0.f;
+    // the largest magnitudes of the lane's two rows of the state, kept up with its updates
+    float ms[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NP / 8; ++j)
 #pragma unroll
-        for (int m = 0; m < 4; ++m) ms = fmaxf(ms, fabsf(s[j][m]));
+        for (int m = 0; m < 4; ++m) ms[m >> 1] = fmaxf(ms[m >> 1], fabsf(s[j][m]));
 
     for (int i = 0; i < count; ++i) {
         const int c = chunk_of(i);
         constexpr int CS = kDeltaSave / C;
         const size_t tok0 = (size_t(b) * p.seqlen + size_t(c) * C) * p.heads + h;
         const int ntok = min(C, p.seqlen - c * C);
-        const unsigned msb = warp_max_bits(ms);
-        const Pow2 cS = pow2_for(msb);
+        RowScale cS;
+        cS.set(ms[0], ms[1]);
         Tok er;
         if constexpr (MODE == 1)
             if (c % CS == 0) {
+                const unsigned msb = warp_max_bits(fmaxf(ms[0], ms[1]));
                 keep_state(p.ck, c / CS);
-                keep_state16(p.s16, cS.c, c / CS);
+                keep_state16(p.s16, pow2_for(msb).c, c / CS);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
             }
         if constexpr (MODE == 2) {
@@ -857,8 +890,9 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                 er[n][0] = f.x; er[n][1] = f.y; er[n][2] = f.z; er[n][3] = f.w;
             }
             if (c % CS == CS - 1 || c == nchunk - 1) {
+                const unsigned msb = warp_max_bits(fmaxf(ms[0], ms[1]));
                 dot_state(c / CS + 1);
-                keep_state16(p.d16, cS.c, c / CS + 1);
+                keep_state16(p.d16, pow2_for(msb).c, c / CS + 1);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
             }
             if (c % CS == 0) fetch_state(c / CS);
@@ -888,7 +922,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
         for (int j = 0; j < NP / 16; ++j) {
             unsigned A[2][4];
-            split_tiles<2>(s[2 * j], s[2 * j + 1], cS.c, A);
+            split_tiles<2>(s[2 * j], s[2 * j + 1], cS.r[0].c, cS.r[1].c, A);
 #pragma unroll
             for (int h2 = 0; h2 < 2; ++h2)
 #pragma unroll
@@ -914,23 +948,23 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) x[n][m] = fmaf(-cS.inv, sk[n][m], v[n][m]);
+                for (int m = 0; m < 4; ++m) x[n][m] = fmaf(-cS.inv(m), sk[n][m], v[n][m]);
         } else {
             // rhs = end (dS k) + Pm^T dO, times beta
             Tok lo;
             unsigned A[2][PV][4];
-            mv = max_tok(v);
-            const Pow2 cv = pow2_for(mv);
-            split_tok<PV>(v, cv.c, A);
+            const RowScale cv = scale_of(v);
+            if constexpr (MODE == 2) mv = max_tok(v);
+            split_tok<PV>(v, cv, A);
             zero_tok(lo);
             mma_triangle<PV, 2, true>(lo, A, tbase + Block::OFF_P);
             scale_tok(lo, lo, vec + kVecL * C, t4);
             scale_tok(sk, sk, vec + kVecEk * C, t4);
-            const float f = one[kInvP] * cv.inv;
+            const float f[2] = {one[kInvP] * cv.r[0].inv, one[kInvP] * cv.r[1].inv};
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv, sk[n][m], f * lo[n][m]);
+                for (int m = 0; m < 4; ++m) du[n][m] = fmaf(cS.inv(m), sk[n][m], f[m >> 1] * lo[n][m]);
         }
         // e = R - G (beta R), or du = rhs - G^T (beta rhs) and w = beta du.  Every operand's scale
         // comes from its own largest value.
@@ -938,17 +972,17 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             unsigned A[2][2][4];
             Tok d;
             scale_tok(d, REV ? du : x, vec + kVecBl * C, t4);
-            const Pow2 cx = pow2_for(max_tok(d));
-            split_tok<2>(d, cx.c, A);
+            const RowScale cx = scale_of(d);
+            split_tok<2>(d, cx, A);
             zero_tok(d);
             mma_triangle<2, 2, REV>(d, A, tbase);
             scale_tok(d, d, vec + kVecL * C, t4);
-            const float f = -one[kInvG] * cx.inv;
+            const float f[2] = {-one[kInvG] * cx.r[0].inv, -one[kInvG] * cx.r[1].inv};
             Tok &to = REV ? du : x;
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) to[n][m] = fmaf(f, d[n][m], to[n][m]);
+                for (int m = 0; m < 4; ++m) to[n][m] = fmaf(f[m >> 1], d[n][m], to[n][m]);
             if constexpr (REV) scale_tok(x, du, vec + kVecBeta * C, t4);
         }
         unsigned mx = 0;                                   // backward: largest |e|, or |w|
@@ -965,16 +999,16 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             // y = scale gam S q + Pm (beta e)
             unsigned A[2][2][4];
             scale_tok(o, x, vec + kVecBl * C, t4);
-            const Pow2 cu = pow2_for(max_tok(o));
-            split_tok<2>(o, cu.c, A);
+            const RowScale cu = scale_of(o);
+            split_tok<2>(o, cu, A);
             zero_tok(o);
             mma_triangle<2, 2, false>(o, A, tbase + Block::OFF_P);
             scale_tok(sq, sq, vec + kVecSgq * C, t4);
-            const float f = one[kInvP] * cu.inv;
+            const float f[2] = {one[kInvP] * cu.r[0].inv, one[kInvP] * cu.r[1].inv};
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f, o[n][m], cS.inv * sq[n][m]);
+                for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f[m >> 1], o[n][m], cS.inv(m) * sq[n][m]);
         }
         if constexpr (!REV) {
             if constexpr (MODE == 1) {
@@ -1011,20 +1045,20 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             unsigned A1[2][2][4], A2[2][REV ? 2 : 1][4];
             Tok w;
             scale_tok(w, x, vec + (REV ? kVecGk : kVecEbk) * C, t4);
-            const Pow2 c1 = pow2_for(max_tok(w));
-            split_tok<2>(w, c1.c, A1);
-            Pow2 c2{0.f, 0.f};
+            const RowScale c1 = scale_of(w);
+            split_tok<2>(w, c1, A1);
+            RowScale c2{};
             if constexpr (REV) {
                 scale_tok(w, v, vec + kVecSgq * C, t4);
-                c2 = pow2_for(max_tok(w));
-                split_tok<2>(w, c2.c, A2);
+                c2 = scale_of(w);
+                split_tok<2>(w, c2, A2);
             }
             auto load_t = [&](unsigned (&f)[KP][4], unsigned base, int h2, int j) {
 #pragma unroll
                 for (int m = 0; m < KP; ++m) ldsm4_t(f[m], base + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bk + j * 32);
             };
-            const float2 f1 = REV ? f2(-c1.inv, -c1.inv) : f2(c1.inv, c1.inv), gl = f2(glast, glast), f2v = f2(c2.inv, c2.inv);
-            ms = 0.f;
+            const float2 gl = f2(glast, glast);
+            ms[0] = ms[1] = 0.f;
 #pragma unroll
             for (int j = 0; j < NP / 16; ++j) {
                 float d[2][4], d2[2][4];
@@ -1047,10 +1081,11 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
                     for (int m = 0; m < 4; m += 2) {
                         float *at = s[2 * j + n] + m;
                         float2 u = fmul2(gl, f2(at[0], at[1]));
-                        if constexpr (REV) u = ffma2(f2v, f2(d2[n][m], d2[n][m + 1]), u);
-                        u = ffma2(f1, f2(d[n][m], d[n][m + 1]), u);
+                        const float f1 = REV ? -c1.inv(m) : c1.inv(m);
+                        if constexpr (REV) u = ffma2(f2(c2.inv(m), c2.inv(m)), f2(d2[n][m], d2[n][m + 1]), u);
+                        u = ffma2(f2(f1, f1), f2(d[n][m], d[n][m + 1]), u);
                         at[0] = u.x; at[1] = u.y;
-                        ms = fmaxf(ms, fmaxf(fabsf(u.x), fabsf(u.y)));
+                        ms[m >> 1] = fmaxf(ms[m >> 1], fmaxf(fabsf(u.x), fabsf(u.y)));
                     }
             }
         }

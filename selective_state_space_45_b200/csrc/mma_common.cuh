@@ -93,17 +93,23 @@ template <int NP> __device__ __forceinline__ void split_f16(float2 x, float c, u
     }
 }
 
-// Two neighbouring accumulator tiles, times c, as the pieces of one A operand.
+// Two neighbouring accumulator tiles, rows g times c0 and rows g + 8 times c1, as the pieces of
+// one A operand.
 template <int NP>
-__device__ __forceinline__ void split_tiles(const float (&lo)[4], const float (&hi)[4], float c, unsigned (&a)[NP][4]) {
+__device__ __forceinline__ void split_tiles(const float (&lo)[4], const float (&hi)[4], float c0, float c1, unsigned (&a)[NP][4]) {
     unsigned p[NP];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const float *x = (r & 2) ? hi : lo;
-        split_f16<NP>(f2(x[2 * (r & 1)], x[2 * (r & 1) + 1]), c, p);
+        split_f16<NP>(f2(x[2 * (r & 1)], x[2 * (r & 1) + 1]), r & 1 ? c1 : c0, p);
 #pragma unroll
         for (int i = 0; i < NP; ++i) a[i][r] = p[i];
     }
+}
+
+template <int NP>
+__device__ __forceinline__ void split_tiles(const float (&lo)[4], const float (&hi)[4], float c, unsigned (&a)[NP][4]) {
+    split_tiles<NP>(lo, hi, c, c, a);
 }
 
 // acc += A B over pieces, the product of two second pieces left out (2^-22 of the leading

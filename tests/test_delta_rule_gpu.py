@@ -192,6 +192,61 @@ def test_forward_keys_of_unlike_lengths(cuda_lib, kind, ratio, dtype):
     run_and_check(unlike_keys(kind, ratio, dtype), F32)
 
 
+def unlike_rows(shape, dtype, seed=15):
+    """Values and states whose rows of headdim differ by up to 2^60."""
+    d = make(*shape, dtype=dtype, seed=seed)
+    P = shape[4]
+    size = 2.0 ** torch.linspace(-30, 30, P)[torch.randperm(P, generator=torch.Generator().manual_seed(seed))].round()
+    d["v"] = (d["v"].float() * size.to(DEV)).to(dtype)
+    d["initial_state"] = d["initial_state"] * size.to(DEV)[:, None]
+    return d
+
+
+def close_rows(got, ref, what, axis, check=close_state):
+    """``check`` row of headdim by row: each against its own size."""
+    for i in range(got.shape[axis]):
+        check(got.select(axis, i), np.take(ref, i, axis), (what, i))
+
+
+@pytest.mark.parametrize("shape", [(1, 70, 2, 2, 32, 32), (2, 97, 2, 1, 72, 104), (1, 2101, 2, 1, 32, 64)], ids=str)
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F32, F32)])
+def test_forward_rows_of_unlike_sizes(cuda_lib, shape, dtype, out):
+    """Rows of headdim never meet in the recurrence: each is as exact as if it were alone."""
+    d = unlike_rows(shape, dtype)
+    y, S = ssm.delta_rule(**d, scale=0.7, out_dtype=out)
+    yr, Sr = oracle.delta_rule(**d, scale=0.7)
+    close_rows(y, yr, "y", 3, close_y)
+    close_rows(S, Sr, "final state", 2)
+
+
+def bad_rows(shape, dtype):
+    """Infinities and NaN in single rows of the start state and of v; the rows they are in."""
+    d = make(*shape, dtype=dtype, seed=16)
+    d["initial_state"][0, 0, 3, 5] = float("inf")
+    d["initial_state"][0, 0, 17, 0] = float("nan")
+    d["v"][0, 40, 0, 9] = float("inf")
+    d["v"][0, 50, 0, 30] = float("nan")
+    clean = {n: t.clone() for n, t in d.items()}
+    clean["initial_state"][~clean["initial_state"].isfinite()] = 0
+    clean["v"][~clean["v"].isfinite()] = 0
+    return d, clean, [3, 9, 17, 30]
+
+
+@pytest.mark.parametrize("shape", [(1, 70, 2, 2, 32, 32), (1, 2101, 2, 1, 32, 64)], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_bad_rows_stay_alone(cuda_lib, shape, dtype):
+    """inf or NaN in a row of the start state or of v reaches that row alone, and there the final
+    state and every y from it on; the others keep their bits."""
+    d, clean, rows = bad_rows(shape, dtype)
+    y, S = ssm.delta_rule(**d, scale=0.7, out_dtype=F32)
+    yc, Sc = ssm.delta_rule(**clean, scale=0.7, out_dtype=F32)
+    keep = [i for i in range(shape[4]) if i not in rows]
+    assert torch.equal(y[:, :, 0][..., keep], yc[:, :, 0][..., keep]) and torch.equal(S[:, 0, keep], Sc[:, 0, keep])
+    assert torch.equal(y[:, :, 1], yc[:, :, 1]) and torch.equal(S[:, 1], Sc[:, 1])
+    assert not S[:, 0, rows].isfinite().any() and not y[0, :, 0][:, [3, 17]].isfinite().any()
+    assert not y[0, 50:, 0][:, rows].isfinite().any()
+
+
 def test_forward_continues(cuda_lib):
     """A sequence in two calls is the sequence in one, also with the state carried in place."""
     d = make(2, 150, 4, 2, 64, 128, seed=5)
@@ -377,6 +432,20 @@ def test_growing_states(cuda_lib, dtype):
 @pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
 def test_backward_keys_of_unlike_lengths(cuda_lib, kind, ratio, dtype, grad):
     check_bwd(unlike_keys(kind, ratio, dtype), grad, seed=6)
+
+
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_backward_rows_of_unlike_sizes(cuda_lib, dtype, grad):
+    """The gradients of v and of the start state go row by row, too."""
+    d = make(2, 97, 2, 1, 72, 104, dtype=dtype, seed=15)
+    g = torch.Generator().manual_seed(7)
+    size = (2.0 ** torch.linspace(-30, 30, 72)[torch.randperm(72, generator=g)].round()).to(DEV)
+    dy = (torch.randn(d["v"].shape, generator=g).to(DEV) * size).to(grad)
+    dS = torch.randn(2, 2, 72, 104, generator=g).to(DEV) * size[:, None]
+    got = ssm.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=0.7)
+    ref = oracle.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=0.7)
+    close_rows(got["dv"], ref["dv"], "dv", 3, close_y)
+    close_rows(got["dinitial_state"], ref["dinitial_state"], "dinitial_state", 2)
 
 
 def test_backward_tiny_gradients(cuda_lib):
