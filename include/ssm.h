@@ -335,7 +335,8 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * bits.
  * Rows of headdim are independent, whatever their sizes.  A value of v or of a state that is not
  * finite stays in its row and spreads there to the sequence's end and over its chunk of 32
- * tokens, earlier ones included; one of q, k, a or beta spreads over all rows.  Long sequences of few heads are cut into segments that run at once (the sizes alone
+ * tokens, earlier ones included; one of q, k, a or beta spreads over all rows.  What comes out
+ * finite is right.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.
  * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
  * 224 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
@@ -380,8 +381,9 @@ int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *
  *   dv            : [batch][seqlen][heads][headdim], grad_dtype, written.
  *   da, dbeta     : [batch][seqlen][heads] fp32, written.
  *   dinitial_state: [batch][heads][headdim][dstate] fp32 or NULL.
- * Every sum has a fixed order: results are deterministic.  Takes scratch (see the
- * conventions above) of about 8 * batch * heads * headdim' * (seqlen + dstate * (seqlen / 64 + 2))
+ * Every sum has a fixed order: results are deterministic.  A value that is not finite spreads over
+ * its chunk of 64 tokens here, over all of dq, dk, da and dbeta; what comes out finite is right.
+ * Takes scratch (see the conventions above) of about 8 * batch * heads * headdim' * (seqlen + dstate * (seqlen / 64 + 2))
  * bytes, headdim' = headdim rounded up to 64: mostly e, w and the state and its gradient every
  * 64 tokens; and what the forward takes for segments, into which long sequences of few heads
  * are cut here too.

@@ -201,9 +201,9 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
         return reinterpret_cast<const float *>(p.prep + ((size_t(b) * p.heads + hk * group) * nck + c32 + (x < n32 ? x : 0)) *
                                                             DeltaBlock::BYTES + DeltaBlock::OFF_VEC);
     };
-    float icq[2];                        // 1 / scales of q in the chunk's halves (powers of two: exact)
+    float icq[2];                        // 1 / scales of q in the chunk's halves
 #pragma unroll
-    for (int x = 0; x < 2; ++x) icq[x] = 1.f / __ldg(vec_of(x) + kVecScalars * kDeltaC + kCq);
+    for (int x = 0; x < 2; ++x) icq[x] = __ldg(vec_of(x) + kVecScalars * kDeltaC + kInvQ);
     if (tid < C) ick[tid] = __ldg(vec_of(tid >> 5) + kVecL * kDeltaC + (tid & 31)) * (1.f / 8192.f);
     bool dead = false;
     for (int hg = 0; hg < group && !dead; ++hg) {
@@ -245,13 +245,15 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
         // Scales as powers of two: per product the smallest over the parts (the products come out
         // times 2^it) and each part's distance to it.
         int ly[2], le[2], lw[2];
-        auto log_scale = [&](unsigned m) { return int(__float_as_uint(pow2_for(m).c) >> 23) - 127; };
+        constexpr int kBad = -(1 << 16);                  // of a part with an infinite value
+        auto log_scale = [&](unsigned m) { return m >= 0x7f800000u ? kBad : int(__float_as_uint(pow2_for(m).c) >> 23) - 127; };
 #pragma unroll
         for (int x = 0; x < 2; ++x) { ly[x] = log_scale(bits[x]); le[x] = log_scale(bits[2 + x]); lw[x] = log_scale(bits[4 + x]); }
         const int ls = log_scale(bits[6]), ld = log_scale(bits[7]);
         auto common = [&](int l, float &inv) {
             const int least = __reduce_min_sync(0xffffffffu, lane < kp ? l : 1 << 20);
             inv = exp2_int(-(least >> 1)) * exp2_int((least >> 1) - least);       // 0 when too small for a float
+            if (least < kBad / 2) inv = __uint_as_float(kNanBits);
             return lane < kp ? half2_exp2(least - l) : 0u;
         };
         float i1[2], i2[2], i3[2], i4[2], i5, i6, i7;

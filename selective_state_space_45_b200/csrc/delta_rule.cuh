@@ -118,7 +118,7 @@ enum {
     kVecScalars,   // then the scalars below
     kVecs
 };
-enum { kGamLast, kCq, kInvG, kInvP };             // the chunk's decay, the scale of q, 1 / scales of G and Pm
+enum { kGamLast, kInvQ, kInvG, kInvP };           // the chunk's decay, 1 / scales of q, G and Pm
 struct DeltaBlock {
     static constexpr int OFF_P = 6 * kTri, OFF_VEC = OFF_P + 6 * kTri, BYTES = OFF_VEC + kVecs * kDeltaC * 4;
 };
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(128) delta_prep_kernel(const DeltaArgs p) {
         sc.beta[lane] = beta * len * len;
         if (lane == 0) {
             one[kGamLast] = rat[(C - 1) * RATROW];
-            one[kCq] = cq.c;
+            one[kInvQ] = cq.inv;
         }
     }
     // A and Pm: the products times their decays, over the keys' lengths

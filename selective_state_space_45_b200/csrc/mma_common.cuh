@@ -72,11 +72,13 @@ __device__ __forceinline__ unsigned pack_f16x2(float lo, float hi) {
 }
 
 // The power of two c for values whose largest magnitude has the bits `m` (as an integer), and
-// its inverse.  Both are ordinary numbers for any m, inf and NaN included.
+// its inverse.  Of an infinite one the inverse is NaN: beside it the other values vanish, and a
+// product without them must not look like a result.
 struct Pow2 { float c, inv; };
+constexpr unsigned kNanBits = 0x7fffffffu;
 __device__ __forceinline__ Pow2 pow2_for(unsigned m) {
     const unsigned f = min(267u - (m >> 23), 253u);
-    return {__uint_as_float(f << 23), __uint_as_float((254u - f) << 23)};
+    return {__uint_as_float(f << 23), __uint_as_float(m >= 0x7f800000u ? kNanBits : (254u - f) << 23)};
 }
 __device__ __forceinline__ unsigned warp_max_bits(float m) {
     return __reduce_max_sync(0xffffffffu, __float_as_uint(m));      // m >= 0: ordered as integers

@@ -487,6 +487,62 @@ def test_results_do_not_vary(cuda_lib):
         assert all(torch.equal(g[n], g2[n]) for n in g)
 
 
+# ---- values that are not finite --------------------------------------------------------------
+
+
+def right_or_not_finite(got, ref, what, elem, of_max):
+    """Where a result is finite it is the right one."""
+    g, r = to64(got), np.asarray(ref)
+    ok, M = np.isfinite(g), np.abs(r[np.isfinite(r)]).max()
+    with np.errstate(invalid="ignore"):
+        assert (np.abs(g - r)[ok] <= elem * np.abs(r[ok]) + of_max * M).all(), what
+
+
+INF, NAN = float("inf"), float("nan")
+BAD = [(n, t, x) for n in ("q", "k", "v", "beta", "a") for t in (52, 40, 75) for x in (INF, NAN)] + [
+    ("initial_state", 3, INF), ("initial_state", 3, NAN)]
+
+
+def with_bad(name, at, value, dtype):
+    d = make(1, 150, 2, 2, 40, 48, dtype=dtype, seed=19)
+    d[name][(0, 0, at, 5) if name == "initial_state" else (0, at, 0) + (7,) * (d[name].dim() - 3)] = value
+    return d
+
+
+@pytest.mark.parametrize("name,at,value", BAD)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_forward_not_finite(cuda_lib, name, at, value, dtype):
+    """An inf or NaN anywhere: what comes out finite is right, and chunks of 32 tokens before it
+    and the other head come out as without it."""
+    d = with_bad(name, at, value, dtype)
+    y, S = ssm.delta_rule(**d, scale=0.7, out_dtype=F32)
+    with np.errstate(invalid="ignore", over="ignore"):
+        yr, Sr = oracle.delta_rule(**d, scale=0.7)
+    right_or_not_finite(y, yr, "y", 0, 2.0 ** -13)
+    right_or_not_finite(S, Sr, "final state", 0, 2.0 ** -13)
+    before = 0 if name == "initial_state" else at // 32 * 32
+    assert y[:, :before].isfinite().all() and y[:, :, 1].isfinite().all() and S[:, 1].isfinite().all()
+
+
+@pytest.mark.parametrize("name,at,value", [b for b in BAD if b[0] != "a"] + [
+    ("dy", 52, INF), ("dy", 40, NAN), ("dfinal_state", 3, INF), ("dfinal_state", 3, NAN)])
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_backward_not_finite(cuda_lib, name, at, value, dtype, grad):
+    ours = name not in ("dy", "dfinal_state")
+    d = with_bad(name, at, value, dtype) if ours else make(1, 150, 2, 2, 40, 48, dtype=dtype, seed=19)
+    g = torch.Generator().manual_seed(8)
+    more = dict(dy=torch.randn(d["v"].shape, generator=g).to(DEV).to(grad),
+                dfinal_state=torch.randn(1, 2, 40, 48, generator=g).to(DEV))
+    if not ours:
+        more[name][(0, at, 0, 7) if name == "dy" else (0, 0, at, 5)] = value
+    got = ssm.delta_rule_bwd(more["dy"], **d, dfinal_state=more["dfinal_state"], scale=0.7)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = oracle.delta_rule_bwd(more["dy"], **d, dfinal_state=more["dfinal_state"], scale=0.7)
+    for n in got:
+        right_or_not_finite(got[n], ref[n], n, 2.0 ** -8 if got[n].dtype == BF16 else 0, 2.0 ** -12)
+        assert (got[n][:, 1] if n == "dinitial_state" else got[n][:, :, 1]).isfinite().all(), n
+
+
 # ---- streams and graphs --------------------------------------------------------------------
 
 
