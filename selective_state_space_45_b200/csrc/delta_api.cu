@@ -52,7 +52,7 @@ template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *works
         const long long chunks = (long long)delta_chunks(a.seqlen);
         a.seg_chunks = int((chunks + at.nseg - 1) / at.nseg);
         const int nseg = int((chunks + a.seg_chunks - 1) / a.seg_chunks);
-        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, Tout, 3>(a, s, nseg);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tout, 3>(a, s, nseg);
         if (st == SSM_OK) st = launch_fold<false>(a, nseg, s);
         // a state carried in place: the last segment's end must not be written before the first
         // segment has read its start, so it goes by the slot that the last segment leaves unused
@@ -60,12 +60,12 @@ template <typename Tin, typename Tout> int run_fwd(ssm::DeltaArgs a, void *works
         const size_t state = size_t(a.P) * a.N * 4;
         const bool in_place = end != nullptr && end == a.h0;
         a.end_slot = in_place;
-        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, Tout, 0>(a, s, nseg);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tout, 0>(a, s, nseg);
         if (st == SSM_OK && in_place)
             st = status_of(cudaMemcpy2DAsync(end, state, ws.p + at.seg_state + (nseg - 1) * state, nseg * state, state,
                                              size_t(a.batch) * a.heads, cudaMemcpyDeviceToDevice, s));
     } else if (st == SSM_OK) {
-        st = dispatch_chain<KP, Tin, Tin, Tout, 0>(a, s);
+        st = dispatch_chain<KP, Tin, Tout, 0>(a, s);
     }
     return ws.release(st);
 }

@@ -29,30 +29,24 @@ template <int PW, typename Tin, typename Tg> int dispatch_grad(const ssm::DeltaG
 
 // The parts of a call's scratch, in this order; each starts on 16 bytes.
 struct BwdParts {
-    size_t prep, rows, e, ck, e16, w16, y16, s16, d16, dyy, edu, vw, zsum, smax, dsmax, emax, wmax, ymax, part, seg_state, seg_map, all;
+    size_t prep, rows, e16, w16, y16, s16, d16, smax, dsmax, emax, wmax, ymax, part, seg_state, seg_map, all;
     int nseg;
     BwdParts(int batch, int seqlen, int heads, int qk_heads, int P, int N, int in_dtype, int grad_dtype) {
-        const size_t bh = size_t(batch) * heads, tok = bh * seqlen;
+        const size_t bh = size_t(batch) * heads;
         const size_t nbound = (size_t(seqlen) + ssm::kDeltaSave - 1) / ssm::kDeltaSave + 1;
         const size_t parts = size_t(delta_slices(P)) * kDeltaWarps;       // of 16 rows
-        const size_t sum = parts * tok * 4, state = bh * nbound * parts * 16 * padded_state(N) * 4;
+        const size_t state = bh * nbound * parts * 16 * padded_state(N) * 4;
         const size_t tok16 = bh * delta_chunks(seqlen) * parts * ssm::kTok16;       // a piece of e, w or dy
         size_t at = 0;
         auto add = [&](size_t &where, size_t bytes) { where = at; at += round16(bytes); };
         add(prep, prep_bytes(batch, seqlen, heads));
         add(rows, rows_bytes(batch, seqlen, qk_heads, N, in_dtype));
-        add(e, 2 * tok16);                              // as fp32
-        add(ck, state);
         add(e16, 2 * tok16);
         add(w16, 2 * tok16);
         add(y16, grad_dtype == SSM_BF16 ? tok16 : 2 * tok16);
         add(s16, state);
         add(d16, state);
-        add(dyy, sum);
-        add(edu, sum);
-        add(vw, sum);
-        add(zsum, 4 * parts * bh * nbound);
-        add(smax, 4 * parts * bh * nbound);             // these five together: zeroed
+        add(smax, 4 * parts * bh * nbound);
         add(dsmax, 4 * parts * bh * nbound);
         add(emax, 4 * parts * bh * delta_chunks(seqlen));
         add(wmax, 4 * parts * bh * delta_chunks(seqlen));
@@ -80,10 +74,8 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
     f.timeouts = wait_counter();
     auto bits = [&](size_t off) { return reinterpret_cast<unsigned *>(ws.p + off); };
     int st = f.timeouts ? dispatch_prep<Tin>(f, s) : int(SSM_ERR_CUDA);
-    if (st == SSM_OK) st = status_of(cudaMemsetAsync(ws.p + at.smax, 0, at.part - at.smax, s));
     f.smax = bits(at.smax); f.emax = bits(at.emax);
-    f.v = v; f.v2 = dy; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;
-    f.e = part(at.e); f.ck = part(at.ck); f.sum = part(at.dyy);
+    f.v = v; f.e16 = ws.p + at.e16; f.s16 = ws.p + at.s16;
     // segments: whole spans of the kept states
     int nseg = 1;
     if (at.nseg > 1) {
@@ -92,25 +84,24 @@ int run_bwd(ssm::DeltaArgs f, const void *v, const void *dy, const float *dfinal
         f.seg_chunks = ((chunks + at.nseg - 1) / at.nseg + span - 1) / span * span;
         nseg = (chunks + f.seg_chunks - 1) / f.seg_chunks;
         f.seg_state = part(at.seg_state); f.seg_map = part(at.seg_map);
-        if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tin, float, 3>(f, s, nseg);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tin, float, 3>(f, s, nseg);
         if (st == SSM_OK) st = launch_fold<false>(f, nseg, s);
     }
-    if (st == SSM_OK) st = dispatch_chain<KP, Tin, Tg, float, 1>(f, s, nseg);
+    if (st == SSM_OK) st = dispatch_chain<KP, Tin, float, 1>(f, s, nseg);
     if (st == SSM_OK) {
         ssm::DeltaArgs r = f;
-        r.v = dy; r.v2 = v; r.y = dv; r.h0 = dfinal; r.hN = dh0;
+        r.v = dy; r.y = dv; r.h0 = dfinal; r.hN = dh0;
         r.d16 = ws.p + at.d16; r.w16 = ws.p + at.w16; r.y16 = ws.p + at.y16;
-        r.sum = part(at.edu); r.sum2 = part(at.vw); r.zsum = part(at.zsum);
         r.smax = bits(at.dsmax); r.emax = bits(at.wmax); r.ymax = bits(at.ymax);
         if (nseg > 1) {
-            st = dispatch_chain<KP, Tg, Tg, float, 4>(r, s, nseg);
+            st = dispatch_chain<KP, Tg, float, 4>(r, s, nseg);
             if (st == SSM_OK) st = launch_fold<true>(r, nseg, s);
         }
-        if (st == SSM_OK) st = dispatch_chain<KP, Tg, Tin, Tg, 2>(r, s, nseg);
+        if (st == SSM_OK) st = dispatch_chain<KP, Tg, Tg, 2>(r, s, nseg);
     }
     if (st == SSM_OK) {
         const ssm::DeltaGradArgs g{f.a, f.beta, f.rows, f.prep, ws.p + at.e16, ws.p + at.w16, ws.p + at.y16,
-                                   ws.p + at.s16, ws.p + at.d16, f.timeouts, part(at.dyy), part(at.edu), part(at.vw), part(at.zsum), bits(at.smax),
+                                   ws.p + at.s16, ws.p + at.d16, f.timeouts, bits(at.smax),
                                    bits(at.dsmax), bits(at.emax), bits(at.wmax), bits(at.ymax), part(at.part), dq, dk,
                                    da, dbeta, f.batch, f.seqlen, f.heads, f.qk_heads, f.P, f.N,
                                    delta_slices(f.P) * kDeltaWarps, f.scale};

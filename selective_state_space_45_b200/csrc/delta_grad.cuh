@@ -8,12 +8,15 @@
 // the chunk's gradients are
 //     dq_t = scale (gam_t S0^T dy_t + sum_s M1(t,s) k_s)
 //     dk_s = end_s dE^T u_s + scale sum_t M1(t,s) q_t - gam_s S0^T w_s - sum_t (M2 + M2^T)(s,t) k_t
-// summed over the value heads that share the key head, in their order.  The gradient of a is
-// <dS', S'>, S' the state after its decay; between tokens it changes by dy_t.y_t - v_t.w_t
-// (q_t.dq_t - v_t.dv_t), so
-//     da_t = <dS, S>(chunk's end) + sum_{t'>=t} (dy.y - v.w)_t'
-//          = <dS, S>(chunk's start) - sum_{t'<t} (dy.y - v.w)_t'
-// with the inner products taken afresh every 64 tokens: at most 32 terms are summed.
+// summed over the value heads that share the key head, in their order.  With
+//     X(t,s) = r(t,s) (scale (dy_t.e_s) (q_t.k_s) - [s < t] (w_t.e_s) (k_t.k_s))  for s <= t,
+//     F_s = end_s e_s.(dE k_s),   R_t = gam_t (scale dy_t.(S0 q_t) - w_t.(S0 k_t))
+// the other two are what passes between the tokens on either side of a decay:
+//     dbeta_s = F_s + sum_{t>=s} X(t,s)
+//     da_t = sum_{t'>=t} sum_{s<t} X(t',s) beta_s + sum_{t'>=t} R_t' + sum_{s<t} beta_s F_s + gam_last <dE, S0>
+// Every term of da_t has the decay exp(a_t) in it, so da_t is as exact beside its own size as the
+// products are, and 0 where the decay is.  (<dS, S> at the chunk's end plus the sums of dy.y - v.w
+// from there is the same number, but its terms have not: at a = -12 a third of it was rounding.)
 //
 // Operands.  Every product runs on the tensor cores with scaled fp16 operands, two pieces for
 // each value (one for dy, q and k where they come as bf16), as in the passes; the passes leave
@@ -41,8 +44,6 @@ struct DeltaGradArgs {
     const unsigned char *rows, *prep;  // k and q as operands, and the chunk blocks (their scales)
     const unsigned char *e16, *w16, *y16, *s16, *d16;      // the passes' tiles
     unsigned *timeouts;
-    const float *dyy, *edu, *vw;       // [zparts][batch][heads][seqlen]
-    const float *zsum;                 // [zparts][batch][heads][boundaries]
     const unsigned *smax, *dsmax;      // [batch][heads][boundaries][zparts]
     const unsigned *emax, *wmax, *ymax;// [batch][heads][chunks of 32][zparts]
     float *part;                       // heads that share a key head: running sums of dq, dk, [2][tokens][qk_heads][N]
@@ -63,11 +64,11 @@ template <int NP_, int PW_, int KP_, typename Tg_> struct GradCfg {
     static constexpr int OFF_E = 0, OFF_W = 2 * TOK, OFF_Y = 4 * TOK;
     static constexpr int OFF_KQ = OFF_Y + PY * TOK;                           // [half] k and q
     static constexpr int OFF_VEC = OFF_KQ + 2 * Rows::BYTES;
-    static constexpr int OFF_OUT = OFF_VEC + 7 * kGradC * 4 + 64;             // per-warp output tiles
-    static constexpr int OUT = sizeof(Tg) == 2 ? kTok16 : 0;
+    static constexpr int OFF_OUT = OFF_VEC + 11 * kGradC * 4 + 128;           // X on the diagonal, later the warps' output tiles
+    static constexpr int OUT = kTok16;
     static constexpr int SLICE = 4 * PARTS * kTok16;                          // S and dE, 32 columns: [S, dE][part][piece]
     static constexpr int HALF = 113 * 1024, WHOLE = 227 * 1024;               // shared memory for two CTAs on an SM, or one
-    static constexpr int fixed(int groups) { return OFF_OUT + 4 * groups * OUT; }
+    static constexpr int fixed(int groups) { return OFF_OUT + 4 * (sizeof(Tg) == 2 ? groups : 1) * OUT; }
     static constexpr int CTAS = fixed(1) + SLICE <= HALF ? 2 : 1;
     static constexpr int NG = CTAS == 2 ? 1 : 2, NT = 128 * NG;               // groups of four warps
     static constexpr int CW = NG == 2 && (NP == 32 || fixed(2) + 2 * SLICE > WHOLE) ? 16 : 32;       // a group's columns in a step
@@ -107,9 +108,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
     constexpr int C = kGradC, NP = Cfg::NP, KP = Cfg::KP, PY = Cfg::PY, PARTS = Cfg::PARTS, NT = Cfg::NT;
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
-    float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *bet = gam + C;
-    float *bend = bet + C, *dtok = bend + C, *ick = dtok + C;       // ick: 1 / scales of the keys
-    double *half = reinterpret_cast<double *>(ick + C);
+    // per token: the decays (Gh + Gl the sum of a from the chunk's start, gam its exponential, end that
+    // of the rest), beta, 1 / scales of the keys, row sums of X beta left of the diagonal tile, and
+    // column sums of X in the tiles of row tile 0..3; then the sums of the tiles left of the diagonal.
+    // Gh, Gl, gam and end later hold R and F, a pair for each group of warps, tile those of Z.
+    float *Gh = reinterpret_cast<float *>(smem + Cfg::OFF_VEC), *Gl = Gh + C, *gam = Gl + C, *end = gam + C;
+    float *bet = end + C, *ick = bet + C, *rowx = ick + C, *colx = rowx + C, *tile = colx + 4 * C;
+    double *half = reinterpret_cast<double *>(tile + 16);
     uint64_t *tokbar = reinterpret_cast<uint64_t *>(half + 2), *stbar = tokbar + 1;
     const int tid = threadIdx.x, lane = tid & 31, rt = (tid >> 5) & 3, gr = tid >> 7, ht = rt >> 1, g = lane >> 2, t4 = lane & 3;
     const int nchunk = (p.seqlen + C - 1) / C, nbound = nchunk + 1, nck = (p.seqlen + kDeltaC - 1) / kDeltaC;
@@ -117,7 +122,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
     const int b = bk / p.qk_heads, hk = bk - b * p.qk_heads;
     const int t0 = c * C, nt = min(C, p.seqlen - t0), group = p.heads / p.qk_heads;
     const int c32 = 2 * c, n32 = min(2, nck - c32), kp = (p.P + 15) / 16;
-    const size_t all = size_t(p.batch) * p.heads, krow = size_t(p.qk_heads) * p.N;
+    const size_t krow = size_t(p.qk_heads) * p.N;
     const size_t k0 = (size_t(b) * p.seqlen + t0) * krow + size_t(hk) * p.N;
     const int total = group * Cfg::STEPS;
     if (tid == 0) {
@@ -205,6 +210,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
 #pragma unroll
     for (int x = 0; x < 2; ++x) icq[x] = __ldg(vec_of(x) + kVecScalars * kDeltaC + kInvQ);
     if (tid < C) ick[tid] = __ldg(vec_of(tid >> 5) + kVecL * kDeltaC + (tid & 31)) * (1.f / 8192.f);
+    const unsigned own = sbase + Cfg::OFF_KQ + ht * Rows::BYTES;         // the half's k and q, and the warp's rows of them
+    const unsigned a_kq = own + ((rt & 1) * 16 + (lane & 15)) * Rows::ROW + (lane >> 4) * 16, n_kq = b_rows_n(lane, Rows::ROW);
     bool dead = false;
     for (int hg = 0; hg < group && !dead; ++hg) {
         const int h = hk * group + hg;
@@ -222,25 +229,10 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
         bits[6] = max_at(p.smax, (bh * nbound + c) * p.zparts);
         bits[7] = max_at(p.dsmax, (bh * nbound + c + 1) * p.zparts);
         const size_t gate = (size_t(b) * p.seqlen + t0 + (tid & 63)) * p.heads + h;
-        float av = 0.f, bv = 0.f, dyy = 0.f, db = 0.f, z = 0.f;
-        const bool front = 2 * tid < nt;
+        float av = 0.f, bv = 0.f, last = 0.f;
         if (tid < nt) {
-            av = __ldg(p.a + gate);
+            av = fmaxf(__ldg(p.a + gate), -1e4f);
             bv = __ldg(p.beta + gate);
-            float v[4][4];
-            for (int s0 = 0; s0 < p.zparts; s0 += 4) {    // zparts is a multiple of 4
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const size_t x = ((s0 + s) * all + bh) * p.seqlen + t0 + tid;
-                    v[s][0] = __ldg(p.dyy + x);
-                    v[s][1] = __ldg(p.vw + x);
-                    v[s][2] = __ldg(p.edu + x);
-                    v[s][3] = __ldg(p.zsum + ((s0 + s) * all + bh) * nbound + c + (front ? 0 : 1));
-                }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) { dyy += v[s][0] - v[s][1]; db += v[s][2]; z += v[s][3]; }
-            }
-            av = fmaxf(av, -1e4f);
         }
         // Scales as powers of two: per product the smallest over the parts (the products come out
         // times 2^it) and each part's distance to it.
@@ -284,17 +276,11 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
             Gh[tid] = float(G);
             Gl[tid] = float(G - double(float(G)));
             gam[tid] = expf(float(G));
+            end[tid] = expf(float(Gend - G));
             bet[tid] = bv;
-            bend[tid] = bv * expf(float(Gend - G));
-            dtok[tid] = dyy;
+            last = expf(float(Gend));
         }
         __syncthreads();
-        if (tid < nt) {
-            if (front) for (int x = 0; x < tid; ++x) z -= dtok[x];
-            else for (int x = nt - 1; x >= tid; --x) z += dtok[x];
-            p.da[gate] = z;
-            p.dbeta[gate] = db;
-        }
         wait(tokbar, hg);
 
         // The token-by-token matrices of this warp's rows, in four tiles of 16 columns: dy e^T;
@@ -351,16 +337,39 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
             }
         }
         // times the decays, beta and the scales taken back out: M1 / ck for dq; M1^T scale / cq
-        // and -(M2 + M2^T) / ck for dk
-        float m1 = 0.f, m2 = 0.f;
-        float grh[2], grl[2], br[2];
+        // and -(M2 + M2^T) / ck for dk; and X up to the diagonal, its sums (one group of warps)
+        float m1 = 0.f, m2 = 0.f, rowsum[2] = {0.f, 0.f};
+        float grh[2], grl[2], br[2], kr[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int t = 16 * rt + g + 8 * r;
-            grh[r] = Gh[t]; grl[r] = Gl[t]; br[r] = bet[t];
+            grh[r] = Gh[t]; grl[r] = Gl[t]; br[r] = bet[t]; kr[r] = ick[t];
         }
+        float *diag = reinterpret_cast<float *>(smem + Cfg::OFF_OUT);
+        auto diag_at = [&](int tl, int r, int q) { return tl * 256 + r * 16 + (q ^ r); };       // rows' values in other banks
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
+            float qk[2][4], kk[2][4], xe[2][4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) { zero4(qk[n]); zero4(kk[n]); zero4(xe[n]); }
+            if (gr == 0 && u <= rt) {        // q.k and k.k of the tile
+#pragma unroll 2
+                for (int j = 0; j < NP / 16; ++j) {
+                    unsigned ak[KP][4], aq[KP][4], bK[KP][4];
+                    const unsigned at = sbase + Cfg::OFF_KQ + (u >> 1) * Rows::BYTES + (u & 1) * 16 * Rows::ROW + n_kq + j * 32;
+#pragma unroll
+                    for (int x = 0; x < KP; ++x) {
+                        ldsm4(ak[x], a_kq + x * Rows::PIECE + j * 32);
+                        ldsm4(aq[x], a_kq + (KP + x) * Rows::PIECE + j * 32);
+                        ldsm4(bK[x], at + x * Rows::PIECE);
+                    }
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        mma_pieces<KP, KP>(qk[n], aq, bK, n);
+                        mma_pieces<KP, KP>(kk[n], ak, bK, n);
+                    }
+                }
+            }
             const float e1 = i1[u >> 1] * p.scale, e2 = i2[u >> 1] * p.scale * icq[u >> 1];
             const float e3 = -i3[u >> 1], e4 = -i4[u >> 1];
 #pragma unroll
@@ -375,11 +384,18 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                         f(m, ((grh[m >> 1] - (m & 1 ? gh.y : gh.x)) + (grl[m >> 1] - (m & 1 ? gl.y : gl.x))) * kLog2e,
                           m & 1 ? bq.y : bq.x, m & 1 ? kq.y : kq.x);
                 };
+                // a value of X from those of M1 and M2 over beta
+                auto pair = [&](int m, float v1, float v3) {
+                    xe[n][m] = fmaf(v1, qk[n][m] * icq[ht], v3 * (kk[n][m] * kr[m >> 1]));
+                };
                 if (u < rt) {
                     each([&](int m, float gd, float bc, float kc) {
-                        const float d = ex2_approx(gd) * bc * kc;
-                        x1[u][n][m] *= d * e1;
-                        x3[u][n][m] *= d * e3;
+                        const float d = ex2_approx(gd) * kc;
+                        const float v1 = x1[u][n][m] * (d * e1), v3 = x3[u][n][m] * (d * e3);
+                        pair(m, v1, v3);
+                        x1[u][n][m] = v1 * bc;
+                        x3[u][n][m] = v3 * bc;
+                        rowsum[m >> 1] = fmaf(xe[n][m], bc, rowsum[m >> 1]);
                     });
                 } else if (u > rt) {
                     each([&](int m, float gd, float, float kc) {
@@ -390,10 +406,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                 } else {
                     each([&](int m, float gd, float bc, float kc) {
                         const int r = g + 8 * (m >> 1), q = 8 * n + 2 * t4 + (m & 1);
-                        const float d = ex2_approx(q <= r ? gd : -gd) * (q < r ? bc : br[m >> 1]);       // r(the later, the earlier)
-                        x1[u][n][m] = q <= r ? x1[u][n][m] * (d * kc * e1) : 0.f;
-                        x2[u][n][m] = q >= r ? x2[u][n][m] * (d * e2) : 0.f;
-                        x3[u][n][m] = q < r ? x3[u][n][m] * (d * kc * e3) : q > r ? x4[n][m] * (d * kc * e4) : 0.f;
+                        const float d = ex2_approx(q <= r ? gd : -gd), dk = d * kc;       // r(the later, the earlier)
+                        const float v1 = q <= r ? x1[u][n][m] * (dk * e1) : 0.f, v3 = q < r ? x3[u][n][m] * (dk * e3) : 0.f;
+                        pair(m, v1, v3);
+                        x1[u][n][m] = v1 * bc;
+                        x2[u][n][m] = q >= r ? x2[u][n][m] * (d * br[m >> 1] * e2) : 0.f;
+                        x3[u][n][m] = q < r ? v3 * bc : q > r ? x4[n][m] * (dk * br[m >> 1] * e4) : 0.f;
+                        if (gr == 0) diag[diag_at(rt, r, q)] = xe[n][m] * bc;
                     });
                 }
 #pragma unroll
@@ -402,6 +421,29 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                     m2 = fmaxf(m2, fmaxf(fabsf(x2[u][n][m]), fabsf(x3[u][n][m])));
                 }
             }
+            if (gr == 0 && u <= rt) {        // the tile's column sums, and its own
+                float whole = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float s = xe[n][y] + xe[n][y + 2];
+#pragma unroll
+                        for (int o = 4; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                        const int q = 16 * u + 8 * n + 2 * t4 + y;
+                        if (g == 0) colx[rt * C + q] = s;
+                        whole = fmaf(s, bet[q], whole);
+                    }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) whole += __shfl_xor_sync(0xffffffffu, whole, o);
+                if (lane == 0) tile[4 * rt + u] = whole;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) rowsum[r] += __shfl_xor_sync(0xffffffffu, rowsum[r], o);
+            if (gr == 0 && t4 == 0) rowx[16 * rt + g + 8 * r] = rowsum[r];
         }
         const Pow2 c1 = pow2_for(warp_max_bits(m1)), c2 = pow2_for(warp_max_bits(m2));
         unsigned a1[4][2][4], a2[4][2][4], a3[4][2][4];
@@ -417,20 +459,60 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
             const int t = 16 * rt + g + 8 * r;
             fq[r] = p.scale * gam[t] * i5;
             fw[r] = -gam[t] * i6;
-            fe[r] = bend[t] * i7;
+            fe[r] = end[t] * i7;
         }
+        __syncthreads();
+        // thread t: the pairs on either side of token t's decay, by tiles (both beside t's; one in it; in
+        // the diagonal tile by its rows' running sums), and the column t
+        float da = 0.f, db = 0.f;
+        if (tid < C) {
+            const int tl = tid >> 4, i = tid & 15;
+            float run = 0.f;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                run += diag[diag_at(tl, i, q)];
+                diag[diag_at(tl, i, q)] = run;
+            }
+            __syncwarp();
+            for (int r = i; r < 16; ++r) da += rowx[16 * tl + r] + (i > 0 ? diag[diag_at(tl, r, i - 1)] : 0.f);
+            for (int m = tl; m < 4; ++m) {
+                db += colx[m * C + tid];
+                if (m > tl) {
+                    for (int q = 0; q < i; ++q) da = fmaf(bet[16 * tl + q], colx[m * C + 16 * tl + q], da);
+                    for (int n = 0; n < tl; ++n) da += tile[4 * m + n];
+                }
+            }
+        }
+        __syncthreads();
+        float rq[2] = {0.f, 0.f}, rk[2] = {0.f, 0.f}, ek[2] = {0.f, 0.f}, z = 0.f;       // parts of R, of F and of Z = <dE, S0>
         // CW columns a step and group
         constexpr int NJ = Cfg::CW / 16;
 #pragma unroll 1
         for (int i = 0; i < Cfg::STEPS; ++i) {
             const int it = hg * Cfg::STEPS + i, col0 = i * Cfg::COLS + gr * Cfg::CW;
             wait(&stbar[it % Cfg::STAGES], it / Cfg::STAGES);
+            const unsigned char *slices = smem + Cfg::OFF_ST + (it % Cfg::STAGES) * (Cfg::SL * Cfg::SLICE);
+            for (int x = tid; x < min(Cfg::SL, NP / 32 - i * Cfg::SL) * PARTS * 64; x += NT) {      // <dE, S0>, 16 bytes a turn
+                const int k = (x >> 6) % PARTS;           // the same for a warp
+                const unsigned char *at = slices + x / (64 * PARTS) * Cfg::SLICE + k * (2 * kTok16) + (x & 63) * 16;
+                uint4 w[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint4 *>(at + (y >> 1) * (Cfg::SLICE / 2) + (y & 1) * kTok16);
+                auto value = [&](int m, int y) {
+                    auto h = [&](const uint4 &v) { return __half22float2(*(reinterpret_cast<const __half2 *>(&v) + y)); };
+                    return fadd2(h(w[2 * m]), h(w[2 * m + 1]));
+                };
+                float2 s = f2(0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s = ffma2(value(0, y), value(1, y), s);
+                const int l = __shfl_sync(0xffffffffu, ls, k) + __shfl_sync(0xffffffffu, ld, k);
+                z += l < kBad / 2 ? __uint_as_float(kNanBits) : (s.x + s.y) * exp2_int(-(l >> 1)) * exp2_int((l >> 1) - l);
+            }
             if (col0 < NP) {
                 float aq[2 * NJ][4], am[2 * NJ][4];       // dq, dk
                 {
                     // the products with the states
-                    const unsigned st = sbase + Cfg::OFF_ST + (it % Cfg::STAGES) * (Cfg::SL * Cfg::SLICE) +
-                                        (gr * Cfg::CW / 32) * Cfg::SLICE;
+                    const unsigned st = smem_u32(slices) + (gr * Cfg::CW / 32) * Cfg::SLICE;
                     const int piece0 = (gr * Cfg::CW % 32) / 8;
                     float aw[2 * NJ][4], ae[2 * NJ][4];
 #pragma unroll
@@ -458,12 +540,30 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                             }
                         }
                     }
+                    // row by row with the token's own q and k: R and F
 #pragma unroll
                     for (int n = 0; n < 2 * NJ; ++n)
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            aq[n][m] *= fq[m >> 1];
-                            am[n][m] = fmaf(fw[m >> 1], aw[n][m], fe[m >> 1] * ae[n][m]);
+                        for (int r = 0; r < 2; ++r) {
+                            const unsigned char *at = smem + Cfg::OFF_KQ + ht * Rows::BYTES + ((rt & 1) * 16 + g + 8 * r) * Rows::ROW +
+                                                      (col0 + 8 * n + 2 * t4) * 2;
+                            float2 k = f2(0.f, 0.f), q = f2(0.f, 0.f);
+#pragma unroll
+                            for (int x = 0; x < KP; ++x) {
+                                k = fadd2(k, __half22float2(*reinterpret_cast<const __half2 *>(at + x * Rows::PIECE)));
+                                q = fadd2(q, __half22float2(*reinterpret_cast<const __half2 *>(at + (KP + x) * Rows::PIECE)));
+                            }
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int m = 2 * r + y;
+                                aq[n][m] *= fq[r];
+                                aw[n][m] *= fw[r];
+                                ae[n][m] *= fe[r];
+                                rq[r] = fmaf(aq[n][m], y ? q.y : q.x, rq[r]);
+                                rk[r] = fmaf(aw[n][m], y ? k.y : k.x, rk[r]);
+                                ek[r] = fmaf(ae[n][m], y ? k.y : k.x, ek[r]);
+                                am[n][m] = fmaf(br[r], ae[n][m], aw[n][m]);
+                            }
                         }
                 }
                 // and with the other tokens' k and q
@@ -522,7 +622,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                 }
                 if constexpr (sizeof(Tg) == 2)
                     if (hg + 1 == group) {       // 16 rows through the warp's tile: whole 16-byte stores
-                        unsigned char *tile = smem + Cfg::OFF_OUT + (tid >> 5) * Cfg::OUT;
+                        unsigned char *to = smem + Cfg::OFF_OUT + (tid >> 5) * Cfg::OUT;
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             const float (&f)[2 * NJ][4] = x ? am : aq;
@@ -531,13 +631,13 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                                 unsigned r[4];
 #pragma unroll
                                 for (int m = 0; m < 4; ++m) r[m] = pack_bf16x2(f[2 * h2 + (m >> 1)][2 * (m & 1)], f[2 * h2 + (m >> 1)][2 * (m & 1) + 1]);
-                                stsm4(smem_u32(tile) + tok16_at(rb, 2 * h2 + (lane >> 4)), r);
+                                stsm4(smem_u32(to) + tok16_at(rb, 2 * h2 + (lane >> 4)), r);
                             }
                             __syncwarp();
 #pragma unroll
                             for (int y = 0; y < NJ; ++y) {
                                 const int r = (16 / NJ) * y + lane / (2 * NJ), pc = lane % (2 * NJ), col = col0 + 8 * pc;
-                                const uint4 w = *reinterpret_cast<const uint4 *>(tile + tok16_at(r, pc));
+                                const uint4 w = *reinterpret_cast<const uint4 *>(to + tok16_at(r, pc));
                                 if (16 * rt + r < nt && col < p.N)
                                     *reinterpret_cast<uint4 *>(static_cast<Tg *>(x ? p.dk : p.dq) + k0 + size_t(16 * rt + r) * krow + col) = w;
                             }
@@ -554,6 +654,40 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
                 }
             }
         }
+        if (dead) break;
+        // the head's da and dbeta
+        float *R = gr ? gam : Gh, *F = gr ? end : Gl;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            rq[r] = fmaf(rq[r], icq[ht], rk[r] * kr[r]);
+            ek[r] *= kr[r];
+#pragma unroll
+            for (int o = 1; o < 4; o <<= 1) {
+                rq[r] += __shfl_xor_sync(0xffffffffu, rq[r], o);
+                ek[r] += __shfl_xor_sync(0xffffffffu, ek[r], o);
+            }
+            if (t4 == 0) {
+                R[16 * rt + g + 8 * r] = rq[r];
+                F[16 * rt + g + 8 * r] = ek[r];
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) tile[tid >> 5] = z;
+        __syncthreads();
+        if (tid < nt) {
+            z = 0.f;
+#pragma unroll
+            for (int w = 0; w < NT / 32; ++w) z += tile[w];
+            for (int x = 0; x < nt; ++x) {
+                const float f = Gl[x] + (Cfg::NG == 2 ? end[x] : 0.f), r = Gh[x] + (Cfg::NG == 2 ? gam[x] : 0.f);
+                da += x < tid ? bet[x] * f : r;
+                if (x == tid) db += f;
+            }
+            p.da[gate] = fmaf(last, z, da);
+            p.dbeta[gate] = db;
+        }
+        if (hg + 1 < group) __syncthreads();
     }
     if (!alive)                          // results are void; copies may still be on their way: wait (bounded) for them
         for (int x = 0; x < 2; ++x) {

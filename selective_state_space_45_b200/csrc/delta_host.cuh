@@ -65,9 +65,9 @@ template <typename Tin> int dispatch_prep(const ssm::DeltaArgs &a, cudaStream_t 
 constexpr int kDeltaWarps = 4;
 inline int delta_slices(int P) { return (P + 16 * kDeltaWarps - 1) / (16 * kDeltaWarps); }
 
-template <int NP, int KP, typename Tv, typename Tv2, typename Tout, int MODE>
+template <int NP, int KP, typename Tv, typename Tout, int MODE>
 int launch_chain(ssm::DeltaArgs a, int nseg, cudaStream_t s) {
-    using Cfg = ssm::DeltaCfg<NP, kDeltaWarps, KP, Tv, Tv2, Tout, MODE>;
+    using Cfg = ssm::DeltaCfg<NP, kDeltaWarps, KP, Tv, Tout, MODE>;
     a.slices = delta_slices(a.P);
     if (nseg == 1) a.seg_chunks = int(delta_chunks(a.seqlen));
     // MODE 3 has the identity's rows beside those of headdim
@@ -78,13 +78,13 @@ int launch_chain(ssm::DeltaArgs a, int nseg, cudaStream_t s) {
     return status_of(cudaGetLastError());
 }
 
-template <int KP, typename Tv, typename Tv2, typename Tout, int MODE>
+template <int KP, typename Tv, typename Tout, int MODE>
 int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s, int nseg = 1) {
     switch (padded_state(a.N)) {
-    case 32: return launch_chain<32, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
-    case 64: return launch_chain<64, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
-    case 96: return launch_chain<96, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
-    default: return launch_chain<128, KP, Tv, Tv2, Tout, MODE>(a, nseg, s);
+    case 32: return launch_chain<32, KP, Tv, Tout, MODE>(a, nseg, s);
+    case 64: return launch_chain<64, KP, Tv, Tout, MODE>(a, nseg, s);
+    case 96: return launch_chain<96, KP, Tv, Tout, MODE>(a, nseg, s);
+    default: return launch_chain<128, KP, Tv, Tout, MODE>(a, nseg, s);
     }
 }
 

@@ -30,9 +30,8 @@
 // of a chunk, and one warp's tiles are 16 rows.
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
-//     rhs = end (dS k) + Pm^T dO,  du = rhs - G^T (beta rhs),  dv = w = beta du,  dbeta = e.du,
+//     rhs = end (dS k) + Pm^T dO,  du = rhs - G^T (beta rhs),  dv = w = beta du,
 //     dS <- gam_last dS + (scale gam dO) q^T - (gam w) k^T
-// (G without beta in its columns keeps du, and with it dbeta, exact where beta is small or 0.)
 //
 // Precision: the products run on the tensor cores in fp16 with fp32 accumulation, every
 // operand scaled by a power of two: one per token for k, one per chunk for q and the triangles,
@@ -62,24 +61,16 @@ struct DeltaArgs {
     unsigned char *rows;    // [batch][qk_heads][chunks] k and q as operands, from the prep kernel
     unsigned *timeouts;     // counts waits that gave up
     const void *v;          // [batch][seqlen][heads][headdim]; the reverse pass: dy
-    const void *v2;         // backward: dy in the forward pass, v in the reverse pass
     const float *a, *beta;  // [batch][seqlen][heads]
     void *y;                // forward: y; reverse pass: dv
     const float *h0;        // start state (reverse pass: the final state's gradient) or NULL
     float *hN;              // end state (reverse pass: the start state's gradient) or NULL
-    // The backward's scratch.  A "part" is a warp's 16 rows: part = slice * warps + warp.  What one
-    // pass leaves for the next is laid out as the warps hold it (accumulator tiles, four values a
-    // lane), so that every access is a whole 16 bytes a lane in order.
-    float *e;               // [batch][heads][chunks][parts][4 tiles of 8 tokens][lane][4]
-    float *ck;              // [batch][heads][boundaries][parts][dstate tiles of 8][lane][4]: the state
-                            // at every boundary of 64 tokens and at the end
-    // The last kernel takes scaled fp16 operands, tiles of its shared memory as they stand, in two
-    // pieces (one of a bf16 dy): e, w and dy of a part and chunk, S and dS of a part and 32 columns.
+    // The backward's scratch.  A "part" is a warp's 16 rows: part = slice * warps + warp.  The last
+    // kernel takes scaled fp16 operands, tiles of its shared memory as they stand, in two pieces
+    // (one of a bf16 dy): e, w and dy of a part and chunk, and of a part and 32 columns the state
+    // and its gradient at every boundary of 64 tokens (the first has no gradient, the end no state).
     unsigned char *e16, *w16, *y16;     // [batch][heads][chunks][parts][pieces] 16 rows of 32 tokens
     unsigned char *s16, *d16;           // [batch][heads][boundaries][dstate / 32][parts][pieces] 16 rows of 32 columns
-    float *sum, *sum2;      // [parts][batch][heads][seqlen] sums over a part's rows: dy.y; in the
-                            // reverse pass e.du (the gradient of beta) and v.w
-    float *zsum;            // [parts][batch][heads][boundaries] <dS, S>
     unsigned *smax;         // [batch][heads][boundaries][parts] largest |S| (reverse pass: |dS|), as bits
     unsigned *emax, *ymax;  // [batch][heads][chunks][parts] largest |e| (reverse pass: |w|) and, in the
                             // reverse pass, |dy|
@@ -138,34 +129,29 @@ __device__ __forceinline__ int tok16_at(int r, int n) { return r * 64 + ((n ^ (r
 constexpr long long kDeltaWaitCycles = 2000000000LL;        // a bounded wait's limit, about a second
 
 // NP: dstate rounded up; NW: warps with 16 rows each.  KP: pieces of q and k.  MODE 0:
-// forward (y); 1: forward of the backward pass (e and the kept states); 2: the reverse pass; 3:
+// forward (y); 1: the forward again for the backward (e and the kept states); 2: the reverse pass; 3:
 // a segment's end state and map (the recurrence of the identity's rows with v = 0); 4: the
 // reverse of 3, a segment's gradient of its start state (its map is the forward's, transposed).
-template <int NP_, int NW_, int KP_, typename Tv_, typename Tv2_, typename Tout_, int MODE_> struct DeltaCfg {
+template <int NP_, int NW_, int KP_, typename Tv_, typename Tout_, int MODE_> struct DeltaCfg {
     static constexpr int NP = NP_, NW = NW_, MODE = MODE_, KP = KP_;
     using Tv = Tv_;        // v, or dy in the reverse pass
-    using Tv2 = Tv2_;      // MODE 1: dy; MODE 2: v
     using Tout = Tout_;
     static constexpr int C = kDeltaC, NT = 32 * NW;
-    static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 && sizeof(Tv2) == 2 ? 2 : 1;       // per SM
+    static constexpr int CTAS = KP == 1 && sizeof(Tv) == 2 ? 2 : 1;       // per SM
     static constexpr int PV = sizeof(Tv) == 4 ? 2 : 1;                        // pieces of v (dy)
     using Block = DeltaBlock;
     using Rows = DeltaRows<NP, KP>;
     static constexpr int KROW = Rows::ROW;
     static constexpr int VROW = NW * 16 * int(sizeof(Tv)) + 16;
-    static constexpr int V2ROW = NW * 16 * int(sizeof(Tv2)) + 16;
     static constexpr int PIECE = Rows::PIECE;
     static constexpr int OFF_K = 0, OFF_Q = KP * PIECE, OFF_TRI = Rows::BYTES;
-    static constexpr int OFF_V = OFF_TRI + Block::BYTES, OFF_V2 = OFF_V + C * VROW;
+    static constexpr int OFF_V = OFF_TRI + Block::BYTES, STAGE = OFF_V + C * VROW;
     static constexpr bool BWD = MODE == 1 || MODE == 2;
-    static constexpr int STAGE = OFF_V2 + (BWD ? C * V2ROW : 0);
-    static constexpr int STAGES = !BWD && KP == 1 ? 3 : 2;                // three where two CTAs still fit
+    static constexpr int STAGES = KP == 1 ? 3 : 2;                        // three where two CTAs still fit
     static constexpr int OFF_BAR = STAGES * STAGE;                                 // mbarriers: full, empty
     static constexpr int OFF_OUT = OFF_BAR + 64;                              // per-warp output tiles
     static constexpr int OUT = BWD ? 2 * kTok16 : 1024;                       // bytes of a warp's tile
-    static constexpr int OFF_ST = OFF_OUT + NW * OUT;                         // kept states on their way
-    static constexpr int ST = MODE == 2 ? NP * 16 * 4 : 0;                    // bytes of a part's state
-    static constexpr int SMEM_BYTES = OFF_ST + NW * ST;
+    static constexpr int SMEM_BYTES = OFF_OUT + NW * OUT;
 };
 
 // acc += A B of operands in KP bf16 pieces (1: exact, 3: all bits of fp32), the products of
@@ -638,11 +624,11 @@ __device__ __forceinline__ void scale_tok(Tok &out, const Tok &x, const float *f
 template <class Cfg>
 __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const DeltaArgs p) {
     using Tv = typename Cfg::Tv;
-    using Tv2 = typename Cfg::Tv2;
     using Tout = typename Cfg::Tout;
     using Block = typename Cfg::Block;
     constexpr int C = Cfg::C, NP = Cfg::NP, NW = Cfg::NW, MODE = Cfg::MODE, KP = Cfg::KP, PV = Cfg::PV;
     constexpr bool REV = MODE == 2 || MODE == 4, BWD = Cfg::BWD, STATE = MODE == 3 || MODE == 4, MAP = MODE == 3;
+    constexpr bool OUT = MODE == 0;                        // y as well
     extern __shared__ __align__(128) unsigned char delta_smem[];
     unsigned char *smem = delta_smem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -685,8 +671,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     };
 
     // Start the copies of loop step i into its stage, once the warps are done with what is there:
-    // lane 0 the operands and the block, all lanes the rows of v (and of v2), zeros
-    // past the end and past headdim.
+    // lane 0 the operands and the block, all lanes the rows of v, zeros past the end and past
+    // headdim.
     const size_t voff = size_t(b) * p.seqlen * vrow + size_t(h) * p.P + slice * NW * 16;
     auto copy_v = [&](unsigned dst, int rowbytes, const auto *src, int ntok) {
         using T = std::remove_const_t<std::remove_pointer_t<decltype(src)>>;
@@ -713,7 +699,6 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         __syncwarp();
         const size_t at = voff + size_t(c) * C * vrow;
         if (!ident) copy_v(smem_u32(st) + Cfg::OFF_V, Cfg::VROW, static_cast<const Tv *>(p.v) + at, ntok);
-        if constexpr (BWD) copy_v(smem_u32(st) + Cfg::OFF_V2, Cfg::V2ROW, static_cast<const Tv2 *>(p.v2) + at, ntok);
         mbar_arrive_cp_async(&full[slot]);
     };
     if (warp == 0)
@@ -759,52 +744,6 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     const unsigned tr = REV ? tri_rows_k(lane) : tri_rows_n(lane);
     const int nbound = (p.seqlen + kDeltaSave - 1) / kDeltaSave + 1;       // boundaries, the end among them
     const size_t part = slice * NW + warp, parts = size_t(p.slices) * NW;
-    auto keep_state = [&](float *ck, int x) {
-        float4 *to = reinterpret_cast<float4 *>(ck + ((size_t(bh) * nbound + x) * parts + part) * (NP * 16)) + lane;
-#pragma unroll
-        for (int j = 0; j < NP / 8; ++j) to[32 * j] = make_float4(s[j][0], s[j][1], s[j][2], s[j][3]);
-    };
-    // reverse pass: the kept state of boundary x into the warp's shared memory, and its inner
-    // product with the gradient
-    unsigned char *strow = smem + Cfg::OFF_ST + warp * Cfg::ST + lane * 16;
-    auto fetch_state = [&](int x) {
-        const float4 *from = reinterpret_cast<const float4 *>(p.ck + ((size_t(bh) * nbound + x) * parts + part) * (NP * 16)) + lane;
-#pragma unroll
-        for (int j = 0; j < NP / 8; ++j) cp_async_16(strow + 512 * j, from + 32 * j);
-        cp_async_commit();
-    };
-    auto dot_state = [&](int x) {
-        cp_async_wait<0>();                                // this lane's own copies
-        float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < NP / 8; ++j) {
-            const float4 f = *reinterpret_cast<const float4 *>(strow + 512 * j);
-            z0 = fmaf(f.x, s[j][0], fmaf(f.z, s[j][2], z0));
-            z1 = fmaf(f.y, s[j][1], fmaf(f.w, s[j][3], z1));
-        }
-        z0 += z1;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) z0 += __shfl_xor_sync(0xffffffffu, z0, o);
-        if (lane == 0) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = z0;
-        __syncwarp();                                      // the memory may be used again
-    };
-    // sums over the part's 16 rows of f[row][token], tokens from t0 on: the eight values a lane
-    // has are halved in three exchanges, after which it holds one token's sum
-    auto token_sums = [&](float *sum, const Tok &f, int t0) {
-        float v[8];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) { v[2 * n] = f[n][0] + f[n][2]; v[2 * n + 1] = f[n][1] + f[n][3]; }
-#pragma unroll
-        for (int o = 16, h = 4; h > 0; o >>= 1, h >>= 1)
-#pragma unroll
-            for (int k = 0; k < h; ++k) {
-                const bool up = lane & o;
-                const float got = __shfl_xor_sync(0xffffffffu, up ? v[k] : v[k + h], o);
-                v[k] = (up ? v[k + h] : v[k]) + got;
-            }
-        const int t = t0 + 8 * (g >> 1) + 2 * t4 + (g & 1);
-        if (t < p.seqlen) sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = v[0];
-    };
     // a shared tile to global memory, as it stands
     auto copy_out = [&](unsigned char *to, const unsigned char *from, auto bytes) {
         __syncwarp();
@@ -842,23 +781,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         }
     };
     using std::integral_constant;
-    // a Tok as the next pass reads it
-    auto keep_tok = [&](float *to, const Tok &f, int c) {
-        float4 *at = reinterpret_cast<float4 *>(to + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) at[32 * n] = make_float4(f[n][0], f[n][1], f[n][2], f[n][3]);
-    };
-    if (nrow <= 0) {                                       // rows past headdim
-        if constexpr (BWD)
-            for (int t = lane; t < p.seqlen; t += 32) {
-                p.sum[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
-                if constexpr (MODE == 2) p.sum2[(part * p.batch * p.heads + bh) * p.seqlen + t] = 0.f;
-            }
-        if constexpr (MODE == 2)
-            for (int x = lane; x < nbound; x += 32) p.zsum[(part * p.batch * p.heads + bh) * nbound + x] = 0.f;
-        return;
-    }
-    if constexpr (MODE == 2) fetch_state(inner ? (first + count) / (kDeltaSave / C) : nbound - 1);
+    if (nrow <= 0) return;                                 // rows past headdim
     int turn = warp + 1;                                   // loop steps until it is this warp's to start copies
     // the largest magnitudes of the lane's two rows of the state, kept up with its updates
     float ms[2] = {0.f, 0.f};
@@ -874,29 +797,18 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
         const int ntok = min(C, p.seqlen - c * C);
         RowScale cS;
         cS.set(ms[0], ms[1]);
-        Tok er;
         if constexpr (MODE == 1)
             if (c % CS == 0) {
                 const unsigned msb = warp_max_bits(fmaxf(ms[0], ms[1]));
-                keep_state(p.ck, c / CS);
                 keep_state16(p.s16, pow2_for(msb).c, c / CS);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS) * parts + part] = msb;
             }
-        if constexpr (MODE == 2) {
-            const float4 *ep = reinterpret_cast<const float4 *>(p.e + ((size_t(bh) * nchunk + c) * parts + part) * 512) + lane;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const float4 f = __ldg(ep + 32 * n);
-                er[n][0] = f.x; er[n][1] = f.y; er[n][2] = f.z; er[n][3] = f.w;
-            }
+        if constexpr (MODE == 2)
             if (c % CS == CS - 1 || c == nchunk - 1) {
                 const unsigned msb = warp_max_bits(fmaxf(ms[0], ms[1]));
-                dot_state(c / CS + 1);
                 keep_state16(p.d16, pow2_for(msb).c, c / CS + 1);
                 if (lane == 0) p.smax[(size_t(bh) * nbound + c / CS + 1) * parts + part] = msb;
             }
-            if (c % CS == 0) fetch_state(c / CS);
-        }
 
         const int slot = i % Cfg::STAGES;
         wait(&full[slot], i / Cfg::STAGES);
@@ -915,7 +827,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < KP; ++m) {
                     ldsm4(kb[h2][m], kbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
-                    if constexpr (!REV && !STATE) ldsm4(qb[h2][m], qbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
+                    if constexpr (OUT) ldsm4(qb[h2][m], qbase + m * Cfg::PIECE + 16 * h2 * Cfg::KROW + bn + j * 32);
                 }
         };
         load_kq(0);
@@ -928,7 +840,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
                     mma_pieces<2, KP>(sk[2 * h2 + n], A, kb[h2], n);
-                    if constexpr (!REV && !STATE) mma_pieces<2, KP>(sq[2 * h2 + n], A, qb[h2], n);
+                    if constexpr (OUT) mma_pieces<2, KP>(sq[2 * h2 + n], A, qb[h2], n);
                 }
             if (j + 1 < NP / 16) load_kq(j + 1);
         }
@@ -995,7 +907,7 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
             }
         }
         Tok o;
-        if constexpr (!REV && !STATE) {
+        if constexpr (OUT) {
             // y = scale gam S q + Pm (beta e)
             unsigned A[2][2][4];
             scale_tok(o, x, vec + kVecBl * C, t4);
@@ -1010,31 +922,9 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
 #pragma unroll
                 for (int m = 0; m < 4; ++m) o[n][m] = fmaf(f[m >> 1], o[n][m], cS.inv(m) * sq[n][m]);
         }
-        if constexpr (!REV) {
-            if constexpr (MODE == 1) {
-                keep_tok(p.e, x, c);
-                keep_tok16(integral_constant<int, 2>(), p.e16, x, pow2_for(mx).c, c);
-                Tok dy;
-                load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, dy);
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) dy[n][m] *= o[n][m];
-                token_sums(p.sum, dy, c * C);
-            }
+        if constexpr (MODE == 1) {
+            keep_tok16(integral_constant<int, 2>(), p.e16, x, pow2_for(mx).c, c);
         } else if constexpr (MODE == 2) {
-            // the gradient of beta
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] *= er[n][m];
-            token_sums(p.sum, du, c * C);
-            load_tok<Tv2>(stage + Cfg::OFF_V2 + warp * 16 * int(sizeof(Tv2)), Cfg::V2ROW, lane, du);
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int m = 0; m < 4; ++m) du[n][m] *= x[n][m];
-            token_sums(p.sum2, du, c * C);
             keep_tok16(integral_constant<int, 2>(), p.w16, x, pow2_for(mx).c, c);
             keep_tok16(integral_constant<int, PV>(), p.y16, v, pow2_for(mv).c, c);
             store_tok<Tout>(static_cast<Tout *>(p.y) + tok0 * p.P + p0, vrow, ntok, nrow, tile, lane, x);
@@ -1097,12 +987,6 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_chain_kernel(const D
     if (!alive)                                            // copies may still be on their way: wait (bounded) for them
         for (int i = max(0, count - Cfg::STAGES); i < count; ++i)
             mbar_wait(&full[i % Cfg::STAGES], uint32_t(i / Cfg::STAGES) & 1, kDeltaWaitCycles);
-    if constexpr (MODE == 1)
-        if (seg + 1 == nseg) keep_state(p.ck, nbound - 1);
-    if constexpr (MODE == 2) {
-        if (seg == 0) dot_state(0);
-        else cp_async_wait<0>();
-    }
     float *end = ident ? p.seg_map + (size_t(bh) * nseg + seg) * p.N * p.N
                  : STATE ? p.seg_state + (size_t(bh) * nseg + seg) * p.P * p.N
                  : !p.hN || seg != (REV ? 0 : nseg - 1) ? nullptr

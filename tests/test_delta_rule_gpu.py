@@ -24,6 +24,7 @@ from tests.helpers import to64
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 F32, BF16 = torch.float32, torch.bfloat16
+INF, NAN = float("inf"), float("nan")
 
 
 def make(b, L, H, K, P, N, dtype=BF16, seed=0, state=True, decay=0.3):
@@ -448,6 +449,61 @@ def test_backward_rows_of_unlike_sizes(cuda_lib, dtype, grad):
     close_rows(got["dinitial_state"], ref["dinitial_state"], "dinitial_state", 2)
 
 
+def sizes_of_da(dy, d, dS, scale):
+    """Per token and head the size that da's terms have: |S'| |adjoint of S'|, the norms of the
+    two matrices (in 64 bits) whose inner product it is."""
+    q, k, v, a, beta = (to64(d[n]) for n in ("q", "k", "v", "a", "beta"))
+    H = v.shape[2]
+    q, k = (np.repeat(t, H // t.shape[2], 2) for t in (q, k))
+    dy, S, mu, dec = to64(dy), to64(d["initial_state"]), to64(dS), []
+    for t in range(v.shape[1]):
+        S = S * np.exp(a[:, t])[..., None, None]
+        dec.append(np.sqrt((S ** 2).sum((-1, -2))))
+        e = v[:, t] - np.einsum("bhpn,bhn->bhp", S, k[:, t])
+        S = S + (beta[:, t][..., None] * e)[..., None] * k[:, t][..., None, :]
+    out = np.empty_like(a)
+    for t in reversed(range(v.shape[1])):
+        lam = mu + scale * dy[:, t][..., None] * q[:, t][..., None, :]
+        de = beta[:, t][..., None] * np.einsum("bhpn,bhn->bhp", lam, k[:, t])
+        lam = lam - de[..., None] * k[:, t][..., None, :]
+        out[:, t] = np.sqrt((lam ** 2).sum((-1, -2))) * dec[t]
+        mu = np.exp(a[:, t])[..., None, None] * lam
+    return out
+
+
+@pytest.mark.parametrize("decay", [0.1, 2, 8, 12, 20, 60])
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_backward_da_beside_its_own_size(cuda_lib, decay, dtype, grad):
+    """da_t is the inner product of S' = exp(a_t) S and its adjoint: off by the products' 2^-13 of
+    |S'| |adjoint|, which falls with exp(a_t), not of what the tokens around it have.  Between
+    strong decays every term holds one, so the bound is small beside the tensor's largest."""
+    d = make(2, 139, 4, 2, 40, 48, dtype=dtype, seed=22)
+    d["a"] = -decay * (0.9 + 0.2 * torch.rand(d["a"].shape, generator=torch.Generator().manual_seed(9)).to(DEV))
+    d["a"][:, ::9] = -0.01                                 # mild ones between them
+    dy, dS, got = check_bwd(d, grad, seed=10)
+    ref = oracle.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=0.7)
+    err = np.abs(to64(got["da"]) - ref["da"])
+    assert (err <= 2.0 ** -13 * sizes_of_da(dy, d, dS, 0.7)).all()
+
+
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_backward_da_at_resets(cuda_lib, dtype, grad):
+    """Packed sequences: where exp(a) is 0, da is 0, and a sequence's da does not hold rounding of
+    another one's that is 2^13 larger."""
+    d = make(1, 200, 2, 1, 64, 64, dtype=dtype, seed=23)
+    cuts = [5, 31, 32, 64, 70, 100, 127, 128, 163]
+    d["a"][:, cuts] = -INF
+    d["a"][:, 100] = -2e4
+    for i, (lo, hi) in enumerate(zip([0] + cuts, cuts + [200])):
+        if i % 2:
+            d["v"][:, lo:hi] *= 2.0 ** 13
+    dy, dS, got = check_bwd(d, grad, seed=11)
+    ref = oracle.delta_rule_bwd(dy, **d, dfinal_state=dS, scale=0.7)
+    assert not got["da"][:, cuts].any()
+    err = np.abs(to64(got["da"]) - ref["da"])
+    assert (err <= 2.0 ** -13 * sizes_of_da(dy, d, dS, 0.7)).all()
+
+
 def test_backward_tiny_gradients(cuda_lib):
     """Gradients of 1e-9, as behind a mean over a large batch: the scaled operands keep them."""
     d = make(1, 90, 2, 2, 64, 64, seed=13)
@@ -498,7 +554,6 @@ def right_or_not_finite(got, ref, what, elem, of_max):
         assert (np.abs(g - r)[ok] <= elem * np.abs(r[ok]) + of_max * M).all(), what
 
 
-INF, NAN = float("inf"), float("nan")
 BAD = [(n, t, x) for n in ("q", "k", "v", "beta", "a") for t in (52, 40, 75) for x in (INF, NAN)] + [
     ("initial_state", 3, INF), ("initial_state", 3, NAN)]
 
