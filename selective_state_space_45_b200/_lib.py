@@ -145,6 +145,13 @@ def _stream(stream, *tensors):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _fits(what, *sizes):
+    """Raise ValueError for a size that the library's int does not hold: ctypes would cut it down
+    to 32 bits without a word."""
+    if max(sizes) >= 2 ** 31:
+        raise ValueError("%s: at most 2^31 - 1, got %d" % (what, max(sizes)))
+
+
 _HERE_IS_FINE = contextlib.nullcontext()
 
 
@@ -173,6 +180,7 @@ def ssm_selective_scan_fwd(x, delta, delta_bias, delta_softplus, A, B, C, D, z, 
     D, delta_bias [dim]; final_state [batch, dim, N].  Writes y and final_state in place."""
     batch, dim, L = x.shape
     N = A.shape[1]
+    _fits("sizes", batch, dim, L)
     _check(load_library().ssm_selective_scan_fwd(
         _ptr(x), _ptr(delta), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(A), _ptr(B),
         _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(final_state), batch, dim, L, N,
@@ -185,6 +193,7 @@ def ssm_selective_scan_fwd_ex(x, delta, delta_bias, delta_softplus, A, B, C, D, 
     (see include/ssm.h); initial_state is [batch, dim, N] fp32 or None."""
     batch, dim, L = x.shape
     N = A.shape[1]
+    _fits("sizes", batch, dim, L)
     _check(load_library().ssm_selective_scan_fwd_ex(
         _ptr(x), _ptr(delta), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(A), _ptr(B),
         _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(final_state), _ptr(initial_state),
@@ -198,6 +207,7 @@ def ssm_selective_scan_fwd_noalloc(x, delta, delta_bias, delta_softplus, A, B, C
     arguments and results; long sequences use a fixed device array for their scratch."""
     batch, dim, L = x.shape
     N = A.shape[1]
+    _fits("sizes", batch, dim, L)
     _check(load_library().ssm_selective_scan_fwd_noalloc(
         _ptr(x), _ptr(delta), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(A), _ptr(B),
         _ptr(C), _ptr(D), _ptr(z), _ptr(y), _ptr(final_state), batch, dim, L, N,
@@ -208,6 +218,7 @@ def ssm_state_step(state, x, delta, A, B, C, D, z, y, stream=None):
     """One decode step (see include/ssm.h): state [batch, dim, N] fp32 updated in place;
     x, delta, z, y [batch, dim]; B, C [batch, N]."""
     batch, dim, N = state.shape
+    _fits("sizes", batch, dim, N)
     _check(load_library().ssm_state_step(
         _ptr(state), _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y),
         batch, dim, N, _DTYPE_CODE[x.dtype], _DTYPE_CODE[y.dtype], _stream(stream, state, y)))
@@ -218,6 +229,7 @@ def ssm_ssd_fwd(x, a, B, C, y, initial_state=None, final_state=None, stream=None
     heads] fp32; B, C [batch, L, heads, N] bf16; states [batch, heads, P, N] fp32."""
     batch, L, heads, P = x.shape
     N = B.shape[-1]
+    _fits("sizes", batch, L, heads, P)
     _check(load_library().ssm_ssd_fwd(
         _ptr(x), _ptr(a), _ptr(B), _ptr(C), _ptr(y), _ptr(initial_state), _ptr(final_state),
         batch, L, heads, P, N, _DTYPE_CODE[x.dtype], _DTYPE_CODE[y.dtype], _stream(stream, x, y)))
@@ -240,6 +252,7 @@ def ssm_state_step_multi(state, x, delta, A, B, C, D, z, y, stream=None):
     fp32 updated in place; x, delta, z, y [ntok, batch, dim]; B, C [ntok, batch, N]."""
     batch, dim, N = state.shape
     ntok = x.shape[0]
+    _fits("sizes", batch, dim, N, ntok)
     _check(load_library().ssm_state_step_multi(
         _ptr(state), _ptr(x), _ptr(delta), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z), _ptr(y),
         ntok, batch, dim, N, _DTYPE_CODE[x.dtype], _DTYPE_CODE[y.dtype], _stream(stream, state, y)))
@@ -253,6 +266,7 @@ def ssm_selective_scan_bwd(x, delta, delta_bias, delta_softplus, A, B, C, D, z, 
     arguments are None.  Writes the gradients in place."""
     batch, dim, L = x.shape
     N = A.shape[1]
+    _fits("sizes", batch, dim, L)
     _check(load_library().ssm_selective_scan_bwd(
         _ptr(x), _ptr(delta), _ptr(delta_bias), int(bool(delta_softplus)), _ptr(A), _ptr(B),
         _ptr(C), _ptr(D), _ptr(z), _ptr(initial_state), _ptr(dy), _ptr(dfinal_state),
@@ -293,6 +307,7 @@ def ssm_causal_conv1d_fwd(x, weight, bias, initial_window, u, final_window, silu
     [batch, dim, width-1] fp32 or None.  Writes u (and final_window) in place."""
     batch, dim, L = x.shape
     width = weight.shape[1]
+    _fits("sizes", batch, dim, L)
     _check(load_library().ssm_causal_conv1d_fwd(
         _ptr(x), _ptr(weight), _ptr(bias), _ptr(initial_window), _ptr(u), _ptr(final_window),
         batch, dim, L, width, int(bool(silu)), _DTYPE_CODE[x.dtype], _DTYPE_CODE[u.dtype],
@@ -304,6 +319,7 @@ def ssm_causal_conv1d_step(window, x, weight, bias, u, silu=True, stream=None):
     fp32 updated in place (may be None for width 1); x, u [batch, dim]."""
     batch, dim = x.shape
     width = weight.shape[1]
+    _fits("sizes", batch, dim)
     _check(load_library().ssm_causal_conv1d_step(
         _ptr(window), _ptr(x), _ptr(weight), _ptr(bias), _ptr(u), batch, dim, width,
         int(bool(silu)), _DTYPE_CODE[x.dtype], _DTYPE_CODE[u.dtype], _stream(stream, x, u)))
@@ -352,6 +368,13 @@ def _require(shapes):
                 raise ValueError("libssm needs CUDA tensors, got %s" % device)
         elif t.device != device:
             raise ValueError("%s is on %s, other tensors on %s" % (name, t.device, device))
+
+
+def _rows(x, dim):
+    """Rows of ``dim`` values."""
+    rows = x.numel() // dim if dim else 0
+    _fits("rows", rows)
+    return rows
 
 
 def _dtype_code(name, t):
@@ -482,7 +505,7 @@ def ssm_layer_norm_fwd(x, weight, bias, y, mean=None, rstd=None, eps=1e-5, strea
 
 def _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, dim, stream):
     _call_on(x, stream, "ssm_layer_norm_fwd", _at(x), _at(weight), _at(bias), _at(y), _at(mean),
-             _at(rstd), float(eps), x.numel() // dim if dim else 0, dim, _dtype_code("x", x), _dtype_code("y", y))
+             _at(rstd), float(eps), _rows(x, dim), dim, _dtype_code("x", x), _dtype_code("y", y))
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats=False, stream=None):
@@ -508,7 +531,7 @@ def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, 
     _require([("dy", dy, x.shape, dy.dtype), ("x", x, x.shape, x.dtype), ("weight", weight, (dim,), f32),
                     ("mean", mean, x.shape[:-1], f32), ("rstd", rstd, x.shape[:-1], f32),
                     ("dx", dx, x.shape, dy.dtype), ("dweight", dweight, (dim,), f32), ("dbias", dbias, (dim,), f32)])
-    rows = x.numel() // dim if dim else 0
+    rows = _rows(x, dim)
     _call_on(x, stream, "ssm_layer_norm_bwd", _at(dy), _at(x), _at(weight), _at(mean), _at(rstd),
              _at(dx), _at(dweight), _at(dbias), rows, dim, _dtype_code("x", x), _dtype_code("dy", dy),
              workspace=(rows, dim))

@@ -159,3 +159,47 @@ def test_binding_refuses_before_the_library():
             ssm.layer_norm(*args)
     with pytest.raises(ValueError):
         ssm.layer_norm_bwd(x, x, None, t(3), t(4))
+
+
+@pytest.mark.parametrize("rows", [2 ** 31, 2 ** 32, 2 ** 32 + 8])
+def test_norm_rows_past_32_bits_are_refused(monkeypatch, rows):
+    """A count of rows that the library's int does not hold raises; nothing is called with what is
+    left of it."""
+    from selective_state_space_45_b200 import _lib
+
+    called = []
+    monkeypatch.setattr(_lib, "_require", lambda shapes: None)
+    monkeypatch.setattr(_lib, "_call_on", lambda *a, **k: called.append(a))
+    x = torch.empty(rows, 8, dtype=torch.bfloat16, device="meta")
+    s = torch.empty(rows, device="meta")
+    monkeypatch.setattr(_lib, "_at", lambda t: None)
+    for call in (lambda: ssm.layer_norm(x), lambda: ssm.ssm_layer_norm_fwd(x, None, None, x),
+                 lambda: ssm.layer_norm_bwd(x, x, None, s, s), lambda: ssm.ssm_layer_norm_bwd(x, x, None, s, s, x)):
+        with pytest.raises(ValueError, match="rows: at most"):
+            call()
+    assert not called
+
+
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """The same for the lengths of the scan, the convolution and their decode forms."""
+    from selective_state_space_45_b200 import _lib
+
+    class Never:
+        def __getattr__(self, name):
+            raise AssertionError(name + " was called")
+
+    monkeypatch.setattr(_lib, "load_library", Never)
+    L = 2 ** 32
+    bf = dict(dtype=torch.bfloat16, device="meta")
+    x, B, h = torch.empty(1, 1, L, **bf), torch.empty(1, L, 1, **bf), torch.empty(L, 1, 1, device="meta")
+    A, xb, Bb = torch.empty(1, 1, device="meta"), torch.empty(L, 1, **bf), torch.empty(L, 1, **bf)
+    xs, Bs, a = torch.empty(1, L, 1, 32, **bf), torch.empty(1, L, 1, 64, **bf), torch.empty(1, L, 1, device="meta")
+    for call in (lambda: ssm.selective_scan(x, x, A, B, B), lambda: ssm.selective_scan_bwd(x, x, x, A, B, B),
+                 lambda: ssm.ssm_selective_scan_fwd(x, x, None, 0, A, B, B, None, None, x, None),
+                 lambda: ssm.ssm_selective_scan_fwd_noalloc(x, x, None, 0, A, B, B, None, None, x, None),
+                 lambda: ssm.ssm_state_step(h, xb, xb, A, Bb, Bb, None, None, xb),
+                 lambda: ssm.ssm_state_step_multi(h, xb[None], xb[None], A, Bb[None], Bb[None], None, None, xb[None]),
+                 lambda: ssm.causal_conv1d(x, A), lambda: ssm.ssm_causal_conv1d_step(None, xb, A, None, xb),
+                 lambda: ssm.ssd(xs, a, Bs, Bs)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
