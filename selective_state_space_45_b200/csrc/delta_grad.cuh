@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(Cfg::NT, Cfg::CTAS) delta_grad_kernel(const De
         const size_t gate = (size_t(b) * p.seqlen + t0 + (tid & 63)) * p.heads + h;
         float av = 0.f, bv = 0.f, last = 0.f;
         if (tid < nt) {
-            av = fmaxf(__ldg(p.a + gate), -1e4f);
+            av = __ldg(p.a + gate);
+            av = av < -1e4f ? -1e4f : av;                 // (fmaxf would drop a NaN)
             bv = __ldg(p.beta + gate);
         }
         // Scales as powers of two: per product the smallest over the parts (the products come out
