@@ -331,8 +331,8 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * two for each fp32 value, with fp32 accumulation: the final state and y come out as from fp32
  * arithmetic (about 2^-21 of their size), a bf16 y rounded once from that.
  * This holds for states that do not grow: a <= 0 and beta k.k in [0, 2].  Growth by up to 2^16
- * within a chunk costs nothing; by 2^g the terms of the chunk's first tokens keep about 38 - g
- * bits.
+ * within a chunk costs nothing; by 2^g the smallest terms of a chunk's sums keep about 38 - g
+ * bits beside the largest.
  * Rows of headdim are independent, whatever their sizes.  A value of v or of a state that is not
  * finite stays in its row and spreads there to the sequence's end and over its chunk of 32
  * tokens, earlier ones included; one of q, k, a or beta spreads over all rows.  What comes out

@@ -504,6 +504,30 @@ def test_backward_da_at_resets(cuda_lib, dtype, grad):
     assert (err <= 2.0 ** -13 * sizes_of_da(dy, d, dS, 0.7)).all()
 
 
+@pytest.mark.parametrize("doublings", [8, 16, 24])
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_growth_within_a_chunk(cuda_lib, doublings, dtype, grad):
+    """States that grow by 2^8, 2^16 and 2^24 within each chunk of 32 tokens.  What a chunk's first
+    token adds is by so much larger at its end than what the last one does, and two fp16 pieces
+    keep 38 - 24 = 14 bits of the smallest beside the largest: the bounds, relative to the largest
+    values, hold."""
+    d = make(1, 75, 2, 1, 32, 64, dtype=dtype, seed=24)
+    d["a"] = torch.full_like(d["a"], doublings * float(np.log(2)) / 32)
+    run_and_check(d, F32)
+    check_bwd(d, grad, seed=12)
+
+
+@pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
+def test_growth_across_segments(cuda_lib, dtype, grad):
+    """A long sequence of few heads whose states grow by 2^20 over each of its segments' 16 chunks
+    or more, the segments' maps with them."""
+    L = 2101
+    d = make(1, L, 2, 1, 32, 64, dtype=dtype, seed=25)
+    d["a"] = torch.full_like(d["a"], 20 * float(np.log(2)) / 512)
+    run_and_check(d, F32)
+    check_bwd(d, grad, seed=13)
+
+
 def test_backward_tiny_gradients(cuda_lib):
     """Gradients of 1e-9, as behind a mean over a large batch: the scaled operands keep them."""
     d = make(1, 90, 2, 2, 64, 64, seed=13)
@@ -579,7 +603,7 @@ def test_forward_not_finite(cuda_lib, name, at, value, dtype):
     assert y[:, :before].isfinite().all() and y[:, :, 1].isfinite().all() and S[:, 1].isfinite().all()
 
 
-@pytest.mark.parametrize("name,at,value", [b for b in BAD if b[0] != "a"] + [
+@pytest.mark.parametrize("name,at,value", BAD + [
     ("dy", 52, INF), ("dy", 40, NAN), ("dfinal_state", 3, INF), ("dfinal_state", 3, NAN)])
 @pytest.mark.parametrize("dtype,grad", [(BF16, BF16), (F32, F32)])
 def test_backward_not_finite(cuda_lib, name, at, value, dtype, grad):
