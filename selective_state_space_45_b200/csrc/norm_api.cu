@@ -28,8 +28,8 @@ template <bool BWD, typename F> int by_width(int dim, F f) {
     return f(integral_constant<int, 0>(), integral_constant<int, 2>(), (dim + 511) / 512 * 32);
 }
 
-// CTAs: one for the rows it takes, at most what the GPU's SMs hold at `per_sm` threads each
-// (the kernels' registers allow 512 of the widest variants; a CTA walks the rest of its rows).
+// CTAs: one for the rows it takes, at most what the GPU's SMs hold at `per_sm` threads each (a CTA
+// walks the rest of its rows).
 int grid_of(int lanes, int threads, int per_sm, int rows) {
     const int per_cta = lanes ? threads / lanes : 1;
     return std::min((rows - 1) / per_cta + 1, kSMs * std::max(1, per_sm / threads));
@@ -65,18 +65,24 @@ template <bool VEC, typename Tin, typename Tout> int run_fwd(const ssm::NormArgs
     });
 }
 
+// The backward's CTAs at most, whatever the types: what the workspace has room for.
+constexpr int kBwdPerSm = 512;
 int bwd_grid(int rows, int dim) {
-    return by_width<true>(dim, [&](auto lanes, auto, int threads) { return grid_of(lanes(), threads, 512, rows); });
+    return by_width<true>(dim, [&](auto lanes, auto, int threads) { return grid_of(lanes(), threads, kBwdPerSm, rows); });
 }
 
 template <bool VEC, typename Tin, typename Tg>
 int run_bwd(ssm::NormArgs a, float *dw, float *db, void *workspace, size_t bytes, cudaStream_t s) {
-    const int grid = bwd_grid(int(a.rows), a.dim);
+    int grid = 0;
     Scratch ws;
     if (const int st = ws.take(workspace, bytes, ssm_layer_norm_bwd_workspace(int(a.rows), a.dim), s)) return st;
     a.part = reinterpret_cast<float *>(ws.p);
     int st = by_width<true>(a.dim, [&](auto lanes, auto v, int threads) {
         auto kernel = ssm::layer_norm_bwd_kernel<lanes(), v(), VEC, Tin, Tg>;
+        // one wave: rows of 257 to 512 values with an fp32 side take 150 registers a thread, which one
+        // CTA of 256 fits and two do not (65536 rows of 512, fp32: 92.0 us in two waves, 83.2 so)
+        static const int per_sm = std::min(kBwdPerSm, resident(kernel));
+        grid = grid_of(lanes(), threads, per_sm, int(a.rows));
         kernel<<<grid, threads, lanes() ? 2 * size_t(a.dim) * sizeof(float) : 0, s>>>(a);
         return status_of(cudaGetLastError());
     });
