@@ -338,9 +338,10 @@ int ssm_ssd_fwd(const void *x, const float *a, const void *B, const void *C, voi
  * tokens, earlier ones included; one of q, k, a or beta spreads over all rows.  What comes out
  * finite is right.  Long sequences of few heads are cut into segments that run at once (the sizes alone
  * decide); a segment's map of start states must then be finite too.
- * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): about
- * 224 bytes per token and head, the keys and queries again (as fp16, twice for fp32), and for
- * each segment and head 4 * (headdim + dstate) * dstate bytes.
+ * seqlen = 0 copies the start state through.  Takes scratch (see the conventions above): 224
+ * bytes per token and head, 4 dstate' + 32 bytes per token and key head (twice that for fp32
+ * inputs; dstate' = dstate rounded up to 32), tokens rounded up to 32, and for each segment and
+ * head 4 * (headdim + dstate) * dstate bytes.
  */
 int ssm_delta_rule_fwd(const void *q, const void *k, const void *v, const float *a, const float *beta,
                        void *y, const float *initial_state, float *final_state, float scale,
@@ -383,10 +384,13 @@ int ssm_delta_rule_step(float *state, const void *q, const void *k, const void *
  *   dinitial_state: [batch][heads][headdim][dstate] fp32 or NULL.
  * Every sum has a fixed order: results are deterministic.  A value that is not finite spreads over
  * its chunk of 64 tokens here, over all of dq, dk, da and dbeta; what comes out finite is right.
- * Takes scratch (see the conventions above) of about 8 * batch * heads * headdim' * (seqlen + dstate * (seqlen / 64 + 2))
- * bytes, headdim' = headdim rounded up to 64: mostly e, w and the state and its gradient every
- * 64 tokens; and what the forward takes for segments, into which long sequences of few heads
- * are cut here too.
+ * da_t is as exact beside its own size, which falls with exp(a_t), as the other results are
+ * beside theirs, and 0 where exp(a_t) is.
+ * Takes scratch (see the conventions above): the forward's, and per token and head
+ * 10 headdim' + headdim' dstate' / 8 bytes (12 headdim' for fp32 gradients; headdim' = headdim
+ * rounded up to 64): e, w and dy, and the state and its gradient every 64 tokens, at a sequence's
+ * ends too.  Heads that share a key head take 8 dstate bytes more per token and key head.
+ * 8 x 2048 tokens of 24 heads of 64 x 128 in bf16 take 0.97 GB.
  * seqlen = 0 writes dinitial_state = dfinal_state.
  */
 int ssm_delta_rule_bwd(const void *q, const void *k, const void *v, const float *a, const float *beta,

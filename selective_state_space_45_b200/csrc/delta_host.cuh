@@ -91,26 +91,27 @@ int dispatch_chain(const ssm::DeltaArgs &a, cudaStream_t s, int nseg = 1) {
 // How many segments a sequence is cut into.  A chain's chunks follow one another, so with few
 // heads most of the GPU is idle.  Segments run at once: first every segment's end state from a
 // zero start and its map (dstate more rows), then, from the folded start states, the outputs.
-// In units of a chunk's time in a CTA (1.5 us; 0.9 of it without outputs): two CTAs on an SM take
-// 1.9, more share it; fp32 inputs leave room for one CTA.  Folding costs about four units a
-// segment.  Segments have at least 16 chunks, and what they save must be a tenth.  32749 tokens
-// of 16 heads of 128 x 128: one piece 1565 us, five 1044 us, nine 850 us (and 94 us for the
-// chunk blocks).  The backward's two passes take 1.3 and 1.55 units a chunk, and its segments
-// need their gradients of the start states (1.1) and a second fold too: 8192 tokens of 8 heads of
-// 128 x 128, 1505 us in one piece, 584 in segments; 2 x 4096 of 12 heads of 64 x 128, 803 and 489.
+// In units of a chunk's time in a CTA (2.0 us; 0.8 of it for end states and maps): two CTAs on an
+// SM take 1.8, more share it; fp32 inputs leave room for one CTA.  Folding costs about four units
+// a segment.  Segments have at least 16 chunks, and what they save must be a tenth.  32749 tokens
+// of 16 heads of 128 x 128: one piece 2090 us, nine segments 1088; 8 heads 2046 and 633; 8192
+// tokens of 8 heads in fp32, 726 and 357.  The backward's two passes take 2.5 units a chunk
+// together, and its segments need their gradients of the start states (1.1) and a second fold too:
+// 8192 tokens of 8 heads of 128 x 128, 1455 us in one piece, 689 in segments; 2 x 4096 of 12 heads
+// of 64 x 128, 835 and 599.
 inline int segments(int batch, int seqlen, int heads, int P, int N, bool one_per_sm, bool backward) {
     const long long chunks = (long long)delta_chunks(seqlen), all = (long long)batch * heads;
     auto cost = [&](double ctas) {
         const double r = ctas / 148;
-        return r <= 1 ? 1.0 : one_per_sm ? std::ceil(r) : r <= 2 ? 1.9 : r;
+        return r <= 1 ? 1.0 : one_per_sm ? std::ceil(r) : r <= 2 ? 1.8 : 0.9 * r;
     };
     const double rows = double(all) * delta_slices(P), maps = double(all) * delta_slices(N);
-    const double last = backward ? 2.85 : 1.0;
+    const double last = backward ? 2.5 : 1.0;
     int best = 1;
     double least = chunks * last * cost(rows);
     const double bar = 0.9 * least;
     for (int n = 2; n <= 64 && chunks / n >= 16; ++n) {
-        const double t = double((chunks + n - 1) / n) * (0.9 * cost((n - 1) * rows + (n - 2) * maps) +
+        const double t = double((chunks + n - 1) / n) * (0.8 * cost((n - 1) * rows + (n - 2) * maps) +
                                                          (backward ? 1.1 * cost((n - 1) * rows) : 0.0) + last * cost(n * rows)) +
                          (backward ? 8 : 4) * n;
         if (t < bar && t < least) { least = t; best = n; }

@@ -21,13 +21,15 @@
 // rows in the chains instead cost 1100 of 3700 cycles a chunk; a fifth warp for the copies
 // costs the others the registers that they need (168 instead of 255: spills).
 //
-// What bounds it: the chain of dependent products of a chunk, not HBM and not the rate of the
-// tensor cores.  bf16, dstate 128: a chunk takes 1.5 us in a CTA that has its SM to itself
-// and 2.9 us where two share one; 8 x 2048 tokens x 24 heads of 64 x 128 (192 CTAs) 185 us, and
-// the prep kernel 99 us (74% of HBM's copy rate: it writes the blocks and the operands).
-// mma.sync rather than tcgen05: the state and its products stay in registers with the warp that
-// needs them next, where tensor memory would put a round trip behind each of the four products
-// of a chunk, and one warp's tiles are 16 rows.
+// What bounds it.  bf16, dstate 128: a chunk takes 2.0 us in a CTA that has its SM to itself and
+// 3.6 us where two share one; 8 x 2048 tokens x 24 heads of 64 x 128 (192 CTAs) 226 us, and the
+// prep kernel 102 us (75% of HBM's copy rate: it writes the blocks and the operands).  Alone, the
+// mma.sync pipe is active for 51% of the time and half of the warps' cycles go to the fixed
+// latencies of dependent instructions.  Two warps on a scheduler overlap those, but then meet in
+// the pipe (59% active, a fifth of the cycles waiting for it; the products of a chunk come in
+// bursts), which is most of the 1.8.  Shared memory (48% of its wavefronts) and HBM are not it.
+// mma.sync rather than tcgen05 was chosen to keep the state and its products in registers with
+// the warp that needs them next; the other has not been measured.
 //
 // The reverse pass runs the same chain backwards on the state's gradient dS, with dO = dy:
 //     rhs = end (dS k) + Pm^T dO,  du = rhs - G^T (beta rhs),  dv = w = beta du,
@@ -44,7 +46,9 @@
 // never meet, in range no more than in value: a row's inf or NaN stays in its row.  bf16
 // inputs are then exact; fp32 operands go in as two fp16 values (22 bits or more), whatever
 // the type of y: one behind a bf16 y made 11% of its values round the other way (8 x 2048
-// tokens x 24 heads of 64 x 128: 280 us with the call, 312 with two).  Three bf16 pieces hold
+// tokens x 24 heads of 64 x 128: 280 us with the call, 312 with two).  The product of two second
+// pieces is left out.  An fp32 y and state then come out at 5e-7 of the definition in 64 bits,
+// gradients at 8e-7, where torch's fp32 products give 2e-7 and 4e-7.  Three bf16 pieces hold
 // the same bits but cost half as many products again; two bf16 pieces gave 6e-6.
 #pragma once
 

@@ -48,7 +48,7 @@ const char *ssm_status_string(int status) {
     case SSM_ERR_ALIGNMENT: return "pointer not 16-byte aligned";
     case SSM_ERR_CUDA: return "CUDA runtime error at launch";
     case SSM_ERR_SCRATCH:
-        return "the allocation-free scan needs more scratch than its fixed 4 MiB device array";
+        return "scratch too small (a given workspace, or the allocation-free scan's fixed 4 MiB device array)";
     default: return "unknown status";
     }
 }

@@ -203,3 +203,24 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
                  lambda: ssm.ssd(xs, a, Bs, Bs)):
         with pytest.raises(ValueError, match="2\\^31"):
             call()
+
+
+def test_scratch_status_names_both_causes():
+    ssm_build.build()
+    text = ssm.ssm_status_string(SCR)
+    assert "workspace" in text and "allocation-free" in text
+
+
+@pytest.mark.parametrize("kw", [dict(batch=8, L=2048, H=24, K=24), dict(batch=3, L=1021, H=8, K=4, P=128, N=64, din=0, dout=0),
+                                dict(batch=8, L=2048, H=24, K=24, P=64, N=64, din=0, dout=0), dict(batch=2, L=4096, H=48, K=48, P=8)])
+def test_scratch_is_what_the_header_says(lib, kw):
+    """The sums that include/ssm.h states, for sizes that are not cut into segments: within 5%
+    above for the rest (a few values per chunk, a chunk's and a span's ends)."""
+    a = {**SIZES, **kw}
+    tok, P, N = a["batch"] * a["L"], -(-a["P"] // 64) * 64, -(-a["N"] // 32) * 32
+    rows = a["K"] * (4 * N + 32) * (2 if a["din"] == ssm.SSM_F32 else 1)
+    bwd = a["H"] * (224 + (12 if a["dout"] == ssm.SSM_F32 else 10) * P + P * N / 8) + rows
+    bwd += 8 * a["N"] * a["K"] if a["H"] > a["K"] else 0
+    for got, want in ((lib.ssm_delta_rule_fwd_workspace(*_sizes(a)), tok * (224 * a["H"] + rows)),
+                      (lib.ssm_delta_rule_bwd_workspace(*_sizes(a)), tok * bwd)):
+        assert want <= got <= 1.05 * want

@@ -10,6 +10,7 @@ Bounds, derived before the first run (per output tensor, M = max|ref|, u(t) = ha
   * a bf16 y: u = 2^-8 of the value, and behind it one fp16 piece per operand (2^-12 each, two
     operands): |err| <= 2^-8 |ref| + 2^-10 M.  bf16 dq, dk chain two such products (four
     roundings): 2^-8 |ref| + 2^-9 M.  bf16 dv is an fp32 value rounded: 2^-8 |ref| + 2^-13 M.
+    (The kernels have taken two pieces there, too, since; the tests of rounded values hold them to it.)
   * decode tokens are fp32 arithmetic throughout: sums of 128 terms, 128 * 2^-24 = 2^-17 at
     worst per token: |err| <= 2^-16 M (+ u |ref|).
 """
