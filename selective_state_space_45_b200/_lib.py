@@ -152,19 +152,19 @@ def _fits(what, *sizes):
         raise ValueError("%s: at most 2^31 - 1, got %d" % (what, max(sizes)))
 
 
-_HERE_IS_FINE = contextlib.nullcontext()
-
-
-def _allocating_on(stream, like):
-    """The context in which a call on ``stream`` takes its memory: torch's allocator hands a block
-    out again to the stream that it was taken on, so outputs and scratch have to be of the
-    stream whose kernels write them."""
-    if stream is None or not like.is_cuda:
-        return _HERE_IS_FINE
+def _current(stream, like):
+    """The context that makes ``stream`` (of torch, or a handle) current on ``like``'s device.  A
+    call that is given a stream runs whole in it: torch's allocator hands a block out again to
+    the stream that it was taken on, so outputs and scratch have to be of the stream whose
+    kernels write them."""
+    if not like.is_cuda:
+        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         # (an external stream of handle 0 would be some stream of torch's pool)
         stream = (torch.cuda.ExternalStream(raw, device=like.device) if raw else torch.cuda.default_stream(like.device))
+    if stream.device != like.device:
+        raise ValueError("a stream of %s for tensors on %s" % (stream.device, like.device))
     return torch.cuda.stream(stream)
 
 
@@ -236,13 +236,14 @@ def ssm_ssd_fwd(x, a, B, C, y, initial_state=None, final_state=None, stream=None
 
 
 def ssd(x, a, B, C, initial_state=None, out_dtype=None, return_final_state=True, stream=None):
-    """Allocate y (and the final state) with torch, on ``stream`` if one is given, and run
-    ``ssm_ssd_fwd``."""
+    """Allocate y (and the final state) with torch and run ``ssm_ssd_fwd``."""
+    if stream is not None:
+        with _current(stream, x):
+            return ssd(x, a, B, C, initial_state, out_dtype, return_final_state)
     batch, L, heads, P = x.shape
-    with _allocating_on(stream, x):
-        y = torch.empty(x.shape, device=x.device, dtype=out_dtype or torch.float32)
-        fs = (torch.empty((batch, heads, P, B.shape[-1]), device=x.device, dtype=torch.float32)
-              if return_final_state else None)
+    y = torch.empty(x.shape, device=x.device, dtype=out_dtype or torch.float32)
+    fs = (torch.empty((batch, heads, P, B.shape[-1]), device=x.device, dtype=torch.float32)
+          if return_final_state else None)
     ssm_ssd_fwd(x, a, B, C, y, initial_state, fs, stream)
     return (y, fs) if return_final_state else y
 
@@ -280,20 +281,22 @@ def selective_scan_bwd(dy, x, delta, A, B, C, D=None, z=None, delta_bias=None,
     """Allocate the gradients with torch (dy's dtype for the tensor gradients) and run the
     backward; returns a dict dx, ddelta, dz, dA, dB, dC, dD, ddelta_bias, dinitial_state
     (None where the input was absent)."""
+    if stream is not None:
+        with _current(stream, x):
+            return selective_scan_bwd(dy, x, delta, A, B, C, D, z, delta_bias, delta_softplus, initial_state, dfinal_state)
     batch, dim, L = x.shape
     N = A.shape[1]
     dev, gd, f32 = x.device, dy.dtype, torch.float32
-    with _allocating_on(stream, x):
-        g = dict(dx=torch.empty((batch, dim, L), device=dev, dtype=gd),
-                 ddelta=torch.empty((batch, dim, L), device=dev, dtype=gd),
-                 dz=None if z is None else torch.empty((batch, dim, L), device=dev, dtype=gd),
-                 dA=torch.empty((dim, N), device=dev, dtype=f32),
-                 dB=torch.empty((batch, L, N), device=dev, dtype=gd),
-                 dC=torch.empty((batch, L, N), device=dev, dtype=gd),
-                 dD=None if D is None else torch.empty(dim, device=dev, dtype=f32),
-                 ddelta_bias=None if delta_bias is None else torch.empty(dim, device=dev, dtype=f32),
-                 dinitial_state=None if initial_state is None else
-                 torch.empty((batch, dim, N), device=dev, dtype=f32))
+    g = dict(dx=torch.empty((batch, dim, L), device=dev, dtype=gd),
+             ddelta=torch.empty((batch, dim, L), device=dev, dtype=gd),
+             dz=None if z is None else torch.empty((batch, dim, L), device=dev, dtype=gd),
+             dA=torch.empty((dim, N), device=dev, dtype=f32),
+             dB=torch.empty((batch, L, N), device=dev, dtype=gd),
+             dC=torch.empty((batch, L, N), device=dev, dtype=gd),
+             dD=None if D is None else torch.empty(dim, device=dev, dtype=f32),
+             ddelta_bias=None if delta_bias is None else torch.empty(dim, device=dev, dtype=f32),
+             dinitial_state=None if initial_state is None else
+             torch.empty((batch, dim, N), device=dev, dtype=f32))
     ssm_selective_scan_bwd(x, delta, delta_bias, delta_softplus, A, B, C, D, z, initial_state,
                            dy, dfinal_state, g["dx"], g["ddelta"], g["dA"], g["dB"], g["dC"],
                            g["dD"], g["dz"], g["ddelta_bias"], g["dinitial_state"], stream)
@@ -328,11 +331,13 @@ def ssm_causal_conv1d_step(window, x, weight, bias, u, silu=True, stream=None):
 def causal_conv1d(x, weight, bias=None, initial_window=None, silu=True, out_dtype=None,
                   return_final_window=False, stream=None):
     """Allocate u (and the final window) with torch and run the convolution."""
+    if stream is not None:
+        with _current(stream, x):
+            return causal_conv1d(x, weight, bias, initial_window, silu, out_dtype, return_final_window)
     batch, dim, L = x.shape
-    with _allocating_on(stream, x):
-        u = torch.empty((batch, dim, L), device=x.device, dtype=out_dtype or x.dtype)
-        fw = (torch.empty((batch, dim, weight.shape[1] - 1), device=x.device, dtype=torch.float32)
-              if return_final_window else None)
+    u = torch.empty((batch, dim, L), device=x.device, dtype=out_dtype or x.dtype)
+    fw = (torch.empty((batch, dim, weight.shape[1] - 1), device=x.device, dtype=torch.float32)
+          if return_final_window else None)
     ssm_causal_conv1d_fwd(x, weight, bias, initial_window, u, fw, silu, stream)
     return (u, fw) if return_final_window else u
 
@@ -341,11 +346,14 @@ def selective_scan(x, delta, A, B, C, D=None, z=None, delta_bias=None, delta_sof
                    out_dtype=None, return_final_state=True, initial_state=None, zoh_exact=False,
                    stream=None):
     """Allocate y (and the final state) with torch and run the scan."""
+    if stream is not None:
+        with _current(stream, x):
+            return selective_scan(x, delta, A, B, C, D, z, delta_bias, delta_softplus, out_dtype, return_final_state,
+                                  initial_state, zoh_exact)
     batch, dim, L = x.shape
-    with _allocating_on(stream, x):
-        y = torch.empty((batch, dim, L), device=x.device, dtype=out_dtype or x.dtype)
-        fs = (torch.empty((batch, dim, A.shape[1]), device=x.device, dtype=torch.float32)
-              if return_final_state else None)
+    y = torch.empty((batch, dim, L), device=x.device, dtype=out_dtype or x.dtype)
+    fs = (torch.empty((batch, dim, A.shape[1]), device=x.device, dtype=torch.float32)
+          if return_final_state else None)
     ssm_selective_scan_fwd_ex(x, delta, delta_bias, delta_softplus, A, B, C, D, z, y, fs,
                               initial_state, zoh_exact, stream)
     return (y, fs) if return_final_state else y
@@ -373,7 +381,8 @@ def _require(shapes):
 def _rows(x, dim):
     """Rows of ``dim`` values."""
     rows = x.numel() // dim if dim else 0
-    _fits("rows", rows)
+    if rows >= 2 ** 31:
+        _fits("rows", rows)
     return rows
 
 
@@ -391,19 +400,19 @@ def _at(t):
 def _call_on(like, stream, name, *args, workspace=None):
     """Run a library call with ``like``'s device current (its kernels and scratch live there).  Scratch
     comes from torch's allocator, on the stream that the call runs on."""
+    if stream is not None:
+        with _current(stream, like):
+            return _call_on(like, None, name, *args, workspace=workspace)
     index = like.device.index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _call_on(like, stream, name, *args, workspace=workspace)
+            return _call_on(like, None, name, *args, workspace=workspace)
     lib = _lib or load_library()
     if workspace is not None:
         nbytes = getattr(lib, name + "_workspace")(*workspace)
-        with _allocating_on(stream, like):
-            ws = like.new_empty(nbytes, dtype=torch.uint8)
+        ws = like.new_empty(nbytes, dtype=torch.uint8)
         args += (ws.data_ptr() if nbytes else None, nbytes)
-    raw = (torch._C._cuda_getCurrentRawStream(index) if stream is None else
-           stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
-    _check(getattr(lib, name)(*args, raw))
+    _check(getattr(lib, name)(*args, torch._C._cuda_getCurrentRawStream(index)))
 
 
 def _delta_dims(q, k, v):
@@ -436,10 +445,12 @@ def ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state=None, final_state=None
 def delta_rule(q, k, v, a, beta, initial_state=None, scale=1.0, out_dtype=None, return_final_state=True,
                stream=None):
     """Allocate y (and the final state) with torch and run ``ssm_delta_rule_fwd``."""
+    if stream is not None:
+        with _current(stream, v):
+            return delta_rule(q, k, v, a, beta, initial_state, scale, out_dtype, return_final_state)
     _delta_dims(q, k, v)
-    with _allocating_on(stream, v):
-        y = torch.empty_like(v, dtype=out_dtype)
-        fs = a.new_empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1])) if return_final_state else None
+    y = torch.empty_like(v, dtype=out_dtype)
+    fs = a.new_empty((v.shape[0], v.shape[2], v.shape[3], k.shape[-1])) if return_final_state else None
     ssm_delta_rule_fwd(q, k, v, a, beta, y, initial_state, fs, scale, stream)
     return (y, fs) if return_final_state else y
 
@@ -457,8 +468,10 @@ def ssm_delta_rule_step(state, q, k, v, a, beta, y, scale=1.0, stream=None):
 
 def delta_rule_step(state, q, k, v, a, beta, scale=1.0, out_dtype=None, stream=None):
     """Allocate y with torch and run ``ssm_delta_rule_step``."""
-    with _allocating_on(stream, v):
-        y = torch.empty_like(v, dtype=out_dtype)
+    if stream is not None:
+        with _current(stream, v):
+            return delta_rule_step(state, q, k, v, a, beta, scale, out_dtype)
+    y = torch.empty_like(v, dtype=out_dtype)
     ssm_delta_rule_step(state, q, k, v, a, beta, y, scale, stream)
     return y
 
@@ -484,10 +497,12 @@ def ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, dq, dk
 def delta_rule_bwd(dy, q, k, v, a, beta, initial_state=None, dfinal_state=None, scale=1.0, stream=None):
     """Allocate the gradients with torch and run ``ssm_delta_rule_bwd``; returns a dict dq, dk,
     dv (dy's dtype), da, dbeta, dinitial_state (fp32; None without an initial_state)."""
-    with _allocating_on(stream, v):
-        g = dict(dq=torch.empty_like(q, dtype=dy.dtype), dk=torch.empty_like(k, dtype=dy.dtype),
-                 dv=torch.empty_like(v, dtype=dy.dtype), da=torch.empty_like(a), dbeta=torch.empty_like(beta),
-                 dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
+    if stream is not None:
+        with _current(stream, v):
+            return delta_rule_bwd(dy, q, k, v, a, beta, initial_state, dfinal_state, scale)
+    g = dict(dq=torch.empty_like(q, dtype=dy.dtype), dk=torch.empty_like(k, dtype=dy.dtype),
+             dv=torch.empty_like(v, dtype=dy.dtype), da=torch.empty_like(a), dbeta=torch.empty_like(beta),
+             dinitial_state=None if initial_state is None else torch.empty_like(initial_state))
     ssm_delta_rule_bwd(q, k, v, a, beta, initial_state, dy, dfinal_state, g["dq"], g["dk"], g["dv"], g["da"],
                        g["dbeta"], g["dinitial_state"], scale, stream)
     return g
@@ -511,13 +526,15 @@ def _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, dim, stream):
 def layer_norm(x, weight=None, bias=None, eps=1e-5, out_dtype=None, return_stats=False, stream=None):
     """Allocate y (and mean, rstd) with torch and run the layer norm; returns y, or (y, mean,
     rstd) for the backward."""
+    if stream is not None:
+        with _current(stream, x):
+            return layer_norm(x, weight, bias, eps, out_dtype, return_stats)
     shape = x.shape
     mean, rstd = None, None
-    with _allocating_on(stream, x):
-        y = torch.empty_like(x, dtype=out_dtype)
-        if return_stats:
-            mean = x.new_empty(shape[:-1], dtype=torch.float32)
-            rstd = torch.empty_like(mean)
+    y = torch.empty_like(x, dtype=out_dtype)
+    if return_stats:
+        mean = x.new_empty(shape[:-1], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
     _require((("x", x, shape, x.dtype), ("weight", weight, shape[-1:], torch.float32),
                     ("bias", bias, shape[-1:], torch.float32)))
     _layer_norm_fwd(x, weight, bias, y, mean, rstd, eps, shape[-1], stream)
@@ -540,8 +557,10 @@ def ssm_layer_norm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, 
 def layer_norm_bwd(dy, x, weight, mean, rstd, stream=None):
     """Allocate the gradients with torch and run ``ssm_layer_norm_bwd``; returns a dict dx
     (dy's dtype), dweight, dbias (fp32)."""
-    with _allocating_on(stream, x):
-        dw = x.new_empty(x.shape[-1:], dtype=torch.float32)
-        g = dict(dx=torch.empty_like(dy), dweight=dw, dbias=torch.empty_like(dw))
+    if stream is not None:
+        with _current(stream, x):
+            return layer_norm_bwd(dy, x, weight, mean, rstd)
+    dw = x.new_empty(x.shape[-1:], dtype=torch.float32)
+    g = dict(dx=torch.empty_like(dy), dweight=dw, dbias=torch.empty_like(dw))
     ssm_layer_norm_bwd(dy, x, weight, mean, rstd, g["dx"], g["dweight"], g["dbias"], stream)
     return g

@@ -224,3 +224,18 @@ def test_scratch_is_what_the_header_says(lib, kw):
     for got, want in ((lib.ssm_delta_rule_fwd_workspace(*_sizes(a)), tok * (224 * a["H"] + rows)),
                       (lib.ssm_delta_rule_bwd_workspace(*_sizes(a)), tok * bwd)):
         assert want <= got <= 1.05 * want
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """The call would run on another stream than the given one."""
+    from selective_state_space_45_b200 import _lib
+
+    class On:
+        is_cuda, device = True, torch.device("cuda", 1)
+
+    class Stream:
+        device = torch.device("cuda", 0)
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    with pytest.raises(ValueError, match="stream of cuda:0"):
+        _lib._current(Stream(), On)
