@@ -574,7 +574,7 @@ def test_results_do_not_vary(cuda_lib):
 def right_or_not_finite(got, ref, what, elem, of_max):
     """Where a result is finite it is the right one."""
     g, r = to64(got), np.asarray(ref)
-    ok, M = np.isfinite(g), np.abs(r[np.isfinite(r)]).max()
+    ok, M = np.isfinite(g), np.abs(r[np.isfinite(r)]).max(initial=0)
     with np.errstate(invalid="ignore"):
         assert (np.abs(g - r)[ok] <= elem * np.abs(r[ok]) + of_max * M).all(), what
 
@@ -621,6 +621,26 @@ def test_backward_not_finite(cuda_lib, name, at, value, dtype, grad):
     for n in got:
         right_or_not_finite(got[n], ref[n], n, 2.0 ** -8 if got[n].dtype == BF16 else 0, 2.0 ** -12)
         assert (got[n][:, 1] if n == "dinitial_state" else got[n][:, :, 1]).isfinite().all(), n
+
+
+@pytest.mark.parametrize("name,value", [(n, x) for n in ("q", "k", "v", "beta", "a", "initial_state") for x in (INF, NAN)])
+def test_not_finite_in_segments(cuda_lib, name, value):
+    """The same in a long sequence whose segments run at once, with their maps."""
+    d = make(1, 2101, 2, 1, 32, 64, dtype=F32, seed=26, decay=0.02)
+    at = (0, 0, 3, 5) if name == "initial_state" else (0, 1200, 0) + (7,) * (d[name].dim() - 3)
+    d[name][at] = value
+    dy = torch.randn(d["v"].shape, generator=torch.Generator().manual_seed(14)).to(DEV)
+    y, S = ssm.delta_rule(**d, scale=0.7)
+    got = ssm.delta_rule_bwd(dy, **d, scale=0.7)
+    with np.errstate(invalid="ignore", over="ignore"):
+        yr, Sr = oracle.delta_rule(**d, scale=0.7)
+        ref = oracle.delta_rule_bwd(dy, **d, scale=0.7)
+    right_or_not_finite(y, yr, "y", 0, 2.0 ** -13)
+    right_or_not_finite(S, Sr, "final state", 0, 2.0 ** -13)
+    for n in got:
+        right_or_not_finite(got[n], ref[n], n, 0, 2.0 ** -12)
+    if name != "initial_state":
+        assert y[:, :1184].isfinite().all()
 
 
 # ---- streams and graphs --------------------------------------------------------------------
